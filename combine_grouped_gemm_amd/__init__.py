@@ -21,19 +21,25 @@ __all__ = ["MoeError", "lib", "library_path", "moe_version", "moe_route",
            "moe_ffn_workspace_bytes", "moe_ffn_gate_up", "moe_ffn_down",
            "moe_grouped_ffn", "moe_combine", "moe_layout_masked", "moe_ffn_gate_up_masked",
            "moe_ffn_down_masked", "moe_grouped_ffn_masked", "moe_route_mapped", "moe_eplb_place", "moe_route_shared",
+           "moe_route_scored", "moe_quant_rows", "moe_quant_rows_masked",
            "moe_weight_ld", "moe_packed_weight_bytes", "moe_pack_weights",
-           "MOE_F32", "MOE_BF16", "MOE_FP8_E4M3", "MOE_FP8_E4M3_PO2", "MOE_W_PACKED",
+           "MOE_F32", "MOE_BF16", "MOE_FP8_E4M3", "MOE_FP8_E4M3_PO2", "MOE_INT8", "MOE_W_PACKED",
+           "MOE_SCORE_SOFTMAX", "MOE_SCORE_SIGMOID",
            "MoELayer"]
 
 MOE_OK, MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED, MOE_ERR_HIP = 0, 1, 2, 3
-MOE_F32, MOE_BF16, MOE_FP8_E4M3, MOE_FP8_E4M3_PO2 = 0, 1, 2, 3
+MOE_F32, MOE_BF16, MOE_FP8_E4M3, MOE_FP8_E4M3_PO2, MOE_INT8 = 0, 1, 2, 3, 4
+MOE_SCORE_SOFTMAX, MOE_SCORE_SIGMOID = 0, 1
 MOE_W_PACKED = 0x100
 FP8_BLOCK = 128
 MAX_SEGMENTS = 64
+INT8_MAX_COLS = 131056       # largest H and I of int8 operands (exact int32 sums)
 
-_DT = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16, torch.float8_e4m3fn: MOE_FP8_E4M3}
+_DT = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16, torch.float8_e4m3fn: MOE_FP8_E4M3,
+       torch.int8: MOE_INT8}
 _TORCH = {v: k for k, v in _DT.items()}
-_NAMES = {"f32": MOE_F32, "bf16": MOE_BF16, "fp8": MOE_FP8_E4M3}
+_NAMES = {"f32": MOE_F32, "bf16": MOE_BF16, "fp8": MOE_FP8_E4M3, "int8": MOE_INT8}
+_SCORES = {"softmax": MOE_SCORE_SOFTMAX, "sigmoid": MOE_SCORE_SIGMOID}
 
 library_path = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libmoeep.so")
 _lib = None
@@ -60,6 +66,7 @@ def lib() -> ctypes.CDLL:
                            "'python -m combine_grouped_gemm_amd.build'")
     L = ctypes.CDLL(library_path)
     P, I, Z, S = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t, ctypes.c_int
+    F = ctypes.c_float
     sig = {
         "moe_status_string": ([I], ctypes.c_char_p),
         "moe_last_error": ([], ctypes.c_char_p),
@@ -78,6 +85,9 @@ def lib() -> ctypes.CDLL:
         "moe_route_mapped": ([P, I, I, I, P, P, P, P], S),
         "moe_eplb_place": ([P, I, I, P], S),
         "moe_route_shared": ([P, I, I, I, I, P, P, P], S),
+        "moe_route_scored": ([P, I, P, I, I, I, I, I, I, I, I, F, P, I, P, P, P], S),
+        "moe_quant_rows": ([P, I, P, I, I, I, P, P, P], S),
+        "moe_quant_rows_masked": ([P, I, P, I, I, I, P, P, P], S),
         "moe_weight_ld": ([I, I], I),
         "moe_packed_weight_bytes": ([I, I, I, I], Z),
         "moe_pack_weights": ([P, I, I, I, I, P, P], S),
@@ -134,6 +144,13 @@ def _need(t, name, numel=None, shape=None):
         raise ValueError(f"{name} must have shape {tuple(shape)} (got {tuple(t.shape)})")
     if numel is not None and t.numel() < numel:
         raise ValueError(f"{name} needs at least {numel} elements (got {t.numel()})")
+
+
+def _same_device(t, name, *others):
+    """Every tensor of a call lives on the device of its first one (None: not given)."""
+    for o in others:
+        if o is not None and o.device != t.device:
+            raise ValueError(f"all tensors must be on {name}'s device {t.device} (got {o.device})")
 
 
 def _dtype_code(d):
@@ -202,6 +219,46 @@ def moe_route_shared(logits, K: int, n_shared: int, topk_ids=None, topk_w=None, 
         raise ValueError(f"outputs must be ({B}, {Kt})")
     _check(lib().moe_route_shared(_ptr(logits), B, E, K, int(n_shared), _ptr(topk_ids), _ptr(topk_w),
                                   _stream(stream)))
+    return topk_ids, topk_w
+
+
+def moe_route_scored(logits, K: int, score: str = "sigmoid", bias=None, n_groups: int = 1, topk_groups: int = 1,
+                     group_top: int = 2, renorm: bool = True, scale: float = 1.0, phys_of_logical=None,
+                     n_shared: int = 0, topk_ids=None, topk_w=None, stream=None):
+    """Top-K experts by ``score`` ('sigmoid' or 'softmax' over all experts) plus
+    ``bias`` (E,) inside the ``topk_groups`` best of ``n_groups`` expert groups
+    (a group scores the sum of its ``group_top`` best); weights are the picks'
+    scores, renormalised and scaled.  logits (B, E) fp32 or bf16; ids / weights
+    (B, K + n_shared); slots that find no unmasked expert get id -1, weight 0."""
+    _dev(logits, "logits", None, 2)
+    if logits.dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError(f"logits must be float32 or bfloat16 (got {logits.dtype})")
+    if score not in _SCORES:
+        raise ValueError(f"score must be one of {sorted(_SCORES)} (got {score!r})")
+    B, E = logits.shape
+    Kt = K + n_shared
+    dev = logits.device
+    if bias is not None:
+        _dev(bias, "bias", torch.float32, 1)
+        _need(bias, "bias", shape=(E,))
+    if phys_of_logical is not None:
+        _dev(phys_of_logical, "phys_of_logical", torch.int32, 1)
+        _need(phys_of_logical, "phys_of_logical", shape=(E,))
+    if topk_ids is None:
+        topk_ids = torch.empty((B, max(Kt, 0)), dtype=torch.int32, device=dev)
+    else:
+        _dev(topk_ids, "topk_ids", torch.int32)
+        _need(topk_ids, "topk_ids", shape=(B, Kt))
+    if topk_w is None:
+        topk_w = torch.empty((B, max(Kt, 0)), dtype=torch.float32, device=dev)
+    else:
+        _dev(topk_w, "topk_w", torch.float32)
+        _need(topk_w, "topk_w", shape=(B, Kt))
+    _same_device(logits, "logits", bias, phys_of_logical, topk_ids, topk_w)
+    with torch.cuda.device(dev):
+        _check(lib().moe_route_scored(_ptr(logits), _DT[logits.dtype], _ptr(bias), B, E, K, _SCORES[score], n_groups,
+                                      topk_groups, group_top, 1 if renorm else 0, scale, _ptr(phys_of_logical),
+                                      n_shared, _ptr(topk_ids), _ptr(topk_w), _stream(stream)))
     return topk_ids, topk_w
 
 
@@ -309,7 +366,8 @@ def moe_layout_masked(topk_ids, E: int, e_begin: int, e_end: int, cap_per_expert
 def moe_dispatch(seg_x, row_of, cap_rows: int, xd_dtype=None, xd=None, xd_scales=None,
                  stream=None):
     """Scatter the token rows of the segments into xd (cap_rows, H); fp8
-    storage also fills xd_scales (cap_rows, ceil(H/128))."""
+    storage also fills xd_scales (cap_rows, ceil(H/128)), int8 storage
+    xd_scales (cap_rows,)."""
     if isinstance(seg_x, torch.Tensor):
         seg_x = [seg_x]
     seg_x = list(seg_x)
@@ -329,21 +387,68 @@ def moe_dispatch(seg_x, row_of, cap_rows: int, xd_dtype=None, xd=None, xd_scales
         xd = torch.empty((max(cap_rows, 1), H), dtype=_TORCH[xd_code], device=dev)
     if xd_code == MOE_FP8_E4M3 and xd_scales is None:
         xd_scales = torch.empty((max(cap_rows, 1), -(-H // FP8_BLOCK)), dtype=torch.float32, device=dev)
+    if xd_code == MOE_INT8 and xd_scales is None:
+        xd_scales = torch.empty(max(cap_rows, 1), dtype=torch.float32, device=dev)
     _dev(xd, "xd")
     B = sum(int(t.shape[0]) for t in seg_x)
     _need(row_of, "row_of", shape=(B, K))
     if xd.dtype != _TORCH[xd_code]:
         raise ValueError(f"xd must be {_TORCH[xd_code]} (got {xd.dtype})")
     _need(xd, "xd", numel=cap_rows * H)
-    if xd_code == MOE_FP8_E4M3:
+    if xd_code in (MOE_FP8_E4M3, MOE_INT8):
         _dev(xd_scales, "xd_scales", torch.float32)
-        _need(xd_scales, "xd_scales", numel=cap_rows * (-(-H // FP8_BLOCK)))
+        _need(xd_scales, "xd_scales", numel=cap_rows * _scale_cols(xd_code, H))
+    if xd_code == MOE_INT8:
+        _same_device(row_of, "row_of", xd, xd_scales, *seg_x)
     ptrs = (ctypes.c_void_p * len(seg_x))(*[s.data_ptr() for s in seg_x])
     rows = (ctypes.c_int32 * len(seg_x))(*[s.shape[0] for s in seg_x])
-    _check(lib().moe_dispatch(ctypes.cast(ptrs, ctypes.c_void_p), ctypes.cast(rows, ctypes.c_void_p),
-                              len(seg_x), _DT[x_dt], H, _ptr(row_of), K, _ptr(xd), xd_code,
-                              _ptr(xd_scales), cap_rows, _stream(stream)))
+    with torch.cuda.device(dev):
+        _check(lib().moe_dispatch(ctypes.cast(ptrs, ctypes.c_void_p), ctypes.cast(rows, ctypes.c_void_p),
+                                  len(seg_x), _DT[x_dt], H, _ptr(row_of), K, _ptr(xd), xd_code,
+                                  _ptr(xd_scales), cap_rows, _stream(stream)))
     return xd, xd_scales
+
+
+def _scale_cols(code, cols):
+    """fp32 scales of a quantised row of ``cols`` elements: fp8 one per block, int8 one."""
+    return -(-cols // FP8_BLOCK) if code == MOE_FP8_E4M3 else 1
+
+
+def moe_quant_rows(x, rows=None, cap_per_expert=None, q=None, scales=None, stream=None):
+    """int8 codes (cap_rows, cols) and a scale (cap_rows,) for each valid row of x
+    (fp32 or bf16).  rows: the contiguous layout's offsets (E_loc + 1), or with
+    cap_per_expert the masked layout's m (E_loc) (moe_quant_rows_masked); None
+    quantises every row, e.g. weight rows (a scale for each output channel).
+    Other rows of given q and scales are left as they were."""
+    _dev(x, "x", None, 2)
+    if x.dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError(f"x must be float32 or bfloat16 (got {x.dtype})")
+    cap, cols = x.shape
+    E_loc, third = 0, cap
+    if rows is None:
+        if cap_per_expert is not None:
+            raise ValueError("cap_per_expert needs the masked layout's m")
+    else:
+        E_loc = rows.numel() - 1 if cap_per_expert is None else rows.numel()
+        third = _rows_arg(rows, cap_per_expert, E_loc, cap)
+    if q is None:
+        q = torch.empty((cap, cols), dtype=torch.int8, device=x.device)
+    if scales is None:
+        scales = torch.empty(cap, dtype=torch.float32, device=x.device)
+    _dev(q, "q", torch.int8)
+    _dev(scales, "scales", torch.float32)
+    _need(q, "q", shape=(cap, cols))
+    _need(scales, "scales", numel=cap)
+    _same_device(x, "x", rows, q, scales)
+    fn = lib().moe_quant_rows if cap_per_expert is None else lib().moe_quant_rows_masked
+    with torch.cuda.device(x.device):
+        _check(fn(_ptr(x), _DT[x.dtype], _ptr(rows), E_loc, third, cols, _ptr(q), _ptr(scales), _stream(stream)))
+    return q, scales
+
+
+def moe_quant_rows_masked(x, m, cap_per_expert, **kw):
+    """moe_quant_rows over the masked layout (rows [j*cap_per_expert, +m[j]))."""
+    return moe_quant_rows(x, m, cap_per_expert=cap_per_expert, **kw)
 
 
 def moe_ffn_workspace_bytes(cap_rows: int, I: int, act_dtype) -> int:
@@ -413,18 +518,26 @@ def _rows_arg(rows, cap_per_expert, E_loc, n_rows):
 
 
 def _check_ffn(a, a_scales, rows, cap_per_expert, E_loc, Kdim, cap, act, **tensors):
-    """Shapes of the FFN operands: the activation rows (cap, Kdim) [+ fp8
-    scales], the row description (offsets E_loc + 1, or m E_loc), and each
+    """Shapes of the FFN operands: the activation rows (cap, Kdim) [+ fp8 or
+    int8 scales], the row description (offsets E_loc + 1, or m E_loc), and each
     named (tensor, shape or minimum element count) pair."""
     if a.shape[1] != Kdim:
         raise ValueError(f"activations must have {Kdim} columns (got {a.shape[1]})")
     _need(rows, "offsets" if cap_per_expert is None else "m",
           numel=E_loc + 1 if cap_per_expert is None else E_loc)
-    if act == MOE_FP8_E4M3:
+    if act in (MOE_FP8_E4M3, MOE_INT8):
         if a_scales is None:
-            raise ValueError("fp8 activations need their block scales")
+            raise ValueError("fp8 activations need their block scales" if act == MOE_FP8_E4M3
+                             else "int8 activations need their row scales")
         _dev(a_scales, "activation scales", torch.float32)
-        _need(a_scales, "activation scales", numel=cap * (-(-Kdim // FP8_BLOCK)))
+        _need(a_scales, "activation scales", numel=cap * _scale_cols(act, Kdim))
+    if act == MOE_INT8:
+        for name, (t, _) in tensors.items():
+            if name.startswith("w_") and name.endswith("_scales"):
+                if t is None:
+                    raise ValueError(f"int8 weights need {name}")
+                _dev(t, name, torch.float32)
+        _same_device(a, "activations", a_scales, rows, *(t for t, _ in tensors.values()))
     for name, (t, want) in tensors.items():
         if t is None:
             continue
@@ -433,6 +546,19 @@ def _check_ffn(a, a_scales, rows, cap_per_expert, E_loc, Kdim, cap, act, **tenso
             _need(t, name, shape=want)
         else:
             _need(t, name, numel=want)
+
+
+def _w_scales(act, scales, E_loc, rows, cols):
+    """(weight scales, their shape) of a quantised weight (E_loc, rows, cols) for _check_ffn."""
+    if act == MOE_FP8_E4M3:
+        return scales, (E_loc, rows, -(-cols // FP8_BLOCK))
+    return (scales, (E_loc, rows)) if act == MOE_INT8 else (None, None)
+
+
+def _h_dtype_for(xd):
+    """Storage of gate/up's output: the activations' own, but bf16 for int8 (moe_quant_rows
+    makes its int8 rows, whose scale takes a whole row)."""
+    return torch.bfloat16 if xd.dtype == torch.int8 else xd.dtype
 
 
 def _w_code(act, w_scales_pow2):
@@ -450,7 +576,8 @@ def moe_ffn_gate_up(xd, xd_scales, offsets, w_gate, w_up, w_gate_scales=None, w_
     expected_rows: rows a local expert is expected to get (tile-shape hint only).
     With cap_per_expert given, ``offsets`` is the masked layout's m and the call
     is moe_ffn_gate_up_masked.  w_scales_pow2: the fp8 weight scales are all
-    powers of two (weight dtype MOE_FP8_E4M3_PO2)."""
+    powers of two (weight dtype MOE_FP8_E4M3_PO2).  int8: xd_scales (cap_rows,),
+    weight scales (E_loc, I), h is bf16 and h_scales None (see moe_quant_rows)."""
     _dev(xd, "xd", ndim=2)
     _dev(w_gate, "w_gate", xd.dtype, 3)
     _dev(w_up, "w_up", xd.dtype, 3)
@@ -460,23 +587,24 @@ def moe_ffn_gate_up(xd, xd_scales, offsets, w_gate, w_up, w_gate_scales=None, w_
     act = _DT[xd.dtype]
     packed = _pack_flag(_w_packed(w_gate, H, act, "w_gate"))
     if h is None:
-        h = torch.empty((cap, I), dtype=xd.dtype, device=xd.device)
+        h = torch.empty((cap, I), dtype=_h_dtype_for(xd), device=xd.device)
     if act == MOE_FP8_E4M3 and h_scales is None:
         h_scales = torch.empty((cap, -(-I // FP8_BLOCK)), dtype=torch.float32, device=xd.device)
-    if h.dtype != xd.dtype:
-        raise ValueError(f"h must be {xd.dtype} (got {h.dtype})")
-    nbH, nbI = -(-H // FP8_BLOCK), -(-I // FP8_BLOCK)
+    if h.dtype != _h_dtype_for(xd):
+        raise ValueError(f"h must be {_h_dtype_for(xd)} (got {h.dtype})")
+    nbI = -(-I // FP8_BLOCK)
     fp8 = act == MOE_FP8_E4M3
     _check_ffn(xd, xd_scales, offsets, cap_per_expert, E_loc, H, cap, act,
                w_up=(w_up, tuple(w_gate.shape)), h=(h, cap * I),
                h_scales=(h_scales if fp8 else None, cap * nbI),
-               w_gate_scales=(w_gate_scales if fp8 else None, (E_loc, I, nbH)),
-               w_up_scales=(w_up_scales if fp8 else None, (E_loc, I, nbH)))
+               w_gate_scales=_w_scales(act, w_gate_scales, E_loc, I, H),
+               w_up_scales=_w_scales(act, w_up_scales, E_loc, I, H))
     fn = lib().moe_ffn_gate_up if cap_per_expert is None else lib().moe_ffn_gate_up_masked
-    _check(fn(_ptr(xd), _ptr(xd_scales), _ptr(offsets), E_loc, third, H, I, act,
-              _ptr(w_gate), _ptr(w_up), _ptr(w_gate_scales), _ptr(w_up_scales),
-              _w_code(act, w_scales_pow2) | packed, _ptr(h), _ptr(h_scales), int(expected_rows),
-              _stream(stream)))
+    with torch.cuda.device(xd.device):
+        _check(fn(_ptr(xd), _ptr(xd_scales), _ptr(offsets), E_loc, third, H, I, act,
+                  _ptr(w_gate), _ptr(w_up), _ptr(w_gate_scales), _ptr(w_up_scales),
+                  _w_code(act, w_scales_pow2) | packed, _ptr(h), _ptr(h_scales), int(expected_rows),
+                  _stream(stream)))
     return h, h_scales
 
 
@@ -487,7 +615,8 @@ def _y_dtype_for(act):
 def moe_ffn_down(h, h_scales, offsets, w_down, w_down_scales=None, y=None, y_dtype=None,
                  expected_rows=0, stream=None, cap_per_expert=None, w_scales_pow2=False):
     """y = h Wd^T per local expert -> (cap_rows, H).  cap_per_expert and
-    w_scales_pow2: as in moe_ffn_gate_up (moe_ffn_down_masked)."""
+    w_scales_pow2: as in moe_ffn_gate_up (moe_ffn_down_masked).  int8: h_scales
+    (cap_rows,), weight scales (E_loc, H), y bf16 (the default) or fp32."""
     _dev(h, "h", ndim=2)
     _dev(w_down, "w_down", h.dtype, 3)
     E_loc, H, I = w_down.shape[0], w_down.shape[1], h.shape[1]
@@ -498,20 +627,21 @@ def moe_ffn_down(h, h_scales, offsets, w_down, w_down_scales=None, y=None, y_dty
     y_dtype = _y_dtype_for(act) if y_dtype is None else y_dtype
     if y is None:
         y = torch.empty((cap, H), dtype=y_dtype, device=h.device)
-    fp8 = act == MOE_FP8_E4M3
     _check_ffn(h, h_scales, offsets, cap_per_expert, E_loc, I, cap, act, y=(y, cap * H),
-               w_down_scales=(w_down_scales if fp8 else None, (E_loc, H, -(-I // FP8_BLOCK))))
+               w_down_scales=_w_scales(act, w_down_scales, E_loc, H, I))
     fn = lib().moe_ffn_down if cap_per_expert is None else lib().moe_ffn_down_masked
-    _check(fn(_ptr(h), _ptr(h_scales), _ptr(offsets), E_loc, third, H, I, act,
-              _ptr(w_down), _ptr(w_down_scales), _w_code(act, w_scales_pow2) | packed, _ptr(y), _DT[y.dtype],
-              int(expected_rows), _stream(stream)))
+    with torch.cuda.device(h.device):
+        _check(fn(_ptr(h), _ptr(h_scales), _ptr(offsets), E_loc, third, H, I, act,
+                  _ptr(w_down), _ptr(w_down_scales), _w_code(act, w_scales_pow2) | packed, _ptr(y), _DT[y.dtype],
+                  int(expected_rows), _stream(stream)))
     return y
 
 
 def moe_grouped_ffn(xd, xd_scales, offsets, w_gate, w_up, w_down, w_gate_scales=None,
                     w_up_scales=None, w_down_scales=None, y=None, y_dtype=None, ws=None,
                     expected_rows=0, stream=None, cap_per_expert=None, w_scales_pow2=False):
-    """Both FFN stages with h held in the workspace ``ws``.  cap_per_expert
+    """Both FFN stages (int8: and the quantisation of h between them) with h held
+    in the workspace ``ws``.  cap_per_expert
     and w_scales_pow2: as in moe_ffn_gate_up (moe_grouped_ffn_masked)."""
     _dev(xd, "xd", ndim=2)
     for n, w in (("w_gate", w_gate), ("w_up", w_up), ("w_down", w_down)):
@@ -527,20 +657,19 @@ def moe_grouped_ffn(xd, xd_scales, offsets, w_gate, w_up, w_down, w_gate_scales=
     need = moe_ffn_workspace_bytes(cap, I, act)
     if ws is None:
         ws = torch.empty(max(need, 256), dtype=torch.uint8, device=xd.device)
-    fp8 = act == MOE_FP8_E4M3
-    nbH, nbI = -(-H // FP8_BLOCK), -(-I // FP8_BLOCK)
     _check_ffn(xd, xd_scales, offsets, cap_per_expert, E_loc, H, cap, act,
                w_up=(w_up, tuple(w_gate.shape)), w_down=(w_down, (E_loc, H, w_down.shape[2])),
                y=(y, cap * H),
-               w_gate_scales=(w_gate_scales if fp8 else None, (E_loc, I, nbH)),
-               w_up_scales=(w_up_scales if fp8 else None, (E_loc, I, nbH)),
-               w_down_scales=(w_down_scales if fp8 else None, (E_loc, H, nbI)))
+               w_gate_scales=_w_scales(act, w_gate_scales, E_loc, I, H),
+               w_up_scales=_w_scales(act, w_up_scales, E_loc, I, H),
+               w_down_scales=_w_scales(act, w_down_scales, E_loc, H, I))
     fn = lib().moe_grouped_ffn if cap_per_expert is None else lib().moe_grouped_ffn_masked
-    _check(fn(_ptr(xd), _ptr(xd_scales), _ptr(offsets), E_loc, third, H, I, act,
-              _ptr(w_gate), _ptr(w_up), _ptr(w_down), _ptr(w_gate_scales),
-              _ptr(w_up_scales), _ptr(w_down_scales), _w_code(act, w_scales_pow2) | packed, _ptr(y),
-              _DT[y.dtype], _ptr(ws), ws.numel() * ws.element_size(),
-              int(expected_rows), _stream(stream)))
+    with torch.cuda.device(xd.device):
+        _check(fn(_ptr(xd), _ptr(xd_scales), _ptr(offsets), E_loc, third, H, I, act,
+                  _ptr(w_gate), _ptr(w_up), _ptr(w_down), _ptr(w_gate_scales),
+                  _ptr(w_up_scales), _ptr(w_down_scales), _w_code(act, w_scales_pow2) | packed, _ptr(y),
+                  _DT[y.dtype], _ptr(ws), ws.numel() * ws.element_size(),
+                  int(expected_rows), _stream(stream)))
     return y
 
 

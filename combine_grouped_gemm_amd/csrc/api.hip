@@ -1,6 +1,7 @@
 // C ABI of libmoeep: host-side argument checks, then kernel launches on the
 // caller's stream.  Nothing here allocates, synchronises or copies from the
 // device; a failed check returns before anything is enqueued.
+#include <cmath>
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
@@ -74,24 +75,31 @@ struct Rows {
 
 moe_status_t check_ffn_common(const void* a, Rows rows, int E_local, int cap_rows,
                               int H, int I, moe_dtype_t act_dt, moe_dtype_t w_dt) {
-    REQUIRE(a && (rows.offsets || rows.m), "null activation or row-count pointer");
+    // a buffer of no rows has no address to give
+    REQUIRE((a || cap_rows == 0) && (rows.offsets || rows.m), "null activation or row-count pointer");
     REQUIRE(E_local >= 1 && E_local <= 1024, "E_local must be in [1, 1024] (got %d)", E_local);
     REQUIRE(cap_rows >= 0, "cap_rows must be >= 0");
-    // rows move in 16-byte pieces: 8 elements (bf16, fp32), 16 for fp8
-    const int q = act_dt == MOE_FP8_E4M3 ? 16 : 8;
+    // rows move in 16-byte pieces: 8 elements (bf16, fp32), 16 for fp8 and int8
+    const int q = act_dt == MOE_FP8_E4M3 || act_dt == MOE_INT8 ? 16 : 8;
     REQUIRE(H >= q && H % q == 0 && I >= q && I % q == 0,
             "H and I must be positive multiples of %d for this dtype (got H=%d, I=%d)", q, H, I);
     REQUIRE((long long)cap_rows * (H > I ? H : I) <= 0x7fffffffLL * 4LL, "cap_rows * H too large");
     REQUIRE(aligned16(a), "activation pointer must be 16-byte aligned");
     const bool ok = (act_dt == MOE_F32 && w_dt == MOE_F32) || (act_dt == MOE_BF16 && w_dt == MOE_BF16) ||
-                    (act_dt == MOE_FP8_E4M3 && (w_dt == MOE_FP8_E4M3 || w_dt == MOE_FP8_E4M3_PO2));
+                    (act_dt == MOE_FP8_E4M3 && (w_dt == MOE_FP8_E4M3 || w_dt == MOE_FP8_E4M3_PO2)) ||
+                    (act_dt == MOE_INT8 && w_dt == MOE_INT8);
     if (!ok) return fail(MOE_ERR_UNSUPPORTED, "unsupported (act_dt, w_dt) = (%d, %d)", act_dt, w_dt);
+    // 2^14 per product of two codes: the int32 sums are exact up to this length
+    if (act_dt == MOE_INT8)
+        REQUIRE(H <= MOE_INT8_MAX_COLS && I <= MOE_INT8_MAX_COLS, "int8 H and I must be at most %d (got H=%d, I=%d)",
+                MOE_INT8_MAX_COLS, H, I);
     return MOE_OK;
 }
 
 moe_status_t check_y_dtype(moe_dtype_t act_dt, moe_dtype_t y_dt) {
     const bool ok = (act_dt == MOE_F32 && y_dt == MOE_F32) || (act_dt == MOE_BF16 && y_dt == MOE_BF16) ||
-                    (act_dt == MOE_FP8_E4M3 && y_dt == MOE_BF16);
+                    (act_dt == MOE_FP8_E4M3 && y_dt == MOE_BF16) ||
+                    (act_dt == MOE_INT8 && (y_dt == MOE_BF16 || y_dt == MOE_F32));
     if (!ok) return fail(MOE_ERR_UNSUPPORTED, "unsupported (act_dt, y_dt) = (%d, %d)", act_dt, y_dt);
     return MOE_OK;
 }
@@ -102,6 +110,7 @@ moeep::FfnArgs ffn_args(const void* a, const float* a_scales, Rows rows, int E_l
                         int expected_rows, moe_dtype_t w_dt, int ldw) {
     moeep::FfnArgs f;
     f.w_scales_pow2 = w_dt == MOE_FP8_E4M3_PO2;
+    f.out_f32 = false;
     f.ldw = ldw;
     f.a = a;
     f.a_scales = a_scales;
@@ -127,6 +136,7 @@ hipError_t run_ffn(const moeep::FfnArgs& f, moe_dtype_t act_dt, bool gated, hipS
     switch (act_dt) {
         case MOE_F32: return moeep::launch_ffn_f32(f, gated, stream);
         case MOE_BF16: return moeep::launch_ffn_bf16(f, gated, stream);
+        case MOE_INT8: return moeep::launch_ffn_i8(f, gated, stream);
         default: return moeep::launch_ffn_fp8(f, gated, stream);
     }
 }
@@ -154,6 +164,10 @@ size_t round256(size_t v) { return (v + 255) / 256 * 256; }
 
 size_t ffn_workspace_bytes(int cap_rows, int I, moe_dtype_t act_dt) {
     if (cap_rows < 0 || I < 1) return 0;
+    // int8: h as gate/up writes it (bf16), its codes and its row scales
+    if (act_dt == MOE_INT8)
+        return round256((size_t)cap_rows * I * 2) + round256((size_t)cap_rows * I) +
+               round256((size_t)cap_rows * sizeof(float));
     size_t bytes = round256((size_t)cap_rows * I * elem_size(act_dt));
     if (act_dt == MOE_FP8_E4M3) bytes += round256((size_t)cap_rows * (((size_t)I + 127) / 128) * sizeof(float));
     return bytes;
@@ -167,10 +181,13 @@ moe_status_t ffn_gate_up(const void* xd, const float* xd_scales, Rows rows,
     const WType wt = split_w(w_dt);
     moe_status_t s = check_ffn_common(xd, rows, E_local, cap_rows, H, I, act_dt, wt.dt);
     if (s != MOE_OK) return s;
-    REQUIRE(w_gate && w_up && h, "null weight or h pointer");
+    REQUIRE(w_gate && w_up && (h || cap_rows == 0), "null weight or h pointer");
     REQUIRE(aligned16(w_gate) && aligned16(w_up) && aligned16(h), "weights and h must be 16-byte aligned");
     if (act_dt == MOE_FP8_E4M3)
         REQUIRE(xd_scales && w_gate_scales && w_up_scales && h_scales, "fp8 needs all scale pointers");
+    if (act_dt == MOE_INT8)
+        REQUIRE((xd_scales || cap_rows == 0) && w_gate_scales && w_up_scales,
+                "int8 needs the row and channel scale pointers");
     auto f = ffn_args(xd, xd_scales, rows, E_local, cap_rows, H, I, w_gate, w_up, w_gate_scales,
                       w_up_scales, h, h_scales, expected_rows, wt.dt, weight_ld(wt, H));
     return launched(run_ffn(f, act_dt, true, stream), "ffn gate/up");
@@ -185,12 +202,41 @@ moe_status_t ffn_down(const void* h, const float* h_scales, Rows rows, int E_loc
     if (s != MOE_OK) return s;
     s = check_y_dtype(act_dt, y_dt);
     if (s != MOE_OK) return s;
-    REQUIRE(w_down && y, "null weight or y pointer");
+    REQUIRE(w_down && (y || cap_rows == 0), "null weight or y pointer");
     REQUIRE(aligned16(w_down) && aligned16(y), "weights and y must be 16-byte aligned");
     if (act_dt == MOE_FP8_E4M3) REQUIRE(h_scales && w_down_scales, "fp8 needs all scale pointers");
+    if (act_dt == MOE_INT8)
+        REQUIRE((h_scales || cap_rows == 0) && w_down_scales, "int8 needs the row and channel scale pointers");
     auto f = ffn_args(h, h_scales, rows, E_local, cap_rows, I, H, w_down, nullptr, w_down_scales,
                       nullptr, y, nullptr, expected_rows, wt.dt, weight_ld(wt, I));
+    f.out_f32 = act_dt == MOE_INT8 && y_dt == MOE_F32;
     return launched(run_ffn(f, act_dt, false, stream), "ffn down");
+}
+
+// rows of (cap_rows, cols) named by `rows` (all when it names none)
+moe_status_t quant_rows(const void* x, moe_dtype_t x_dt, Rows rows, int E_local, int cap_rows, int cols, int8_t* q,
+                        float* scales, hipStream_t stream) {
+    if (x_dt != MOE_F32 && x_dt != MOE_BF16) return fail(MOE_ERR_UNSUPPORTED, "unsupported x_dt %d", x_dt);
+    REQUIRE(cap_rows >= 0, "cap_rows must be >= 0");
+    REQUIRE(cols >= 16 && cols % 16 == 0 && cols <= MOE_INT8_MAX_COLS,
+            "cols must be a positive multiple of 16, at most %d (got %d)", MOE_INT8_MAX_COLS, cols);
+    if (rows.offsets || rows.m)
+        REQUIRE(E_local >= 1 && E_local <= 1024, "E_local must be in [1, 1024] (got %d)", E_local);
+    if (cap_rows > 0) {
+        REQUIRE(x && q && scales, "null x, q or scales pointer");
+        REQUIRE(aligned16(x) && aligned16(q), "x and q must be 16-byte aligned");
+    }
+    moeep::QuantArgs a;
+    a.x = x;
+    a.offsets = rows.offsets;
+    a.m_counts = rows.m;
+    a.E_loc = E_local;
+    a.cap = cap_rows;
+    a.cap_e = rows.cap_e;
+    a.cols = cols;
+    a.q = q;
+    a.scales = scales;
+    return launched(moeep::launch_quant_rows(a, x_dt == MOE_F32, stream), "moe_quant_rows");
 }
 
 moe_status_t grouped_ffn(const void* xd, const float* xd_scales, Rows rows,
@@ -211,6 +257,23 @@ moe_status_t grouped_ffn(const void* xd, const float* xd_scales, Rows rows,
     float* h_scales = nullptr;
     if (act_dt == MOE_FP8_E4M3)
         h_scales = reinterpret_cast<float*>(static_cast<char*>(ws) + round256((size_t)cap_rows * I));
+    if (act_dt == MOE_INT8) {
+        // everything the three calls check is checked before the first is enqueued
+        REQUIRE(w_gate && w_up && w_down && (y || cap_rows == 0), "null weight or y pointer");
+        REQUIRE(aligned16(w_gate) && aligned16(w_up) && aligned16(w_down) && aligned16(y),
+                "weights and y must be 16-byte aligned");
+        REQUIRE((xd_scales || cap_rows == 0) && w_gate_scales && w_up_scales && w_down_scales,
+                "int8 needs the row and channel scale pointers");
+        int8_t* hq = reinterpret_cast<int8_t*>(static_cast<char*>(ws) + round256((size_t)cap_rows * I * 2));
+        float* hs = reinterpret_cast<float*>(hq + round256((size_t)cap_rows * I));
+        s = ffn_gate_up(xd, xd_scales, rows, E_local, cap_rows, H, I, act_dt, w_gate, w_up, w_gate_scales,
+                        w_up_scales, w_dt, h, nullptr, expected_rows, stream);
+        if (s != MOE_OK) return s;
+        s = quant_rows(h, MOE_BF16, rows, E_local, cap_rows, I, hq, hs, stream);
+        if (s != MOE_OK) return s;
+        return ffn_down(hq, hs, rows, E_local, cap_rows, H, I, act_dt, w_down, w_down_scales, w_dt, y, y_dt,
+                        expected_rows, stream);
+    }
     s = ffn_gate_up(xd, xd_scales, rows, E_local, cap_rows, H, I, act_dt, w_gate, w_up,
                         w_gate_scales, w_up_scales, w_dt, h, h_scales, expected_rows, stream);
     if (s != MOE_OK) return s;
@@ -264,6 +327,46 @@ moe_status_t moe_route_shared(const float* logits, int B, int E, int K, int n_sh
     if (B > 0) REQUIRE(logits && ids && w, "null pointer argument");
     return launched(moeep::launch_route(logits, B, E, K, ids, w, nullptr, n_shared, stream),
                     "moe_route_shared");
+}
+
+moe_status_t moe_route_scored(const void* logits, moe_dtype_t logits_dt, const float* bias, int B, int E, int K,
+                              moe_score_t score, int n_groups, int topk_groups, int group_top, int renorm,
+                              float scale, const int32_t* phys_of_logical, int n_shared, int32_t* ids, float* w,
+                              hipStream_t stream) {
+    moe_status_t s = check_route_shape(B, E, K);
+    if (s != MOE_OK) return s;
+    if (logits_dt != MOE_F32 && logits_dt != MOE_BF16)
+        return fail(MOE_ERR_UNSUPPORTED, "unsupported logits_dt %d", logits_dt);
+    if (score != MOE_SCORE_SOFTMAX && score != MOE_SCORE_SIGMOID)
+        return fail(MOE_ERR_UNSUPPORTED, "unsupported score %d", score);
+    REQUIRE(n_groups >= 1 && E % n_groups == 0, "n_groups must divide E (got E=%d, n_groups=%d)", E, n_groups);
+    REQUIRE(topk_groups >= 1 && topk_groups <= n_groups, "topk_groups must be in [1, n_groups] (got %d of %d)",
+            topk_groups, n_groups);
+    REQUIRE(group_top == 1 || group_top == 2, "group_top must be 1 or 2 (got %d)", group_top);
+    REQUIRE(K <= topk_groups * (E / n_groups), "K=%d exceeds the %d experts of %d groups", K,
+            topk_groups * (E / n_groups), topk_groups);
+    REQUIRE(std::isfinite(scale), "scale must be finite");
+    REQUIRE(n_shared >= 0 && n_shared <= 1024 - E, "need 0 <= n_shared and E + n_shared <= 1024");
+    REQUIRE((long long)B * (K + n_shared) <= 0x7fffffffLL, "B*(K+n_shared) must fit in int32");
+    if (B > 0) REQUIRE(logits && ids && w, "null pointer argument");
+    moeep::RouteScoredArgs a;
+    a.logits = logits;
+    a.bias = bias;
+    a.map = phys_of_logical;
+    a.ids = ids;
+    a.w = w;
+    a.scale = scale;
+    a.B = B;
+    a.E = E;
+    a.K = K;
+    a.G = n_groups;
+    a.topk_groups = topk_groups;
+    a.group_top = group_top;
+    a.n_shared = n_shared;
+    a.bf16 = logits_dt == MOE_BF16;
+    a.sigmoid = score == MOE_SCORE_SIGMOID;
+    a.renorm = renorm != 0;
+    return launched(moeep::launch_route_scored(a, stream), "moe_route_scored");
 }
 
 moe_status_t moe_eplb_place(const int64_t* load, int E, int n_groups, int32_t* phys_of_logical) {
@@ -359,15 +462,18 @@ moe_status_t moe_dispatch(const void* const* seg_x, const int32_t* seg_rows, int
     REQUIRE(n_seg >= 1 && n_seg <= MOE_MAX_SEGMENTS, "n_seg must be in [1, %d]", MOE_MAX_SEGMENTS);
     REQUIRE(seg_x && seg_rows, "null segment tables");
     REQUIRE(K >= 1 && K <= 1024, "K must be in [1, 1024]");
-    // 16-byte pieces: 8 elements; fp8 rows feed the fp8 GEMMs, which need 16
-    const int q = xd_dt == MOE_FP8_E4M3 ? 16 : 8;
+    // 16-byte pieces: 8 elements; fp8 and int8 rows feed GEMMs that need 16
+    const int q = xd_dt == MOE_FP8_E4M3 || xd_dt == MOE_INT8 ? 16 : 8;
     REQUIRE(H >= q && H % q == 0, "H must be a positive multiple of %d for this dtype (got %d)", q, H);
     REQUIRE(cap_rows >= 0, "cap_rows must be >= 0");
     int kind;
     if (x_dt == MOE_F32 && xd_dt == MOE_F32) kind = 0;
     else if (x_dt == MOE_BF16 && xd_dt == MOE_BF16) kind = 1;
     else if (x_dt == MOE_BF16 && xd_dt == MOE_FP8_E4M3) kind = 2;
+    else if ((x_dt == MOE_BF16 || x_dt == MOE_F32) && xd_dt == MOE_INT8) kind = 3;
     else return fail(MOE_ERR_UNSUPPORTED, "unsupported dispatch (x_dt, xd_dt) = (%d, %d)", x_dt, xd_dt);
+    if (kind == 3)
+        REQUIRE(H <= MOE_INT8_MAX_COLS, "int8 H must be at most %d (got %d)", MOE_INT8_MAX_COLS, H);
     moeep::SegTable seg;
     seg.n = n_seg;
     seg.start[0] = 0;
@@ -387,7 +493,12 @@ moe_status_t moe_dispatch(const void* const* seg_x, const int32_t* seg_rows, int
         REQUIRE(row_of && xd, "null row_of or xd");
         REQUIRE(aligned16(xd), "xd must be 16-byte aligned");
         if (kind == 2) REQUIRE(xd_scales, "fp8 dispatch needs xd_scales");
+        if (kind == 3) REQUIRE(xd_scales, "int8 dispatch needs xd_scales");
     }
+    if (kind == 3)
+        return launched(moeep::launch_dispatch_i8(seg, (int)B, H, x_dt == MOE_F32, row_of, K, xd, xd_scales, cap_rows,
+                                                  stream),
+                        "moe_dispatch");
     return launched(moeep::launch_dispatch(seg, (int)B, H, kind, row_of, K, xd, xd_scales, cap_rows, stream),
                     "moe_dispatch");
 }
@@ -397,7 +508,8 @@ size_t moe_ffn_workspace_bytes(int cap_rows, int I, moe_dtype_t act_dt) {
 }
 
 static bool packable_dtype(moe_dtype_t w_dt) {
-    return w_dt == MOE_F32 || w_dt == MOE_BF16 || w_dt == MOE_FP8_E4M3 || w_dt == MOE_FP8_E4M3_PO2;
+    return w_dt == MOE_F32 || w_dt == MOE_BF16 || w_dt == MOE_FP8_E4M3 || w_dt == MOE_FP8_E4M3_PO2 ||
+           w_dt == MOE_INT8;
 }
 
 int moe_weight_ld(int cols, moe_dtype_t w_dt) {
@@ -434,6 +546,11 @@ moe_status_t moe_pack_weights(const void* w, int E_local, int rows, int cols, mo
                     "moe_pack_weights");
 }
 
+moe_status_t moe_quant_rows(const void* x, moe_dtype_t x_dt, const int32_t* offsets, int E_local, int cap_rows,
+                            int cols, int8_t* q, float* scales, hipStream_t stream) {
+    return quant_rows(x, x_dt, Rows{offsets, nullptr, 0}, E_local, cap_rows, cols, q, scales, stream);
+}
+
 moe_status_t moe_ffn_gate_up(const void* xd, const float* xd_scales, const int32_t* offsets,
                              int E_local, int cap_rows, int H, int I, moe_dtype_t act_dt,
                              const void* w_gate, const void* w_up, const float* w_gate_scales,
@@ -468,6 +585,14 @@ moe_status_t moe_grouped_ffn(const void* xd, const float* xd_scales, const int32
     REQUIRE(cap_per_expert >= 1, "cap_per_expert must be >= 1 (got %d)", cap_per_expert);     \
     REQUIRE(E_local >= 1 && E_local <= 1024, "E_local must be in [1, 1024] (got %d)", E_local); \
     REQUIRE((long long)E_local * cap_per_expert <= 0x7fffffffLL, "E_local * cap_per_expert must fit in int32")
+
+moe_status_t moe_quant_rows_masked(const void* x, moe_dtype_t x_dt, const int32_t* m, int E_local,
+                                   int cap_per_expert, int cols, int8_t* q, float* scales, hipStream_t stream) {
+    MASKED_ROWS();
+    REQUIRE(m, "null m");
+    return quant_rows(x, x_dt, Rows{nullptr, m, cap_per_expert}, E_local, E_local * cap_per_expert, cols, q, scales,
+                      stream);
+}
 
 moe_status_t moe_ffn_gate_up_masked(const void* xd, const float* xd_scales, const int32_t* m,
                                     int E_local, int cap_per_expert, int H, int I, moe_dtype_t act_dt,

@@ -14,6 +14,19 @@ namespace moeep {
 hipError_t launch_route(const float* logits, int B, int E, int K, int32_t* ids, float* w,
                         const int32_t* map, int n_shared, hipStream_t stream);
 
+// route_scored.hip
+struct RouteScoredArgs {
+    const void* logits;       // (B, E) fp32 or bf16
+    const float* bias;        // (E) or nullptr
+    const int32_t* map;       // (E) logical -> physical id, or nullptr
+    int32_t* ids;             // (B, K + n_shared)
+    float* w;
+    float scale;
+    int B, E, K, G, topk_groups, group_top, n_shared;
+    bool bf16, sigmoid, renorm;
+};
+hipError_t launch_route_scored(const RouteScoredArgs& a, hipStream_t stream);
+
 // placement.hip (host): balanced equal-size expert groups, see the file header
 bool place_experts(const int64_t* load, int E, int G, int32_t* phys_of_logical);
 
@@ -45,6 +58,19 @@ struct SegTable {
 hipError_t launch_dispatch(const SegTable& seg, int B, int H, int kind, const int32_t* row_of,
                            int K, void* xd, float* xd_scales, int cap, hipStream_t stream);
 
+// quant_i8.hip: the same scatter with per-token int8 quantisation (x fp32 or bf16)
+hipError_t launch_dispatch_i8(const SegTable& seg, int B, int H, bool f32, const int32_t* row_of, int K, void* xd,
+                              float* xd_scales, int cap, hipStream_t stream);
+struct QuantArgs {
+    const void* x;            // (cap, cols) fp32 or bf16
+    const int32_t* offsets;   // contiguous layout: (E_loc + 1), or nullptr
+    const int32_t* m_counts;  // masked layout: (E_loc), or nullptr (both null: all rows)
+    int E_loc, cap, cap_e, cols;
+    void* q;                  // (cap, cols) int8
+    float* scales;            // (cap)
+};
+hipError_t launch_quant_rows(const QuantArgs& a, bool f32, hipStream_t stream);
+
 // combine.hip
 // kind: 0 = f32 -> f32, 1 = bf16 -> bf16, 2 = bf16 -> f32
 hipError_t launch_combine(const void* y, int kind, const int32_t* row_of, const float* w,
@@ -53,7 +79,7 @@ hipError_t launch_combine(const void* y, int kind, const int32_t* row_of, const 
 // ffn kernels: shared argument block
 struct FfnArgs {
     const void* a;            // activations (cap, Kdim)
-    const float* a_scales;    // fp8 only: (cap, ceil(Kdim/128))
+    const float* a_scales;    // fp8: (cap, ceil(Kdim/128)); int8: (cap)
     const int32_t* offsets;   // contiguous layout: (E_loc + 1); nullptr for the masked layout
     const int32_t* m_counts;  // masked layout: (E_loc) valid rows of expert j, in [j*cap_e, ...)
     int cap_e;                // masked layout: rows per expert block (cap = E_loc * cap_e)
@@ -61,17 +87,19 @@ struct FfnArgs {
     int ldw;                  // weight row pitch in elements (Kdim, or the packed pitch)
     const void* w0;           // gate or down (E_loc, N, ldw): rows of Kdim at pitch ldw
     const void* w1;           // up (gate/up only)
-    const float* w0_scales;   // fp8 only: (E_loc, N, ceil(Kdim/128))
+    const float* w0_scales;   // fp8: (E_loc, N, ceil(Kdim/128)); int8: (E_loc, N)
     const float* w1_scales;
     void* out;                // (cap, N)
     float* out_scales;        // fp8 h only: (cap, ceil(N/128))
     int rows_hint;            // cap / E_loc, picks the tile shape
     bool w_scales_pow2;       // fp8: every weight scale is a power of two
+    bool out_f32;             // int8 down: fp32 outputs instead of bf16
 };
 
 hipError_t launch_ffn_f32(const FfnArgs& a, bool gated, hipStream_t stream);   // ffn_f32.hip
 hipError_t launch_ffn_bf16(const FfnArgs& a, bool gated, hipStream_t stream);  // ffn_bf16.hip
 hipError_t launch_ffn_fp8(const FfnArgs& a, bool gated, hipStream_t stream);   // ffn_fp8.hip
+hipError_t launch_ffn_i8(const FfnArgs& a, bool gated, hipStream_t stream);    // ffn_i8.hip
 
 int device_cu_count();   // api.hip: compute units of the current device (cached)
 

@@ -5,6 +5,7 @@ asks of an EP decode step).
 
     route -> layout -> dispatch -> gate/up (+SwiGLU) -> down -> combine
 
+(with int8 experts a quantisation of h between gate/up and down).
 Every stage is one call into libmoeep; this class only owns the buffers
 and orders the calls on one stream.
 """
@@ -13,10 +14,10 @@ from __future__ import annotations
 import torch
 
 from . import (FP8_BLOCK, moe_combine, moe_dispatch, moe_ffn_down, moe_ffn_gate_up,
-               moe_layout, moe_layout_masked, moe_layout_workspace_bytes, moe_route,
-               moe_route_mapped, moe_route_shared)
+               moe_layout, moe_layout_masked, moe_layout_workspace_bytes, moe_quant_rows, moe_route,
+               moe_route_mapped, moe_route_scored, moe_route_shared)
 
-_TORCH = {"f32": torch.float32, "bf16": torch.bfloat16, "fp8": torch.float8_e4m3fn}
+_TORCH = {"f32": torch.float32, "bf16": torch.bfloat16, "fp8": torch.float8_e4m3fn, "int8": torch.int8}
 
 
 class MoELayer:
@@ -24,7 +25,9 @@ class MoELayer:
 
     seg_rows: tokens per simulated source segment (T = sum); E routed experts,
     K per token; H hidden, I expert intermediate; local experts
-    [e_begin, e_end); act_dtype stores Xd and h ('f32' | 'bf16' | 'fp8');
+    [e_begin, e_end); act_dtype stores Xd and h ('f32' | 'bf16' | 'fp8' |
+    'int8': a scale for each token in Xd and h and for each output channel of
+    the weights; gate/up's bf16 h is quantised in a stage of its own);
     y_dtype / out_dtype store the expert outputs and the combined rows.
     layout: 'contiguous' (rows of the local experts back to back, cap_rows
     rows, default T*K) or 'masked' (a fixed block of cap_per_expert rows per
@@ -33,10 +36,21 @@ class MoELayer:
     E, E+1, ... of the same grouped FFN; the local range must end at E and the
     weights hold the shared experts after the routed ones.  self.E, self.K
     and self.e_end then count them (self.E_routed, self.K_routed do not).
+    router: None routes by moe_route's rule (top-K logits, softmax over the
+    picks); a dict of moe_route_scored's keywords (score, n_groups,
+    topk_groups, group_top, renorm, scale) routes by that call, with the
+    balance bias (E,) in self.router_bias when set.  moe_route_scored takes a
+    placement map beside shared experts; the map then covers the routed ids.
     """
 
     def __init__(self, seg_rows, E, K, H, I, e_begin, e_end, act_dtype, y_dtype, out_dtype,
-                 device="cuda", cap_rows=None, layout="contiguous", cap_per_expert=None, n_shared=0):
+                 device="cuda", cap_rows=None, layout="contiguous", cap_per_expert=None, n_shared=0,
+                 router=None):
+        self.router = None if router is None else dict(router)
+        if self.router is not None:
+            unknown = set(self.router) - {"score", "n_groups", "topk_groups", "group_top", "renorm", "scale"}
+            if unknown:
+                raise ValueError(f"unknown router options {sorted(unknown)}")
         self.seg_rows = tuple(int(b) for b in seg_rows)
         self.T = sum(self.seg_rows)
         self.n_shared = int(n_shared)
@@ -72,18 +86,29 @@ class MoELayer:
         act = _TORCH[act_dtype]
         self.xd = torch.empty((cap, H), dtype=act, device=dev)
         self.h = torch.empty((cap, I), dtype=act, device=dev)
-        fp8 = act_dtype == "fp8"
+        fp8, int8 = act_dtype == "fp8", act_dtype == "int8"
         self.xd_scales = torch.empty((cap, -(-H // FP8_BLOCK)), dtype=torch.float32, device=dev) if fp8 else None
         self.h_scales = torch.empty((cap, -(-I // FP8_BLOCK)), dtype=torch.float32, device=dev) if fp8 else None
+        self.h_act = None
+        if int8:
+            self.xd_scales = torch.empty(cap, dtype=torch.float32, device=dev)
+            self.h_scales = torch.empty(cap, dtype=torch.float32, device=dev)
+            self.h_act = torch.empty((cap, I), dtype=torch.bfloat16, device=dev)   # gate/up's h
         self.y = torch.empty((cap, H), dtype=_TORCH[y_dtype], device=dev)
         self.out = torch.empty((T, H), dtype=_TORCH[out_dtype], device=dev)
         # placement map (E,) int32 on the device, logical -> physical expert id; when
         # set, routing emits physical ids and [e_begin, e_end) is a physical range
         self.expert_map = None
+        # balance bias (E,) fp32 on the device for the scored router (None: no bias)
+        self.router_bias = None
 
     # individual stages (each one library call) ---------------------------------
     def route(self, logits, stream=None):
-        if self.n_shared:
+        if self.router is not None:
+            moe_route_scored(logits, self.K_routed, bias=self.router_bias, phys_of_logical=self.expert_map,
+                             n_shared=self.n_shared, topk_ids=self.topk_ids, topk_w=self.topk_w, stream=stream,
+                             **self.router)
+        elif self.n_shared:
             if self.expert_map is not None:
                 raise ValueError("a placement map with shared experts is not supported")
             moe_route_shared(logits, self.K_routed, self.n_shared, self.topk_ids, self.topk_w,
@@ -113,9 +138,14 @@ class MoELayer:
 
     def gate_up(self, w, stream=None):
         moe_ffn_gate_up(self.xd, self.xd_scales, self.rows, w["gate"], w["up"],
-                        w.get("gate_scale"), w.get("up_scale"), self.h, self.h_scales,
-                        expected_rows=self.expected_rows, stream=stream, cap_per_expert=self.cap_e,
+                        w.get("gate_scale"), w.get("up_scale"), self.h if self.h_act is None else self.h_act,
+                        self.h_scales if self.h_act is None else None, expected_rows=self.expected_rows, stream=stream, cap_per_expert=self.cap_e,
                         w_scales_pow2=bool(w.get("scales_pow2", False)))
+
+    def quant_h(self, stream=None):
+        """int8 only: gate/up's bf16 h to int8 rows and their scales."""
+        moe_quant_rows(self.h_act, self.rows, cap_per_expert=self.cap_e, q=self.h, scales=self.h_scales,
+                       stream=stream)
 
     def down(self, w, stream=None):
         moe_ffn_down(self.h, self.h_scales, self.rows, w["down"], w.get("down_scale"), self.y,
@@ -126,11 +156,13 @@ class MoELayer:
         moe_combine(self.y, self.row_of, self.topk_w, self.out, stream=stream)
 
     def stages(self, x_segments, logits, w):
-        """(name, thunk) pairs of the six calls, in order."""
+        """(name, thunk) pairs of the six calls (int8: seven), in order."""
+        quant = [("quant_h", lambda s=None: self.quant_h(s))] if self.h_act is not None else []
         return [("route", lambda s=None: self.route(logits, s)),
                 ("layout", lambda s=None: self.layout(s)),
                 ("dispatch", lambda s=None: self.dispatch(x_segments, s)),
                 ("ffn_gate_up", lambda s=None: self.gate_up(w, s)),
+                *quant,
                 ("ffn_down", lambda s=None: self.down(w, s)),
                 ("combine", lambda s=None: self.combine(s))]
 
@@ -200,11 +232,15 @@ class MicroBatchedLayer:
         b.layout(self.side)
         b.dispatch(xb, self.side)
         a.gate_up(w, main)
+        if a.h_act is not None:
+            a.quant_h(main)
         a.down(w, main)
         self._ev_a_ffn.record(main)
         a.combine(main)
         self.side.wait_event(self._ev_a_ffn)
         b.gate_up(w, self.side)
+        if b.h_act is not None:
+            b.quant_h(self.side)
         b.down(w, self.side)
         b.combine(self.side)
         self._ev_b_done.record(self.side)

@@ -28,13 +28,15 @@
  *   - MOE_ERR_HIP reports a failed kernel launch.  Faults inside a kernel
  *     surface, as always with HIP, at the caller's next synchronisation.
  *   - Sizes: 1 <= K <= E <= 1024; 0 <= e_begin < e_end <= E; B >= 0;
- *     H and I multiples of 8 (of 16 when activations are fp8); row base
- *     pointers 16-byte aligned.
+ *     H and I multiples of 8 (of 16 when activations are fp8 or int8); row
+ *     base pointers 16-byte aligned.
  *   - Calls on one stream run in order; calls that share output or
  *     workspace buffers on different streams race.
  *   - Expert ids outside [0, E) in topk_ids are treated as unrouted slots.
  *   - Non-finite logits or activations are outside the method; results
- *     are then unspecified (but all memory accesses stay in bounds).
+ *     are then unspecified (but all memory accesses stay in bounds), except
+ *     where an entry point says what it does with them (moe_route_scored,
+ *     the int8 quantisation).
  */
 #ifndef MOEEP_H
 #define MOEEP_H
@@ -64,10 +66,24 @@ enum {
     MOE_F32 = 0,
     MOE_BF16 = 1,
     MOE_FP8_E4M3 = 2,          /* OCP e4m3fn (finite max 448), with fp32 1x128 block scales */
-    MOE_FP8_E4M3_PO2 = 3       /* weights only: e4m3fn whose fp32 block scales are all powers
+    MOE_FP8_E4M3_PO2 = 3,      /* weights only: e4m3fn whose fp32 block scales are all powers
                                   of two 2^e, e in [-127, 127] (the E8M0 scale convention of
                                   the microscaling formats); the matrix cores apply such
                                   scales, and only a scale's exponent field is read */
+    MOE_INT8 = 4               /* two's complement codes with one fp32 scale per row: per token
+                                  for activations, per output channel for weights; a code c
+                                  stands for c * scale */
+};
+
+/* Largest H and I of int8 operands: sums of this many products of two codes
+   stay below 2^31. */
+#define MOE_INT8_MAX_COLS 131056
+
+/* Expert scores of moe_route_scored. */
+typedef int32_t moe_score_t;
+enum {
+    MOE_SCORE_SOFTMAX = 0,     /* softmax over all E logits */
+    MOE_SCORE_SIGMOID = 1      /* 1 / (1 + exp(-logit)) */
 };
 
 /* Largest number of simulated source segments moe_dispatch accepts. */
@@ -148,6 +164,39 @@ moe_status_t moe_route_mapped(const float* logits, int B, int E, int K, const in
  */
 moe_status_t moe_route_shared(const float* logits, int B, int E, int K, int n_shared, int32_t* ids,
                               float* w, hipStream_t stream);
+
+/*
+ * moe_route_scored -- top-K selection by a score and a balance bias, inside
+ * the best expert groups.
+ *   logits (B, E) of logits_dt (MOE_F32 or MOE_BF16); bias (E) fp32 or NULL.
+ *   s_e = softmax over the E logits, or sigmoid of each (moe_score_t);
+ *   c_e = s_e + bias_e decides the choice, s_e alone the weights.
+ *   The E experts form n_groups groups of E / n_groups consecutive ids.  A
+ *   group's score is the sum of its group_top (1 or 2) largest c; the
+ *   topk_groups best groups stay, and the K largest c among their experts are
+ *   picked, largest first.  c is computed and compared in 64 bits; ties go to
+ *   the lower group and the lower id.  n_groups = topk_groups = 1: no groups.
+ *   topk_w = s of the picks, divided by their sum if renorm is not 0 (a sum of
+ *   zero gives zeros), times scale.
+ *   An expert is out where its logit or bias is at or below the lowest finite
+ *   bf16 value, -(2 - 2^-7) * 2^127, which -inf and the lowest fp32 value are
+ *   too: it is never picked, it does not count for its group, and a masked
+ *   logit adds nothing to the softmax.  Slots that find no expert get id -1
+ *   (an unrouted slot for moe_layout) and weight 0.  A NaN logit ranks behind
+ *   every number and its weight is NaN (softmax: every weight of the row).
+ *   phys_of_logical (E) int32 or NULL, as in moe_route_mapped; n_shared >= 0
+ *   always-on slots after the K picks, ids E, E+1, ... with weight 1.0, as in
+ *   moe_route_shared (not mapped).
+ *   ids, w (B, K + n_shared) int32 / fp32 out.
+ * B = 0 is a no-op.  Errors as for moe_route_shared; MOE_ERR_INVALID_ARG
+ * for n_groups not dividing E, topk_groups outside [1, n_groups], group_top
+ * other than 1 or 2, K > topk_groups * E / n_groups, or a scale that is not
+ * finite; MOE_ERR_UNSUPPORTED for another logits_dt or score.
+ */
+moe_status_t moe_route_scored(const void* logits, moe_dtype_t logits_dt, const float* bias, int B, int E, int K,
+                              moe_score_t score, int n_groups, int topk_groups, int group_top, int renorm,
+                              float scale, const int32_t* phys_of_logical, int n_shared, int32_t* ids, float* w,
+                              hipStream_t stream);
 
 /*
  * moe_eplb_place -- expert placement for load balancing (host function; no
@@ -237,13 +286,15 @@ moe_status_t moe_layout_masked(const int32_t* topk_ids, int B, int K, int E, int
  *   row_of   (B, K) int32 from moe_layout.
  *   xd       (cap_rows, H) of xd_dt out: xd[row_of[t,k]] = x[t] for every
  *            local slot.  Rows not named by row_of are not written.
- *   xd_scales (cap_rows, ceil(H/128)) fp32 out, fp8 only (else may be NULL).
+ *   xd_scales fp32 out: fp8 (cap_rows, ceil(H/128)), int8 (cap_rows) -- else
+ *            may be NULL.
  * Supported (x_dt -> xd_dt): F32 -> F32 and BF16 -> BF16 (bit-exact
  * copies); BF16 -> FP8_E4M3 (each token quantised once: per 128-element
  * block s = the smallest power of two 2^e with amax <= 448 * 2^e, e >= -127
  * (1 if amax = 0; the E8M0 scale convention), code = RNE(v/s) saturated to
  * +-448, with fp32 arithmetic; all K copies carry identical codes and
- * scales).
+ * scales); BF16 or F32 -> INT8 (each token quantised once, as moe_quant_rows
+ * does a row; H <= MOE_INT8_MAX_COLS).
  */
 moe_status_t moe_dispatch(const void* const* seg_x, const int32_t* seg_rows, int n_seg,
                           moe_dtype_t x_dt, int H, const int32_t* row_of, int K,
@@ -269,12 +320,20 @@ moe_status_t moe_dispatch(const void* const* seg_x, const int32_t* seg_rows, int
  * offsets[E_local] of h and y are not written.
  *
  * Supported (act_dt, w_dt, y_dt): (F32, F32, F32), (BF16, BF16, BF16),
- * (FP8_E4M3, FP8_E4M3, BF16), (FP8_E4M3, FP8_E4M3_PO2, BF16).  The
+ * (FP8_E4M3, FP8_E4M3, BF16), (FP8_E4M3, FP8_E4M3_PO2, BF16),
+ * (INT8, INT8, BF16), (INT8, INT8, F32).  The
  * activation block scales of the fp8 path (xd_scales from moe_dispatch,
  * h_scales) are always powers of two; FP8_E4M3_PO2 declares that the
  * weight scales are too, which lets the row-rich kernels apply every scale
  * in the matrix cores (same results up to fp32 rounding order).  Any w_dt
  * may carry MOE_W_PACKED: weights packed by moe_pack_weights (below).
+ *
+ * int8: xd codes with xd_scales (cap_rows), weight codes with one scale per
+ * output channel, w_gate_scales, w_up_scales (E_local, I), w_down_scales
+ * (E_local, H); products are summed exactly in int32 and scaled in fp32.
+ * moe_ffn_gate_up writes h as bf16 (rounded once; h_scales unused, may be
+ * NULL), moe_quant_rows turns it into the int8 rows and h_scales (cap_rows)
+ * that moe_ffn_down takes; moe_grouped_ffn makes the three calls.
  *
  * moe_ffn_gate_up computes h; moe_ffn_down computes y from h;
  * moe_grouped_ffn runs both with h (and h_scales) carved from `ws`, which
@@ -318,6 +377,26 @@ int moe_weight_ld(int cols, moe_dtype_t w_dt);
 size_t moe_packed_weight_bytes(int E_local, int rows, int cols, moe_dtype_t w_dt);
 moe_status_t moe_pack_weights(const void* w, int E_local, int rows, int cols, moe_dtype_t w_dt,
                               void* w_packed, hipStream_t stream);
+
+/*
+ * moe_quant_rows -- int8 codes and a scale for each row of x (cap_rows, cols).
+ *   x      F32 or BF16; cols a multiple of 16, at most MOE_INT8_MAX_COLS.
+ *   Valid rows: [offsets[0], offsets[E_local]) of the contiguous layout; all
+ *   cap_rows rows when offsets is NULL (E_local unused), e.g. weight rows,
+ *   whose scales are then one per output channel.  Other rows of q and scales
+ *   are not written.
+ *   q      (cap_rows, cols) int8 out; scales (cap_rows) fp32 out.
+ *   scale = max |v| / 127 rounded to fp32 (at least 2^-126; 1 for a row of
+ *   zeros); code = v / scale rounded to the nearest integer, ties to even,
+ *   from the exact quotient.  A row with a NaN or an infinity gets scale NaN
+ *   and codes 0, so every product with it is NaN.
+ * The masked variant takes m (E_local) of moe_layout_masked instead; x, q and
+ * scales have E_local * cap_per_expert rows.
+ */
+moe_status_t moe_quant_rows(const void* x, moe_dtype_t x_dt, const int32_t* offsets, int E_local, int cap_rows,
+                            int cols, int8_t* q, float* scales, hipStream_t stream);
+moe_status_t moe_quant_rows_masked(const void* x, moe_dtype_t x_dt, const int32_t* m, int E_local,
+                                   int cap_per_expert, int cols, int8_t* q, float* scales, hipStream_t stream);
 
 moe_status_t moe_ffn_gate_up(const void* xd, const float* xd_scales, const int32_t* offsets,
                              int E_local, int cap_rows, int H, int I, moe_dtype_t act_dt,

@@ -20,6 +20,8 @@ Parity status of each function (what pins it, in tests/test_oracle_*.py):
                  at K = E, brute-force top-K over {-1,0,1}^E.
   route_shared   pinned: the layer with a shared expert equals the routed
                  layer plus a dense SwiGLU of the shared weights per token.
+  route_scored   pinned: hand-worked groups and masks, agreement with route where
+                 the rules coincide, a ranking by counting.
   layout         pinned: brute-force construction, sum of counts, bijection.
   layout_masked  pinned: agrees with the contiguous layout (a different
                  construction) shifted to fixed row blocks; overflow keeps the
@@ -30,13 +32,14 @@ Parity status of each function (what pins it, in tests/test_oracle_*.py):
                  optima of small instances, and the report's outcome (2x ->
                  within 5%) on the EP-share workload's routing.
   expert_ffn     pinned: dense SwiGLU via torch CPU, pure-Python brute force.
-  numerics       pinned: exhaustive bf16 / e4m3 casts against torch.
+  numerics       pinned: exhaustive bf16 / e4m3 casts against torch; int8 rows
+                 against rational arithmetic.
   fp8 block geometry and scale rule: parity unpinned by the pages (a reading
   both sides implement); its properties are checked.
 """
 from . import eplb, numerics
-from .moe import (route, route_shared, layout, layout_masked, dispatch, silu, expert_ffn, grouped_ffn,
+from .moe import (route, route_scored, route_shared, layout, layout_masked, dispatch, silu, expert_ffn, grouped_ffn,
                   grouped_ffn_masked, combine, layer)
 
-__all__ = ["eplb", "numerics", "route", "route_shared", "layout", "layout_masked", "dispatch", "silu", "expert_ffn",
+__all__ = ["eplb", "numerics", "route", "route_scored", "route_shared", "layout", "layout_masked", "dispatch", "silu", "expert_ffn",
            "grouped_ffn", "grouped_ffn_masked", "combine", "layer"]

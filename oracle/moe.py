@@ -67,6 +67,61 @@ def route(logits, K: int):
     return ids, gates
 
 
+LOWEST_BF16 = -(2.0 - 2.0**-7) * 2.0**127
+
+
+def route_scored(logits, K: int, score: str, bias=None, n_groups: int = 1, topk_groups: int = 1,
+                 group_top: int = 2, renorm: bool = True, scale: float = 1.0):
+    """Top-K by score plus bias inside the best expert groups, token by token.
+
+    s = sigmoid of each logit, or softmax over the logits that are not masked;
+    c = s + bias orders the experts (ties: lower id), and the groups of E /
+    n_groups consecutive experts by the sum of their group_top largest c (ties:
+    lower group).  An expert whose logit or bias is at or below the lowest
+    finite bf16 value is out.  Gates are the picks' s, divided by their sum
+    (zero: zeros) if renorm, times scale; slots without an expert get id -1 and
+    gate 0.  NaN scores rank behind every number.
+    """
+    lg = np.asarray(logits, dtype=np.float64)
+    B, E = lg.shape
+    b = np.zeros(E) if bias is None else np.asarray(bias, dtype=np.float64)
+    size = E // n_groups
+    ids = np.full((B, K), -1, dtype=np.int32)
+    gates = np.zeros((B, K))
+
+    def best_first(values, names):
+        return [n for v, n in sorted(((np.isnan(v), -v if not np.isnan(v) else 0.0), n)
+                                     for v, n in zip(values, names))]
+
+    for t in range(B):
+        seen = [e for e in range(E) if not lg[t, e] <= LOWEST_BF16]
+        s = np.zeros(E)
+        with np.errstate(over="ignore", invalid="ignore"):
+            if score == "sigmoid":
+                s[seen] = 1.0 / (1.0 + np.exp(-lg[t, seen]))
+            elif seen:
+                m = np.fmax.reduce(lg[t, seen])          # NaN only if all are
+                p = np.exp(lg[t, seen] - m)
+                s[seen] = p / p.sum()
+        c = s + b
+        on = [e for e in seen if not b[e] <= LOWEST_BF16]
+        if topk_groups < n_groups:
+            members = {}
+            for e in on:
+                members.setdefault(e // size, []).append(e)
+            names = sorted(members)
+            sums = [sum(c[best_first(c[members[g]], members[g])[:group_top]]) for g in names]
+            kept = set(best_first(sums, names)[:topk_groups])
+            on = [e for e in on if e // size in kept]
+        pick = best_first(c[on], on)[:K]
+        v = s[pick]
+        if renorm and len(pick):
+            v = np.zeros(len(pick)) if v.sum() == 0.0 else v / v.sum()
+        ids[t, :len(pick)] = pick
+        gates[t, :len(pick)] = v * scale
+    return ids, gates
+
+
 # ----------------------------------------------------------------------------
 # layout
 # ----------------------------------------------------------------------------
@@ -91,7 +146,8 @@ def route_shared(logits, K: int, n_shared: int):
 def layout(ids, E: int, e_begin: int, e_end: int, cap: int):
     """Per-expert counts, offsets and the (token, slot) <-> row permutation.
 
-    counts[e]   number of (t, k) with ids[t, k] == e, over all E experts.
+    counts[e]   number of (t, k) with ids[t, k] == e, over all E experts (ids
+                outside [0, E) are unrouted slots).
     offsets     exclusive prefix sum of counts over the local experts
                 [e_begin, e_end), with the total appended (length E_loc + 1).
     row_of[t,k] destination row of slot (t, k) in the expert-contiguous
@@ -103,7 +159,7 @@ def layout(ids, E: int, e_begin: int, e_end: int, cap: int):
     ids = np.asarray(ids)
     B, K = ids.shape
     flat = ids.reshape(-1).astype(np.int64)
-    counts = np.bincount(flat, minlength=E).astype(np.int32)
+    counts = np.bincount(flat[(flat >= 0) & (flat < E)], minlength=E).astype(np.int32)
     E_loc = e_end - e_begin
     offsets = np.zeros(E_loc + 1, dtype=np.int32)
     offsets[1:] = np.cumsum(counts[e_begin:e_end])
@@ -170,14 +226,19 @@ def dispatch(x, row_of, n_rows: int, act: str):
     of Xd: 'f32' / 'bf16' copy the row unchanged (x must already be on that
     grid); 'fp8' quantises each token row once (block-wise, see numerics) and
     every one of its K copies holds the same codes and scales.
-    Returns (xd, xd_scales) with xd of shape (n_rows, H) (codes for fp8) and
-    xd_scales (n_rows, ceil(H/128)) fp32 for fp8, else None.
+    'int8' likewise with one scale per token.
+    Returns (xd, xd_scales) with xd of shape (n_rows, H) (codes for fp8 and
+    int8) and xd_scales (n_rows, ceil(H/128)) fp32 for fp8, (n_rows, 1) for
+    int8, else None.
     """
     x = np.asarray(x, dtype=np.float64)
     row_of = np.asarray(row_of)
     T, H = x.shape
     if act == "fp8":
         src, scales_src = nx.quantize_fp8_blocks(x)
+    elif act == "int8":
+        codes, scales_src = nx.quantize_i8_rows(x)
+        src, scales_src = codes.astype(np.float64), scales_src[:, None]
     elif act in ("f32", "bf16"):
         src, scales_src = x, None
     else:
@@ -219,6 +280,8 @@ def expert_ffn(X, Wg, Wu, Wd, h_dtype: str, y_dtype: str):
     hr = nx.round_act(h, h_dtype)
     if h_dtype == "fp8":
         hr = nx.dequantize_fp8_blocks(*hr)
+    elif h_dtype == "int8":
+        hr = hr[0].astype(np.float64) * hr[1].astype(np.float64)[:, None]
     y = hr @ np.asarray(Wd, dtype=np.float64).T
     return nx.round_act(y, y_dtype)
 
@@ -275,7 +338,7 @@ def combine(y, row_of, gates, out_dtype: str):
 # whole layer
 # ----------------------------------------------------------------------------
 def layer(x, logits, K, E, e_begin, e_end, weights_of, act, y_dtype, out_dtype,
-          gates_dtype="f32", n_shared=0):
+          gates_dtype="f32", n_shared=0, routing=None):
     """route -> layout -> dispatch -> grouped FFN -> combine on one GPU's share.
 
     x (T, H) token rows (values on their storage grid), logits (T, E).
@@ -283,9 +346,14 @@ def layer(x, logits, K, E, e_begin, e_end, weights_of, act, y_dtype, out_dtype,
     stored as fp32 before use (gates_dtype) as the layer hands them between
     steps in fp32.  With n_shared > 0 the shared experts E.. are appended to
     the routing (route_shared) and to the local range, which must then end
-    at E.  Returns a dict with every intermediate.
+    at E.  routing: (ids, gates) to use in place of route's (e.g. from
+    route_scored).  Returns a dict with every intermediate.
     """
-    if n_shared:
+    if routing is not None:
+        ids, gates = routing
+        K = ids.shape[1]
+        E, e_end = E + n_shared, e_end + n_shared
+    elif n_shared:
         if e_end != E:
             raise ValueError("shared experts need the local range to end at E")
         ids, gates = route_shared(logits, K, n_shared)
@@ -297,7 +365,7 @@ def layer(x, logits, K, E, e_begin, e_end, weights_of, act, y_dtype, out_dtype,
     lay = layout(ids, E, e_begin, e_end, T * K)
     R = int(lay["offsets"][-1])
     xd, xs = dispatch(x, lay["row_of"], R, act)
-    xd_val = nx.dequantize_fp8_blocks(xd, xs) if act == "fp8" else xd
+    xd_val = nx.dequantize_fp8_blocks(xd, xs) if act == "fp8" else xd * xs if act == "int8" else xd
     y = grouped_ffn(xd_val, lay["offsets"], weights_of, act, y_dtype)
     out = combine(y, lay["row_of"], gates_s, out_dtype)
     return {"ids": ids, "gates": gates, **lay, "xd": xd, "xd_scales": xs,

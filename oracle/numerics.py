@@ -126,12 +126,34 @@ def dequantize_fp8_blocks(codes, scales, block: int = FP8_BLOCK) -> np.ndarray:
     return codes * s
 
 
+def quantize_i8_rows(v):
+    """int8 quantisation of each row (last axis): scale = max |v| / 127 stored in
+    fp32 (at least 2^-126, 1 for a row of zeros), code = v / scale from the exact
+    quotient to the nearest integer, ties to even.  A row holding a NaN or an
+    infinity gets scale NaN and codes 0.
+
+    v: fp32-representable values, finite or not.  Returns (codes int8, scales
+    fp32).  The quotient of two fp32 values that is no tie is further from one
+    than an fp64 division's error, so np.rint of the fp64 quotient is exact.
+    """
+    v = np.asarray(v, dtype=np.float64)
+    amax = np.max(np.abs(v), axis=-1)                 # NaN if the row holds one
+    bad = ~np.isfinite(amax)
+    s = np.where(amax > 0, np.maximum(np.where(bad, 1.0, amax) / 127.0, 2.0**-126), 1.0)
+    s = s.astype(np.float32)
+    with np.errstate(invalid="ignore"):
+        codes = np.where(bad[..., None], 0.0, np.rint(v / s.astype(np.float64)[..., None]))
+    return codes.astype(np.int8), np.where(bad, np.float32(np.nan), s)
+
+
 def round_act(v, dtype: str, rule: str = "pow2"):
     """Round activations to the storage type named by ``dtype``.
 
     'f32' and 'bf16' return fp64 values on that grid; 'fp8' returns the
     (codes, scales) pair of :func:`quantize_fp8_blocks` (scale rule ``rule``)
-    taken on the fp32 rounding of ``v``.
+    taken on the fp32 rounding of ``v``, 'int8' that of
+    :func:`quantize_i8_rows` on its bf16 rounding (gate/up stores h in bf16
+    before its rows are quantised).
     """
     if dtype == "f32":
         return to_f32(v)
@@ -139,4 +161,6 @@ def round_act(v, dtype: str, rule: str = "pow2"):
         return to_bf16(v)
     if dtype == "fp8":
         return quantize_fp8_blocks(to_f32(v), rule=rule)
+    if dtype == "int8":
+        return quantize_i8_rows(to_bf16(v))
     raise ValueError(f"unknown dtype {dtype!r}")
