@@ -15,6 +15,7 @@
 //
 // h leaves gate/up as bf16, not int8: its scale is the largest magnitude of a
 // whole row, which many tiles write; moe_quant_rows makes the int8 rows.
+#include "gemm_wide_i8.hpp"
 #include "grouped_tiles.hpp"
 
 namespace moeep {
@@ -195,9 +196,28 @@ hipError_t launch_cfg(const FfnArgs& a, hipStream_t stream) {
                              &per_cu);
 }
 
+template <int BM, bool GATED, bool OUT_F32>
+hipError_t launch_wide(const FfnArgs& a, hipStream_t stream) {
+    static int per_cu = 0;
+    return launch_persistent(widei8::grouped_gemm_i8_wide_kernel<BM, GATED, OUT_F32>, 512, a, stream, &per_cu);
+}
+
+template <int BM>
+hipError_t launch_wide_any(const FfnArgs& a, bool gated, hipStream_t stream) {
+    if (gated) return launch_wide<BM, true, false>(a, stream);
+    return a.out_f32 ? launch_wide<BM, false, true>(a, stream) : launch_wide<BM, false, false>(a, stream);
+}
+
 }  // namespace
 
 hipError_t launch_ffn_i8(const FfnArgs& a, bool gated, hipStream_t stream) {
+    // the wide kernels address one expert's weight matrix with 32-bit offsets
+    // and keep every resource extent (plus the k-step offset) below 2^31, so
+    // that an out-of-range lane offset exists
+    const bool wide_ok = (unsigned long long)a.N * a.ldw < (1ull << 31) &&
+                         (unsigned long long)320 * (a.Kdim + 128) < (1ull << 31);
+    if (wide_ok && a.rows_hint >= 192) return launch_wide_any<320>(a, gated, stream);
+    if (wide_ok && a.rows_hint >= 64) return launch_wide_any<256>(a, gated, stream);
     if (gated) return launch_cfg<128, 128, 2, 2, true, false>(a, stream);
     return a.out_f32 ? launch_cfg<128, 128, 2, 2, false, true>(a, stream)
                      : launch_cfg<128, 128, 2, 2, false, false>(a, stream);
