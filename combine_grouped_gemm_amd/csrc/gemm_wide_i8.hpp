@@ -1,19 +1,33 @@
-// Wide int8 grouped GEMM tile for experts with many rows (SwiGLU gate/up or
-// plain down projection), used by ffn_i8.hip.
+// Int8 grouped GEMM tile (SwiGLU gate/up or plain down projection), used by
+// ffn_i8.hip.
 //
-// A tile is up to BM rows of one expert by 256 weight rows (gate/up: 128 gate
-// + 128 up rows of the same output columns, so the SwiGLU epilogue has g and u
-// of a column in one wave).  A row's step of the contraction is 128 codes, the
-// 128 bytes of a bf16 step, and v_mfma_i32_16x16x64_i8 takes the same 16 bytes
-// per lane in the same layout as the bf16 instruction, so the operands move
-// through the ring of gemm_wide.hpp: loads straight into LDS through bounded
-// buffer resources, two stages, chunks XOR-swizzled by (row & 7), one copy of
-// the k-loop per number of valid fragments, the weight stream two steps ahead.
-// Half the bf16 kernel's bytes and instructions for the same product.
+// A tile is up to BM rows of one expert by BN weight rows (gate/up: BN / 2
+// gate + BN / 2 up rows of the same output columns, so the SwiGLU epilogue has
+// g and u of a column in one wave).  A row's step of the contraction is 128
+// codes, one cache line; v_mfma_i32_16x16x64_i8 takes 16 bytes per lane of
+// each operand.  Operands go from global memory straight into LDS through
+// bounded buffer resources, in two stages; the 16-byte chunks of an LDS row
+// are XOR-swizzled by (row & 7), so the rows of one MFMA operand read fall
+// into distinct banks; a tile runs one of FM + 1 copies of the k-loop by its
+// count of valid row fragments (as gemm_wide.hpp does, with which it shares
+// the load and wait helpers).
+//
+// Where it differs is what is in flight.  The second k-half's fragments are
+// read under the first half's MFMAs, so that half-way through step k every
+// wave holds all it needs of the stage, rows and weights alike, and step
+// k + 2's loads go into it: one and a half steps ahead for both operands.
+// With the weights ahead but the rows only one step (the bf16 scheme) every
+// step waited for its rows' first touch of the XCD's L2.
 //
 // The sums stay in int32 to the end: no scale touches the k-loop.  The tile's
 // row and column scales are asked for before it and applied in the epilogue
 // (row scales through LDS, a lane's column scales in registers).
+//
+// Measured (MI355X; DeepSeek-shaped layer, H = 7168, I = 2048, 256 experts):
+// decode gate/up, T = 128: 0.98-1.00 ms, 7.4-7.6 TB/s, 92% of the HBM peak.
+// Prefill, T = 8192: 2.08-2.18 ms, 1.8 POP/s; counters (256-row tiles) show
+// the MFMAs busy 54% of the cycles at a clock of 1.4 GHz, and versions with 10%
+// fewer cycles took the same time: the part's power holds it there.
 #pragma once
 
 #include "gemm_wide.hpp"
@@ -25,10 +39,7 @@ using wide::block_barrier;
 using wide::ic;
 using wide::kNonTemporal;
 using wide::kOutOfRange;
-using wide::lds_addr;
 using wide::lds_buf16;
-using wide::lds_read16x4;
-using wide::lds_read16x8;
 using wide::make_rsrc;
 using wide::rsrc_t;
 using wide::swz;
@@ -37,7 +48,6 @@ using wide::wait_vmcnt;
 
 typedef int intx4 __attribute__((ext_vector_type(4)));
 
-constexpr int BN = 256;
 constexpr int BK = 128;             // codes per k-step: 128 bytes per row
 constexpr int CPR = 8;              // 16-byte chunks per row
 constexpr int ROWB = 128;           // bytes per LDS row
@@ -45,28 +55,22 @@ constexpr int ROWB = 128;           // bytes per LDS row
 // 8 waves laid out 2 (rows) x 4 (weight rows).  A wave owns the interleaved
 // 16-row fragments {wm, wm + 2, ...} (so a short tile still spreads its valid
 // rows over both row-waves) and 64 weight rows.
-template <int BM, bool GATED, bool OUT_F32>
-__global__ __launch_bounds__(512, 1) void grouped_gemm_i8_wide_kernel(FfnArgs p) {
+template <int BM, int BN, bool GATED, bool OUT_F32, bool NT_W>
+__global__ __launch_bounds__(512, BM + BN > 256 ? 1 : 4) void grouped_gemm_i8_wide_kernel(FfnArgs p) {
     constexpr int WMW = 2, WNW = 4, NT = 512, NW = 8;
     constexpr int A_BLOCKS = BM * CPR / 64;          // 1 KiB blocks of a row stage
     constexpr int BLOCKS = (BM + BN) * CPR / 64;
     constexpr int LPS = BLOCKS / NW;                 // direct loads per wave per stage
     constexpr int FM = BM / 16 / WMW;                // 16-row fragments per wave
-    constexpr int WN = BN / WNW;                     // 64 weight rows per wave
-    constexpr int FN = WN / 16;                      // 4
+    constexpr int WN = BN / WNW;                     // weight rows per wave
+    constexpr int FN = WN / 16;                      // 16-row weight fragments per wave
     constexpr int BNO = GATED ? BN / 2 : BN;         // output columns per tile
     static_assert(BM % 32 == 0 && BLOCKS % NW == 0 && (!GATED || FN % 2 == 0), "tile shape");
-    // block q = i * NW + wave: whether it is a row block and which weight half it
-    // covers depends only on i, so both are compile-time after unrolling
-    static_assert(A_BLOCKS % NW == 0 && (BN / 16) % NW == 0, "block split");
+    // load i of the 8 waves covers 64 operand rows: whether they are token rows
+    // and which weight half they belong to is compile-time after unrolling
+    static_assert(BM % 64 == 0 && BN % 128 == 0, "64-row blocks");
     constexpr int A_ITERS = A_BLOCKS / NW;           // i < A_ITERS: row blocks
-    constexpr int G_ITERS = (BN / 16) / NW;          // next G_ITERS: gate (or first) weight half
-    constexpr int B_ITERS = LPS - A_ITERS;           // weight loads per wave per stage
-    // Tiles of at most 256 rows keep both k-halves' weight fragments of a step
-    // in registers, so the weight buffer of step k takes step k + 2's weights
-    // as soon as every wave holds them (the weight stream keeps up to two
-    // steps in flight); 320-row tiles have no registers to spare for that.
-    constexpr bool LOOK = BM <= 256;
+    constexpr int G_ITERS = BN / 128;                // next G_ITERS: the gate half's 64-row blocks
 
     __shared__ uint4 sa0[BM * CPR];
     __shared__ uint4 sb0[BN * CPR];
@@ -110,51 +114,49 @@ __global__ __launch_bounds__(512, 1) void grouped_gemm_i8_wide_kernel(FfnArgs p)
     const uint8_t* __restrict__ W0 = static_cast<const uint8_t*>(p.w0);
     const uint8_t* __restrict__ W1 = static_cast<const uint8_t*>(p.w1);
 
-    for (int tau = v; tau < total; tau += G) {
+    // tiles come in order of decreasing cost: every other round runs backwards over
+    // the blocks, so that none gets the largest tile of every round
+    for (int base = 0, rnd = 0; base < total; base += G, ++rnd) {
+        const int tau = base + (rnd & 1 ? G - 1 - v : v);
+        if (tau >= total) continue;
         const TileCoord tc = decode_tile<BM>(tau, n_tiles_n, s_pre, p, s_ord);
         const int j = tc.j, row0 = tc.row0, nvalid = tc.nvalid;
         const int col0 = tc.nt * BNO;
-        const uint8_t* wg = W0 + (size_t)j * N * ldw;
-        const uint8_t* wu = GATED ? W1 + (size_t)j * N * ldw : nullptr;
+        // the tile's weight rows start at output column col0
+        const size_t w0 = ((size_t)j * N + col0) * ldw;
+        const uint8_t* wg = W0 + w0;
+        const uint8_t* wu = GATED ? W1 + w0 : nullptr;
 
         // Operands come in by buffer loads straight into LDS: a scalar resource
-        // per operand (base, byte extent) plus a 32-bit per-lane offset and the
-        // k-step as scalar offset.  Rows past the tile's valid rows and weight
-        // rows past N lie outside their resource's extent, so those lanes read
-        // nothing from memory and land zeros.  Each lane's offset is fixed for
-        // the tile.
-        const char* abase = reinterpret_cast<const char*>(A + (size_t)row0 * Kdim);
-        const uint32_t a_bytes = (uint32_t)nvalid * (uint32_t)Kdim;
-        const uint32_t w_bytes = (uint32_t)N * (uint32_t)ldw;
-        uint32_t off[LPS];
-#pragma unroll
-        for (int i = 0; i < LPS; ++i) {
-            const bool is_a = i < A_ITERS;
-            const int r = (is_a ? i * NW : (i - A_ITERS) * NW) * 8 + wave * 8 + lane / 8;
-            const uint32_t c16 = (uint32_t)swz(r, lane % 8) * 16;   // logical chunk this lane fetches
-            const int rr = (!is_a && GATED && r >= BN / 2) ? r - BN / 2 : r;
-            off[i] = (is_a ? (uint32_t)r * (uint32_t)Kdim : (uint32_t)(col0 + rr) * (uint32_t)ldw) + c16;
-        }
-        // direct load i of a stage; `live` false (the step after the last) reads
+        // (base, byte extent) for each block of 64 operand rows, the k-step as
+        // scalar offset and one 32-bit lane offset per operand.  Rows past the
+        // tile's valid rows and weight rows past N lie outside their resource's
+        // extent, so those lanes read nothing from memory and land zeros.
+        const uint8_t* abase = A + (size_t)row0 * Kdim;
+        const int wrows = min(N - col0, BNO);                   // weight rows of the tile (of each half)
+        const uint32_t lrow = wave * 8 + lane / 8;              // this lane's row of a 64-row block
+        const uint32_t off_a = lrow * (uint32_t)Kdim + lane_k, off_w = lrow * (uint32_t)ldw + lane_k;
+        // direct load i of a stage; `live` false (a step past the last) reads
         // nothing, so every step issues the same LPS loads without a branch
         auto issue_one = [&](auto I, int i, int kstep, bool live) {
             const bool is_a = i < A_ITERS;
-            const bool up = GATED && i >= A_ITERS + G_ITERS;
-            char* dst = is_a ? a_base(I) + (i * NW + wave) * 1024
-                             : b_base(I) + ((i - A_ITERS) * NW + wave) * 1024;
-            // the step after the last gets an empty extent: every access out of range
-            const rsrc_t r = make_rsrc(is_a ? (const void*)abase : (up ? (const void*)wu : (const void*)wg),
-                                       live ? (is_a ? a_bytes : w_bytes) : 0u);
+            const int q = i - A_ITERS;                          // 64-row block of the weights
+            const bool up = GATED && q >= G_ITERS;
+            const int first = is_a ? i * 64 : (up ? q - G_ITERS : q) * 64;
+            char* dst = is_a ? a_base(I) + (i * NW + wave) * 1024 : b_base(I) + (q * NW + wave) * 1024;
+            const int pitch = is_a ? Kdim : ldw;
+            const uint8_t* base = is_a ? abase : up ? wu : wg;
+            const int left = (is_a ? nvalid : wrows) - first;
+            const rsrc_t r = make_rsrc(base + (size_t)first * pitch, live && left > 0 ? (uint32_t)left * pitch : 0u);
             // chunks past K (a partial last step) get an offset beyond every
             // extent, so they read nothing and land zeros in both operands
-            const uint32_t vo = kstep * BK + lane_k < Kdim ? off[i] : kOutOfRange;
+            const uint32_t vo = kstep * BK + lane_k < Kdim ? (is_a ? off_a : off_w) : kOutOfRange;
             // the row block is re-read by every n-tile of the expert (kept in
-            // L2); weight tiles are read by one or two m-tiles close together in
-            // tile order, so only the weights stream (non-temporal)
+            // L2); the weights' cache policy is the launcher's choice
             if (is_a)
                 lds_buf16<0>(r, dst, vo, kstep * BK);
             else
-                lds_buf16<kNonTemporal>(r, dst, vo, kstep * BK);
+                lds_buf16<NT_W ? kNonTemporal : 0>(r, dst, vo, kstep * BK);
         };
 
         // per-lane LDS byte offset of the 16-byte chunk this lane feeds to an
@@ -203,10 +205,10 @@ __global__ __launch_bounds__(512, 1) void grouped_gemm_i8_wide_kernel(FfnArgs p)
 #pragma unroll
         for (int i = 0; i < LPS; ++i) issue_one(ic<0>{}, i, 0, true);
         {
-            // and step 1's weights (nothing read when there is no step 1)
+            // and step 1 (nothing read when there is no step 1)
             const bool l1 = __builtin_amdgcn_readfirstlane(nk > 1 ? 1 : 0) != 0;
 #pragma unroll
-            for (int i = A_ITERS; i < LPS; ++i) issue_one(ic<1>{}, i, 1, l1);
+            for (int i = 0; i < LPS; ++i) issue_one(ic<1>{}, i, 1, l1);
         }
 
         // The tile for NF valid fragments: no branch inside a step.
@@ -221,125 +223,74 @@ __global__ __launch_bounds__(512, 1) void grouped_gemm_i8_wide_kernel(FfnArgs p)
 #pragma unroll
                 for (int f = 0; f < FN; ++f) acc[i][f] = intx4{0, 0, 0, 0};
 
-            // LOOK: read both k-halves' weight fragments of step k, and once every
-            // wave holds them issue, one after each fragment's MFMA group, step
-            // k + 1's row loads into the other row buffer and then step k + 2's
-            // weight loads into this step's weight buffer (loads past the last
-            // step read nothing but count, so every step issues LPS loads)
-            auto compute_look = [&](auto I, int k, bool liveA, bool liveB) {
-                const char* ab = a_base(I);
+            // Step k out of stage I.  The second k-half's fragments are read under
+            // the first half's MFMAs; once every wave holds them the stage is
+            // free, rows and weights alike, and step k + 2's loads go into it
+            // between the second half's MFMA groups (loads past the last step
+            // read nothing but count).
+            auto compute = [&](auto I, int k, bool live) {
+                const char* ab = a_base(I) + wm * 16 * ROWB;
                 const char* bb = b_base(I);
-                constexpr auto nextbuf = ic<1 - decltype(I)::value>{};
-                static_assert(2 * FN == 8, "weight fragment reads");
-                intx4 bfr[2][FN];
-                {
-                    uint32_t ad[8];
-                    uint4 t[8];
-#pragma unroll
-                    for (int kk = 0; kk < 2; ++kk)
-#pragma unroll
-                        for (int f = 0; f < FN; ++f) ad[kk * FN + f] = lds_addr(bb + lds_lane[kk] + brow0(f) * ROWB);
-                    lds_read16x8(t, ad);
-#pragma unroll
-                    for (int kk = 0; kk < 2; ++kk)
-#pragma unroll
-                        for (int f = 0; f < FN; ++f) bfr[kk][f] = __builtin_bit_cast(intx4, t[kk * FN + f]);
-                }
-                block_barrier();
-                auto issue_slot = [&](int q) {
-                    if (q < A_ITERS) issue_one(nextbuf, q, k + 1, liveA);
-                    else issue_one(I, q, k + 2, liveB);
+                auto read_a = [&](int kk, int i) {
+                    return *reinterpret_cast<const intx4*>(ab + lds_lane[kk] + i * WMW * 16 * ROWB);
                 };
+                auto read_b = [&](int kk, int f) {
+                    return *reinterpret_cast<const intx4*>(bb + lds_lane[kk] + brow0(f) * ROWB);
+                };
+                intx4 af[2][NF > 0 ? NF : 1], bf[2][FN];
+                if (NF > 0) {
 #pragma unroll
-                for (int kk = 0; kk < 2; ++kk) {
-                    intx4 acur;
-                    if (NF > 0) acur = *reinterpret_cast<const intx4*>(ab + lds_lane[kk] + wm * 16 * ROWB);
+                    for (int f = 0; f < FN; ++f) bf[0][f] = read_b(0, f);
 #pragma unroll
-                    for (int i = 0; i < NF; ++i) {
-                        intx4 anext;
-                        if (i + 1 < NF)
-                            anext = *reinterpret_cast<const intx4*>(
-                                ab + lds_lane[kk] + (wm + WMW * (i + 1)) * 16 * ROWB);
-#pragma unroll
-                        for (int f = 0; f < FN; ++f)
-                            acc[i][f] = __builtin_amdgcn_mfma_i32_16x16x64_i8(acur, bfr[kk][f], acc[i][f], 0, 0, 0);
-                        const int slot = kk * NF + i;
-                        if (slot < LPS) issue_slot(slot);
-                        if (i + 1 < NF) acur = anext;
-                        __builtin_amdgcn_sched_barrier(0);
-                    }
+                    for (int i = 0; i < NF; ++i) af[0][i] = read_a(0, i);
                 }
-                if (2 * NF < LPS) {
+                __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-                    for (int q = 2 * NF; q < LPS; ++q) issue_slot(q);
+                for (int i = 0; i < NF; ++i) {
+#pragma unroll
+                    for (int f = 0; f < FN; ++f)
+                        acc[i][f] = __builtin_amdgcn_mfma_i32_16x16x64_i8(af[0][i], bf[0][f], acc[i][f], 0, 0, 0);
+                    if (i == 0) {
+#pragma unroll
+                        for (int f = 0; f < FN; ++f) bf[1][f] = read_b(1, f);
+                    }
+                    af[1][i] = read_a(1, i);
+                    __builtin_amdgcn_sched_barrier(0);
                 }
-            };
-
-            // !LOOK: the first k-half issues step k + 1's row
-            // loads and the second half, once every wave holds its weight
-            // fragments, step k + 2's weight loads into this step's buffer
-            auto compute_half = [&](auto I, int k, bool liveA, bool liveB) {
-                const char* ab = a_base(I);
-                const char* bb = b_base(I);
-                constexpr auto nextbuf = ic<1 - decltype(I)::value>{};
-#pragma unroll
-                for (int kk = 0; kk < 2; ++kk) {
-                    intx4 bfr[FN];
-                    {
-                        static_assert(FN == 4, "weight fragment reads");
-                        uint32_t ad[4];
-                        uint4 t[4];
-#pragma unroll
-                        for (int f = 0; f < FN; ++f) ad[f] = lds_addr(bb + lds_lane[kk] + brow0(f) * ROWB);
-                        lds_read16x4(t, ad);
-#pragma unroll
-                        for (int f = 0; f < FN; ++f) bfr[f] = __builtin_bit_cast(intx4, t[f]);
-                    }
-                    if (kk == 1) block_barrier();      // every wave holds this step's weight fragments
-                    intx4 acur;
-                    if (NF > 0) acur = *reinterpret_cast<const intx4*>(ab + lds_lane[kk] + wm * 16 * ROWB);
-#pragma unroll
-                    for (int i = 0; i < NF; ++i) {
-                        intx4 anext;
-                        if (i + 1 < NF)
-                            anext = *reinterpret_cast<const intx4*>(
-                                ab + lds_lane[kk] + (wm + WMW * (i + 1)) * 16 * ROWB);
-#pragma unroll
-                        for (int f = 0; f < FN; ++f)
-                            acc[i][f] = __builtin_amdgcn_mfma_i32_16x16x64_i8(acur, bfr[f], acc[i][f], 0, 0, 0);
-                        if (kk == 0 && i < A_ITERS) issue_one(nextbuf, i, k + 1, liveA);
-                        if (kk == 1 && i < B_ITERS) issue_one(I, A_ITERS + i, k + 2, liveB);
-                        if (i + 1 < NF) acur = anext;
-                        __builtin_amdgcn_sched_barrier(0);
-                    }
-                    if (kk == 0 && NF < A_ITERS) {
-#pragma unroll
-                        for (int q = NF; q < A_ITERS; ++q) issue_one(nextbuf, q, k + 1, liveA);
-                    }
-                    if (kk == 1 && NF < B_ITERS) {
-#pragma unroll
-                        for (int q = NF; q < B_ITERS; ++q) issue_one(I, A_ITERS + q, k + 2, liveB);
-                    }
-                }
-            };
-
-            // step k: wait for stage k (step k + 1's weights stay in flight), then
-            // compute k while stage k + 1 is loaded into the other buffer
-            auto step = [&](auto I, int k) {
-                wait_vmcnt<B_ITERS>();
                 wait_lgkm0();
+                block_barrier();
+#pragma unroll
+                for (int i = 0; i < NF; ++i) {
+#pragma unroll
+                    for (int f = 0; f < FN; ++f)
+                        acc[i][f] = __builtin_amdgcn_mfma_i32_16x16x64_i8(af[1][i], bf[1][f], acc[i][f], 0, 0, 0);
+#pragma unroll
+                    for (int q = i * LPS / NF; q < (i + 1) * LPS / NF; ++q) issue_one(I, q, k + 2, live);
+                    __builtin_amdgcn_sched_barrier(0);
+                }
+                if (NF == 0) {
+#pragma unroll
+                    for (int q = 0; q < LPS; ++q) issue_one(I, q, k + 2, live);
+                }
+            };
+
+            // step k: wait for stage k (stage k + 1 stays in flight)
+            auto step = [&](auto I, int k) {
+                wait_vmcnt<LPS>();
                 block_barrier();
                 // wave-uniform by construction; say so, so that the resource
                 // select below stays scalar
-                const bool live = __builtin_amdgcn_readfirstlane(k + 1 < nk ? 1 : 0) != 0;
-                const bool live2 = __builtin_amdgcn_readfirstlane(k + 2 < nk ? 1 : 0) != 0;
-                if constexpr (LOOK) compute_look(I, k, live, live2);
-                else compute_half(I, k, live, live2);
+                const bool live = __builtin_amdgcn_readfirstlane(k + 2 < nk ? 1 : 0) != 0;
+                compute(I, k, live);
             };
-            for (int k = 0; k < nk; k += 2) {
+            // two steps a turn without a branch between them: with one, the compiler
+            // no longer knew which loads were in flight at the top of the loop and
+            // waited for all of them there
+            for (int k = 0; k + 1 < nk; k += 2) {
                 step(ic<0>{}, k);
-                if (k + 1 < nk) step(ic<1>{}, k + 1);
+                step(ic<1>{}, k + 1);
             }
+            if (nk & 1) step(ic<0>{}, nk - 1);
             // the loads issued by the last step read nothing but still count
             wait_vmcnt<0>();
 
@@ -352,9 +303,10 @@ __global__ __launch_bounds__(512, 1) void grouped_gemm_i8_wide_kernel(FfnArgs p)
             constexpr int OCOLS = FO * 16;                  // output columns of a wave
             constexpr int OCH = OCOLS * OSZ / 16;           // 16-byte chunks per staged row
             constexpr int OPITCH = OCOLS * OSZ + 16;        // staged row pitch (bytes)
-            constexpr int PF = OUT_F32 ? 3 : 5;             // fragments per pass
+            constexpr int PF_MAX = (BM < BN ? BM : BN) * ROWB / 2 / (16 * OPITCH);
+            constexpr int PF = PF_MAX < FM ? PF_MAX : FM;   // fragments per pass
             constexpr int RSZ = PF * 16 * OPITCH;           // bytes of a wave's region
-            static_assert(2 * RSZ <= BN * ROWB && 2 * RSZ <= BM * ROWB, "two regions per stage buffer");
+            static_assert(PF >= 1 && 2 * RSZ <= BN * ROWB && 2 * RSZ <= BM * ROWB, "two regions per stage buffer");
             if (tid < BM) s_as[tid] = row_s;
             wait_lgkm0();
             block_barrier();
@@ -400,7 +352,7 @@ __global__ __launch_bounds__(512, 1) void grouped_gemm_i8_wide_kernel(FfnArgs p)
         // a switch, not a chain of ifs: with the chain the compiler no longer
         // treated the tile's scalars as uniform and wrapped every buffer load
         // in a readfirstlane loop
-        static_assert(FM <= 10, "one case per fragment count");
+        static_assert(FM <= 8, "one case per fragment count");
         switch (nf) {
             case 0: if constexpr (0 <= FM) tile(ic<0>{}); break;
             case 1: if constexpr (1 <= FM) tile(ic<1>{}); break;
@@ -411,8 +363,6 @@ __global__ __launch_bounds__(512, 1) void grouped_gemm_i8_wide_kernel(FfnArgs p)
             case 6: if constexpr (6 <= FM) tile(ic<6>{}); break;
             case 7: if constexpr (7 <= FM) tile(ic<7>{}); break;
             case 8: if constexpr (8 <= FM) tile(ic<8>{}); break;
-            case 9: if constexpr (9 <= FM) tile(ic<9>{}); break;
-            case 10: if constexpr (10 <= FM) tile(ic<10>{}); break;
             default: break;
         }
     }
