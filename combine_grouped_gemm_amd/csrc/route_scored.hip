@@ -15,9 +15,22 @@
 //
 // Scores are compared in 64 bits: with a bias the order of two experts is not
 // the order of their logits, and an 8192-token batch holds thousands of
-// neighbours closer than fp32 sigmoids can tell apart.
+// neighbours closer than fp32 sigmoids can tell apart.  Few tokens need all of
+// that, though, so the common kernel narrows in fp32 and settles in fp64:
 //
-// One wave per token, keys in LDS.
+//   A token is 16 lanes (a DPP row), four tokens a wave; a lane holds E / 16
+//   consecutive experts as 32-bit keys (the score's leading bits, then the
+//   place in the lane), sorted once in registers.  Groups are ranked by DPP;
+//   K + 4 rounds of "row maximum, its owner shifts its list" give the
+//   candidates, one to a lane.  Every candidate's score is then computed in 64
+//   bits, one lane each, and ranked exactly, and its gate comes from that.
+//   The answer stands if the K-th exact score lies above what any expert that
+//   is no candidate can have (the last candidate's key plus the fp32 error),
+//   and if the groups' cut is wider than that error; NaN and huge scores never
+//   do.  Otherwise the wave does that token again in 64 bits from the start.
+//
+// Other shapes (E no multiple of 16, other group counts, K > 12) go through
+// that 64-bit routine, one wave a token, keys in LDS.
 #include "device_common.hpp"
 #include "launch.hpp"
 
@@ -40,14 +53,47 @@ __device__ __forceinline__ double key_score(uint64_t k) {
     return __longlong_as_double((long long)((k >> 63) != 0 ? (k & 0x7fffffffffffffffull) : ~k));
 }
 
-__device__ __forceinline__ uint64_t shfl_xor_u64(uint64_t v, int m) {
-    return (uint64_t)__shfl_xor((unsigned long long)v, m, kWave);
+// The DPP move that CTRL names: partners lane ^ 1 (0xB1) and lane ^ 2 (0x4E),
+// the mirrors of half a 16-lane row (0x141) and of a row (0x140), which join
+// what those two have made uniform, and rotation of a row by r (0x120 + r).
+template <int CTRL>
+__device__ __forceinline__ uint32_t dpp(uint32_t v) {
+    return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xF, 0xF, true);
+}
+template <int CTRL>
+__device__ __forceinline__ float dpp(float v) {
+    return __uint_as_float(dpp<CTRL>(__float_as_uint(v)));
+}
+template <int CTRL>
+__device__ __forceinline__ uint64_t dpp(uint64_t v) {
+    return ((uint64_t)dpp<CTRL>((uint32_t)(v >> 32)) << 32) | dpp<CTRL>((uint32_t)v);
+}
+template <int CTRL>
+__device__ __forceinline__ double dpp(double v) {
+    return __longlong_as_double((long long)dpp<CTRL>((uint64_t)__double_as_longlong(v)));
+}
+// Reduction over a 16-lane row, the result in each of its lanes.
+template <typename T, typename Op>
+__device__ __forceinline__ T row_reduce(T v, Op op) {
+    v = op(v, dpp<0xB1>(v));
+    v = op(v, dpp<0x4E>(v));
+    v = op(v, dpp<0x141>(v));
+    return op(v, dpp<0x140>(v));
+}
+template <typename T>
+__device__ __forceinline__ T row_max(T v) { return row_reduce(v, [](T a, T b) { return a > b ? a : b; }); }
+template <typename T>
+__device__ __forceinline__ T row_sum(T v) { return row_reduce(v, [](T a, T b) { return a + b; }); }
+
+__device__ __forceinline__ uint64_t readlane_u64(uint64_t v, int l) {
+    return ((uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(v >> 32), l) << 32) |
+           (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)v, l);
 }
 
-__device__ __forceinline__ double wave_sum_f64(double v) {
-#pragma unroll
-    for (int d = 1; d < kWave; d <<= 1) v += __shfl_xor(v, d, kWave);
-    return v;
+// LDS written by one lane of the wave, read by another.
+__device__ __forceinline__ void wave_lds_sync() {
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
 }
 
 // Largest key of s[0..n) and the lowest index that holds it, the same in
@@ -57,14 +103,16 @@ __device__ __forceinline__ uint64_t wave_argmax(const uint64_t* s, int n, int la
     int idx = n;
     for (int i = lane; i < n; i += kWave)
         if (s[i] > best) { best = s[i]; idx = i; }
-#pragma unroll
-    for (int d = 1; d < kWave; d <<= 1) {
-        const uint64_t k = shfl_xor_u64(best, d);
-        const int i = __shfl_xor(idx, d, kWave);
-        if (k > best || (k == best && i < idx)) { best = k; idx = i; }
-    }
-    *at = idx;
-    return best;
+    const uint64_t m = row_max(best);
+    const uint64_t a = readlane_u64(m, 0), b = readlane_u64(m, 16), c = readlane_u64(m, 32), d = readlane_u64(m, 48);
+    const uint64_t ab = a > b ? a : b, cd = c > d ? c : d, top = ab > cd ? ab : cd;
+    const uint32_t none = 0xffffffffu;
+    const uint32_t i = row_reduce(best == top && top != 0 ? (uint32_t)idx : none, [](uint32_t x, uint32_t y) { return x < y ? x : y; });
+    const uint32_t i0 = (uint32_t)__builtin_amdgcn_readlane((int)i, 0), i1 = (uint32_t)__builtin_amdgcn_readlane((int)i, 16);
+    const uint32_t i2 = (uint32_t)__builtin_amdgcn_readlane((int)i, 32), i3 = (uint32_t)__builtin_amdgcn_readlane((int)i, 48);
+    const uint32_t i01 = i0 < i1 ? i0 : i1, i23 = i2 < i3 ? i2 : i3;
+    *at = (int)(i01 < i23 ? i01 : i23);
+    return top;
 }
 
 __device__ __forceinline__ float load_logit(const void* p, bool bf16, size_t i) {
@@ -72,14 +120,21 @@ __device__ __forceinline__ float load_logit(const void* p, bool bf16, size_t i) 
                 : static_cast<const float*>(p)[i];
 }
 
-__global__ __launch_bounds__(kWave) void route_scored_kernel(RouteScoredArgs p) {
-    extern __shared__ uint64_t smem[];
+// Bytes of LDS that exact_token needs.
+__host__ __device__ inline size_t exact_lds(int E, int G, int K) {
+    return (size_t)E * 16 + (size_t)G * 8 + (size_t)((K + 1) / 2 * 2) * 12;
+}
+
+// One token by one wave, in 64 bits throughout.  smem: exact_lds bytes of the
+// wave's own.
+__device__ void exact_token(const RouteScoredArgs& p, int t, uint64_t* smem) {
     uint64_t* s_key = smem;                                       // E
     double* s_score = reinterpret_cast<double*>(smem + p.E);      // E
     uint64_t* s_group = smem + 2 * (size_t)p.E;                   // G
     double* s_val = reinterpret_cast<double*>(s_group + p.G);     // K
     int* s_id = reinterpret_cast<int*>(s_val + p.K);              // K
-    const int t = blockIdx.x, lane = threadIdx.x;
+    const int lane = threadIdx.x % kWave;
+    wave_lds_sync();                                              // an earlier token's reads are done
     const size_t base = (size_t)t * p.E;
 
     float top = -INFINITY;
@@ -88,8 +143,8 @@ __global__ __launch_bounds__(kWave) void route_scored_kernel(RouteScoredArgs p) 
             const float l = load_logit(p.logits, p.bf16, base + e);
             if (!(l <= kLowestBf16)) top = fmaxf(top, l);
         }
-#pragma unroll
-        for (int d = 1; d < kWave; d <<= 1) top = fmaxf(top, __shfl_xor(top, d, kWave));
+        top = row_reduce(top, [](float x, float y) { return fmaxf(x, y); });
+        top = fmaxf(fmaxf(__shfl(top, 0), __shfl(top, 16)), fmaxf(__shfl(top, 32), __shfl(top, 48)));
     }
     double sum = 0.0;
     for (int e = lane; e < p.E; e += kWave) {
@@ -100,7 +155,10 @@ __global__ __launch_bounds__(kWave) void route_scored_kernel(RouteScoredArgs p) 
         s_score[e] = s;
         sum += s;
     }
-    sum = p.sigmoid ? 1.0 : wave_sum_f64(sum);
+    if (!p.sigmoid) {
+        sum = row_sum(sum);
+        sum = (__shfl(sum, 0) + __shfl(sum, 16)) + (__shfl(sum, 32) + __shfl(sum, 48));
+    }
     for (int e = lane; e < p.E; e += kWave) {
         const float l = load_logit(p.logits, p.bf16, base + e);
         const float b = p.bias != nullptr ? p.bias[e] : 0.0f;
@@ -109,7 +167,7 @@ __global__ __launch_bounds__(kWave) void route_scored_kernel(RouteScoredArgs p) 
         s_score[e] = !(l <= kLowestBf16) ? s : 0.0;
         s_key[e] = score_key(s + (double)b, on);
     }
-    __syncthreads();
+    wave_lds_sync();
 
     if (p.topk_groups < p.G) {
         const int S = p.E / p.G;
@@ -125,19 +183,19 @@ __global__ __launch_bounds__(kWave) void route_scored_kernel(RouteScoredArgs p) 
                 key = p.group_top == 1 || k2 == 0 ? k1 : score_key(key_score(k1) + key_score(k2), true);
             s_group[g] = key;
         }
-        __syncthreads();
+        wave_lds_sync();
         // the groups that stay are taken out of s_group; the others keep their key
         for (int i = 0; i < p.topk_groups; ++i) {
             int g;
             const uint64_t k = wave_argmax(s_group, p.G, lane, &g);
-            __syncthreads();
+            wave_lds_sync();
             if (k == 0) break;
             if (lane == 0) s_group[g] = 0;
-            __syncthreads();
+            wave_lds_sync();
         }
         for (int e = lane; e < p.E; e += kWave)
             if (s_group[e / S] != 0) s_key[e] = 0;
-        __syncthreads();
+        wave_lds_sync();
     }
 
     double total = 0.0;
@@ -145,14 +203,14 @@ __global__ __launch_bounds__(kWave) void route_scored_kernel(RouteScoredArgs p) 
         int e;
         const uint64_t key = wave_argmax(s_key, p.E, lane, &e);
         const double s = key != 0 ? s_score[e] : 0.0;
-        __syncthreads();
+        wave_lds_sync();
         if (lane == 0) {
             if (key != 0) s_key[e] = 0;
             s_val[k] = s;
             s_id[k] = key != 0 ? e : -1;
         }
         total += s;
-        __syncthreads();
+        wave_lds_sync();
     }
     const int ld = p.K + p.n_shared;
     for (int k = lane; k < ld; k += kWave) {
@@ -171,12 +229,285 @@ __global__ __launch_bounds__(kWave) void route_scored_kernel(RouteScoredArgs p) 
     }
 }
 
+__global__ __launch_bounds__(kWave) void route_scored_exact_kernel(RouteScoredArgs p) {
+    extern __shared__ uint64_t smem[];
+    exact_token(p, blockIdx.x, smem);
+}
+
+// ---- four tokens a wave (see the file comment)
+constexpr int kRowWaves = 4;                // waves per block
+constexpr int kExtra = 4;                   // candidates beyond K
+constexpr int kMaxRowK = 16 - kExtra;
+
+__device__ __forceinline__ uint32_t order_key(float v) {
+    const uint32_t u = __float_as_uint(v + 0.0f);                 // -0 becomes +0
+    return u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
+}
+__device__ __forceinline__ float key_value(uint32_t k) {
+    return __uint_as_float(k ^ (~(uint32_t)((int32_t)k >> 31) | 0x80000000u));
+}
+
+// e^x within 2^-22 of its value (down to where it underflows): the hardware's
+// 2^x of the leading part of x / ln 2, times 1 + the rest.
+__device__ __forceinline__ float exp_near(float x) {
+    const float hi = 1.44269502f, lo = 1.925963e-8f;
+    const float p = x * hi;
+    const float r = fmaf(x, lo, fmaf(x, hi, -p));
+    return __builtin_amdgcn_exp2f(p) * fmaf(r, 0.693147182f, 1.0f);
+}
+
+// EPL: registers for a lane's experts, at least E / 16.  VEC: exactly E / 16,
+// and rows and biases can be read in 16-byte pieces.
+template <int EPL, bool VEC, bool SIGMOID, bool BF16>
+__global__ __launch_bounds__(kRowWaves * kWave) void route_scored_kernel(RouteScoredArgs p) {
+    extern __shared__ uint64_t smem[];
+    static_assert((EPL & (EPL - 1)) == 0 && EPL >= 4, "bitonic sort");
+    constexpr uint32_t kPlace = EPL - 1;    // low key bits: the place in the lane, inverted
+    const int wave = threadIdx.x / kWave, lane = threadIdx.x % kWave;
+    const int row = lane >> 4, l16 = lane & 15;
+    const int t = (blockIdx.x * kRowWaves + wave) * 4 + row;
+    const bool live = t < p.B;
+    const size_t base = (size_t)(live ? t : p.B - 1) * p.E;       // idle rows repeat the last token
+    const int chunk = VEC ? EPL : p.E / 16;
+    const int e0 = l16 * chunk;
+
+    // ---- logits and biases of this lane's experts
+    float lg[EPL], bs[EPL];
+    if constexpr (VEC) {
+        if constexpr (BF16) {
+            const uint16_t* src = static_cast<const uint16_t*>(p.logits) + base + e0;
+#pragma unroll
+            for (int j = 0; j < EPL; j += 8) {
+                const uint4 v = *reinterpret_cast<const uint4*>(src + j);
+                lg[j] = bf16_lo(v.x); lg[j + 1] = bf16_hi(v.x); lg[j + 2] = bf16_lo(v.y); lg[j + 3] = bf16_hi(v.y);
+                lg[j + 4] = bf16_lo(v.z); lg[j + 5] = bf16_hi(v.z); lg[j + 6] = bf16_lo(v.w); lg[j + 7] = bf16_hi(v.w);
+            }
+        } else {
+            const float4* src = reinterpret_cast<const float4*>(static_cast<const float*>(p.logits) + base + e0);
+#pragma unroll
+            for (int j = 0; j < EPL; j += 4) {
+                const float4 v = src[j / 4];
+                lg[j] = v.x; lg[j + 1] = v.y; lg[j + 2] = v.z; lg[j + 3] = v.w;
+            }
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < EPL; ++j) lg[j] = j < chunk ? load_logit(p.logits, BF16, base + e0 + j) : -INFINITY;
+    }
+    if (p.bias != nullptr) {
+        if constexpr (VEC) {
+            const float4* src = reinterpret_cast<const float4*>(p.bias + e0);
+#pragma unroll
+            for (int j = 0; j < EPL; j += 4) {
+                const float4 v = src[j / 4];
+                bs[j] = v.x; bs[j + 1] = v.y; bs[j + 2] = v.z; bs[j + 3] = v.w;
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < EPL; ++j) bs[j] = j < chunk ? p.bias[e0 + j] : 0.0f;
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < EPL; ++j) bs[j] = 0.0f;
+    }
+
+    // ---- softmax: the largest logit and the sum, in 64 bits (gates and exact scores need them)
+    float top = -INFINITY;
+    double sum = 1.0, inv = 1.0;
+    double ex[SIGMOID ? 1 : EPL];
+    if constexpr (!SIGMOID) {
+#pragma unroll
+        for (int j = 0; j < EPL; ++j) top = fmaxf(top, lg[j] <= kLowestBf16 ? -INFINITY : lg[j]);
+        top = row_reduce(top, [](float x, float y) { return fmaxf(x, y); });
+        if (top == -INFINITY) top = 0.0f;                        // nothing but masked logits
+        sum = 0.0;
+#pragma unroll
+        for (int j = 0; j < EPL; ++j) {
+            ex[j] = exp((double)lg[j] - (double)top);            // 0 for a masked logit
+            sum += ex[j];
+        }
+        sum = row_sum(sum);
+        inv = 1.0 / sum;
+    }
+
+    // ---- keys.  Error of a 32-bit score against the exact one: for the sigmoid
+    // exp_near's 2^-22 (weighed by 1 - s), the sum's 2^-24 and the reciprocal's
+    // last place, 2^-23; softmax is rounded once; adding the bias rounds once more.
+    // In all less than 2^-21 of s <= 1 and of c: `rel`, and `abs_err` where a
+    // bias may cancel s (without one only what underflows is lost).  No branches
+    // here: they would cost more than what they skip.
+    const float rel = 0x1p-21f, abs_err = p.bias != nullptr ? 0x1p-21f : 1e-37f;
+    uint32_t key[EPL];
+    float c1 = -INFINITY, c2 = -INFINITY;   // the lane's two best
+    bool odd = false;                       // a score that is no ordinary number
+#pragma unroll
+    for (int j = 0; j < EPL; ++j) {
+        const bool off = (lg[j] <= kLowestBf16) | (bs[j] <= kLowestBf16);
+        float c;
+        if constexpr (SIGMOID) c = __builtin_amdgcn_rcpf(1.0f + exp_near(-lg[j])) + bs[j];
+        else c = (float)(ex[j] * inv + (double)bs[j]);
+        odd |= !off & !(fabsf(c) < 1e30f);
+        key[j] = off ? 0u : ((order_key(c) & ~kPlace) | (kPlace - j));
+        c = off ? -INFINITY : c;
+        c2 = __builtin_amdgcn_fmed3f(c1, c2, c);
+        c1 = fmaxf(c1, c);
+    }
+
+    // ---- sorted in the lane, largest first
+#pragma unroll
+    for (int k = 2; k <= EPL; k <<= 1)
+#pragma unroll
+        for (int j = k >> 1; j > 0; j >>= 1)
+#pragma unroll
+            for (int i = 0; i < EPL; ++i) {
+                const int l = i ^ j;
+                if (l > i) {
+                    const uint32_t hi = key[i] > key[l] ? key[i] : key[l], lo = key[i] > key[l] ? key[l] : key[i];
+                    const bool down = (i & k) == 0;
+                    key[i] = down ? hi : lo;
+                    key[l] = down ? lo : hi;
+                }
+            }
+
+    // ---- groups: 16 / G lanes each
+    bool ok = true;
+    if (p.topk_groups < p.G) {
+        const int lanes = 16 / p.G;
+        auto join = [&](float o1, float o2) {
+            c2 = fmaxf(fminf(c1, o1), fmaxf(c2, o2));
+            c1 = fmaxf(c1, o1);
+        };
+        if (lanes > 1) join(dpp<0xB1>(c1), dpp<0xB1>(c2));
+        if (lanes > 2) join(dpp<0x4E>(c1), dpp<0x4E>(c2));
+        if (lanes > 4) join(dpp<0x141>(c1), dpp<0x141>(c2));
+        const float second = (p.group_top == 2) & (c2 != -INFINITY) ? c2 : 0.0f;
+        const float score = c1 + second;
+        // of the two terms, which may cancel
+        const float size = c1 != -INFINITY ? fabsf(c1) + fabsf(second) : 0.0f;
+        // groups ahead of this one, by rotating the row in steps of a group
+        int better = 0;
+        auto against = [&](float os, int r) {
+            better += (int)((os > score) | ((os == score) & (((l16 - r) & 15) < l16)));
+        };
+#define MOEEP_AGAINST(r) against(dpp<0x120 + r>(score), r);
+        if (lanes <= 8) { MOEEP_AGAINST(8) }
+        if (lanes <= 4) { MOEEP_AGAINST(4) MOEEP_AGAINST(12) }
+        if (lanes <= 2) { MOEEP_AGAINST(2) MOEEP_AGAINST(6) MOEEP_AGAINST(10) MOEEP_AGAINST(14) }
+        if (lanes == 1) {
+            MOEEP_AGAINST(1) MOEEP_AGAINST(3) MOEEP_AGAINST(5) MOEEP_AGAINST(7)
+            MOEEP_AGAINST(9) MOEEP_AGAINST(11) MOEEP_AGAINST(13) MOEEP_AGAINST(15)
+        }
+#undef MOEEP_AGAINST
+        const bool kept = better < p.topk_groups;
+        // the cut between the last group kept and the first one dropped
+        const float least = -row_max(kept & (c1 != -INFINITY) ? -score : -INFINITY);
+        const float most = row_max(kept ? -INFINITY : score);
+        const float slack = 2.0f * (row_max(size) * rel + 2.0f * abs_err);
+        ok = (most == -INFINITY) | (least - most > slack);
+#pragma unroll
+        for (int j = 0; j < EPL; ++j) key[j] = kept ? key[j] : 0u;
+    }
+
+    // ---- candidates: candidate i in lane i of the row
+    const int n_cand = min(p.K + kExtra, 16);
+    int ce = -1;                            // its expert
+    uint32_t last = 0;
+    for (int i = 0; i < n_cand; ++i) {
+        last = row_max(key[0]);
+        const uint32_t owners = (uint32_t)(ballot64(key[0] == last) >> (row * 16)) & 0xffffu;
+        const int first = __builtin_ctz(owners | 0x10000u);
+        // the owner's list moves up by one: a bit select by a mask whose origin the
+        // compiler does not see (it made a register index of the plain choice,
+        // fifty instructions a place)
+        uint32_t mine = l16 == first ? 0xffffffffu : 0u;
+        asm("" : "+v"(mine));
+        if ((l16 == i) & (last != 0)) ce = first * chunk + (int)(kPlace - (last & kPlace));
+#pragma unroll
+        for (int j = 0; j + 1 < EPL; ++j) key[j] = (key[j + 1] & mine) | (key[j] & ~mine);
+        key[EPL - 1] &= ~mine;
+    }
+
+    // ---- their exact scores and ranks
+    double s = 0.0, c = -INFINITY;
+    if (ce >= 0) {
+        const double l = (double)load_logit(p.logits, BF16, base + ce);
+        const double b = p.bias != nullptr ? (double)p.bias[ce] : 0.0;
+        s = SIGMOID ? 1.0 / (1.0 + exp(-l)) : exp(l - (double)top) / sum;
+        c = s + b;
+    }
+    const uint32_t id = (uint32_t)ce;       // -1 ranks last
+    int rank = 0;
+    auto behind = [&](double oc, uint32_t oid) { rank += (int)((oc > c) | ((oc == c) & (oid < id))); };
+#define MOEEP_BEHIND(r) behind(dpp<0x120 + r>(c), dpp<0x120 + r>(id));
+    MOEEP_BEHIND(1) MOEEP_BEHIND(2) MOEEP_BEHIND(3) MOEEP_BEHIND(4) MOEEP_BEHIND(5)
+    MOEEP_BEHIND(6) MOEEP_BEHIND(7) MOEEP_BEHIND(8) MOEEP_BEHIND(9) MOEEP_BEHIND(10)
+    MOEEP_BEHIND(11) MOEEP_BEHIND(12) MOEEP_BEHIND(13) MOEEP_BEHIND(14) MOEEP_BEHIND(15)
+#undef MOEEP_BEHIND
+    const bool pick = ce >= 0 && rank < p.K;
+    if (last != 0) {                        // there may be experts that are no candidates
+        const float up = key_value(last | kPlace);                // without the place's bits, rounded up
+        const double most = (double)up + (double)fabsf(up) * rel + abs_err;
+        const double kth = -row_max(pick ? -c : -(double)INFINITY);
+        ok = ok && kth > most;
+    }
+    ok = ok && ((ballot64(odd) >> (row * 16)) & 0xffffu) == 0;
+
+    const double total = row_sum(pick ? s : 0.0);
+    const int ld = p.K + p.n_shared;
+    int32_t* ids = p.ids + (size_t)t * ld;
+    float* w = p.w + (size_t)t * ld;
+    if (live && ok) {
+        if (pick) {
+            const double v = p.renorm ? (total == 0.0 ? 0.0 : s / total) : s;
+            ids[rank] = p.map != nullptr ? p.map[ce] : ce;
+            w[rank] = (float)(v * (double)p.scale);
+        }
+        const int found = __popc((uint32_t)(ballot64(pick) >> (row * 16)) & 0xffffu);
+        if (l16 >= found && l16 < p.K) {
+            ids[l16] = -1;
+            w[l16] = 0.0f;
+        }
+        for (int k = p.K + l16; k < ld; k += 16) {
+            ids[k] = p.E + (k - p.K);
+            w[k] = 1.0f;
+        }
+    }
+    uint64_t again = ballot64(live && !ok && l16 == 0);
+    uint64_t* ws = smem + wave * (exact_lds(p.E, p.G, p.K) / 8);
+    while (again != 0) {
+        const int first = __builtin_ctzll(again);
+        again &= again - 1;
+        exact_token(p, __builtin_amdgcn_readlane(t, first), ws);
+    }
+}
+
+template <int EPL, bool VEC>
+hipError_t launch_rows(const RouteScoredArgs& a, hipStream_t stream) {
+    const int per_block = kRowWaves * 4;
+    const dim3 grid((a.B + per_block - 1) / per_block), block(kRowWaves * kWave);
+    const size_t lds = kRowWaves * exact_lds(a.E, a.G, a.K);
+    if (a.sigmoid && a.bf16) hipLaunchKernelGGL((route_scored_kernel<EPL, VEC, true, true>), grid, block, lds, stream, a);
+    else if (a.sigmoid) hipLaunchKernelGGL((route_scored_kernel<EPL, VEC, true, false>), grid, block, lds, stream, a);
+    else if (a.bf16) hipLaunchKernelGGL((route_scored_kernel<EPL, VEC, false, true>), grid, block, lds, stream, a);
+    else hipLaunchKernelGGL((route_scored_kernel<EPL, VEC, false, false>), grid, block, lds, stream, a);
+    return hipGetLastError();
+}
+
 }  // namespace
 
 hipError_t launch_route_scored(const RouteScoredArgs& a, hipStream_t stream) {
     if (a.B == 0) return hipSuccess;
-    const size_t lds = (size_t)a.E * 16 + (size_t)a.G * 8 + (size_t)a.K * 12;
-    hipLaunchKernelGGL(route_scored_kernel, dim3(a.B), dim3(kWave), lds, stream, a);
+    const bool groups = a.topk_groups < a.G;
+    if (a.E % 16 == 0 && a.E <= 512 && a.K <= kMaxRowK && (!groups || 16 % a.G == 0)) {
+        const int per_lane = a.E / 16;
+        const bool aligned = ((reinterpret_cast<uintptr_t>(a.logits) | reinterpret_cast<uintptr_t>(a.bias)) & 15u) == 0;
+        if (per_lane == 16 && aligned) return launch_rows<16, true>(a, stream);
+        if (per_lane == 8 && aligned) return launch_rows<8, true>(a, stream);
+        if (per_lane <= 8) return launch_rows<8, false>(a, stream);
+        if (per_lane <= 16) return launch_rows<16, false>(a, stream);
+        return launch_rows<32, false>(a, stream);
+    }
+    hipLaunchKernelGGL(route_scored_exact_kernel, dim3(a.B), dim3(kWave), exact_lds(a.E, a.G, a.K), stream, a);
     return hipGetLastError();
 }
 

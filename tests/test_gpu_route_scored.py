@@ -92,6 +92,53 @@ def test_neighbours_that_fp32_scores_cannot_tell_apart(score):
         _check(lg, 8, score, torch.full((E,), 0.25), n_groups=8, topk_groups=4, group_top=1)
 
 
+@pytest.mark.parametrize("E,G,keep", [(256, 16, 5), (256, 2, 1), (256, 4, 3), (512, 16, 9), (512, 8, 4), (16, 8, 4), (32, 16, 16),
+                                       (240, 8, 2), (528, 8, 4), (64, 1, 1)])
+def test_candidate_counts_and_groups(E, G, keep):
+    """K on both sides of the shapes that a row of lanes can hold, with more
+    ties at the cut than it has candidates for."""
+    for K in (1, 2, 11, 12, 13, 16):
+        if K > keep * (E // G):
+            continue
+        for score in ("sigmoid", "softmax"):
+            kw = dict(n_groups=G, topk_groups=keep)
+            lg, bias = _inputs(70, E, E + K)
+            _check(lg, K, score, bias, **kw)
+            lg = torch.round(lg) + 0.3                    # a handful of values: long runs of ties
+            _check(lg, K, score, None, **kw)
+            _check(lg, K, score, torch.full((E,), -0.7), renorm=False, **kw)
+
+
+def test_biases_that_cancel_scores():
+    """c near zero and of both signs: the error of a score no longer shrinks with it."""
+    for seed in range(3):
+        lg, _ = _inputs(200, 256, seed, spread=0.3)
+        g = torch.Generator().manual_seed(seed)
+        bias = -torch.sigmoid(torch.randn(256, generator=g) * 0.3)
+        for top in (1, 2):
+            _check(lg, 8, "sigmoid", bias, n_groups=8, topk_groups=4, group_top=top)
+        _check(lg, 8, "softmax", bias / 128, n_groups=8, topk_groups=4, group_top=2)
+        _check(lg, 8, "sigmoid", bias * 1e4, n_groups=8, topk_groups=4, group_top=2)
+        _check(lg, 8, "sigmoid", bias * 1e33, n_groups=8, topk_groups=4, group_top=2)
+
+
+def test_misaligned_rows():
+    """Contiguous tensors that start in the middle of a 16-byte piece."""
+    for E in (256, 128):
+        for dt in (torch.float32, torch.bfloat16):
+            lg, bias = _inputs(21, E, 5, bf16=dt == torch.bfloat16)
+            import combine_grouped_gemm_amd as m
+            x = torch.empty(21 * E + 1, dtype=dt, device="cuda")[1:].view(21, E)
+            x.copy_(lg)
+            b = torch.empty(E + 3, device="cuda")[3:]
+            b.copy_(bias)
+            for xx, bb in ((x, b), (lg.cuda(), b), (x, bias.cuda())):
+                ids, w = m.moe_route_scored(xx, 8, bias=bb, n_groups=8, topk_groups=4)
+                rid, rw = oracle.route_scored(lg.double().numpy(), 8, "sigmoid", bias.double().numpy(), 8, 4)
+                np.testing.assert_array_equal(ids.cpu().numpy(), rid)
+                np.testing.assert_allclose(w.cpu().numpy(), rw, rtol=RTOL)
+
+
 def test_extreme_logits():
     """Saturated sigmoids tie (lower id), scores that underflow are zero, and a
     sum of zero gives zero weights."""
