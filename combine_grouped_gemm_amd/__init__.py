@@ -112,18 +112,33 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
+# the current stream of a device as an integer: torch.cuda.current_stream() builds an
+# object for it, which costs as much as the rest of a call
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
 def _stream(stream):
     if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+        return _raw_stream(torch.cuda.current_device())
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
     return int(stream)
 
 
+def _call(fn, t, stream, *args):
+    """One library call with t's device current, on `stream` (None: that device's current stream)."""
+    index = t.get_device()
+    if index == torch.cuda.current_device():
+        _check(fn(*args, _raw_stream(index) if stream is None else _stream(stream)))
+    else:
+        with torch.cuda.device(index):
+            _check(fn(*args, _stream(stream)))
+
+
 def _dev(t, name, dtype=None, ndim=None):
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.device.type != "cuda":
+    if not t.is_cuda:
         raise ValueError(f"{name} must be a device tensor (got {t.device})")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
@@ -148,8 +163,9 @@ def _need(t, name, numel=None, shape=None):
 
 def _same_device(t, name, *others):
     """Every tensor of a call lives on the device of its first one (None: not given)."""
+    index = t.get_device()
     for o in others:
-        if o is not None and o.device != t.device:
+        if o is not None and o.get_device() != index:
             raise ValueError(f"all tensors must be on {name}'s device {t.device} (got {o.device})")
 
 
@@ -255,10 +271,9 @@ def moe_route_scored(logits, K: int, score: str = "sigmoid", bias=None, n_groups
         _dev(topk_w, "topk_w", torch.float32)
         _need(topk_w, "topk_w", shape=(B, Kt))
     _same_device(logits, "logits", bias, phys_of_logical, topk_ids, topk_w)
-    with torch.cuda.device(dev):
-        _check(lib().moe_route_scored(_ptr(logits), _DT[logits.dtype], _ptr(bias), B, E, K, _SCORES[score], n_groups,
-                                      topk_groups, group_top, 1 if renorm else 0, scale, _ptr(phys_of_logical),
-                                      n_shared, _ptr(topk_ids), _ptr(topk_w), _stream(stream)))
+    _call(lib().moe_route_scored, logits, stream, logits.data_ptr(), _DT[logits.dtype], _ptr(bias), B, E, K,
+          _SCORES[score], n_groups, topk_groups, group_top, 1 if renorm else 0, scale, _ptr(phys_of_logical), n_shared,
+          topk_ids.data_ptr(), topk_w.data_ptr())
     return topk_ids, topk_w
 
 
@@ -402,10 +417,8 @@ def moe_dispatch(seg_x, row_of, cap_rows: int, xd_dtype=None, xd=None, xd_scales
         _same_device(row_of, "row_of", xd, xd_scales, *seg_x)
     ptrs = (ctypes.c_void_p * len(seg_x))(*[s.data_ptr() for s in seg_x])
     rows = (ctypes.c_int32 * len(seg_x))(*[s.shape[0] for s in seg_x])
-    with torch.cuda.device(dev):
-        _check(lib().moe_dispatch(ctypes.cast(ptrs, ctypes.c_void_p), ctypes.cast(rows, ctypes.c_void_p),
-                                  len(seg_x), _DT[x_dt], H, _ptr(row_of), K, _ptr(xd), xd_code,
-                                  _ptr(xd_scales), cap_rows, _stream(stream)))
+    _call(lib().moe_dispatch, row_of, stream, ctypes.cast(ptrs, ctypes.c_void_p), ctypes.cast(rows, ctypes.c_void_p),
+          len(seg_x), _DT[x_dt], H, _ptr(row_of), K, _ptr(xd), xd_code, _ptr(xd_scales), cap_rows)
     return xd, xd_scales
 
 
@@ -441,8 +454,7 @@ def moe_quant_rows(x, rows=None, cap_per_expert=None, q=None, scales=None, strea
     _need(scales, "scales", numel=cap)
     _same_device(x, "x", rows, q, scales)
     fn = lib().moe_quant_rows if cap_per_expert is None else lib().moe_quant_rows_masked
-    with torch.cuda.device(x.device):
-        _check(fn(_ptr(x), _DT[x.dtype], _ptr(rows), E_loc, third, cols, _ptr(q), _ptr(scales), _stream(stream)))
+    _call(fn, x, stream, _ptr(x), _DT[x.dtype], _ptr(rows), E_loc, third, cols, _ptr(q), _ptr(scales))
     return q, scales
 
 
@@ -600,11 +612,9 @@ def moe_ffn_gate_up(xd, xd_scales, offsets, w_gate, w_up, w_gate_scales=None, w_
                w_gate_scales=_w_scales(act, w_gate_scales, E_loc, I, H),
                w_up_scales=_w_scales(act, w_up_scales, E_loc, I, H))
     fn = lib().moe_ffn_gate_up if cap_per_expert is None else lib().moe_ffn_gate_up_masked
-    with torch.cuda.device(xd.device):
-        _check(fn(_ptr(xd), _ptr(xd_scales), _ptr(offsets), E_loc, third, H, I, act,
-                  _ptr(w_gate), _ptr(w_up), _ptr(w_gate_scales), _ptr(w_up_scales),
-                  _w_code(act, w_scales_pow2) | packed, _ptr(h), _ptr(h_scales), int(expected_rows),
-                  _stream(stream)))
+    _call(fn, xd, stream, _ptr(xd), _ptr(xd_scales), _ptr(offsets), E_loc, third, H, I, act,
+          _ptr(w_gate), _ptr(w_up), _ptr(w_gate_scales), _ptr(w_up_scales),
+          _w_code(act, w_scales_pow2) | packed, _ptr(h), _ptr(h_scales), int(expected_rows))
     return h, h_scales
 
 
@@ -630,10 +640,9 @@ def moe_ffn_down(h, h_scales, offsets, w_down, w_down_scales=None, y=None, y_dty
     _check_ffn(h, h_scales, offsets, cap_per_expert, E_loc, I, cap, act, y=(y, cap * H),
                w_down_scales=_w_scales(act, w_down_scales, E_loc, H, I))
     fn = lib().moe_ffn_down if cap_per_expert is None else lib().moe_ffn_down_masked
-    with torch.cuda.device(h.device):
-        _check(fn(_ptr(h), _ptr(h_scales), _ptr(offsets), E_loc, third, H, I, act,
-                  _ptr(w_down), _ptr(w_down_scales), _w_code(act, w_scales_pow2) | packed, _ptr(y), _DT[y.dtype],
-                  int(expected_rows), _stream(stream)))
+    _call(fn, h, stream, _ptr(h), _ptr(h_scales), _ptr(offsets), E_loc, third, H, I, act,
+          _ptr(w_down), _ptr(w_down_scales), _w_code(act, w_scales_pow2) | packed, _ptr(y), _DT[y.dtype],
+          int(expected_rows))
     return y
 
 
@@ -664,12 +673,10 @@ def moe_grouped_ffn(xd, xd_scales, offsets, w_gate, w_up, w_down, w_gate_scales=
                w_up_scales=_w_scales(act, w_up_scales, E_loc, I, H),
                w_down_scales=_w_scales(act, w_down_scales, E_loc, H, I))
     fn = lib().moe_grouped_ffn if cap_per_expert is None else lib().moe_grouped_ffn_masked
-    with torch.cuda.device(xd.device):
-        _check(fn(_ptr(xd), _ptr(xd_scales), _ptr(offsets), E_loc, third, H, I, act,
-                  _ptr(w_gate), _ptr(w_up), _ptr(w_down), _ptr(w_gate_scales),
-                  _ptr(w_up_scales), _ptr(w_down_scales), _w_code(act, w_scales_pow2) | packed, _ptr(y),
-                  _DT[y.dtype], _ptr(ws), ws.numel() * ws.element_size(),
-                  int(expected_rows), _stream(stream)))
+    _call(fn, xd, stream, _ptr(xd), _ptr(xd_scales), _ptr(offsets), E_loc, third, H, I, act,
+          _ptr(w_gate), _ptr(w_up), _ptr(w_down), _ptr(w_gate_scales),
+          _ptr(w_up_scales), _ptr(w_down_scales), _w_code(act, w_scales_pow2) | packed, _ptr(y),
+          _DT[y.dtype], _ptr(ws), ws.numel() * ws.element_size(), int(expected_rows))
     return y
 
 

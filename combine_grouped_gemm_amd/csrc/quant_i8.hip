@@ -5,11 +5,19 @@
 // For a row v: amax = max |v|, scale = RN(amax / 127) in fp32 (at least the
 // smallest normal number; 1 for amax = 0), code = v / scale rounded to the
 // nearest integer, ties to even.  The quotient is rounded exactly: n =
-// rint(v * (1 / scale)) is off by at most one step, and only next to a tie,
+// RN(v * RN(1 / scale)) is off by at most one step, and only next to a tie,
 // and the remainder v - n * scale is exact in one fma (v and scale share the
 // 24-bit grid of the larger one's last place, and |remainder| <= 0.51 scale),
 // so comparing it with scale / 2 settles the code.  A row with a NaN or an
 // infinity gets scale NaN and codes 0: every product with it is NaN.
+//
+// Both kernels move data and little else: the row is read once into registers
+// (16 consecutive values a lane and piece: 32 bytes of bf16 in, 16 bytes of
+// codes out), reduced, quantised and stored.  n comes from one fma onto 1.5 *
+// 2^23, whose low byte is the code; a piece is done again by the long way only
+// if one of its remainders reaches half a step (a row in fifty at 2048
+// columns).  About six instructions an element, a third of the time that its
+// three bytes take at the rate of a large copy.
 #include "device_common.hpp"
 #include "launch.hpp"
 
@@ -23,138 +31,287 @@ __device__ __forceinline__ float row_scale(uint32_t amax) {
     return fmaxf(__uint_as_float(amax) / 127.0f, 1.17549435e-38f);
 }
 
-// Code of v for the row scale s, rs = 1 / s (see the file comment); 0 when s is NaN.
+// Code of v for the row scale s, rs = 1 / s (see the file comment).
 __device__ __forceinline__ int code_of(float v, float s, float rs) {
     float n = rintf(v * rs);
     const float r = fmaf(-n, s, v), h = 0.5f * s;
-    if (fabsf(r) >= h) {
-        const bool odd = ((int)n & 1) != 0;
-        if (r > h || (r == h && odd)) n += 1.0f;
-        else if (r < -h || (r == -h && odd)) n -= 1.0f;
-    }
-    return s == s ? (int)n : 0;
+    const bool odd = ((int)n & 1) != 0;
+    if (r > h || (r == h && odd)) n += 1.0f;
+    else if (r < -h || (r == -h && odd)) n -= 1.0f;
+    return (int)n;
 }
 
-__device__ __forceinline__ uint32_t pack4(int a, int b, int c, int d) {
-    return (uint32_t)(a & 0xff) | ((uint32_t)(b & 0xff) << 8) | ((uint32_t)(c & 0xff) << 16) | ((uint32_t)d << 24);
-}
-
-// Eight consecutive values of a row: one 16-byte vector of bf16, two of fp32.
+// 16 consecutive values of a row, as they are in memory: 32 bytes of bf16 or 64 of fp32.
 template <bool F32>
-__device__ __forceinline__ void load8(const void* row, int c, float (&f)[8]) {
-    if constexpr (F32) {
-        const uint4 a = static_cast<const uint4*>(row)[2 * c], b = static_cast<const uint4*>(row)[2 * c + 1];
-        f[0] = __uint_as_float(a.x); f[1] = __uint_as_float(a.y); f[2] = __uint_as_float(a.z);
-        f[3] = __uint_as_float(a.w); f[4] = __uint_as_float(b.x); f[5] = __uint_as_float(b.y);
-        f[6] = __uint_as_float(b.z); f[7] = __uint_as_float(b.w);
-    } else {
-        const uint4 v = static_cast<const uint4*>(row)[c];
-        f[0] = bf16_lo(v.x); f[1] = bf16_hi(v.x); f[2] = bf16_lo(v.y); f[3] = bf16_hi(v.y);
-        f[4] = bf16_lo(v.z); f[5] = bf16_hi(v.z); f[6] = bf16_lo(v.w); f[7] = bf16_hi(v.w);
-    }
-}
+struct Piece {
+    static constexpr int kVec = F32 ? 4 : 2;
+    uint4 v[kVec];
 
-__device__ __forceinline__ uint32_t amax8(const float (&f)[8], uint32_t m) {
+    __device__ __forceinline__ void load(const void* row, int c) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const uint32_t u = __float_as_uint(f[i]) & 0x7fffffffu;
-        m = u > m ? u : m;
+        for (int i = 0; i < kVec; ++i) v[i] = static_cast<const uint4*>(row)[c * kVec + i];
     }
-    return m;
-}
+    __device__ __forceinline__ void zero() {
+#pragma unroll
+        for (int i = 0; i < kVec; ++i) v[i] = make_uint4(0, 0, 0, 0);
+    }
+    __device__ __forceinline__ void values(float (&f)[16]) const {
+#pragma unroll
+        for (int i = 0; i < kVec; ++i) {
+            const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                if constexpr (F32) f[i * 4 + k] = __uint_as_float(w[k]);
+                else {
+                    f[i * 8 + k * 2] = bf16_lo(w[k]);
+                    f[i * 8 + k * 2 + 1] = bf16_hi(w[k]);
+                }
+            }
+        }
+    }
+    __device__ __forceinline__ uint32_t amax(uint32_t m) const {
+        float f[16];
+        values(f);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            const uint32_t u = __float_as_uint(f[i]) & 0x7fffffffu;
+            m = u > m ? u : m;
+        }
+        return m;
+    }
+    // the 16 codes; s NaN: zeros
+    __device__ __forceinline__ uint4 codes(float s, float rs) const {
+        float f[16];
+        values(f);
+        constexpr float kMagic = 12582912.0f;                    // 1.5 * 2^23
+        uint32_t t[16], q[4];
+        float far = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            const float m = fmaf(f[i], rs, kMagic);
+            far = fmaxf(far, fabsf(fmaf(kMagic - m, s, f[i])));
+            t[i] = __float_as_uint(m);
+        }
+        if (far >= 0.5f * s) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) t[i] = (uint32_t)code_of(f[i], s, rs);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t lo = __builtin_amdgcn_perm(t[i * 4 + 1], t[i * 4], 0x0c0c0400u);
+            const uint32_t hi = __builtin_amdgcn_perm(t[i * 4 + 3], t[i * 4 + 2], 0x04000c0cu);
+            q[i] = s == s ? lo | hi : 0u;
+        }
+        return make_uint4(q[0], q[1], q[2], q[3]);
+    }
+};
 
-__device__ __forceinline__ uint2 codes8(const float (&f)[8], float s, float rs) {
-    return make_uint2(pack4(code_of(f[0], s, rs), code_of(f[1], s, rs), code_of(f[2], s, rs), code_of(f[3], s, rs)),
-                      pack4(code_of(f[4], s, rs), code_of(f[5], s, rs), code_of(f[6], s, rs), code_of(f[7], s, rs)));
-}
-
+// Maximum over the wave, the same in every lane: within each 16-lane row by
+// DPP (partners lane ^ 1, lane ^ 2, then the half-row and row mirrors), then
+// over one lane of each row.  As integers: bit patterns of magnitudes, NaN above
+// everything.
 __device__ __forceinline__ uint32_t wave_max_u32(uint32_t v) {
-#pragma unroll
-    for (int d = 1; d < kWave; d <<= 1) {
-        const uint32_t o = (uint32_t)__shfl_xor((int)v, d, kWave);
-        v = o > v ? o : v;
-    }
-    return v;
+    auto most = [](uint32_t a, uint32_t b) { return a > b ? a : b; };
+    v = most(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0xB1, 0xF, 0xF, true));
+    v = most(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x4E, 0xF, 0xF, true));
+    v = most(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x141, 0xF, 0xF, true));
+    v = most(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x140, 0xF, 0xF, true));
+    const uint32_t a = (uint32_t)__builtin_amdgcn_readlane((int)v, 0), b = (uint32_t)__builtin_amdgcn_readlane((int)v, 16);
+    const uint32_t c = (uint32_t)__builtin_amdgcn_readlane((int)v, 32), d = (uint32_t)__builtin_amdgcn_readlane((int)v, 48);
+    return most(most(a, b), most(c, d));
 }
 
-// ---- dispatch: one block per token; the token is read once for its scale and
-// once more (from cache) for its codes, which go to every local row.
+// ---- dispatch: one block per token, its pieces spread over the threads, NP
+// to each (0: any number, read a second time from cache for the codes).  The
+// token's destination rows come with one vector load per wave (lane k holds
+// slot k's row; a ballot gives the local slots), as in dispatch.hip; a token
+// without a local slot is not read.
 constexpr int kTokThreads = 256;
 
-template <bool F32>
+__device__ __forceinline__ int slot_row(const int32_t* rows, int K, int k0, int cap, int lane) {
+    const int k = k0 + lane;
+    if (k >= K) return -1;
+    const int r = rows[k];
+    return (r >= 0 && r < cap) ? r : -1;
+}
+
+template <bool F32, int NP>
 __global__ __launch_bounds__(kTokThreads) void dispatch_i8_kernel(
     SegTable seg, int H, const int32_t* __restrict__ row_of, int K, int cap, uint8_t* __restrict__ xd,
     float* __restrict__ xd_scales) {
     __shared__ uint32_t s_max[kTokThreads / kWave];
-    const int t = blockIdx.x, tid = threadIdx.x;
+    const int t = blockIdx.x, tid = threadIdx.x, lane = tid % kWave, nt = blockDim.x, np = H / 16;
     const int32_t* rows = row_of + (size_t)t * K;
-    bool any = false;
-    for (int k = 0; k < K; ++k) any = any || (rows[k] >= 0 && rows[k] < cap);
+    int my = slot_row(rows, K, 0, cap, lane);
+    uint64_t local = ballot64(my >= 0);       // local slots among the first 64, the same in every wave
+    bool any = local != 0;
+    for (int k0 = kWave; k0 < K && !any; k0 += kWave) any = ballot64(slot_row(rows, K, k0, cap, lane) >= 0) != 0;
     if (!any) return;
-    int i = 0;
+    int i = 0;                                // the token's segment
     for (int s = 1; s < seg.n; ++s) i += t >= seg.start[s] ? 1 : 0;
     const char* row = static_cast<const char*>(seg.ptr[i]) + (size_t)(t - seg.start[i]) * H * (F32 ? 4 : 2);
+
+    constexpr int kHeld = NP > 0 ? NP : 1;
+    Piece<F32> piece[kHeld];
     uint32_t m = 0;
-    for (int c = tid; c < H / 8; c += kTokThreads) {
-        float f[8];
-        load8<F32>(row, c, f);
-        m = amax8(f, m);
-    }
-    m = wave_max_u32(m);
-    if (tid % kWave == 0) s_max[tid / kWave] = m;
-    __syncthreads();
+    if constexpr (NP > 0) {
 #pragma unroll
-    for (int w = 0; w < kTokThreads / kWave; ++w) m = s_max[w] > m ? s_max[w] : m;
-    const float s = row_scale(m), rs = 1.0f / s;
-    for (int c = tid; c < H / 8; c += kTokThreads) {
-        float f[8];
-        load8<F32>(row, c, f);
-        const uint2 q = codes8(f, s, rs);
-        for (int k = 0; k < K; ++k) {
-            const int r = rows[k];
-            if (r >= 0 && r < cap) reinterpret_cast<uint2*>(xd + (size_t)r * H)[c] = q;
+        for (int n = 0; n < NP; ++n) {
+            const int c = tid + n * nt;
+            if (c < np) piece[n].load(row, c);
+            else piece[n].zero();
+        }
+#pragma unroll
+        for (int n = 0; n < NP; ++n) m = piece[n].amax(m);
+    } else {
+        for (int c = tid; c < np; c += nt) {
+            piece[0].load(row, c);
+            m = piece[0].amax(m);
         }
     }
-    for (int k = tid; k < K; k += kTokThreads) {
-        const int r = rows[k];
-        if (r >= 0 && r < cap) xd_scales[r] = s;
+    m = wave_max_u32(m);
+    if (nt > kWave) {
+        if (lane == 0) s_max[tid / kWave] = m;
+        __syncthreads();
+        for (int w = 0; w < nt / kWave; ++w) m = s_max[w] > m ? s_max[w] : m;
+    }
+    const float s = row_scale(m), rs = 1.0f / s;
+    if constexpr (NP > 0) {
+        uint4 q[NP];
+#pragma unroll
+        for (int n = 0; n < NP; ++n) q[n] = piece[n].codes(s, rs);
+        for (int k0 = 0;;) {
+            if (my >= 0 && tid < kWave) xd_scales[my] = s;
+            while (local != 0) {
+                const int k = __builtin_ctzll(local);
+                local &= local - 1;
+                uint4* dst = reinterpret_cast<uint4*>(xd + (size_t)__builtin_amdgcn_readlane(my, k) * H);
+#pragma unroll
+                for (int n = 0; n < NP; ++n) {
+                    const int c = tid + n * nt;
+                    if (c < np) dst[c] = q[n];
+                }
+            }
+            k0 += kWave;
+            if (k0 >= K) break;
+            my = slot_row(rows, K, k0, cap, lane);
+            local = ballot64(my >= 0);
+        }
+    } else {
+        for (int k = tid; k < K; k += nt) {
+            const int r = rows[k];
+            if (r >= 0 && r < cap) xd_scales[r] = s;
+        }
+        for (int c = tid; c < np; c += nt) {
+            piece[0].load(row, c);
+            const uint4 q = piece[0].codes(s, rs);
+            for (int k = 0; k < K; ++k) {
+                const int r = rows[k];
+                if (r >= 0 && r < cap) reinterpret_cast<uint4*>(xd + (size_t)r * H)[c] = q;
+            }
+        }
     }
 }
 
-// ---- expert-ordered rows: one wave per row over a persistent grid.  Valid
-// rows are [offsets[0], offsets[E_loc]) of the contiguous layout, the first
-// m[j] of each block of cap_e rows in the masked one, or all rows.
+// ---- expert-ordered rows: one wave per row, NP pieces a lane (0: any number,
+// read twice).  Valid rows are [offsets[0], offsets[E_loc]) of the contiguous
+// layout or all rows: a persistent grid walks them.  In the masked layout
+// (the first m[j] rows of each block of cap_e) blockIdx.y is the expert, and
+// its blocks share its rows.
 constexpr int kRowWaves = 4;
 
-template <bool F32>
+template <bool F32, int NP>
+__device__ __forceinline__ void quant_row(const QuantArgs& p, size_t r, int lane) {
+    const char* row = static_cast<const char*>(p.x) + r * p.cols * (F32 ? 4 : 2);
+    uint4* dst = reinterpret_cast<uint4*>(static_cast<uint8_t*>(p.q) + r * p.cols);
+    const int np = p.cols / 16;
+    constexpr int kHeld = NP > 0 ? NP : 1;
+    Piece<F32> piece[kHeld];
+    uint32_t m = 0;
+    if constexpr (NP > 0) {
+#pragma unroll
+        for (int n = 0; n < NP; ++n) {
+            const int c = lane + n * kWave;
+            if (c < np) piece[n].load(row, c);
+            else piece[n].zero();
+        }
+#pragma unroll
+        for (int n = 0; n < NP; ++n) m = piece[n].amax(m);
+    } else {
+        for (int c = lane; c < np; c += kWave) {
+            piece[0].load(row, c);
+            m = piece[0].amax(m);
+        }
+    }
+    const float s = row_scale(wave_max_u32(m)), rs = 1.0f / s;
+    if constexpr (NP > 0) {
+#pragma unroll
+        for (int n = 0; n < NP; ++n) {
+            const int c = lane + n * kWave;
+            const uint4 q = piece[n].codes(s, rs);
+            if (c < np) dst[c] = q;
+        }
+    } else {
+        for (int c = lane; c < np; c += kWave) {
+            piece[0].load(row, c);
+            dst[c] = piece[0].codes(s, rs);
+        }
+    }
+    if (lane == 0) p.scales[r] = s;
+}
+
+template <bool F32, int NP>
 __global__ __launch_bounds__(kRowWaves * kWave) void quant_rows_kernel(QuantArgs p) {
     const int lane = threadIdx.x % kWave;
-    const int wave = blockIdx.x * kRowWaves + threadIdx.x / kWave;
-    int r0 = 0, r1 = p.cap;
-    if (p.offsets != nullptr) {
+    const int wave = blockIdx.x * kRowWaves + __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    long long r0 = 0, r1 = p.cap;
+    if (p.m_counts != nullptr) {
+        const int j = blockIdx.y;
+        r0 = (long long)j * p.cap_e;
+        r1 = r0 + min(max(p.m_counts[j], 0), p.cap_e);
+    } else if (p.offsets != nullptr) {
         r0 = min(max(p.offsets[0], 0), p.cap);
-        r1 = min(max(p.offsets[p.E_loc], r0), p.cap);
+        r1 = min(max(p.offsets[p.E_loc], (int)r0), p.cap);
     }
-    for (long long r = (long long)r0 + wave; r < r1; r += (long long)gridDim.x * kRowWaves) {
-        if (p.m_counts != nullptr) {
-            const int j = (int)(r / p.cap_e);
-            if ((int)(r % p.cap_e) >= p.m_counts[j]) continue;
-        }
-        const char* row = static_cast<const char*>(p.x) + (size_t)r * p.cols * (F32 ? 4 : 2);
-        uint32_t m = 0;
-        for (int c = lane; c < p.cols / 8; c += kWave) {
-            float f[8];
-            load8<F32>(row, c, f);
-            m = amax8(f, m);
-        }
-        const float s = row_scale(wave_max_u32(m)), rs = 1.0f / s;
-        for (int c = lane; c < p.cols / 8; c += kWave) {
-            float f[8];
-            load8<F32>(row, c, f);
-            reinterpret_cast<uint2*>(static_cast<uint8_t*>(p.q) + (size_t)r * p.cols)[c] = codes8(f, s, rs);
-        }
-        if (lane == 0) p.scales[r] = s;
+    for (long long r = r0 + wave; r < r1; r += (long long)gridDim.x * kRowWaves) quant_row<F32, NP>(p, (size_t)r, lane);
+}
+
+template <bool F32>
+hipError_t launch_dispatch_any(const SegTable& seg, int B, int H, const int32_t* row_of, int K, uint8_t* xd,
+                               float* xd_scales, int cap, hipStream_t stream) {
+    const int np = H / 16, waves = (np + kWave - 1) / kWave;
+    const dim3 grid(B), block(kWave * (waves < kTokThreads / kWave ? waves : kTokThreads / kWave));
+    const int per = (np + (int)block.x - 1) / (int)block.x;
+    if (per <= 1)
+        hipLaunchKernelGGL((dispatch_i8_kernel<F32, 1>), grid, block, 0, stream, seg, H, row_of, K, cap, xd, xd_scales);
+    else if (per <= 2)
+        hipLaunchKernelGGL((dispatch_i8_kernel<F32, 2>), grid, block, 0, stream, seg, H, row_of, K, cap, xd, xd_scales);
+    else if (per <= 4)
+        hipLaunchKernelGGL((dispatch_i8_kernel<F32, 4>), grid, block, 0, stream, seg, H, row_of, K, cap, xd, xd_scales);
+    else
+        hipLaunchKernelGGL((dispatch_i8_kernel<F32, 0>), grid, block, 0, stream, seg, H, row_of, K, cap, xd, xd_scales);
+    return hipGetLastError();
+}
+
+template <bool F32>
+hipError_t launch_quant_any(const QuantArgs& a, hipStream_t stream) {
+    const int per = (a.cols / 16 + kWave - 1) / kWave, most = device_cu_count() * 8;
+    dim3 grid, block(kRowWaves * kWave);
+    if (a.m_counts != nullptr) {
+        // four rows a wave when a block of rows is full: decode fills few of them, and
+        // workgroups with nothing to do cost more than the loop
+        const int share = (most / 2 + a.E_loc - 1) / a.E_loc, need = (a.cap_e + 4 * kRowWaves - 1) / (4 * kRowWaves);
+        grid = dim3(share < need ? share : need, a.E_loc);
+    } else {
+        const int need = (a.cap + kRowWaves - 1) / kRowWaves;
+        grid = dim3(need < most ? need : most);
     }
+    if (per <= 1) hipLaunchKernelGGL((quant_rows_kernel<F32, 1>), grid, block, 0, stream, a);
+    else if (per <= 2) hipLaunchKernelGGL((quant_rows_kernel<F32, 2>), grid, block, 0, stream, a);
+    else if (per <= 4) hipLaunchKernelGGL((quant_rows_kernel<F32, 4>), grid, block, 0, stream, a);
+    else if (per <= 8) hipLaunchKernelGGL((quant_rows_kernel<F32, 8>), grid, block, 0, stream, a);
+    else hipLaunchKernelGGL((quant_rows_kernel<F32, 0>), grid, block, 0, stream, a);
+    return hipGetLastError();
 }
 
 }  // namespace
@@ -162,22 +319,14 @@ __global__ __launch_bounds__(kRowWaves * kWave) void quant_rows_kernel(QuantArgs
 hipError_t launch_dispatch_i8(const SegTable& seg, int B, int H, bool f32, const int32_t* row_of, int K, void* xd,
                               float* xd_scales, int cap, hipStream_t stream) {
     if (B == 0) return hipSuccess;
-    if (f32)
-        hipLaunchKernelGGL(dispatch_i8_kernel<true>, dim3(B), dim3(kTokThreads), 0, stream, seg, H, row_of, K, cap,
-                           static_cast<uint8_t*>(xd), xd_scales);
-    else
-        hipLaunchKernelGGL(dispatch_i8_kernel<false>, dim3(B), dim3(kTokThreads), 0, stream, seg, H, row_of, K, cap,
-                           static_cast<uint8_t*>(xd), xd_scales);
-    return hipGetLastError();
+    uint8_t* q = static_cast<uint8_t*>(xd);
+    return f32 ? launch_dispatch_any<true>(seg, B, H, row_of, K, q, xd_scales, cap, stream)
+               : launch_dispatch_any<false>(seg, B, H, row_of, K, q, xd_scales, cap, stream);
 }
 
 hipError_t launch_quant_rows(const QuantArgs& a, bool f32, hipStream_t stream) {
     if (a.cap == 0) return hipSuccess;
-    const int want = (a.cap + kRowWaves - 1) / kRowWaves, most = device_cu_count() * 8;
-    const dim3 grid(want < most ? want : most), block(kRowWaves * kWave);
-    if (f32) hipLaunchKernelGGL(quant_rows_kernel<true>, grid, block, 0, stream, a);
-    else hipLaunchKernelGGL(quant_rows_kernel<false>, grid, block, 0, stream, a);
-    return hipGetLastError();
+    return f32 ? launch_quant_any<true>(a, stream) : launch_quant_any<false>(a, stream);
 }
 
 }  // namespace moeep
