@@ -135,6 +135,17 @@ def _call(fn, t, stream, *args):
             _check(fn(*args, _stream(stream)))
 
 
+def _new(shape, dtype, device, stream):
+    """An output the caller did not give, allocated for the stream that writes it: memory
+    of another stream may still be in use there."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream), device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 def _dev(t, name, dtype=None, ndim=None):
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
@@ -261,12 +272,12 @@ def moe_route_scored(logits, K: int, score: str = "sigmoid", bias=None, n_groups
         _dev(phys_of_logical, "phys_of_logical", torch.int32, 1)
         _need(phys_of_logical, "phys_of_logical", shape=(E,))
     if topk_ids is None:
-        topk_ids = torch.empty((B, max(Kt, 0)), dtype=torch.int32, device=dev)
+        topk_ids = _new((B, max(Kt, 0)), torch.int32, dev, stream)
     else:
         _dev(topk_ids, "topk_ids", torch.int32)
         _need(topk_ids, "topk_ids", shape=(B, Kt))
     if topk_w is None:
-        topk_w = torch.empty((B, max(Kt, 0)), dtype=torch.float32, device=dev)
+        topk_w = _new((B, max(Kt, 0)), torch.float32, dev, stream)
     else:
         _dev(topk_w, "topk_w", torch.float32)
         _need(topk_w, "topk_w", shape=(B, Kt))
@@ -399,11 +410,11 @@ def moe_dispatch(seg_x, row_of, cap_rows: int, xd_dtype=None, xd=None, xd_scales
     dev = row_of.device
     xd_code = _DT[x_dt] if xd_dtype is None else _dtype_code(xd_dtype)
     if xd is None:
-        xd = torch.empty((max(cap_rows, 1), H), dtype=_TORCH[xd_code], device=dev)
+        xd = _new((max(cap_rows, 1), H), _TORCH[xd_code], dev, stream)
     if xd_code == MOE_FP8_E4M3 and xd_scales is None:
-        xd_scales = torch.empty((max(cap_rows, 1), -(-H // FP8_BLOCK)), dtype=torch.float32, device=dev)
+        xd_scales = _new((max(cap_rows, 1), -(-H // FP8_BLOCK)), torch.float32, dev, stream)
     if xd_code == MOE_INT8 and xd_scales is None:
-        xd_scales = torch.empty(max(cap_rows, 1), dtype=torch.float32, device=dev)
+        xd_scales = _new(max(cap_rows, 1), torch.float32, dev, stream)
     _dev(xd, "xd")
     B = sum(int(t.shape[0]) for t in seg_x)
     _need(row_of, "row_of", shape=(B, K))
@@ -417,8 +428,7 @@ def moe_dispatch(seg_x, row_of, cap_rows: int, xd_dtype=None, xd=None, xd_scales
         _same_device(row_of, "row_of", xd, xd_scales, *seg_x)
     ptrs = (ctypes.c_void_p * len(seg_x))(*[s.data_ptr() for s in seg_x])
     rows = (ctypes.c_int32 * len(seg_x))(*[s.shape[0] for s in seg_x])
-    _call(lib().moe_dispatch, row_of, stream, ctypes.cast(ptrs, ctypes.c_void_p), ctypes.cast(rows, ctypes.c_void_p),
-          len(seg_x), _DT[x_dt], H, _ptr(row_of), K, _ptr(xd), xd_code, _ptr(xd_scales), cap_rows)
+    _call(lib().moe_dispatch, row_of, stream, ptrs, rows, len(seg_x), _DT[x_dt], H, _ptr(row_of), K, _ptr(xd), xd_code, _ptr(xd_scales), cap_rows)
     return xd, xd_scales
 
 
@@ -445,9 +455,9 @@ def moe_quant_rows(x, rows=None, cap_per_expert=None, q=None, scales=None, strea
         E_loc = rows.numel() - 1 if cap_per_expert is None else rows.numel()
         third = _rows_arg(rows, cap_per_expert, E_loc, cap)
     if q is None:
-        q = torch.empty((cap, cols), dtype=torch.int8, device=x.device)
+        q = _new((cap, cols), torch.int8, x.device, stream)
     if scales is None:
-        scales = torch.empty(cap, dtype=torch.float32, device=x.device)
+        scales = _new(cap, torch.float32, x.device, stream)
     _dev(q, "q", torch.int8)
     _dev(scales, "scales", torch.float32)
     _need(q, "q", shape=(cap, cols))
@@ -599,9 +609,9 @@ def moe_ffn_gate_up(xd, xd_scales, offsets, w_gate, w_up, w_gate_scales=None, w_
     act = _DT[xd.dtype]
     packed = _pack_flag(_w_packed(w_gate, H, act, "w_gate"))
     if h is None:
-        h = torch.empty((cap, I), dtype=_h_dtype_for(xd), device=xd.device)
+        h = _new((cap, I), _h_dtype_for(xd), xd.device, stream)
     if act == MOE_FP8_E4M3 and h_scales is None:
-        h_scales = torch.empty((cap, -(-I // FP8_BLOCK)), dtype=torch.float32, device=xd.device)
+        h_scales = _new((cap, -(-I // FP8_BLOCK)), torch.float32, xd.device, stream)
     if h.dtype != _h_dtype_for(xd):
         raise ValueError(f"h must be {_h_dtype_for(xd)} (got {h.dtype})")
     nbI = -(-I // FP8_BLOCK)
@@ -636,7 +646,7 @@ def moe_ffn_down(h, h_scales, offsets, w_down, w_down_scales=None, y=None, y_dty
     packed = _pack_flag(_w_packed(w_down, I, act, "w_down"))
     y_dtype = _y_dtype_for(act) if y_dtype is None else y_dtype
     if y is None:
-        y = torch.empty((cap, H), dtype=y_dtype, device=h.device)
+        y = _new((cap, H), y_dtype, h.device, stream)
     _check_ffn(h, h_scales, offsets, cap_per_expert, E_loc, I, cap, act, y=(y, cap * H),
                w_down_scales=_w_scales(act, w_down_scales, E_loc, H, I))
     fn = lib().moe_ffn_down if cap_per_expert is None else lib().moe_ffn_down_masked
@@ -662,10 +672,11 @@ def moe_grouped_ffn(xd, xd_scales, offsets, w_gate, w_up, w_down, w_gate_scales=
     packed = _pack_flag(_w_packed(w_gate, H, act, "w_gate"), _w_packed(w_down, I, act, "w_down"))
     y_dtype = _y_dtype_for(act) if y_dtype is None else y_dtype
     if y is None:
-        y = torch.empty((cap, H), dtype=y_dtype, device=xd.device)
+        y = _new((cap, H), y_dtype, xd.device, stream)
     need = moe_ffn_workspace_bytes(cap, I, act)
     if ws is None:
-        ws = torch.empty(max(need, 256), dtype=torch.uint8, device=xd.device)
+        ws = _new(max(need, 256), torch.uint8, xd.device, stream)
+    _dev(ws, "ws")
     _check_ffn(xd, xd_scales, offsets, cap_per_expert, E_loc, H, cap, act,
                w_up=(w_up, tuple(w_gate.shape)), w_down=(w_down, (E_loc, H, w_down.shape[2])),
                y=(y, cap * H),

@@ -66,11 +66,12 @@ __global__ __launch_bounds__(512, BM + BN > 256 ? 1 : 4) void grouped_gemm_i8_wi
     constexpr int FN = WN / 16;                      // 16-row weight fragments per wave
     constexpr int BNO = GATED ? BN / 2 : BN;         // output columns per tile
     static_assert(BM % 32 == 0 && BLOCKS % NW == 0 && (!GATED || FN % 2 == 0), "tile shape");
-    // load i of the 8 waves covers 64 operand rows: whether they are token rows
-    // and which weight half they belong to is compile-time after unrolling
-    static_assert(BM % 64 == 0 && BN % 128 == 0, "64-row blocks");
     constexpr int A_ITERS = A_BLOCKS / NW;           // i < A_ITERS: row blocks
-    constexpr int G_ITERS = BN / 128;                // next G_ITERS: the gate half's 64-row blocks
+    constexpr int RPL = NW * 8;                      // operand rows that one load of every wave covers
+    constexpr int G_ITERS = BN / 2 / RPL;            // next G_ITERS: the gate half
+    // whether a load's rows are token rows, and which weight half they belong to,
+    // is compile-time after unrolling
+    static_assert(BM % RPL == 0 && BN / 2 % RPL == 0, "whole loads");
 
     __shared__ uint4 sa0[BM * CPR];
     __shared__ uint4 sb0[BN * CPR];
@@ -128,29 +129,32 @@ __global__ __launch_bounds__(512, BM + BN > 256 ? 1 : 4) void grouped_gemm_i8_wi
         const uint8_t* wu = GATED ? W1 + w0 : nullptr;
 
         // Operands come in by buffer loads straight into LDS: a scalar resource
-        // (base, byte extent) for each block of 64 operand rows, the k-step as
-        // scalar offset and one 32-bit lane offset per operand.  Rows past the
-        // tile's valid rows and weight rows past N lie outside their resource's
-        // extent, so those lanes read nothing from memory and land zeros.
+        // (base, byte extent) per operand, the k-step as scalar offset and a
+        // 32-bit lane offset, the row's.  Rows past the tile's valid rows and
+        // weight rows past N lie outside their resource's extent, so those lanes
+        // read nothing from memory and land zeros.
         const uint8_t* abase = A + (size_t)row0 * Kdim;
-        const int wrows = min(N - col0, BNO);                   // weight rows of the tile (of each half)
-        const uint32_t lrow = wave * 8 + lane / 8;              // this lane's row of a 64-row block
+        const uint32_t a_bytes = (uint32_t)nvalid * (uint32_t)Kdim;
+        const uint32_t w_bytes = (uint32_t)min(N - col0, BNO) * (uint32_t)ldw;   // of the tile (of each half)
+        const uint32_t lrow = wave * 8 + lane / 8;              // this lane's row of a load's RPL rows
         const uint32_t off_a = lrow * (uint32_t)Kdim + lane_k, off_w = lrow * (uint32_t)ldw + lane_k;
         // direct load i of a stage; `live` false (a step past the last) reads
         // nothing, so every step issues the same LPS loads without a branch
         auto issue_one = [&](auto I, int i, int kstep, bool live) {
             const bool is_a = i < A_ITERS;
-            const int q = i - A_ITERS;                          // 64-row block of the weights
+            const int q = i - A_ITERS;                          // RPL-row block of the weights
             const bool up = GATED && q >= G_ITERS;
-            const int first = is_a ? i * 64 : (up ? q - G_ITERS : q) * 64;
+            const int first = is_a ? i * RPL : (up ? q - G_ITERS : q) * RPL;
             char* dst = is_a ? a_base(I) + (i * NW + wave) * 1024 : b_base(I) + (q * NW + wave) * 1024;
-            const int pitch = is_a ? Kdim : ldw;
-            const uint8_t* base = is_a ? abase : up ? wu : wg;
-            const int left = (is_a ? nvalid : wrows) - first;
-            const rsrc_t r = make_rsrc(base + (size_t)first * pitch, live && left > 0 ? (uint32_t)left * pitch : 0u);
+            const rsrc_t r = make_rsrc(is_a ? abase : up ? wu : wg, live ? (is_a ? a_bytes : w_bytes) : 0u);
             // chunks past K (a partial last step) get an offset beyond every
             // extent, so they read nothing and land zeros in both operands
-            const uint32_t vo = kstep * BK + lane_k < Kdim ? (is_a ? off_a : off_w) : kOutOfRange;
+            // (formed anew for every load: kept in registers from step to step, the
+            // offsets push accumulators out to memory)
+            uint32_t down = (uint32_t)first * (uint32_t)(is_a ? Kdim : ldw);
+            asm volatile("" : "+s"(down));
+            const uint32_t row = (is_a ? off_a : off_w) + down;
+            const uint32_t vo = kstep * BK + lane_k < Kdim ? row : kOutOfRange;
             // the row block is re-read by every n-tile of the expert (kept in
             // L2); the weights' cache policy is the launcher's choice
             if (is_a)
@@ -216,8 +220,8 @@ __global__ __launch_bounds__(512, BM + BN > 256 ? 1 : 4) void grouped_gemm_i8_wi
         // of the 64-wide step for both operands and receives rows 4*(l/16)+e,
         // column l % 16 of the 16x16 result.
         auto tile = [&](auto NFc) {
-            constexpr int NF = decltype(NFc)::value;
-            intx4 acc[NF > 0 ? NF : 1][FN];
+            constexpr int NF = decltype(NFc)::value, NG = NF > 0 ? NF : 1;
+            intx4 acc[NG][FN];
 #pragma unroll
             for (int i = 0; i < NF; ++i)
 #pragma unroll
@@ -237,7 +241,7 @@ __global__ __launch_bounds__(512, BM + BN > 256 ? 1 : 4) void grouped_gemm_i8_wi
                 auto read_b = [&](int kk, int f) {
                     return *reinterpret_cast<const intx4*>(bb + lds_lane[kk] + brow0(f) * ROWB);
                 };
-                intx4 af[2][NF > 0 ? NF : 1], bf[2][FN];
+                intx4 af[2][NG], bf[2][FN];
                 if (NF > 0) {
 #pragma unroll
                     for (int f = 0; f < FN; ++f) bf[0][f] = read_b(0, f);
@@ -265,7 +269,7 @@ __global__ __launch_bounds__(512, BM + BN > 256 ? 1 : 4) void grouped_gemm_i8_wi
                     for (int f = 0; f < FN; ++f)
                         acc[i][f] = __builtin_amdgcn_mfma_i32_16x16x64_i8(af[1][i], bf[1][f], acc[i][f], 0, 0, 0);
 #pragma unroll
-                    for (int q = i * LPS / NF; q < (i + 1) * LPS / NF; ++q) issue_one(I, q, k + 2, live);
+                    for (int q = i * LPS / NG; q < (i + 1) * LPS / NG; ++q) issue_one(I, q, k + 2, live);
                     __builtin_amdgcn_sched_barrier(0);
                 }
                 if (NF == 0) {

@@ -479,6 +479,61 @@ def test_two_streams_at_once():
     assert all(torch.equal(o, rp) for o in outs[0]) and all(torch.equal(o, rd) for o in outs[1])
 
 
+def test_rows_past_four_gigabytes():
+    """Buffers whose byte offsets pass 32 bits: dispatch, quantisation and a product
+    that touch only the last rows."""
+    import combine_grouped_gemm_amd as m
+    cap, H, n = 70000, 65536, 6
+    x = _values(n, H, 3)
+    xd = torch.zeros((cap, H), dtype=torch.int8, device="cuda")
+    sc = torch.zeros(cap, device="cuda")
+    row_of = torch.arange(cap - n, cap, dtype=torch.int32, device="cuda").view(n, 1)
+    m.moe_dispatch(x.cuda(), row_of, cap, "int8", xd=xd, xd_scales=sc)
+    rq, rs = nx.quantize_i8_rows(to_np(x))
+    np.testing.assert_array_equal(xd[cap - n:].cpu().numpy(), rq)
+    np.testing.assert_array_equal(sc[cap - n:].cpu().numpy(), rs)
+    assert not xd[cap - n - 3:cap - n].any()
+    off = torch.tensor([cap - n, cap - 2, cap], dtype=torch.int32, device="cuda")
+    w = torch.randint(-127, 128, (2, 16, H), dtype=torch.int8, generator=_gen(1)).cuda()
+    y = m.moe_ffn_down(xd, sc, off, w, torch.ones((2, 16), device="cuda"), y_dtype=torch.float32)
+    for j, (a, b) in enumerate(((cap - n, cap - 2), (cap - 2, cap))):
+        ref = (xd[a:b].double() @ w[j].double().t()) * sc[a:b].double()[:, None]
+        _near(y[a:b], ref, Y_TOL[torch.float32], "y")
+    del xd, y
+    xb = torch.zeros((cap, H), dtype=torch.bfloat16, device="cuda")
+    xb[cap - n:] = x.cuda()
+    q, s = m.moe_quant_rows(xb, off)
+    np.testing.assert_array_equal(q[cap - n:].cpu().numpy(), rq)
+    np.testing.assert_array_equal(s[cap - n:].cpu().numpy(), rs)
+    del xb, q
+    torch.cuda.empty_cache()
+
+
+def test_outputs_allocated_on_the_given_stream():
+    """Outputs that a call makes itself belong to the stream it runs on: memory that
+    the current stream has freed but still uses is not handed to another one."""
+    import combine_grouped_gemm_amd as m
+    x = torch.randn(2000, 512, generator=_gen(2)).to(torch.bfloat16).cuda()
+    rq, rs = m.moe_quant_rows(x)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(5):
+        junk = torch.empty((2000, 512), dtype=torch.int8, device="cuda")
+        big = torch.randn(2048, 2048, device="cuda")
+        for _ in range(4):
+            big = big @ big                                # keeps the current stream busy
+        junk.fill_(1)                                      # runs late, on the current stream
+        del junk
+        q, s = m.moe_quant_rows(x, stream=side)
+        side.synchronize()
+        early = q.clone()
+        torch.cuda.synchronize()
+        assert torch.equal(q, rq) and torch.equal(s, rs) and torch.equal(early, rq)
+    q, s = m.moe_quant_rows(x, stream=side.cuda_stream)
+    torch.cuda.synchronize()
+    assert torch.equal(q, rq)
+
+
 def test_binding_refusals():
     import combine_grouped_gemm_amd as m
     z = lambda *s, dt=torch.int8: torch.zeros(s, dtype=dt, device="cuda")
