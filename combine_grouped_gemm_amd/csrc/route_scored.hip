@@ -256,6 +256,27 @@ __device__ __forceinline__ float exp_near(float x) {
     return __builtin_amdgcn_exp2f(p) * fmaf(r, 0.693147182f, 1.0f);
 }
 
+// How many groups have a larger score than this lane's (an equal one: a lower
+// number); a group is `lanes` lanes that hold the same score.  The row is
+// rotated in steps of a group.
+template <typename T>
+__device__ __forceinline__ int groups_ahead(T score, int lanes, int l16) {
+    int n = 0;
+    auto against = [&](T other, int r) {
+        n += (int)((other > score) | ((other == score) & (((l16 - r) & 15) < l16)));
+    };
+#define MOEEP_AGAINST(r) against(dpp<0x120 + r>(score), r);
+    if (lanes <= 8) { MOEEP_AGAINST(8) }
+    if (lanes <= 4) { MOEEP_AGAINST(4) MOEEP_AGAINST(12) }
+    if (lanes <= 2) { MOEEP_AGAINST(2) MOEEP_AGAINST(6) MOEEP_AGAINST(10) MOEEP_AGAINST(14) }
+    if (lanes == 1) {
+        MOEEP_AGAINST(1) MOEEP_AGAINST(3) MOEEP_AGAINST(5) MOEEP_AGAINST(7)
+        MOEEP_AGAINST(9) MOEEP_AGAINST(11) MOEEP_AGAINST(13) MOEEP_AGAINST(15)
+    }
+#undef MOEEP_AGAINST
+    return n;
+}
+
 // EPL: registers for a lane's experts, at least E / 16.  VEC: exactly E / 16,
 // and rows and biases can be read in 16-byte pieces.
 template <int EPL, bool VEC, bool SIGMOID, bool BF16>
@@ -369,6 +390,19 @@ __global__ __launch_bounds__(kRowWaves * kWave) void route_scored_kernel(RouteSc
                 }
             }
 
+    // an expert's score s and choice c in 64 bits
+    auto exact_score = [&](int e, double* s) {
+        const double l = (double)load_logit(p.logits, BF16, base + e);
+        const double b = p.bias != nullptr ? (double)p.bias[e] : 0.0;
+        *s = SIGMOID ? 1.0 / (1.0 + exp(-l)) : exp(l - (double)top) / sum;
+        return *s + b;
+    };
+    // what no expert's exact score exceeds whose key is k or less
+    auto key_bound = [&](uint32_t k) {
+        const float up = key_value(k | kPlace);                   // without the place's bits, rounded up
+        return (double)up + (double)fabsf(up) * rel + abs_err;
+    };
+
     // ---- groups: 16 / G lanes each
     bool ok = true;
     if (p.topk_groups < p.G) {
@@ -384,26 +418,38 @@ __global__ __launch_bounds__(kRowWaves * kWave) void route_scored_kernel(RouteSc
         const float score = c1 + second;
         // of the two terms, which may cancel
         const float size = c1 != -INFINITY ? fabsf(c1) + fabsf(second) : 0.0f;
-        // groups ahead of this one, by rotating the row in steps of a group
-        int better = 0;
-        auto against = [&](float os, int r) {
-            better += (int)((os > score) | ((os == score) & (((l16 - r) & 15) < l16)));
-        };
-#define MOEEP_AGAINST(r) against(dpp<0x120 + r>(score), r);
-        if (lanes <= 8) { MOEEP_AGAINST(8) }
-        if (lanes <= 4) { MOEEP_AGAINST(4) MOEEP_AGAINST(12) }
-        if (lanes <= 2) { MOEEP_AGAINST(2) MOEEP_AGAINST(6) MOEEP_AGAINST(10) MOEEP_AGAINST(14) }
-        if (lanes == 1) {
-            MOEEP_AGAINST(1) MOEEP_AGAINST(3) MOEEP_AGAINST(5) MOEEP_AGAINST(7)
-            MOEEP_AGAINST(9) MOEEP_AGAINST(11) MOEEP_AGAINST(13) MOEEP_AGAINST(15)
-        }
-#undef MOEEP_AGAINST
-        const bool kept = better < p.topk_groups;
+        bool kept = groups_ahead(score, lanes, l16) < p.topk_groups;
         // the cut between the last group kept and the first one dropped
         const float least = -row_max(kept & (c1 != -INFINITY) ? -score : -INFINITY);
         const float most = row_max(kept ? -INFINITY : score);
         const float slack = 2.0f * (row_max(size) * rel + 2.0f * abs_err);
         ok = (most == -INFINITY) | (least - most > slack);
+        if (ballot64(!ok) != 0) {
+            // too near to tell (a token in five thousand; one in an 8192-token batch
+            // would hold up the kernel by half if it went through exact_token):
+            // the same with exact scores, of each lane's three leading experts,
+            // among which its two best are if the fourth is far enough behind
+            double x1 = -(double)INFINITY, x2 = x1;
+#pragma unroll
+            for (int q = 0; q < 3; ++q) {
+                double s, c = -(double)INFINITY;
+                if (key[q] != 0) c = exact_score(e0 + (int)(kPlace - (key[q] & kPlace)), &s);
+                x2 = fmax(fmin(x1, c), x2);
+                x1 = fmax(x1, c);
+            }
+            const bool sure = (key[3] == 0) | (x2 > key_bound(key[3]));
+            auto join64 = [&](double o1, double o2) {
+                x2 = fmax(fmin(x1, o1), fmax(x2, o2));
+                x1 = fmax(x1, o1);
+            };
+            if (lanes > 1) join64(dpp<0xB1>(x1), dpp<0xB1>(x2));
+            if (lanes > 2) join64(dpp<0x4E>(x1), dpp<0x4E>(x2));
+            if (lanes > 4) join64(dpp<0x141>(x1), dpp<0x141>(x2));
+            const double exact = x1 + ((p.group_top == 2) & (x2 != -(double)INFINITY) ? x2 : 0.0);
+            const bool kept64 = groups_ahead(exact, lanes, l16) < p.topk_groups;
+            kept = ok ? kept : kept64;
+            ok |= ((ballot64(!sure) >> (row * 16)) & 0xffffu) == 0;
+        }
 #pragma unroll
         for (int j = 0; j < EPL; ++j) key[j] = kept ? key[j] : 0u;
     }
@@ -429,12 +475,7 @@ __global__ __launch_bounds__(kRowWaves * kWave) void route_scored_kernel(RouteSc
 
     // ---- their exact scores and ranks
     double s = 0.0, c = -INFINITY;
-    if (ce >= 0) {
-        const double l = (double)load_logit(p.logits, BF16, base + ce);
-        const double b = p.bias != nullptr ? (double)p.bias[ce] : 0.0;
-        s = SIGMOID ? 1.0 / (1.0 + exp(-l)) : exp(l - (double)top) / sum;
-        c = s + b;
-    }
+    if (ce >= 0) c = exact_score(ce, &s);
     const uint32_t id = (uint32_t)ce;       // -1 ranks last
     int rank = 0;
     auto behind = [&](double oc, uint32_t oid) { rank += (int)((oc > c) | ((oc == c) & (oid < id))); };
@@ -445,10 +486,8 @@ __global__ __launch_bounds__(kRowWaves * kWave) void route_scored_kernel(RouteSc
 #undef MOEEP_BEHIND
     const bool pick = ce >= 0 && rank < p.K;
     if (last != 0) {                        // there may be experts that are no candidates
-        const float up = key_value(last | kPlace);                // without the place's bits, rounded up
-        const double most = (double)up + (double)fabsf(up) * rel + abs_err;
         const double kth = -row_max(pick ? -c : -(double)INFINITY);
-        ok = ok && kth > most;
+        ok = ok && kth > key_bound(last);
     }
     ok = ok && ((ballot64(odd) >> (row * 16)) & 0xffffu) == 0;
 

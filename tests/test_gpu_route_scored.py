@@ -122,6 +122,30 @@ def test_biases_that_cancel_scores():
         _check(lg, 8, "sigmoid", bias * 1e33, n_groups=8, topk_groups=4, group_top=2)
 
 
+@pytest.mark.parametrize("E,G,keep,crowd", [(256, 8, 4, 0), (256, 16, 3, 0), (128, 4, 2, 0), (512, 2, 1, 0), (256, 8, 4, 6),
+                                             (64, 8, 1, 0), (240, 8, 5, 4)])
+def test_groups_that_fp32_cannot_tell_apart(E, G, keep, crowd):
+    """Every group holds the same pattern of logits, each group's a few fp32 steps
+    above the last one's, in an order of its own for every token: group scores
+    differ by less than an fp32 score's error.  crowd: that many more experts of
+    each group lie as near to its second best."""
+    S = E // G
+    g = torch.Generator().manual_seed(E + G)
+    pattern = torch.cat([torch.tensor([1.5, 1.25]), torch.randn(S - 2, generator=g) * 0.3]).clamp(max=1.5)
+    for i in range(crowd):
+        pattern[2 + i] = 1.25 - (i + 1) * 2.0**-21
+    lg = torch.empty(48, G, S)
+    for t in range(48):
+        order = torch.randperm(G, generator=g).float()
+        # steps of 2^-23 are exact between 1 and 2
+        lg[t] = pattern[None, torch.randperm(S, generator=g)] + order[:, None] * 2.0**-22
+    lg = lg.view(48, E)
+    for score in ("sigmoid", "softmax"):
+        for top in (1, 2):
+            for bias in (None, torch.full((E,), -0.8)):
+                _check(lg, min(8, keep * S), score, bias, n_groups=G, topk_groups=keep, group_top=top)
+
+
 def test_misaligned_rows():
     """Contiguous tensors that start in the middle of a 16-byte piece."""
     for E in (256, 128):
