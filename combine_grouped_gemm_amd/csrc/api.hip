@@ -225,6 +225,10 @@ moe_status_t quant_rows(const void* x, moe_dtype_t x_dt, Rows rows, int E_local,
     if (cap_rows > 0) {
         REQUIRE(x && q && scales, "null x, q or scales pointer");
         REQUIRE(aligned16(x) && aligned16(q), "x and q must be 16-byte aligned");
+        const size_t n = (size_t)cap_rows * cols;
+        const char* x0 = static_cast<const char*>(x);
+        const char* q0 = reinterpret_cast<const char*>(q);
+        REQUIRE(q0 + n <= x0 || x0 + n * elem_size(x_dt) <= q0, "x and q must not overlap");
     }
     moeep::QuantArgs a;
     a.x = x;

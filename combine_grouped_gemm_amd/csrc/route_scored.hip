@@ -19,9 +19,9 @@
 // that, though, so the common kernel narrows in fp32 and settles in fp64:
 //
 //   A token is 16 lanes (a DPP row), four tokens a wave; a lane holds E / 16
-//   consecutive experts as 32-bit keys (the score's leading bits, then the
-//   place in the lane), sorted once in registers.  Groups are ranked by DPP;
-//   K + 4 rounds of "row maximum, its owner shifts its list" give the
+//   (rounded up) consecutive experts as 32-bit keys (the score's leading bits,
+//   then the place in the lane), sorted once in registers.  Groups are ranked by
+//   DPP; K + 4 rounds of "row maximum, its owner shifts its list" give the
 //   candidates, one to a lane.  Every candidate's score is then computed in 64
 //   bits, one lane each, and ranked exactly, and its gate comes from that.
 //   The answer stands if the K-th exact score lies above what any expert that
@@ -29,8 +29,14 @@
 //   and if the groups' cut is wider than that error; NaN and huge scores never
 //   do.  Otherwise the wave does that token again in 64 bits from the start.
 //
-// Other shapes (E no multiple of 16, other group counts, K > 12) go through
-// that 64-bit routine, one wave a token, keys in LDS.
+// Other shapes (E > 512, K > 12, groups that are no whole lanes) go through that
+// 64-bit routine, one wave a token, keys in LDS.
+//
+// Measured (MI355X, in a graph): one token of 256 experts, 8 groups, 5.2 us;
+// 8192 of them 7.6-8.8 us (bound by the VALU: some 1800 instructions a wave, two
+// waves a SIMD; reading the logits would take 2 us); 4093 tokens of 128 experts,
+// softmax, bf16, 4.0 us.  The 64-bit routine alone: 14.7 and 36.5 us on the first
+// two.
 #include "device_common.hpp"
 #include "launch.hpp"
 
@@ -277,7 +283,7 @@ __device__ __forceinline__ int groups_ahead(T score, int lanes, int l16) {
     return n;
 }
 
-// EPL: registers for a lane's experts, at least E / 16.  VEC: exactly E / 16,
+// EPL: registers for a lane's experts, at least E / 16 rounded up.  VEC: exactly E / 16,
 // and rows and biases can be read in 16-byte pieces.
 template <int EPL, bool VEC, bool SIGMOID, bool BF16>
 __global__ __launch_bounds__(kRowWaves * kWave) void route_scored_kernel(RouteScoredArgs p) {
@@ -289,7 +295,7 @@ __global__ __launch_bounds__(kRowWaves * kWave) void route_scored_kernel(RouteSc
     const int t = (blockIdx.x * kRowWaves + wave) * 4 + row;
     const bool live = t < p.B;
     const size_t base = (size_t)(live ? t : p.B - 1) * p.E;       // idle rows repeat the last token
-    const int chunk = VEC ? EPL : p.E / 16;
+    const int chunk = VEC ? EPL : (p.E + 15) / 16;
     const int e0 = l16 * chunk;
 
     // ---- logits and biases of this lane's experts
@@ -313,7 +319,7 @@ __global__ __launch_bounds__(kRowWaves * kWave) void route_scored_kernel(RouteSc
         }
     } else {
 #pragma unroll
-        for (int j = 0; j < EPL; ++j) lg[j] = j < chunk ? load_logit(p.logits, BF16, base + e0 + j) : -INFINITY;
+        for (int j = 0; j < EPL; ++j) lg[j] = j < chunk && e0 + j < p.E ? load_logit(p.logits, BF16, base + e0 + j) : -INFINITY;
     }
     if (p.bias != nullptr) {
         if constexpr (VEC) {
@@ -325,7 +331,7 @@ __global__ __launch_bounds__(kRowWaves * kWave) void route_scored_kernel(RouteSc
             }
         } else {
 #pragma unroll
-            for (int j = 0; j < EPL; ++j) bs[j] = j < chunk ? p.bias[e0 + j] : 0.0f;
+            for (int j = 0; j < EPL; ++j) bs[j] = j < chunk && e0 + j < p.E ? p.bias[e0 + j] : 0.0f;
         }
     } else {
 #pragma unroll
@@ -537,9 +543,11 @@ hipError_t launch_rows(const RouteScoredArgs& a, hipStream_t stream) {
 hipError_t launch_route_scored(const RouteScoredArgs& a, hipStream_t stream) {
     if (a.B == 0) return hipSuccess;
     const bool groups = a.topk_groups < a.G;
-    if (a.E % 16 == 0 && a.E <= 512 && a.K <= kMaxRowK && (!groups || 16 % a.G == 0)) {
-        const int per_lane = a.E / 16;
-        const bool aligned = ((reinterpret_cast<uintptr_t>(a.logits) | reinterpret_cast<uintptr_t>(a.bias)) & 15u) == 0;
+    // a group is whole lanes, or there are none
+    if (a.E <= 512 && a.K <= kMaxRowK && (!groups || (a.E % 16 == 0 && 16 % a.G == 0))) {
+        const int per_lane = (a.E + 15) / 16;
+        const bool aligned = a.E % 16 == 0 &&
+                              ((reinterpret_cast<uintptr_t>(a.logits) | reinterpret_cast<uintptr_t>(a.bias)) & 15u) == 0;
         if (per_lane == 16 && aligned) return launch_rows<16, true>(a, stream);
         if (per_lane == 8 && aligned) return launch_rows<8, true>(a, stream);
         if (per_lane <= 8) return launch_rows<8, false>(a, stream);

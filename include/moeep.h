@@ -385,7 +385,8 @@ moe_status_t moe_pack_weights(const void* w, int E_local, int rows, int cols, mo
  *   cap_rows rows when offsets is NULL (E_local unused), e.g. weight rows,
  *   whose scales are then one per output channel.  Other rows of q and scales
  *   are not written.
- *   q      (cap_rows, cols) int8 out; scales (cap_rows) fp32 out.
+ *   q      (cap_rows, cols) int8 out, not overlapping x; scales (cap_rows) fp32
+ *          out.
  *   scale = max |v| / 127 rounded to fp32 (at least 2^-126; 1 for a row of
  *   zeros); code = v / scale rounded to the nearest integer, ties to even,
  *   from the exact quotient.  A row with a NaN or an infinity gets scale NaN

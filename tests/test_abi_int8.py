@@ -47,7 +47,10 @@ def test_route_scored_empty_batch_is_noop():
     assert scored(logits=NONE, ids=NONE, w=NONE, B=0) == m.MOE_OK
 
 
-def quant(x=P, dt=m.MOE_BF16, rows=P, E=4, cap=8, cols=64, q=P, s=P, masked=False):
+Q = ctypes.c_void_p(1 << 20)
+
+
+def quant(x=P, dt=m.MOE_BF16, rows=P, E=4, cap=8, cols=64, q=Q, s=P, masked=False):
     fn = m.lib().moe_quant_rows_masked if masked else m.lib().moe_quant_rows
     return fn(x, dt, rows, E, cap, cols, q, s, None)
 
@@ -58,6 +61,8 @@ BAD_QUANT = [
     (dict(cols=131072), ARG, "131056"), (dict(E=0), ARG, "E_local"), (dict(E=1025), ARG, "E_local"),
     (dict(x=NONE), ARG, "null"), (dict(q=NONE), ARG, "null"), (dict(s=NONE), ARG, "null"),
     (dict(x=ODD), ARG, "16-byte"), (dict(q=ODD), ARG, "16-byte"),
+    (dict(q=P), ARG, "overlap"), (dict(q=ctypes.c_void_p(4096 + 1008)), ARG, "overlap"),
+    (dict(q=ctypes.c_void_p(4096 - 496)), ARG, "overlap"),
 ]
 
 

@@ -311,6 +311,15 @@ def test_empty_inputs_are_no_ops():
     torch.cuda.synchronize()
     assert (h == 7.0).all() and (q == 3).all()
     assert m.moe_quant_rows(z(0, 16, dt=f))[0].shape == (0, 16)
+    # a batch without tokens, and one whose tokens have no local slot
+    xd, xs = torch.full((4, 32), 5, dtype=torch.int8, device="cuda"), z(4, dt=f)
+    m.moe_dispatch(z(0, 32, dt=f), z(0, 2, dt=torch.int32), 4, "int8", xd=xd, xd_scales=xs)
+    m.moe_dispatch(z(3, 32, dt=f), z(3, 2, dt=torch.int32) - 1, 4, "int8", xd=xd, xd_scales=xs)
+    torch.cuda.synchronize()
+    assert (xd == 5).all() and (xs == 0).all()
+    y = m.moe_grouped_ffn(z(0, 32), z(0, dt=f), off, z(2, 16, 32), z(2, 16, 32), z(2, 32, 16), z(2, 16, dt=f),
+                          z(2, 16, dt=f), z(2, 32, dt=f))
+    assert y.shape == (0, 32)
 
 
 # ------------------------------------------------------------------ as they are used together
@@ -461,6 +470,24 @@ def test_micro_batches_match_the_single_batch():
         a, b = mb.forward(parts, lg.cuda(), w)
         torch.cuda.synchronize()
         assert torch.equal(torch.cat([a, b]), ref)
+
+
+def test_layer_with_a_placement_map():
+    """The scored router through a placement map: experts renumbered, weights moved
+    along, the same tokens out."""
+    cfg = LAYERS[0]
+    layer, parts, x, lg, w, _, _ = _make_layer(cfg)
+    ref = layer.forward(parts, lg.cuda(), w).clone()
+    ids = layer.topk_ids.clone()
+    perm = torch.randperm(32, generator=_gen(8)).cuda()
+    layer.expert_map = perm.to(torch.int32)
+    back = torch.argsort(perm)
+    moved = {k: v[back].contiguous() for k, v in w.items()}
+    out = layer.forward(parts, lg.cuda(), moved)
+    torch.cuda.synchronize()
+    assert torch.equal(layer.topk_ids, torch.where(ids >= 0, perm[ids.clamp(min=0).long()].to(torch.int32), -1))
+    # the same products and gates, added per token in the same slot order
+    assert torch.equal(out, ref)
 
 
 def test_two_streams_at_once():

@@ -73,6 +73,17 @@ def test_parity(B, E, K, G, keep, top, score):
     _check(lg, K, score, None, renorm=False, scale=0.5, **kw)
 
 
+@pytest.mark.parametrize("E", [2, 3, 8, 15, 17, 60, 127, 129, 250, 255, 257, 500, 511, 513])
+def test_expert_counts_without_groups(E):
+    for K in {1, min(2, E), min(12, E), min(13, E)}:
+        for score in ("sigmoid", "softmax"):
+            lg, bias = _inputs(37, E, E + K)
+            _check(lg, K, score, bias)
+            lg, bias = _inputs(37, E, E + K + 1, bf16=True, ties=True, mask=0.2)
+            _check(lg, K, score, None, renorm=False)
+            _check(lg, K, score, bias, n_groups=E, topk_groups=E, group_top=1)
+
+
 @pytest.mark.parametrize("score", ["sigmoid", "softmax"])
 def test_neighbours_that_fp32_scores_cannot_tell_apart(score):
     """Logits one fp32 step apart, on the flat parts of the score: neighbours
