@@ -23,11 +23,16 @@
 // row and column scales are asked for before it and applied in the epilogue
 // (row scales through LDS, a lane's column scales in registers).
 //
-// Measured (MI355X; DeepSeek-shaped layer, H = 7168, I = 2048, 256 experts):
-// decode gate/up, T = 128: 0.98-1.00 ms, 7.4-7.6 TB/s, 92% of the HBM peak.
-// Prefill, T = 8192: 2.08-2.18 ms, 1.8 POP/s; counters (256-row tiles) show
-// the MFMAs busy 54% of the cycles at a clock of 1.4 GHz, and versions with 10%
-// fewer cycles took the same time: the part's power holds it there.
+// Measured (MI355X, several boxes; DeepSeek-shaped layer, H = 7168, I = 2048,
+// 256 experts): decode gate/up, T = 128: 0.98-1.02 ms, 7.2-7.6 TB/s, over 90% of
+// the HBM peak; down 0.52-0.57 ms.  One token (8 experts): 45 us, 5.3 TB/s.
+// One EP=8 rank's share: 0.21-0.22 ms, 4.4-4.7 TB/s at a 2.25 GHz clock, the CUs
+// busy three quarters of the time (2.2 tiles each, of unequal sizes).  Prefill,
+// T = 8192: 2.1-2.3 ms, 1.7-1.8 POP/s; counters show the MFMAs busy 54% of the
+// cycles at a clock of 1.4 GHz, and versions with 10% fewer cycles took the same
+// time: the part's power holds it there (MFMAs alone, fed from registers, reach
+// 4.2 POP/s; the 32x32x32 form 3.6).  Four waves of 128 x 128 instead of eight
+// of 128 x 64, which read a third less LDS, spill and take 2.6 ms.
 #pragma once
 
 #include "gemm_wide.hpp"

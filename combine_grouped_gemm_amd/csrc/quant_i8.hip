@@ -18,6 +18,11 @@
 // if one of its remainders reaches half a step (a row in fifty at 2048
 // columns).  About six instructions an element, a third of the time that its
 // three bytes take at the rate of a large copy.
+//
+// Measured (MI355X, in a graph): 65536 rows of 2048 bf16 values 80 us, 5.0 TB/s
+// (a large copy: 4.9; reading each row twice 95 us); 1024 rows in 256 blocks of
+// 32 5.5 us.  Dispatch of one EP=8 rank's share, 3684 tokens of 7168: 14-15 us,
+// 4.2 TB/s (21 us with two reads); 128 tokens to 8 rows each 6.3 us (8.0).
 #include "device_common.hpp"
 #include "launch.hpp"
 
