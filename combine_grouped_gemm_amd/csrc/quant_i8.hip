@@ -303,9 +303,9 @@ hipError_t launch_quant_any(const QuantArgs& a, hipStream_t stream) {
     const int per = (a.cols / 16 + kWave - 1) / kWave, most = device_cu_count() * 8;
     dim3 grid, block(kRowWaves * kWave);
     if (a.m_counts != nullptr) {
-        // four rows a wave when a block of rows is full: decode fills few of them, and
+        // two rows a wave when a block of rows is full: decode fills few of them, and
         // workgroups with nothing to do cost more than the loop
-        const int share = (most / 2 + a.E_loc - 1) / a.E_loc, need = (a.cap_e + 4 * kRowWaves - 1) / (4 * kRowWaves);
+        const int share = (most / 2 + a.E_loc - 1) / a.E_loc, need = (a.cap_e + 2 * kRowWaves - 1) / (2 * kRowWaves);
         grid = dim3(share < need ? share : need, a.E_loc);
     } else {
         const int need = (a.cap + kRowWaves - 1) / kRowWaves;
