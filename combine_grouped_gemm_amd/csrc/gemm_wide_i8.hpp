@@ -59,7 +59,7 @@ constexpr int ROWB = 128;           // bytes per LDS row
 
 // 8 waves laid out 2 (rows) x 4 (weight rows).  A wave owns the interleaved
 // 16-row fragments {wm, wm + 2, ...} (so a short tile still spreads its valid
-// rows over both row-waves) and 64 weight rows.
+// rows over both row-waves) and BN / 4 weight rows.
 template <int BM, int BN, bool GATED, bool OUT_F32, bool NT_W>
 __global__ __launch_bounds__(512, BM + BN > 256 ? 1 : 4) void grouped_gemm_i8_wide_kernel(FfnArgs p) {
     constexpr int WMW = 2, WNW = 4, NT = 512, NW = 8;

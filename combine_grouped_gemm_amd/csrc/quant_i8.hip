@@ -22,7 +22,8 @@
 // Measured (MI355X, in a graph): 65536 rows of 2048 bf16 values 80 us, 5.0 TB/s
 // (a large copy: 4.9; reading each row twice 95 us); 1024 rows in 256 blocks of
 // 32 5.5 us.  Dispatch of one EP=8 rank's share, 3684 tokens of 7168: 14-15 us,
-// 4.2 TB/s (21 us with two reads); 128 tokens to 8 rows each 6.3 us (8.0).
+// 4.2 TB/s (21 us with two reads), 19 us from cold caches; 128 tokens to 8 rows
+// each 5.7 us (8.0).
 #include "device_common.hpp"
 #include "launch.hpp"
 
@@ -131,7 +132,7 @@ __device__ __forceinline__ uint32_t wave_max_u32(uint32_t v) {
 // token's destination rows come with one vector load per wave (lane k holds
 // slot k's row; a ballot gives the local slots), as in dispatch.hip; a token
 // without a local slot is not read.
-constexpr int kTokThreads = 256;
+constexpr int kTokThreads = 512;             // most threads per block
 
 __device__ __forceinline__ int slot_row(const int32_t* rows, int K, int k0, int cap, int lane) {
     const int k = k0 + lane;
@@ -284,8 +285,10 @@ __global__ __launch_bounds__(kRowWaves * kWave) void quant_rows_kernel(QuantArgs
 template <bool F32>
 hipError_t launch_dispatch_any(const SegTable& seg, int B, int H, const int32_t* row_of, int K, uint8_t* xd,
                                float* xd_scales, int cap, hipStream_t stream) {
-    const int np = H / 16, waves = (np + kWave - 1) / kWave;
-    const dim3 grid(B), block(kWave * (waves < kTokThreads / kWave ? waves : kTokThreads / kWave));
+    // a batch that leaves CUs with room gets wider blocks (128 tokens of 7168: 5.7 us
+    // with seven waves a token, 7.0 with four; 3684 tokens the other way: 20.6, 18.9)
+    const int np = H / 16, waves = (np + kWave - 1) / kWave, most = B < 2 * device_cu_count() ? kTokThreads / kWave : 4;
+    const dim3 grid(B), block(kWave * (waves < most ? waves : most));
     const int per = (np + (int)block.x - 1) / (int)block.x;
     if (per <= 1)
         hipLaunchKernelGGL((dispatch_i8_kernel<F32, 1>), grid, block, 0, stream, seg, H, row_of, K, cap, xd, xd_scales);

@@ -120,7 +120,9 @@ def test_quant_clamps_row_descriptions_to_the_buffer():
 @pytest.mark.parametrize("f32", [False, True])
 @pytest.mark.parametrize("segs,E,K,first,last,H", [
     ((1,), 8, 2, 0, 8, 16), ((37,), 16, 4, 4, 12, 208), ((5, 0, 60, 1), 32, 8, 0, 32, 7168), ((90,), 128, 100, 30, 99, 96),
-    ((64,), 96, 64, 0, 96, 1040), ((3,), 4, 4, 1, 2, 16400), ((2,), 4, 2, 0, 4, 33008), ((50,), 128, 128, 0, 128, 32)])
+    ((64,), 96, 64, 0, 96, 1040), ((3,), 4, 4, 1, 2, 16400), ((2,), 4, 2, 0, 4, 33008), ((50,), 128, 128, 0, 128, 32),
+    ((9, 3), 8, 2, 0, 8, 8208), ((600, 30), 16, 2, 0, 16, 64), ((650,), 16, 2, 4, 12, 2080), ((600,), 64, 3, 0, 8, 7168),
+    ((610,), 32, 2, 0, 4, 16384), ((603,), 128, 70, 0, 2, 33008)])
 def test_dispatch(segs, E, K, first, last, H, f32):
     import combine_grouped_gemm_amd as m
     print(f"[dispatch] segs={segs} E={E} K={K} local [{first}, {last}) H={H} f32={f32}", flush=True)
