@@ -452,6 +452,9 @@ def moe_quant_rows(x, rows=None, cap_per_expert=None, q=None, scales=None, strea
         if cap_per_expert is not None:
             raise ValueError("cap_per_expert needs the masked layout's m")
     else:
+        name = "offsets" if cap_per_expert is None else "m"
+        _dev(rows, name, torch.int32, 1)
+        _need(rows, name, numel=2 if cap_per_expert is None else 1)    # an empty tensor's null pointer means all rows
         E_loc = rows.numel() - 1 if cap_per_expert is None else rows.numel()
         third = _rows_arg(rows, cap_per_expert, E_loc, cap)
     if q is None:

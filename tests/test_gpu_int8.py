@@ -603,3 +603,18 @@ def test_binding_refusals():
         m.moe_dispatch(x, z(8, 2, dt=i32), 16, "int8", xd_scales=z(15, dt=f))
     with pytest.raises(ValueError, match="xd must"):
         m.moe_dispatch(x, z(8, 2, dt=i32), 16, "int8", xd=z(16, 64, dt=f))
+
+
+@pytest.mark.parametrize("rows,error,msg", [
+    ([0, 4, 8], TypeError, "offsets must be a torch.Tensor"),
+    ("cpu", ValueError, "device tensor"),
+    ("2-D", ValueError, "1 dims"),
+    ("empty", ValueError, "at least 2"),
+])
+def test_quant_rows_refuses_bad_row_descriptions(rows, error, msg):
+    import combine_grouped_gemm_amd as m
+    x = torch.zeros(8, 64, dtype=torch.bfloat16, device="cuda")
+    rows = {"cpu": torch.zeros(3, dtype=torch.int32), "2-D": torch.zeros(1, 3, dtype=torch.int32, device="cuda"),
+            "empty": torch.zeros(0, dtype=torch.int32, device="cuda")}.get(rows, rows) if isinstance(rows, str) else rows
+    with pytest.raises(error, match=msg):
+        m.moe_quant_rows(x, rows)
