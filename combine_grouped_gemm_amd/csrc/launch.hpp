@@ -14,6 +14,10 @@ namespace moeep {
 hipError_t launch_route(const float* logits, int B, int E, int K, int32_t* ids, float* w,
                         const int32_t* map, int n_shared, hipStream_t stream);
 
+// Tokens of one launch of a kernel with up to 512 threads a token: a grid of 2^32
+// threads or more is cut short without an error, so longer batches take several.
+constexpr int kMostTokens = 1 << 22;
+
 // route_scored.hip
 struct RouteScoredArgs {
     const void* logits;       // (B, E) fp32 or bf16

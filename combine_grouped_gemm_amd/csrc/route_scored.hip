@@ -538,10 +538,7 @@ hipError_t launch_rows(const RouteScoredArgs& a, hipStream_t stream) {
     return hipGetLastError();
 }
 
-}  // namespace
-
-hipError_t launch_route_scored(const RouteScoredArgs& a, hipStream_t stream) {
-    if (a.B == 0) return hipSuccess;
+hipError_t launch_tokens(const RouteScoredArgs& a, hipStream_t stream) {
     const bool groups = a.topk_groups < a.G;
     // a group is whole lanes, or there are none
     if (a.E <= 512 && a.K <= kMaxRowK && (!groups || (a.E % 16 == 0 && 16 % a.G == 0))) {
@@ -556,6 +553,22 @@ hipError_t launch_route_scored(const RouteScoredArgs& a, hipStream_t stream) {
     }
     hipLaunchKernelGGL(route_scored_exact_kernel, dim3(a.B), dim3(kWave), exact_lds(a.E, a.G, a.K), stream, a);
     return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_route_scored(const RouteScoredArgs& a, hipStream_t stream) {
+    const int ld = a.K + a.n_shared;
+    for (long long b0 = 0; b0 < a.B; b0 += kMostTokens) {
+        RouteScoredArgs part = a;
+        part.B = a.B - b0 < kMostTokens ? (int)(a.B - b0) : kMostTokens;
+        part.logits = static_cast<const char*>(a.logits) + b0 * a.E * (a.bf16 ? 2 : 4);
+        part.ids = a.ids + b0 * ld;
+        part.w = a.w + b0 * ld;
+        const hipError_t e = launch_tokens(part, stream);
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
 }
 
 }  // namespace moeep

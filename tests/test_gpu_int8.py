@@ -618,3 +618,17 @@ def test_quant_rows_refuses_bad_row_descriptions(rows, error, msg):
             "empty": torch.zeros(0, dtype=torch.int32, device="cuda")}.get(rows, rows) if isinstance(rows, str) else rows
     with pytest.raises(error, match=msg):
         m.moe_quant_rows(x, rows)
+
+
+def test_dispatch_of_more_tokens_than_one_launch_takes():
+    """64 threads a token: as one grid the batch has 2^32 threads; its segments meet inside
+    a launch's share of it."""
+    import combine_grouped_gemm_amd as m
+    B, H = 2**26 + 128, 16
+    few = torch.randn(64, H, generator=torch.Generator().manual_seed(3)).to(torch.bfloat16).cuda()
+    x = few.repeat(B // 64, 1)
+    cut = 2**22 + 5
+    rows = torch.arange(B - 1, -1, -1, dtype=torch.int32, device="cuda").view(B, 1)
+    q, s = m.moe_dispatch([x[:cut], x[cut:]], rows, B, "int8")
+    wq, ws = m.moe_quant_rows(few)
+    assert bool((q.view(-1, 64, H) == wq.flip(0)).all()) and bool((s.view(-1, 64) == ws.flip(0)).all())

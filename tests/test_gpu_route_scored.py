@@ -287,3 +287,14 @@ def test_binding_refusals():
                     (dict(group_top=3), "group_top"), (dict(n_groups=8, topk_groups=1, group_top=1, K=3), "exceeds")):
         with pytest.raises(m.MoeError, match=msg):
             m.moe_route_scored(lg, kw.pop("K", 2), **kw)
+
+
+@pytest.mark.parametrize("B,E,K", [(2**28 + 64, 1, 1), (2**26 + 192, 16, 13)])
+def test_batches_of_more_tokens_than_one_launch_takes(B, E, K):
+    """16 and 64 threads a token: as one grid either batch has 2^32 threads or more."""
+    import combine_grouped_gemm_amd as m
+    few = _inputs(64, E, 5, bf16=True)[0].cuda()
+    ids, w = m.moe_route_scored(few.repeat(B // 64, 1), K)
+    first = m.moe_route_scored(few, K)
+    assert bool((ids.view(-1, 64, K) == first[0]).all()) and bool((w.view(-1, 64, K) == first[1]).all())
+    _check(few.cpu(), K, "sigmoid")
