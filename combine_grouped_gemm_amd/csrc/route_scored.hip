@@ -18,9 +18,10 @@
 // neighbours closer than fp32 sigmoids can tell apart.  Few tokens need all of
 // that, though, so the common kernel narrows in fp32 and settles in fp64:
 //
-//   A token is 16 lanes (a DPP row), four tokens a wave; a lane holds E / 16
-//   (rounded up) consecutive experts as 32-bit keys (the score's leading bits,
-//   then the place in the lane), sorted once in registers.  Groups are ranked by
+//   A token is 16 lanes (a DPP row), four tokens a wave, and a group 16 / G of
+//   them; a lane holds its share (rounded up) of the group's experts as 32-bit
+//   keys (the score's leading bits, then the place in the lane), sorted once in
+//   registers.  Groups are ranked by
 //   DPP; K + 4 rounds of "row maximum, its owner shifts its list" give the
 //   candidates, one to a lane.  Every candidate's score is then computed in 64
 //   bits, one lane each, and ranked exactly, and its gate comes from that.
@@ -29,7 +30,7 @@
 //   and if the groups' cut is wider than that error; NaN and huge scores never
 //   do.  Otherwise the wave does that token again in 64 bits from the start.
 //
-// Other shapes (E > 512, K > 12, groups that are no whole lanes) go through that
+// Other shapes (E > 512, K > 12, a G that does not divide 16) go through that
 // 64-bit routine, one wave a token, keys in LDS.
 //
 // Measured (MI355X, in a graph): one token of 256 experts, 8 groups, 5.2 us;
@@ -283,8 +284,8 @@ __device__ __forceinline__ int groups_ahead(T score, int lanes, int l16) {
     return n;
 }
 
-// EPL: registers for a lane's experts, at least E / 16 rounded up.  VEC: exactly E / 16,
-// and rows and biases can be read in 16-byte pieces.
+// EPL: registers for a lane's experts, at least its share.  VEC: exactly E / 16, and
+// rows and biases can be read in 16-byte pieces.
 template <int EPL, bool VEC, bool SIGMOID, bool BF16>
 __global__ __launch_bounds__(kRowWaves * kWave) void route_scored_kernel(RouteScoredArgs p) {
     extern __shared__ uint64_t smem[];
@@ -295,8 +296,16 @@ __global__ __launch_bounds__(kRowWaves * kWave) void route_scored_kernel(RouteSc
     const int t = (blockIdx.x * kRowWaves + wave) * 4 + row;
     const bool live = t < p.B;
     const size_t base = (size_t)(live ? t : p.B - 1) * p.E;       // idle rows repeat the last token
-    const int chunk = VEC ? EPL : (p.E + 15) / 16;
-    const int e0 = l16 * chunk;
+    const bool grouped = p.topk_groups < p.G;
+    const int log_g = grouped ? __builtin_ctz(p.G) : 0;           // without groups the row is one
+    const int lanes = 16 >> log_g, size = p.E >> log_g;           // of a group
+    const int chunk = VEC ? EPL : (size + lanes - 1) / lanes;
+    // the first expert of a lane; lanes behind a group's last expert have none
+    auto first_expert = [&](int l) {
+        return VEC ? l * EPL : (l >> (4 - log_g)) * size + (l & (lanes - 1)) * chunk;
+    };
+    const int e0 = first_expert(l16);
+    const int mine = VEC ? EPL : min(chunk, size - (l16 & (lanes - 1)) * chunk);
 
     // ---- logits and biases of this lane's experts
     float lg[EPL], bs[EPL];
@@ -319,7 +328,7 @@ __global__ __launch_bounds__(kRowWaves * kWave) void route_scored_kernel(RouteSc
         }
     } else {
 #pragma unroll
-        for (int j = 0; j < EPL; ++j) lg[j] = j < chunk && e0 + j < p.E ? load_logit(p.logits, BF16, base + e0 + j) : -INFINITY;
+        for (int j = 0; j < EPL; ++j) lg[j] = j < mine ? load_logit(p.logits, BF16, base + e0 + j) : -INFINITY;
     }
     if (p.bias != nullptr) {
         if constexpr (VEC) {
@@ -331,7 +340,7 @@ __global__ __launch_bounds__(kRowWaves * kWave) void route_scored_kernel(RouteSc
             }
         } else {
 #pragma unroll
-            for (int j = 0; j < EPL; ++j) bs[j] = j < chunk && e0 + j < p.E ? p.bias[e0 + j] : 0.0f;
+            for (int j = 0; j < EPL; ++j) bs[j] = j < mine ? p.bias[e0 + j] : 0.0f;
         }
     } else {
 #pragma unroll
@@ -409,10 +418,9 @@ __global__ __launch_bounds__(kRowWaves * kWave) void route_scored_kernel(RouteSc
         return (double)up + (double)fabsf(up) * rel + abs_err;
     };
 
-    // ---- groups: 16 / G lanes each
+    // ---- groups
     bool ok = true;
-    if (p.topk_groups < p.G) {
-        const int lanes = 16 / p.G;
+    if (grouped) {
         auto join = [&](float o1, float o2) {
             c2 = fmaxf(fminf(c1, o1), fmaxf(c2, o2));
             c1 = fmaxf(c1, o1);
@@ -423,12 +431,12 @@ __global__ __launch_bounds__(kRowWaves * kWave) void route_scored_kernel(RouteSc
         const float second = (p.group_top == 2) & (c2 != -INFINITY) ? c2 : 0.0f;
         const float score = c1 + second;
         // of the two terms, which may cancel
-        const float size = c1 != -INFINITY ? fabsf(c1) + fabsf(second) : 0.0f;
+        const float terms = c1 != -INFINITY ? fabsf(c1) + fabsf(second) : 0.0f;
         bool kept = groups_ahead(score, lanes, l16) < p.topk_groups;
         // the cut between the last group kept and the first one dropped
         const float least = -row_max(kept & (c1 != -INFINITY) ? -score : -INFINITY);
         const float most = row_max(kept ? -INFINITY : score);
-        const float slack = 2.0f * (row_max(size) * rel + 2.0f * abs_err);
+        const float slack = 2.0f * (row_max(terms) * rel + 2.0f * abs_err);
         ok = (most == -INFINITY) | (least - most > slack);
         if (ballot64(!ok) != 0) {
             // too near to tell (a token in five thousand; one in an 8192-token batch
@@ -471,12 +479,12 @@ __global__ __launch_bounds__(kRowWaves * kWave) void route_scored_kernel(RouteSc
         // the owner's list moves up by one: a bit select by a mask whose origin the
         // compiler does not see (it made a register index of the plain choice,
         // fifty instructions a place)
-        uint32_t mine = l16 == first ? 0xffffffffu : 0u;
-        asm("" : "+v"(mine));
-        if ((l16 == i) & (last != 0)) ce = first * chunk + (int)(kPlace - (last & kPlace));
+        uint32_t up = l16 == first ? 0xffffffffu : 0u;
+        asm("" : "+v"(up));
+        if ((l16 == i) & (last != 0)) ce = first_expert(first) + (int)(kPlace - (last & kPlace));
 #pragma unroll
-        for (int j = 0; j + 1 < EPL; ++j) key[j] = (key[j + 1] & mine) | (key[j] & ~mine);
-        key[EPL - 1] &= ~mine;
+        for (int j = 0; j + 1 < EPL; ++j) key[j] = (key[j + 1] & up) | (key[j] & ~up);
+        key[EPL - 1] &= ~up;
     }
 
     // ---- their exact scores and ranks
@@ -539,10 +547,11 @@ hipError_t launch_rows(const RouteScoredArgs& a, hipStream_t stream) {
 }
 
 hipError_t launch_tokens(const RouteScoredArgs& a, hipStream_t stream) {
-    const bool groups = a.topk_groups < a.G;
-    // a group is whole lanes, or there are none
-    if (a.E <= 512 && a.K <= kMaxRowK && (!groups || (a.E % 16 == 0 && 16 % a.G == 0))) {
-        const int per_lane = (a.E + 15) / 16;
+    // a group is a whole number of a row's 16 lanes, or there are none
+    const bool grouped = a.topk_groups < a.G;
+    if (a.E <= 512 && a.K <= kMaxRowK && (!grouped || 16 % a.G == 0)) {
+        const int lanes = grouped ? 16 / a.G : 16, size = grouped ? a.E / a.G : a.E;
+        const int per_lane = (size + lanes - 1) / lanes;
         const bool aligned = a.E % 16 == 0 &&
                               ((reinterpret_cast<uintptr_t>(a.logits) | reinterpret_cast<uintptr_t>(a.bias)) & 15u) == 0;
         if (per_lane == 16 && aligned) return launch_rows<16, true>(a, stream);

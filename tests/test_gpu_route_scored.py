@@ -298,3 +298,20 @@ def test_batches_of_more_tokens_than_one_launch_takes(B, E, K):
     first = m.moe_route_scored(few, K)
     assert bool((ids.view(-1, 64, K) == first[0]).all()) and bool((w.view(-1, 64, K) == first[1]).all())
     _check(few.cpu(), K, "sigmoid")
+
+
+@pytest.mark.parametrize("E,G,keep", [(60, 4, 2), (60, 2, 1), (8, 8, 3), (8, 4, 2), (8, 2, 1), (2, 2, 1), (72, 8, 5), (24, 8, 7),
+                                       (500, 4, 3), (504, 8, 2), (510, 2, 1), (130, 2, 1), (36, 4, 1), (40, 8, 1)])
+def test_groups_that_do_not_fill_their_lanes(E, G, keep):
+    """Lanes behind a group's last expert hold nothing; a group may be smaller than its lanes."""
+    test_candidate_counts_and_groups(E, G, keep)
+    S = E // G
+    for seed, score in ((1, "sigmoid"), (2, "softmax")):
+        for B in (1, 63):
+            lg, bias = _inputs(B, E, seed, mask=0.4, bf16=B == 1)
+            bias[::4] = -float("inf")
+            for top in (1, 2):
+                _check(lg, min(8, keep * S), score, bias, n_groups=G, topk_groups=keep, group_top=top)
+                _check(lg, min(8, keep * S), score, None, n_groups=G, topk_groups=keep, group_top=top, renorm=False)
+    if S >= 2:
+        test_groups_that_fp32_cannot_tell_apart(E, G, keep, min(3, S - 2))
