@@ -36,8 +36,9 @@
 // Measured (MI355X, in a graph): one token of 256 experts, 8 groups, 5.2 us;
 // 8192 of them 7.6-8.8 us (bound by the VALU: some 1800 instructions a wave, two
 // waves a SIMD; reading the logits would take 2 us); 4093 tokens of 128 experts,
-// softmax, bf16, 4.0 us.  The 64-bit routine alone: 14.7 and 36.5 us on the first
-// two.
+// softmax, bf16, 4.0-4.4 us; 8192 of 512 13.8 us (24.0 with logits read one by
+// one), of 384, softmax, 15.0 (21.5), of 60 in 4 groups 6.4 (14 by the 64-bit
+// routine).  That routine alone: 14.7 and 36.5 us on the first two.
 #include "device_common.hpp"
 #include "launch.hpp"
 
@@ -284,9 +285,11 @@ __device__ __forceinline__ int groups_ahead(T score, int lanes, int l16) {
     return n;
 }
 
-// EPL: registers for a lane's experts, at least its share.  VEC: exactly E / 16, and
-// rows and biases can be read in 16-byte pieces.
-template <int EPL, bool VEC, bool SIGMOID, bool BF16>
+// How a lane reads its share of the experts, EPL at most: one by one, in 16-byte
+// pieces, or in pieces that fill all EPL registers.
+enum Reads { kSingly, kPieces, kWhole };
+
+template <int EPL, Reads READS, bool SIGMOID, bool BF16>
 __global__ __launch_bounds__(kRowWaves * kWave) void route_scored_kernel(RouteScoredArgs p) {
     extern __shared__ uint64_t smem[];
     static_assert((EPL & (EPL - 1)) == 0 && EPL >= 4, "bitonic sort");
@@ -299,22 +302,23 @@ __global__ __launch_bounds__(kRowWaves * kWave) void route_scored_kernel(RouteSc
     const bool grouped = p.topk_groups < p.G;
     const int log_g = grouped ? __builtin_ctz(p.G) : 0;           // without groups the row is one
     const int lanes = 16 >> log_g, size = p.E >> log_g;           // of a group
-    const int chunk = VEC ? EPL : (size + lanes - 1) / lanes;
+    const int chunk = READS == kWhole ? EPL : (size + lanes - 1) / lanes;
     // the first expert of a lane; lanes behind a group's last expert have none
     auto first_expert = [&](int l) {
-        return VEC ? l * EPL : (l >> (4 - log_g)) * size + (l & (lanes - 1)) * chunk;
+        return READS != kSingly ? l * chunk : (l >> (4 - log_g)) * size + (l & (lanes - 1)) * chunk;
     };
     const int e0 = first_expert(l16);
-    const int mine = VEC ? EPL : min(chunk, size - (l16 & (lanes - 1)) * chunk);
+    const int mine = READS != kSingly ? chunk : min(chunk, size - (l16 & (lanes - 1)) * chunk);
 
     // ---- logits and biases of this lane's experts
     float lg[EPL], bs[EPL];
-    if constexpr (VEC) {
+    if constexpr (READS != kSingly) {
         if constexpr (BF16) {
             const uint16_t* src = static_cast<const uint16_t*>(p.logits) + base + e0;
 #pragma unroll
             for (int j = 0; j < EPL; j += 8) {
-                const uint4 v = *reinterpret_cast<const uint4*>(src + j);
+                uint4 v = make_uint4(0xff80ff80u, 0xff80ff80u, 0xff80ff80u, 0xff80ff80u);
+                if (READS == kWhole || j < chunk) v = *reinterpret_cast<const uint4*>(src + j);
                 lg[j] = bf16_lo(v.x); lg[j + 1] = bf16_hi(v.x); lg[j + 2] = bf16_lo(v.y); lg[j + 3] = bf16_hi(v.y);
                 lg[j + 4] = bf16_lo(v.z); lg[j + 5] = bf16_hi(v.z); lg[j + 6] = bf16_lo(v.w); lg[j + 7] = bf16_hi(v.w);
             }
@@ -322,7 +326,8 @@ __global__ __launch_bounds__(kRowWaves * kWave) void route_scored_kernel(RouteSc
             const float4* src = reinterpret_cast<const float4*>(static_cast<const float*>(p.logits) + base + e0);
 #pragma unroll
             for (int j = 0; j < EPL; j += 4) {
-                const float4 v = src[j / 4];
+                float4 v = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+                if (READS == kWhole || j < chunk) v = src[j / 4];
                 lg[j] = v.x; lg[j + 1] = v.y; lg[j + 2] = v.z; lg[j + 3] = v.w;
             }
         }
@@ -331,11 +336,12 @@ __global__ __launch_bounds__(kRowWaves * kWave) void route_scored_kernel(RouteSc
         for (int j = 0; j < EPL; ++j) lg[j] = j < mine ? load_logit(p.logits, BF16, base + e0 + j) : -INFINITY;
     }
     if (p.bias != nullptr) {
-        if constexpr (VEC) {
+        if constexpr (READS != kSingly) {
             const float4* src = reinterpret_cast<const float4*>(p.bias + e0);
 #pragma unroll
             for (int j = 0; j < EPL; j += 4) {
-                const float4 v = src[j / 4];
+                float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                if (READS == kWhole || j < chunk) v = src[j / 4];
                 bs[j] = v.x; bs[j + 1] = v.y; bs[j + 2] = v.z; bs[j + 3] = v.w;
             }
         } else {
@@ -534,15 +540,15 @@ __global__ __launch_bounds__(kRowWaves * kWave) void route_scored_kernel(RouteSc
     }
 }
 
-template <int EPL, bool VEC>
+template <int EPL, Reads READS>
 hipError_t launch_rows(const RouteScoredArgs& a, hipStream_t stream) {
     const int per_block = kRowWaves * 4;
     const dim3 grid((a.B + per_block - 1) / per_block), block(kRowWaves * kWave);
     const size_t lds = kRowWaves * exact_lds(a.E, a.G, a.K);
-    if (a.sigmoid && a.bf16) hipLaunchKernelGGL((route_scored_kernel<EPL, VEC, true, true>), grid, block, lds, stream, a);
-    else if (a.sigmoid) hipLaunchKernelGGL((route_scored_kernel<EPL, VEC, true, false>), grid, block, lds, stream, a);
-    else if (a.bf16) hipLaunchKernelGGL((route_scored_kernel<EPL, VEC, false, true>), grid, block, lds, stream, a);
-    else hipLaunchKernelGGL((route_scored_kernel<EPL, VEC, false, false>), grid, block, lds, stream, a);
+    if (a.sigmoid && a.bf16) hipLaunchKernelGGL((route_scored_kernel<EPL, READS, true, true>), grid, block, lds, stream, a);
+    else if (a.sigmoid) hipLaunchKernelGGL((route_scored_kernel<EPL, READS, true, false>), grid, block, lds, stream, a);
+    else if (a.bf16) hipLaunchKernelGGL((route_scored_kernel<EPL, READS, false, true>), grid, block, lds, stream, a);
+    else hipLaunchKernelGGL((route_scored_kernel<EPL, READS, false, false>), grid, block, lds, stream, a);
     return hipGetLastError();
 }
 
@@ -552,13 +558,14 @@ hipError_t launch_tokens(const RouteScoredArgs& a, hipStream_t stream) {
     if (a.E <= 512 && a.K <= kMaxRowK && (!grouped || 16 % a.G == 0)) {
         const int lanes = grouped ? 16 / a.G : 16, size = grouped ? a.E / a.G : a.E;
         const int per_lane = (size + lanes - 1) / lanes;
-        const bool aligned = a.E % 16 == 0 &&
-                              ((reinterpret_cast<uintptr_t>(a.logits) | reinterpret_cast<uintptr_t>(a.bias)) & 15u) == 0;
-        if (per_lane == 16 && aligned) return launch_rows<16, true>(a, stream);
-        if (per_lane == 8 && aligned) return launch_rows<8, true>(a, stream);
-        if (per_lane <= 8) return launch_rows<8, false>(a, stream);
-        if (per_lane <= 16) return launch_rows<16, false>(a, stream);
-        return launch_rows<32, false>(a, stream);
+        // E a multiple of 16: every lane has the same number of experts
+        const bool pieces = a.E % 16 == 0 && per_lane % (a.bf16 ? 8 : 4) == 0 &&
+                            ((reinterpret_cast<uintptr_t>(a.logits) | reinterpret_cast<uintptr_t>(a.bias)) & 15u) == 0;
+        if (per_lane == 8 && pieces) return launch_rows<8, kWhole>(a, stream);
+        if (per_lane == 16 && pieces) return launch_rows<16, kWhole>(a, stream);
+        if (per_lane <= 8) return launch_rows<8, kSingly>(a, stream);
+        if (per_lane <= 16) return launch_rows<16, kSingly>(a, stream);
+        return pieces ? launch_rows<32, kPieces>(a, stream) : launch_rows<32, kSingly>(a, stream);
     }
     hipLaunchKernelGGL(route_scored_exact_kernel, dim3(a.B), dim3(kWave), exact_lds(a.E, a.G, a.K), stream, a);
     return hipGetLastError();

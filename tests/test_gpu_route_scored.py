@@ -315,3 +315,19 @@ def test_groups_that_do_not_fill_their_lanes(E, G, keep):
                 _check(lg, min(8, keep * S), score, None, n_groups=G, topk_groups=keep, group_top=top, renorm=False)
     if S >= 2:
         test_groups_that_fp32_cannot_tell_apart(E, G, keep, min(3, S - 2))
+
+
+@pytest.mark.parametrize("E", [64, 192, 320, 384, 512])
+def test_misaligned_rows_of_other_lane_shares(E):
+    import combine_grouped_gemm_amd as m
+    for dt in (torch.float32, torch.bfloat16):
+        lg, bias = _inputs(35, E, 8, bf16=dt == torch.bfloat16, mask=0.1)
+        x = torch.empty(35 * E + 1, dtype=dt, device="cuda")[1:].view(35, E)
+        x.copy_(lg)
+        b = torch.empty(E + 3, device="cuda")[3:]
+        b.copy_(bias)
+        rid, rw = oracle.route_scored(lg.double().numpy(), 8, "softmax", bias.double().numpy(), 4, 2)
+        for xx, bb in ((x, b), (lg.cuda(), b), (x, bias.cuda()), (lg.cuda(), bias.cuda())):
+            ids, w = m.moe_route_scored(xx, 8, score="softmax", bias=bb, n_groups=4, topk_groups=2)
+            np.testing.assert_array_equal(ids.cpu().numpy(), rid)
+            np.testing.assert_allclose(w.cpu().numpy(), rw, rtol=RTOL, atol=2.0**-150)
