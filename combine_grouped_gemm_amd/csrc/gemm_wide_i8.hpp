@@ -6,16 +6,16 @@
 // g and u of a column in one wave).  A row's step of the contraction is 128
 // codes, one cache line; v_mfma_i32_16x16x64_i8 takes 16 bytes per lane of
 // each operand.  Operands go from global memory straight into LDS through
-// bounded buffer resources, in two stages; the 16-byte chunks of an LDS row
-// are XOR-swizzled by (row & 7), so the rows of one MFMA operand read fall
-// into distinct banks; a tile runs one of FM + 1 copies of the k-loop by its
-// count of valid row fragments (as gemm_wide.hpp does, with which it shares
-// the load and wait helpers).
+// bounded buffer resources, in S stages (two; three where two workgroups of
+// them fit a CU); the 16-byte chunks of an LDS row are XOR-swizzled by (row &
+// 7), so the rows of one MFMA operand read fall into distinct banks; a tile
+// runs one of FM + 1 copies of the k-loop by its count of valid row fragments
+// (as gemm_wide.hpp does, with which it shares the load and wait helpers).
 //
 // Where it differs is what is in flight.  The second k-half's fragments are
 // read under the first half's MFMAs, so that half-way through step k every
 // wave holds all it needs of the stage, rows and weights alike, and step
-// k + 2's loads go into it: one and a half steps ahead for both operands.
+// k + S's loads go into it: S - 1/2 steps ahead for both operands.
 // With the weights ahead but the rows only one step (the bf16 scheme) every
 // step waited for its rows' first touch of the XCD's L2.
 //
@@ -60,8 +60,8 @@ constexpr int ROWB = 128;           // bytes per LDS row
 
 // 8 waves laid out 2 (rows) x 4 (weight rows).  A wave owns the interleaved
 // 16-row fragments {wm, wm + 2, ...} (so a short tile still spreads its valid
-// rows over both row-waves) and BN / 4 weight rows.
-template <int BM, int BN, bool GATED, bool OUT_F32, bool NT_W>
+// rows over both row-waves) and BN / 4 weight rows.  S: stages, 2 or 3.
+template <int BM, int BN, int S, bool GATED, bool OUT_F32, bool NT_W>
 __global__ __launch_bounds__(512, BM + BN > 256 ? 1 : 4) void grouped_gemm_i8_wide_kernel(FfnArgs p) {
     constexpr int WMW = 2, WNW = 4, NT = 512, NW = 8;
     constexpr int A_BLOCKS = BM * CPR / 64;          // 1 KiB blocks of a row stage
@@ -71,7 +71,7 @@ __global__ __launch_bounds__(512, BM + BN > 256 ? 1 : 4) void grouped_gemm_i8_wi
     constexpr int WN = BN / WNW;                     // weight rows per wave
     constexpr int FN = WN / 16;                      // 16-row weight fragments per wave
     constexpr int BNO = GATED ? BN / 2 : BN;         // output columns per tile
-    static_assert(BM % 32 == 0 && BLOCKS % NW == 0 && (!GATED || FN % 2 == 0), "tile shape");
+    static_assert((S == 2 || S == 3) && BM % 32 == 0 && BLOCKS % NW == 0 && (!GATED || FN % 2 == 0), "tile shape");
     constexpr int A_ITERS = A_BLOCKS / NW;           // i < A_ITERS: row blocks
     constexpr int RPL = NW * 8;                      // operand rows that one load of every wave covers
     constexpr int G_ITERS = BN / 2 / RPL;            // next G_ITERS: the gate half
@@ -83,6 +83,8 @@ __global__ __launch_bounds__(512, BM + BN > 256 ? 1 : 4) void grouped_gemm_i8_wi
     __shared__ uint4 sb0[BN * CPR];
     __shared__ uint4 sa1[BM * CPR];
     __shared__ uint4 sb1[BN * CPR];
+    __shared__ uint4 sa2[S > 2 ? BM * CPR : 1];
+    __shared__ uint4 sb2[S > 2 ? BN * CPR : 1];
     __shared__ int s_pre[kMaxExperts + 1];
     __shared__ uint16_t s_ord[kMaxExperts];          // experts, most rows first
     static_assert(sizeof(sa0) >= kMaxExperts * sizeof(int), "row counts fit in the first row stage");
@@ -92,11 +94,13 @@ __global__ __launch_bounds__(512, BM + BN > 256 ? 1 : 4) void grouped_gemm_i8_wi
 
     auto a_base = [&](auto I) -> char* {
         if constexpr (decltype(I)::value == 0) return reinterpret_cast<char*>(sa0);
-        else return reinterpret_cast<char*>(sa1);
+        else if constexpr (decltype(I)::value == 1) return reinterpret_cast<char*>(sa1);
+        else return reinterpret_cast<char*>(sa2);
     };
     auto b_base = [&](auto I) -> char* {
         if constexpr (decltype(I)::value == 0) return reinterpret_cast<char*>(sb0);
-        else return reinterpret_cast<char*>(sb1);
+        else if constexpr (decltype(I)::value == 1) return reinterpret_cast<char*>(sb1);
+        else return reinterpret_cast<char*>(sb2);
     };
 
     const int tid = threadIdx.x, lane = tid % kWave;
@@ -216,17 +220,18 @@ __global__ __launch_bounds__(512, BM + BN > 256 ? 1 : 4) void grouped_gemm_i8_wi
             col_s[f] = col < N ? s[(size_t)j * N + col] : 0.0f;
         }
 
-        // the previous tile's reads of both stages must be complete before new loads land
+        // the previous tile's reads of the stages must be complete before new loads land
         wait_lgkm0();
         block_barrier();
+        // steps 0 .. S - 1 (nothing read for a step that does not exist)
+        auto fill = [&](auto I) {
+            const bool exists = __builtin_amdgcn_readfirstlane(decltype(I)::value < nk ? 1 : 0) != 0;
 #pragma unroll
-        for (int i = 0; i < LPS; ++i) issue_one(ic<0>{}, i, 0, true);
-        {
-            // and step 1 (nothing read when there is no step 1)
-            const bool l1 = __builtin_amdgcn_readfirstlane(nk > 1 ? 1 : 0) != 0;
-#pragma unroll
-            for (int i = 0; i < LPS; ++i) issue_one(ic<1>{}, i, 1, l1);
-        }
+            for (int i = 0; i < LPS; ++i) issue_one(I, i, decltype(I)::value, exists);
+        };
+        fill(ic<0>{});
+        fill(ic<1>{});
+        if constexpr (S > 2) fill(ic<2>{});
 
         // The tile for NF valid fragments: no branch inside a step.
         // v_mfma_i32_16x16x64_i8: lane l feeds row (l % 16) with k-chunk (l / 16)
@@ -242,7 +247,7 @@ __global__ __launch_bounds__(512, BM + BN > 256 ? 1 : 4) void grouped_gemm_i8_wi
 
             // Step k out of stage I.  The second k-half's fragments are read under
             // the first half's MFMAs; once every wave holds them the stage is
-            // free, rows and weights alike, and step k + 2's loads go into it
+            // free, rows and weights alike, and step k + S's loads go into it
             // between the second half's MFMA groups (loads past the last step
             // read nothing but count).
             auto compute = [&](auto I, int k, bool live) {
@@ -282,37 +287,42 @@ __global__ __launch_bounds__(512, BM + BN > 256 ? 1 : 4) void grouped_gemm_i8_wi
                     for (int f = 0; f < FN; ++f)
                         acc[i][f] = __builtin_amdgcn_mfma_i32_16x16x64_i8(af[1][i], bf[1][f], acc[i][f], 0, 0, 0);
 #pragma unroll
-                    for (int q = i * LPS / NG; q < (i + 1) * LPS / NG; ++q) issue_one(I, q, k + 2, live);
+                    for (int q = i * LPS / NG; q < (i + 1) * LPS / NG; ++q) issue_one(I, q, k + S, live);
                     __builtin_amdgcn_sched_barrier(0);
                 }
                 if (NF == 0) {
 #pragma unroll
-                    for (int q = 0; q < LPS; ++q) issue_one(I, q, k + 2, live);
+                    for (int q = 0; q < LPS; ++q) issue_one(I, q, k + S, live);
                 }
             };
 
-            // step k: wait for stage k (stage k + 1 stays in flight)
+            // step k: wait for its stage (the S - 1 later ones stay in flight)
             auto step = [&](auto I, int k) {
-                wait_vmcnt<LPS>();
+                wait_vmcnt<(S - 1) * LPS>();
                 block_barrier();
                 // wave-uniform by construction; say so, so that the resource
                 // select below stays scalar
-                const bool live = __builtin_amdgcn_readfirstlane(k + 2 < nk ? 1 : 0) != 0;
+                const bool live = __builtin_amdgcn_readfirstlane(k + S < nk ? 1 : 0) != 0;
                 compute(I, k, live);
             };
-            // two steps a turn without a branch between them: with one, the compiler
-            // no longer knew which loads were in flight at the top of the loop and
-            // waited for all of them there
-            for (int k = 0; k + 1 < nk; k += 2) {
+            // S steps a turn without a branch between them: with one, the compiler no
+            // longer knew which loads were in flight at the top of the loop and waited
+            // for all of them there
+            int k = 0;
+            for (; k + S - 1 < nk; k += S) {
                 step(ic<0>{}, k);
                 step(ic<1>{}, k + 1);
+                if constexpr (S > 2) step(ic<2>{}, k + 2);
             }
-            if (nk & 1) step(ic<0>{}, nk - 1);
+            if (k < nk) step(ic<0>{}, k);
+            if constexpr (S > 2) {
+                if (k + 1 < nk) step(ic<1>{}, k + 1);
+            }
             // the loads issued by the last step read nothing but still count
             wait_vmcnt<0>();
 
             // ---- epilogue: every wave stages its outputs in a private LDS region
-            // (both stages are free once every wave is past the k-loop) and
+            // (the stages are free once every wave is past the k-loop) and
             // stores whole 16-byte row chunks.  PF fragments per pass; staged
             // rows are padded by 16 bytes so that the four row groups of one LDS
             // write fall into different banks.
