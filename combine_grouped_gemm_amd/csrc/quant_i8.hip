@@ -21,7 +21,7 @@
 //
 // Measured (MI355X, in a graph): 65536 rows of 2048 bf16 values 80 us, 5.0 TB/s
 // (a large copy: 4.9; reading each row twice 95 us); 1024 rows in 256 blocks of
-// 32 5.5 us.  Dispatch of one EP=8 rank's share, 3684 tokens of 7168: 14-15 us,
+// 32, from cold caches, 6.1 us.  Dispatch of one EP=8 rank's share, 3684 tokens of 7168: 14-15 us,
 // 4.2 TB/s (21 us with two reads), 19 us from cold caches; 128 tokens to 8 rows
 // each 5.7 us (8.0).
 #include "device_common.hpp"
@@ -219,15 +219,24 @@ __global__ __launch_bounds__(kTokThreads) void dispatch_i8_kernel(
     }
 }
 
-// ---- expert-ordered rows: one wave per row, NP pieces a lane (0: any number,
-// read twice).  Valid rows are [offsets[0], offsets[E_loc]) of the contiguous
-// layout or all rows: a persistent grid walks them.  In the masked layout
-// (the first m[j] rows of each block of cap_e) blockIdx.y is the expert, and
-// its blocks share its rows.
+// ---- expert-ordered rows.  Valid rows are [offsets[0], offsets[E_loc]) of the
+// contiguous layout or all rows: a persistent grid walks them.  In the masked
+// layout (the first m[j] rows of each block of cap_e) blockIdx.y is the expert,
+// and its blocks share its rows.  A row goes to a wave or to a block of four,
+// whichever hides the row's latency better: short rows (up to 1024 columns) to a
+// wave, long ones (over 4096) to a block, those between to a block while there
+// are few of them (`few`, of the layout or of the expert; the device knows how
+// many there are).  Measured, us, wave against block, 256 / 4096 / 16384 rows of
+// bf16: 1024 columns 3.4 / 5.4 / 12.7, 3.3 / 8.6 / 27.3; 2048 5.3 / 9.2 / 21.2,
+// 3.4 / 10.5 / 31.9; 4096 8.6 / 15.8 / 41.9, 4.1 / 13.0 / 40.7; 8192 14.0 / 29.3 /
+// 90.5, 6.4 / 21.9 / 83.9.  At 2048 columns they meet at 2048 rows (6.7, 6.2).
 constexpr int kRowWaves = 4;
 
-template <bool F32, int NP>
-__device__ __forceinline__ void quant_row(const QuantArgs& p, size_t r, int lane) {
+// t: this thread among the row's W waves; s_max: W words of LDS that no other wave
+// still reads
+template <bool F32, int NP, int W>
+__device__ __forceinline__ void quant_row(const QuantArgs& p, size_t r, int t, uint32_t* s_max) {
+    constexpr int kStride = W * kWave;
     const char* row = static_cast<const char*>(p.x) + r * p.cols * (F32 ? 4 : 2);
     uint4* dst = reinterpret_cast<uint4*>(static_cast<uint8_t*>(p.q) + r * p.cols);
     const int np = p.cols / 16;
@@ -237,39 +246,50 @@ __device__ __forceinline__ void quant_row(const QuantArgs& p, size_t r, int lane
     if constexpr (NP > 0) {
 #pragma unroll
         for (int n = 0; n < NP; ++n) {
-            const int c = lane + n * kWave;
+            const int c = t + n * kStride;
             if (c < np) piece[n].load(row, c);
             else piece[n].zero();
         }
 #pragma unroll
         for (int n = 0; n < NP; ++n) m = piece[n].amax(m);
     } else {
-        for (int c = lane; c < np; c += kWave) {
+        for (int c = t; c < np; c += kStride) {
             piece[0].load(row, c);
             m = piece[0].amax(m);
         }
     }
-    const float s = row_scale(wave_max_u32(m)), rs = 1.0f / s;
+    m = wave_max_u32(m);
+    if constexpr (W > 1) {
+        if (t % kWave == 0) s_max[t / kWave] = m;
+        __syncthreads();
+#pragma unroll
+        for (int w = 0; w < W; ++w) m = s_max[w] > m ? s_max[w] : m;
+    }
+    const float s = row_scale(m), rs = 1.0f / s;
     if constexpr (NP > 0) {
 #pragma unroll
         for (int n = 0; n < NP; ++n) {
-            const int c = lane + n * kWave;
+            const int c = t + n * kStride;
             const uint4 q = piece[n].codes(s, rs);
             if (c < np) dst[c] = q;
         }
     } else {
-        for (int c = lane; c < np; c += kWave) {
+        for (int c = t; c < np; c += kStride) {
             piece[0].load(row, c);
             dst[c] = piece[0].codes(s, rs);
         }
     }
-    if (lane == 0) p.scales[r] = s;
+    if (t == 0) p.scales[r] = s;
 }
 
-template <bool F32, int NP>
-__global__ __launch_bounds__(kRowWaves * kWave) void quant_rows_kernel(QuantArgs p) {
-    const int lane = threadIdx.x % kWave;
-    const int wave = blockIdx.x * kRowWaves + __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+// WAVE, BLOCK: pieces a lane of a row that goes to a wave (0: none do) or to a
+// block (-1: none do; 0: any number)
+// Two pieces: eight waves a SIMD, which the scalar registers of both loops would
+// otherwise not leave room for (65536 rows of 2048: 82.4 us with seven).
+template <bool F32, int WAVE, int BLOCK>
+__global__ __launch_bounds__(kRowWaves * kWave, WAVE == 2 ? 8 : 1) void quant_rows_kernel(QuantArgs p, int few) {
+    __shared__ uint32_t s_max[2][kRowWaves];
+    const int tid = threadIdx.x;
     long long r0 = 0, r1 = p.cap;
     if (p.m_counts != nullptr) {
         const int j = blockIdx.y;
@@ -279,7 +299,17 @@ __global__ __launch_bounds__(kRowWaves * kWave) void quant_rows_kernel(QuantArgs
         r0 = min(max(p.offsets[0], 0), p.cap);
         r1 = min(max(p.offsets[p.E_loc], (int)r0), p.cap);
     }
-    for (long long r = r0 + wave; r < r1; r += (long long)gridDim.x * kRowWaves) quant_row<F32, NP>(p, (size_t)r, lane);
+    if (BLOCK >= 0 && (WAVE == 0 || r1 - r0 <= few)) {
+        // rows take turns with the two sets of s_max: the barrier of the row between
+        // two that share one parts their reads and writes
+        int turn = 0;
+        for (long long r = r0 + blockIdx.x; r < r1; r += gridDim.x, turn ^= 1)
+            quant_row<F32, BLOCK < 0 ? 0 : BLOCK, kRowWaves>(p, (size_t)r, tid, s_max[turn]);
+    } else if (WAVE > 0) {
+        const int wave = blockIdx.x * kRowWaves + __builtin_amdgcn_readfirstlane(tid / kWave);
+        for (long long r = r0 + wave; r < r1; r += (long long)gridDim.x * kRowWaves)
+            quant_row<F32, WAVE, 1>(p, (size_t)r, tid % kWave, nullptr);
+    }
 }
 
 template <bool F32>
@@ -301,25 +331,37 @@ hipError_t launch_dispatch_any(const SegTable& seg, int B, int H, const int32_t*
     return hipGetLastError();
 }
 
-template <bool F32>
-hipError_t launch_quant_any(const QuantArgs& a, hipStream_t stream) {
-    const int per = (a.cols / 16 + kWave - 1) / kWave, most = device_cu_count() * 8;
+// few_per_cu: rows per CU up to which a row goes to a block
+template <bool F32, int WAVE, int BLOCK>
+hipError_t launch_quant_as(const QuantArgs& a, int few_per_cu, hipStream_t stream) {
+    constexpr int kRows = BLOCK < 0 ? kRowWaves : 1;              // rows of a block at a time
+    const int cus = device_cu_count(), most = cus * 8;
+    int few = cus * few_per_cu;
     dim3 grid, block(kRowWaves * kWave);
     if (a.m_counts != nullptr) {
-        // two rows a wave when a block of rows is full: decode fills few of them, and
+        few = (few + a.E_loc - 1) / a.E_loc;
+        // two rows at least when a block of rows is full: decode fills few of them, and
         // workgroups with nothing to do cost more than the loop
-        const int share = (most / 2 + a.E_loc - 1) / a.E_loc, need = (a.cap_e + 2 * kRowWaves - 1) / (2 * kRowWaves);
+        const int share = (most / 2 + a.E_loc - 1) / a.E_loc, need = (a.cap_e + 2 * kRows - 1) / (2 * kRows);
         grid = dim3(share < need ? share : need, a.E_loc);
     } else {
-        const int need = (a.cap + kRowWaves - 1) / kRowWaves;
+        const int need = (a.cap + kRows - 1) / kRows;
         grid = dim3(need < most ? need : most);
     }
-    if (per <= 1) hipLaunchKernelGGL((quant_rows_kernel<F32, 1>), grid, block, 0, stream, a);
-    else if (per <= 2) hipLaunchKernelGGL((quant_rows_kernel<F32, 2>), grid, block, 0, stream, a);
-    else if (per <= 4) hipLaunchKernelGGL((quant_rows_kernel<F32, 4>), grid, block, 0, stream, a);
-    else if (per <= 8) hipLaunchKernelGGL((quant_rows_kernel<F32, 8>), grid, block, 0, stream, a);
-    else hipLaunchKernelGGL((quant_rows_kernel<F32, 0>), grid, block, 0, stream, a);
+    hipLaunchKernelGGL((quant_rows_kernel<F32, WAVE, BLOCK>), grid, block, 0, stream, a, few);
     return hipGetLastError();
+}
+
+template <bool F32>
+hipError_t launch_quant_any(const QuantArgs& a, hipStream_t stream) {
+    const int per = (a.cols / 16 + kWave - 1) / kWave;            // pieces a lane of a wave
+    if (per <= 1) return launch_quant_as<F32, 1, -1>(a, 0, stream);
+    if (per <= 2) return launch_quant_as<F32, 2, 1>(a, 8, stream);
+    if (per <= 4) return launch_quant_as<F32, 4, 1>(a, 16, stream);
+    if (per <= 8) return launch_quant_as<F32, 0, 2>(a, 0, stream);
+    if (per <= 16) return launch_quant_as<F32, 0, 4>(a, 0, stream);
+    if (per <= 32) return launch_quant_as<F32, 0, 8>(a, 0, stream);
+    return launch_quant_as<F32, 0, 0>(a, 0, stream);
 }
 
 }  // namespace

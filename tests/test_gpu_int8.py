@@ -632,3 +632,50 @@ def test_dispatch_of_more_tokens_than_one_launch_takes():
     q, s = m.moe_dispatch([x[:cut], x[cut:]], rows, B, "int8")
     wq, ws = m.moe_quant_rows(few)
     assert bool((q.view(-1, 64, H) == wq.flip(0)).all()) and bool((s.view(-1, 64) == ws.flip(0)).all())
+
+
+@pytest.mark.parametrize("cols", [1024, 1040, 2048, 2064, 4096, 4112, 8192, 8208, 16384, 16400, 32768, 32784, 65552])
+@pytest.mark.parametrize("f32", [False, True])
+def test_quant_row_widths(cols, f32):
+    """Both sides of every width at which the row's share of a lane changes; rows that
+    are no numbers among them; fewer rows than blocks, and more."""
+    import combine_grouped_gemm_amd as m
+    for rows in (1, 5, 67):
+        x = _values(rows, cols, cols + rows, f32)
+        x[0, cols - 1] = -x[0, cols - 1].abs() - 3
+        if rows > 5:
+            x[3, cols - 1] = float("nan")
+            x[4, cols // 3] = -float("inf")
+            x[5] = 0.0
+        q, s = m.moe_quant_rows(x.cuda())
+        rq, rs = nx.quantize_i8_rows(to_np(x))
+        np.testing.assert_array_equal(q.cpu().numpy(), rq)
+        np.testing.assert_array_equal(s.cpu().numpy(), rs)
+
+
+@pytest.mark.parametrize("cols,per_cu", [(1040, 8), (2064, 16), (4112, 0)])
+@pytest.mark.parametrize("more", [0, 1, 9])
+def test_quant_row_counts_where_the_split_changes(cols, per_cu, more):
+    """As many rows as go to blocks and a few more, in either layout; the rows behind
+    them are left as they were."""
+    import combine_grouped_gemm_amd as m
+    few = max(per_cu, 8) * torch.cuda.get_device_properties(0).multi_processor_count
+    n, E = few + more, 16
+    x = _values(n + 5, cols, more).cuda()
+    rq, rs = (torch.from_numpy(np.ascontiguousarray(v)).cuda() for v in nx.quantize_i8_rows(to_np(x)))
+    q = torch.full((n + 5, cols), 99, dtype=torch.int8, device="cuda")
+    s = torch.full((n + 5,), -3.0, device="cuda")
+    m.moe_quant_rows(x, torch.tensor([0, 3, n], dtype=torch.int32, device="cuda"), q=q, scales=s)
+    assert bool((q[:n] == rq[:n]).all()) and bool((s[:n] == rs[:n]).all())
+    assert bool((q[n:] == 99).all()) and bool((s[n:] == -3.0).all())
+    # masked: experts with few rows, with few / E of them, and with more
+    cap = few // E + 12
+    counts = torch.tensor([few // E, few // E + 1, few // E + more, 0, 1, 2, cap, few // E - 1] * (E // 8), dtype=torch.int32)
+    x = x[:cap].repeat(E, 1)
+    q = torch.full((E * cap, cols), 99, dtype=torch.int8, device="cuda")
+    s = torch.full((E * cap,), -3.0, device="cuda")
+    m.moe_quant_rows(x, counts.cuda(), cap_per_expert=cap, q=q, scales=s)
+    valid = torch.arange(cap, device="cuda")[None] < counts.cuda()[:, None]
+    want = torch.where(valid[..., None], rq[None, :cap], torch.tensor(99, dtype=torch.int8, device="cuda"))
+    assert bool((q.view(E, cap, cols) == want).all())
+    assert bool((s.view(E, cap) == torch.where(valid, rs[None, :cap], torch.tensor(-3.0, device="cuda"))).all())
