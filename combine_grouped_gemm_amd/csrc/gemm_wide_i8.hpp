@@ -24,9 +24,9 @@
 // (row scales through LDS, a lane's column scales in registers).
 //
 // Measured (MI355X, several boxes; DeepSeek-shaped layer, H = 7168, I = 2048,
-// 256 experts): decode gate/up, T = 128: 0.98-1.02 ms, 6.7-6.9 TB/s (some 230 of
-// the experts have a row; counters: 6.68 GB in 977 us); down 0.52-0.57 ms, 6.0-6.2
-// TB/s.  One token (8 experts): 45 us, 5.3 TB/s.
+// 256 experts): decode gate/up, T = 128: 0.97-0.99 ms, 6.7-6.9 TB/s (some 230 of
+// the experts have a row; counters: 6.68 GB in 969 us; two stages 977); down 0.55-
+// 0.56 ms, 6.1 TB/s (two stages 0.56).  One token (8 experts): 45 us, 5.3 TB/s.
 // One EP=8 rank's share: 0.21-0.22 ms, 4.4-4.7 TB/s at a 2.25 GHz clock, the CUs
 // busy three quarters of the time (2.2 tiles each, of unequal sizes).  Prefill,
 // T = 8192: 2.1-2.3 ms, 1.7-1.8 POP/s; counters show the MFMAs busy 54% of the
