@@ -26,7 +26,7 @@
 // Measured (MI355X, several boxes; DeepSeek-shaped layer, H = 7168, I = 2048,
 // 256 experts): decode gate/up, T = 128: 0.97-0.99 ms, 6.7-6.9 TB/s (some 230 of
 // the experts have a row; counters: 6.68 GB in 969 us; two stages 977); down 0.55-
-// 0.56 ms, 6.1 TB/s (two stages 0.56).  One token (8 experts): 45 us, 5.3 TB/s.
+// 0.56 ms, 6.1 TB/s (two stages 0.56).  One token (8 experts): 39 us, 6.0 TB/s.
 // One EP=8 rank's share: 0.21-0.22 ms, 4.4-4.7 TB/s at a 2.25 GHz clock, the CUs
 // busy three quarters of the time (2.2 tiles each, of unequal sizes).  Prefill,
 // T = 8192: 2.1-2.3 ms, 1.7-1.8 POP/s; counters show the MFMAs busy 54% of the
@@ -86,7 +86,12 @@ __global__ __launch_bounds__(512, BM + BN > 256 ? 1 : 4) void grouped_gemm_i8_wi
     __shared__ uint4 sa2[S > 2 ? BM * CPR : 1];
     __shared__ uint4 sb2[S > 2 ? BN * CPR : 1];
     __shared__ int s_pre[kMaxExperts + 1];
-    __shared__ uint16_t s_ord[kMaxExperts];          // experts, most rows first
+    // experts, most rows first.  Small tiles keep the experts' own order: theirs are
+    // nearly all alike (weights, whatever the rows), and ranking 256 experts takes
+    // 7 us (one token at H = 7168 46.4 us with it, 39.1 without; 16 tokens 473, 435;
+    // decode down 562, 553).
+    constexpr bool SORTED = BM > 64;
+    __shared__ uint16_t s_ord[SORTED ? kMaxExperts : 1];
     static_assert(sizeof(sa0) >= kMaxExperts * sizeof(int), "row counts fit in the first row stage");
     __shared__ int s_tmp[NT / kWave];
     __shared__ float s_as[BM];                       // the tile's row scales
@@ -114,8 +119,9 @@ __global__ __launch_bounds__(512, BM + BN > 256 ? 1 : 4) void grouped_gemm_i8_wi
     // multiples of 8, so a row's (row & 7) is lane / 8)
     const int lane_k = swz(lane / 8, lane % 8) * 16;
 
-    // largest experts' tiles first; the first row stage is free scratch until the first load
-    build_tile_prefix_sorted<NT, BM>(p, s_pre, s_ord, reinterpret_cast<int*>(sa0), s_tmp);
+    // the first row stage is free scratch until the first load
+    if constexpr (SORTED) build_tile_prefix_sorted<NT, BM>(p, s_pre, s_ord, reinterpret_cast<int*>(sa0), s_tmp);
+    else build_tile_prefix<NT, BM>(p, s_pre, s_tmp);
     const int n_tiles_n = (N + BNO - 1) / BNO;
     const int total = n_tiles_n * s_pre[p.E_loc];
     const int G = gridDim.x;
@@ -137,7 +143,7 @@ __global__ __launch_bounds__(512, BM + BN > 256 ? 1 : 4) void grouped_gemm_i8_wi
         const int at = sparse ? (int)blockIdx.x : v;
         const int tau = base + (rnd & 1 ? G - 1 - at : at);
         if (tau >= total) continue;
-        const TileCoord tc = decode_tile<BM>(tau, n_tiles_n, s_pre, p, s_ord);
+        const TileCoord tc = decode_tile<BM>(tau, n_tiles_n, s_pre, p, SORTED ? s_ord : nullptr);
         const int j = tc.j, row0 = tc.row0, nvalid = tc.nvalid;
         const int col0 = tc.nt * BNO;
         // the tile's weight rows start at output column col0
