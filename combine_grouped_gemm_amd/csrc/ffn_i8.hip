@@ -59,7 +59,8 @@ hipError_t launch_out(const FfnArgs& a, bool gated, hipStream_t stream) {
 hipError_t launch_ffn_i8(const FfnArgs& a, bool gated, hipStream_t stream) {
     constexpr int BM = 64, BN = 128;
     const int cols = gated ? BN / 2 : BN;
-    const long long small = (long long)a.E_loc * ((a.rows_hint + BM - 1) / BM) * ((a.N + cols - 1) / cols);
+    const long long row_tiles = ((long long)a.rows_hint + BM - 1) / BM;
+    const long long small = a.E_loc * row_tiles * ((a.N + cols - 1) / cols);
     if (a.rows_hint >= 32 && small > 2 * device_cu_count()) return launch_out<256, 256, 2>(a, gated, stream);
     // two steps have nothing for a third stage (31 experts, K = 144, 14.7 us against 16.6)
     return a.Kdim > 2 * widei8::BK ? launch_out<BM, BN, 3>(a, gated, stream) : launch_out<BM, BN, 2>(a, gated, stream);

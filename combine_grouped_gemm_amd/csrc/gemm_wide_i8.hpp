@@ -131,8 +131,8 @@ __global__ __launch_bounds__(512, BM + BN > 256 ? 1 : 4) void grouped_gemm_i8_wi
     const uint8_t* __restrict__ W0 = static_cast<const uint8_t*>(p.w0);
     const uint8_t* __restrict__ W1 = static_cast<const uint8_t*>(p.w1);
 
-    // Tiles come in order of decreasing cost: every other round runs backwards over
-    // the blocks, so that none gets the largest tile of every round.  A round that
+    // Large tiles come in order of decreasing cost: every other round runs backwards
+    // over the blocks, so that none gets the largest tile of every round.  A round that
     // fills less than three quarters of the grid goes in hardware order, over all
     // XCDs; in XCD-major order it would leave some of them idle (one token's 8
     // experts, gate/up at H = 7168: 69.7 -> 44.7 us; 16 tokens 476 -> 454).  Large

@@ -679,3 +679,46 @@ def test_quant_row_counts_where_the_split_changes(cols, per_cu, more):
     want = torch.where(valid[..., None], rq[None, :cap], torch.tensor(99, dtype=torch.int8, device="cuda"))
     assert bool((q.view(E, cap, cols) == want).all())
     assert bool((s.view(E, cap) == torch.where(valid, rs[None, :cap], torch.tensor(-3.0, device="cuda"))).all())
+
+
+@pytest.mark.parametrize("gated", [True, False])
+@pytest.mark.parametrize("counts,K,N", PRODUCTS, ids=[f"{len(c)}x{max(c)}-K{k}-N{n}" for c, k, n in PRODUCTS])
+def test_products_in_large_tiles(counts, K, N, gated):
+    """Expected rows past what one round of small tiles holds."""
+    N = -(-N // 16) * 16
+    p = Problem(counts, K, N, seed=K + N, gated=gated, lead=3)
+    ref = p.run(1)
+    p.check(ref, "small tiles")
+    for hint in (10**6, 2**31 - 1):
+        print(f"[product] counts={counts[:6]} K={K} N={N} gated={gated} hint={hint}", flush=True)
+        assert torch.equal(p.run(hint), ref)
+        assert torch.equal(p.run(hint, pack=True), ref)
+        if not gated:
+            p.check(p.run(hint, y_dtype=torch.float32), f"fp32 y, hint {hint}")
+
+
+@pytest.mark.parametrize("gated", [True, False])
+@pytest.mark.parametrize("K,N", [(128, 2048), (384, 1040), (640, 1552), (400, 1040), (256, 2000)])
+def test_products_of_many_experts(K, N, gated):
+    """Large tiles at ordinary hints, with weights read either way; ranks of experts
+    with equal, no and many rows."""
+    counts = [0, 33, 257, 64, 1, 33, 256, 0, 129, 300, 7, 33] * 8
+    p = Problem(counts, K, N, seed=K + N, gated=gated, lead=5)
+    ref = p.run(1)
+    p.check(ref, "small tiles")
+    for hint in (32, 40, 100, 191, 192, 600):
+        print(f"[product] K={K} N={N} gated={gated} hint={hint}", flush=True)
+        assert torch.equal(p.run(hint), ref)
+    if not gated:
+        p.check(p.run(100, y_dtype=torch.float32), "fp32 y")
+
+
+@pytest.mark.parametrize("steps", [1, 2, 3, 4, 5, 6, 7, 8, 9, 10])
+def test_products_by_number_of_steps(steps):
+    """Every remainder of the k-loop's turns, with a whole and a partial last step."""
+    for K in (128 * steps, 128 * steps - 48):
+        for gated in (True, False):
+            p = Problem([5, 0, 70, 200, 1], K, 208, seed=K, gated=gated, lead=1)
+            ref = p.run(1)
+            p.check(ref, f"K={K} gated={gated}")
+            assert torch.equal(p.run(100), ref) and torch.equal(p.run(10**6), ref)
