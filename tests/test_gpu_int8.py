@@ -722,3 +722,41 @@ def test_products_by_number_of_steps(steps):
             ref = p.run(1)
             p.check(ref, f"K={K} gated={gated}")
             assert torch.equal(p.run(100), ref) and torch.equal(p.run(10**6), ref)
+
+
+def test_extreme_codes_and_scales_in_large_tiles():
+    test_extreme_codes_and_scales(10**6)
+
+
+@pytest.mark.parametrize("cols", [512, 2048, 4096])
+def test_quant_rows_past_four_gigabytes(cols):
+    """The last rows of a long buffer, however a row is shared out."""
+    import combine_grouped_gemm_amd as m
+    cap, n = 2**32 // cols + 5000, 4500
+    x = torch.zeros((cap, cols), dtype=torch.bfloat16, device="cuda")
+    x[cap - n:] = torch.randn(n, cols, generator=_gen(cols)).to(torch.bfloat16).cuda()
+    rq, rs = nx.quantize_i8_rows(to_np(x[cap - n:]))
+    for first in (cap - n, cap - 9):
+        q, s = m.moe_quant_rows(x, torch.tensor([first, cap], dtype=torch.int32, device="cuda"))
+        np.testing.assert_array_equal(q[first:].cpu().numpy(), rq[first - cap:])
+        np.testing.assert_array_equal(s[first:].cpu().numpy(), rs[first - cap:])
+    del x, q
+    torch.cuda.empty_cache()
+
+
+def test_small_tiles_past_four_gigabytes():
+    import combine_grouped_gemm_amd as m
+    cap, H, n = 70000, 65536, 6
+    a = torch.zeros((cap, H), dtype=torch.int8, device="cuda")
+    a[cap - n:] = torch.randint(-127, 128, (n, H), dtype=torch.int8, generator=_gen(4)).cuda()
+    off = torch.tensor([cap - n, cap - 2, cap], dtype=torch.int32, device="cuda")
+    w = torch.randint(-127, 128, (2, 16, H), dtype=torch.int8, generator=_gen(1)).cuda()
+    sa, sw = torch.full((cap,), 2.0**-7, device="cuda"), torch.ones((2, 16), device="cuda")
+    y = m.moe_ffn_down(a, sa, off, w, sw, y_dtype=torch.float32, expected_rows=3)
+    h, _ = m.moe_ffn_gate_up(a, sa, off, w, w, sw, sw, expected_rows=3)
+    for j, (b, e) in enumerate(((cap - n, cap - 2), (cap - 2, cap))):
+        ref = (a[b:e].double() @ w[j].double().t()) * 2.0**-7
+        _near(y[b:e], ref, Y_TOL[torch.float32], "y")
+        _near(h[b:e], ref / (1 + torch.exp(-ref)) * ref, H_TOL, "h")
+    del a, y, h
+    torch.cuda.empty_cache()
