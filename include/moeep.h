@@ -330,7 +330,9 @@ moe_status_t moe_dispatch(const void* const* seg_x, const int32_t* seg_rows, int
  *
  * int8: xd codes with xd_scales (cap_rows), weight codes with one scale per
  * output channel, w_gate_scales, w_up_scales (E_local, I), w_down_scales
- * (E_local, H); products are summed exactly in int32 and scaled in fp32.
+ * (E_local, H); products are summed exactly in int32 and scaled in fp32, in an
+ * order that reaches every result fp32 can hold, whatever the two scales (g, u
+ * and y past its range are infinities; silu of -infinity is 0).
  * moe_ffn_gate_up writes h as bf16 (rounded once; h_scales unused, may be
  * NULL), moe_quant_rows turns it into the int8 rows and h_scales (cap_rows)
  * that moe_ffn_down takes; moe_grouped_ffn makes the three calls.
