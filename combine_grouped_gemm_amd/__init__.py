@@ -136,8 +136,9 @@ def _call(fn, t, stream, *args):
 
 
 def _new(shape, dtype, device, stream):
-    """An output the caller did not give, allocated for the stream that writes it: memory
-    of another stream may still be in use there."""
+    """An output or workspace the caller did not give, allocated for the stream that uses
+    it: memory of another stream may still be in use there, and a workspace freed on return
+    would go to that stream's next allocation while the call is still running."""
     if stream is None:
         return torch.empty(shape, dtype=dtype, device=device)
     if not isinstance(stream, torch.cuda.Stream):
@@ -198,9 +199,9 @@ def moe_route(logits, K: int, topk_ids=None, topk_w=None, stream=None):
     _dev(logits, "logits", torch.float32, 2)
     B, E = logits.shape
     if topk_ids is None:
-        topk_ids = torch.empty((B, K), dtype=torch.int32, device=logits.device)
+        topk_ids = _new((B, K), torch.int32, logits.device, stream)
     if topk_w is None:
-        topk_w = torch.empty((B, K), dtype=torch.float32, device=logits.device)
+        topk_w = _new((B, K), torch.float32, logits.device, stream)
     _dev(topk_ids, "topk_ids", torch.int32)
     _dev(topk_w, "topk_w", torch.float32)
     _need(topk_ids, "topk_ids", shape=(B, K))
@@ -218,9 +219,9 @@ def moe_route_mapped(logits, K: int, phys_of_logical, topk_ids=None, topk_w=None
     if phys_of_logical.numel() != E:
         raise ValueError("phys_of_logical needs E entries")
     if topk_ids is None:
-        topk_ids = torch.empty((B, K), dtype=torch.int32, device=logits.device)
+        topk_ids = _new((B, K), torch.int32, logits.device, stream)
     if topk_w is None:
-        topk_w = torch.empty((B, K), dtype=torch.float32, device=logits.device)
+        topk_w = _new((B, K), torch.float32, logits.device, stream)
     _dev(topk_ids, "topk_ids", torch.int32, 2)
     _dev(topk_w, "topk_w", torch.float32, 2)
     _need(topk_ids, "topk_ids", shape=(B, K))
@@ -237,9 +238,9 @@ def moe_route_shared(logits, K: int, n_shared: int, topk_ids=None, topk_w=None, 
     B, E = logits.shape
     Kt = K + n_shared
     if topk_ids is None:
-        topk_ids = torch.empty((B, Kt), dtype=torch.int32, device=logits.device)
+        topk_ids = _new((B, Kt), torch.int32, logits.device, stream)
     if topk_w is None:
-        topk_w = torch.empty((B, Kt), dtype=torch.float32, device=logits.device)
+        topk_w = _new((B, Kt), torch.float32, logits.device, stream)
     _dev(topk_ids, "topk_ids", torch.int32, 2)
     _dev(topk_w, "topk_w", torch.float32, 2)
     if topk_ids.shape != (B, Kt) or topk_w.shape != (B, Kt):
@@ -317,13 +318,13 @@ def moe_layout(topk_ids, E: int, e_begin: int, e_end: int, cap_rows: int, counts
     B, K = topk_ids.shape
     dev = topk_ids.device
     E_loc = e_end - e_begin
-    counts = torch.empty(E, dtype=torch.int32, device=dev) if counts is None else counts
-    offsets = torch.empty(max(E_loc, 0) + 1, dtype=torch.int32, device=dev) if offsets is None else offsets
-    row_of = torch.empty((B, K), dtype=torch.int32, device=dev) if row_of is None else row_of
-    src_of = torch.empty(max(cap_rows, 1), dtype=torch.int32, device=dev) if src_of is None else src_of
+    counts = _new(E, torch.int32, dev, stream) if counts is None else counts
+    offsets = _new(max(E_loc, 0) + 1, torch.int32, dev, stream) if offsets is None else offsets
+    row_of = _new((B, K), torch.int32, dev, stream) if row_of is None else row_of
+    src_of = _new(max(cap_rows, 1), torch.int32, dev, stream) if src_of is None else src_of
     need = moe_layout_workspace_bytes(B, K, E)
     if ws is None:
-        ws = torch.empty(max(need, 256), dtype=torch.uint8, device=dev)
+        ws = _new(max(need, 256), torch.uint8, dev, stream)
     for n, t in (("counts", counts), ("offsets", offsets), ("row_of", row_of), ("src_of", src_of)):
         _dev(t, n, torch.int32)
     _check_layout_outputs(B, K, E, E_loc, cap_rows, counts, offsets, row_of, src_of)
@@ -348,10 +349,10 @@ def moe_layout_noalloc(topk_ids, E: int, e_begin: int, e_end: int, cap_rows: int
     B, K = topk_ids.shape
     dev = topk_ids.device
     E_loc = e_end - e_begin
-    counts = torch.empty(E, dtype=torch.int32, device=dev) if counts is None else counts
-    offsets = torch.empty(max(E_loc, 0) + 1, dtype=torch.int32, device=dev) if offsets is None else offsets
-    row_of = torch.empty((B, K), dtype=torch.int32, device=dev) if row_of is None else row_of
-    src_of = torch.empty(max(cap_rows, 1), dtype=torch.int32, device=dev) if src_of is None else src_of
+    counts = _new(E, torch.int32, dev, stream) if counts is None else counts
+    offsets = _new(max(E_loc, 0) + 1, torch.int32, dev, stream) if offsets is None else offsets
+    row_of = _new((B, K), torch.int32, dev, stream) if row_of is None else row_of
+    src_of = _new(max(cap_rows, 1), torch.int32, dev, stream) if src_of is None else src_of
     for n, t in (("counts", counts), ("offsets", offsets), ("row_of", row_of), ("src_of", src_of)):
         _dev(t, n, torch.int32)
     _check_layout_outputs(B, K, E, E_loc, cap_rows, counts, offsets, row_of, src_of)
@@ -368,14 +369,14 @@ def moe_layout_masked(topk_ids, E: int, e_begin: int, e_end: int, cap_per_expert
     B, K = topk_ids.shape
     dev = topk_ids.device
     E_loc = e_end - e_begin
-    counts = torch.empty(E, dtype=torch.int32, device=dev) if counts is None else counts
-    m = torch.empty(max(E_loc, 1), dtype=torch.int32, device=dev) if m is None else m
-    row_of = torch.empty((B, K), dtype=torch.int32, device=dev) if row_of is None else row_of
+    counts = _new(E, torch.int32, dev, stream) if counts is None else counts
+    m = _new(max(E_loc, 1), torch.int32, dev, stream) if m is None else m
+    row_of = _new((B, K), torch.int32, dev, stream) if row_of is None else row_of
     if src_of is None:
-        src_of = torch.empty(max(E_loc * cap_per_expert, 1), dtype=torch.int32, device=dev)
+        src_of = _new(max(E_loc * cap_per_expert, 1), torch.int32, dev, stream)
     need = moe_layout_workspace_bytes(B, K, E)
     if ws is None:
-        ws = torch.empty(max(need, 256), dtype=torch.uint8, device=dev)
+        ws = _new(max(need, 256), torch.uint8, dev, stream)
     for n, t in (("counts", counts), ("m", m), ("row_of", row_of), ("src_of", src_of)):
         _dev(t, n, torch.int32)
     _need(counts, "counts", numel=E)
@@ -501,7 +502,7 @@ def moe_pack_weights(w, out=None, stream=None):
     code = _DT[w.dtype]
     ld = moe_weight_ld(cols, code)
     if out is None:
-        out = torch.empty((E_loc, rows, ld), dtype=w.dtype, device=w.device)
+        out = _new((E_loc, rows, ld), w.dtype, w.device, stream)
     _dev(out, "out", w.dtype)
     _need(out, "out", shape=(E_loc, rows, ld))
     _check(lib().moe_pack_weights(_ptr(w), E_loc, rows, cols, code, _ptr(out), _stream(stream)))
@@ -717,7 +718,7 @@ def moe_combine(y, row_of, topk_w, out=None, out_dtype=None, stream=None):
     B, K = row_of.shape
     H = y.shape[1]
     if out is None:
-        out = torch.empty((B, H), dtype=y.dtype if out_dtype is None else out_dtype, device=y.device)
+        out = _new((B, H), y.dtype if out_dtype is None else out_dtype, y.device, stream)
     _dev(out, "out")
     _need(topk_w, "topk_w", shape=(B, K))
     _need(out, "out", numel=B * H)
