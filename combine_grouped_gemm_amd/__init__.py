@@ -128,6 +128,8 @@ def _stream(stream):
 def _call(fn, t, stream, *args):
     """One library call with t's device current, on `stream` (None: that device's current stream)."""
     index = t.get_device()
+    if isinstance(stream, torch.cuda.Stream) and stream.device_index != index:
+        raise ValueError(f"stream must be of the tensors' device {t.device} (got one of cuda:{stream.device_index})")
     if index == torch.cuda.current_device():
         _check(fn(*args, _raw_stream(index) if stream is None else _stream(stream)))
     else:
@@ -206,7 +208,8 @@ def moe_route(logits, K: int, topk_ids=None, topk_w=None, stream=None):
     _dev(topk_w, "topk_w", torch.float32)
     _need(topk_ids, "topk_ids", shape=(B, K))
     _need(topk_w, "topk_w", shape=(B, K))
-    _check(lib().moe_route(_ptr(logits), B, E, K, _ptr(topk_ids), _ptr(topk_w), _stream(stream)))
+    _same_device(logits, "logits", topk_ids, topk_w)
+    _call(lib().moe_route, logits, stream, _ptr(logits), B, E, K, _ptr(topk_ids), _ptr(topk_w))
     return topk_ids, topk_w
 
 
@@ -226,8 +229,9 @@ def moe_route_mapped(logits, K: int, phys_of_logical, topk_ids=None, topk_w=None
     _dev(topk_w, "topk_w", torch.float32, 2)
     _need(topk_ids, "topk_ids", shape=(B, K))
     _need(topk_w, "topk_w", shape=(B, K))
-    _check(lib().moe_route_mapped(_ptr(logits), B, E, K, _ptr(phys_of_logical), _ptr(topk_ids),
-                                  _ptr(topk_w), _stream(stream)))
+    _same_device(logits, "logits", phys_of_logical, topk_ids, topk_w)
+    _call(lib().moe_route_mapped, logits, stream, _ptr(logits), B, E, K, _ptr(phys_of_logical), _ptr(topk_ids),
+          _ptr(topk_w))
     return topk_ids, topk_w
 
 
@@ -245,8 +249,8 @@ def moe_route_shared(logits, K: int, n_shared: int, topk_ids=None, topk_w=None, 
     _dev(topk_w, "topk_w", torch.float32, 2)
     if topk_ids.shape != (B, Kt) or topk_w.shape != (B, Kt):
         raise ValueError(f"outputs must be ({B}, {Kt})")
-    _check(lib().moe_route_shared(_ptr(logits), B, E, K, int(n_shared), _ptr(topk_ids), _ptr(topk_w),
-                                  _stream(stream)))
+    _same_device(logits, "logits", topk_ids, topk_w)
+    _call(lib().moe_route_shared, logits, stream, _ptr(logits), B, E, K, int(n_shared), _ptr(topk_ids), _ptr(topk_w))
     return topk_ids, topk_w
 
 
@@ -329,9 +333,9 @@ def moe_layout(topk_ids, E: int, e_begin: int, e_end: int, cap_rows: int, counts
         _dev(t, n, torch.int32)
     _check_layout_outputs(B, K, E, E_loc, cap_rows, counts, offsets, row_of, src_of)
     _dev(ws, "ws")
-    _check(lib().moe_layout(_ptr(topk_ids), B, K, E, e_begin, e_end, _ptr(counts), _ptr(offsets),
-                            _ptr(row_of), _ptr(src_of), cap_rows, _ptr(ws),
-                            ws.numel() * ws.element_size(), _stream(stream)))
+    _same_device(topk_ids, "topk_ids", counts, offsets, row_of, src_of, ws)
+    _call(lib().moe_layout, topk_ids, stream, _ptr(topk_ids), B, K, E, e_begin, e_end, _ptr(counts), _ptr(offsets),
+          _ptr(row_of), _ptr(src_of), cap_rows, _ptr(ws), ws.numel() * ws.element_size())
     return {"counts": counts, "offsets": offsets, "row_of": row_of, "src_of": src_of}
 
 
@@ -356,8 +360,9 @@ def moe_layout_noalloc(topk_ids, E: int, e_begin: int, e_end: int, cap_rows: int
     for n, t in (("counts", counts), ("offsets", offsets), ("row_of", row_of), ("src_of", src_of)):
         _dev(t, n, torch.int32)
     _check_layout_outputs(B, K, E, E_loc, cap_rows, counts, offsets, row_of, src_of)
-    _check(lib().moe_layout_noalloc(_ptr(topk_ids), B, K, E, e_begin, e_end, _ptr(counts), _ptr(offsets),
-                                    _ptr(row_of), _ptr(src_of), cap_rows, _stream(stream)))
+    _same_device(topk_ids, "topk_ids", counts, offsets, row_of, src_of)
+    _call(lib().moe_layout_noalloc, topk_ids, stream, _ptr(topk_ids), B, K, E, e_begin, e_end, _ptr(counts),
+          _ptr(offsets), _ptr(row_of), _ptr(src_of), cap_rows)
     return {"counts": counts, "offsets": offsets, "row_of": row_of, "src_of": src_of}
 
 
@@ -384,9 +389,9 @@ def moe_layout_masked(topk_ids, E: int, e_begin: int, e_end: int, cap_per_expert
     _need(row_of, "row_of", numel=B * K)
     _need(src_of, "src_of", numel=max(E_loc, 0) * cap_per_expert)
     _dev(ws, "ws")
-    _check(lib().moe_layout_masked(_ptr(topk_ids), B, K, E, e_begin, e_end, _ptr(counts), _ptr(m),
-                                   _ptr(row_of), _ptr(src_of), cap_per_expert, _ptr(ws),
-                                   ws.numel() * ws.element_size(), _stream(stream)))
+    _same_device(topk_ids, "topk_ids", counts, m, row_of, src_of, ws)
+    _call(lib().moe_layout_masked, topk_ids, stream, _ptr(topk_ids), B, K, E, e_begin, e_end, _ptr(counts), _ptr(m),
+          _ptr(row_of), _ptr(src_of), cap_per_expert, _ptr(ws), ws.numel() * ws.element_size())
     return {"counts": counts, "m": m, "row_of": row_of, "src_of": src_of}
 
 
@@ -425,8 +430,7 @@ def moe_dispatch(seg_x, row_of, cap_rows: int, xd_dtype=None, xd=None, xd_scales
     if xd_code in (MOE_FP8_E4M3, MOE_INT8):
         _dev(xd_scales, "xd_scales", torch.float32)
         _need(xd_scales, "xd_scales", numel=cap_rows * _scale_cols(xd_code, H))
-    if xd_code == MOE_INT8:
-        _same_device(row_of, "row_of", xd, xd_scales, *seg_x)
+    _same_device(row_of, "row_of", xd, xd_scales if xd_code in (MOE_FP8_E4M3, MOE_INT8) else None, *seg_x)
     ptrs = (ctypes.c_void_p * len(seg_x))(*[s.data_ptr() for s in seg_x])
     rows = (ctypes.c_int32 * len(seg_x))(*[s.shape[0] for s in seg_x])
     _call(lib().moe_dispatch, row_of, stream, ptrs, rows, len(seg_x), _DT[x_dt], H, _ptr(row_of), K, _ptr(xd), xd_code, _ptr(xd_scales), cap_rows)
@@ -505,7 +509,8 @@ def moe_pack_weights(w, out=None, stream=None):
         out = _new((E_loc, rows, ld), w.dtype, w.device, stream)
     _dev(out, "out", w.dtype)
     _need(out, "out", shape=(E_loc, rows, ld))
-    _check(lib().moe_pack_weights(_ptr(w), E_loc, rows, cols, code, _ptr(out), _stream(stream)))
+    _same_device(w, "w", out)
+    _call(lib().moe_pack_weights, w, stream, _ptr(w), E_loc, rows, cols, code, _ptr(out))
     return out
 
 
@@ -546,7 +551,7 @@ def _rows_arg(rows, cap_per_expert, E_loc, n_rows):
 def _check_ffn(a, a_scales, rows, cap_per_expert, E_loc, Kdim, cap, act, **tensors):
     """Shapes of the FFN operands: the activation rows (cap, Kdim) [+ fp8 or
     int8 scales], the row description (offsets E_loc + 1, or m E_loc), and each
-    named (tensor, shape or minimum element count) pair."""
+    named (tensor, shape or minimum element count or None) pair; one device for all."""
     if a.shape[1] != Kdim:
         raise ValueError(f"activations must have {Kdim} columns (got {a.shape[1]})")
     _need(rows, "offsets" if cap_per_expert is None else "m",
@@ -563,7 +568,6 @@ def _check_ffn(a, a_scales, rows, cap_per_expert, E_loc, Kdim, cap, act, **tenso
                 if t is None:
                     raise ValueError(f"int8 weights need {name}")
                 _dev(t, name, torch.float32)
-        _same_device(a, "activations", a_scales, rows, *(t for t, _ in tensors.values()))
     for name, (t, want) in tensors.items():
         if t is None:
             continue
@@ -572,6 +576,8 @@ def _check_ffn(a, a_scales, rows, cap_per_expert, E_loc, Kdim, cap, act, **tenso
             _need(t, name, shape=want)
         else:
             _need(t, name, numel=want)
+    _same_device(a, "activations", a_scales if act in (MOE_FP8_E4M3, MOE_INT8) else None, rows,
+                 *(t for t, _ in tensors.values()))
 
 
 def _w_scales(act, scales, E_loc, rows, cols):
@@ -621,7 +627,7 @@ def moe_ffn_gate_up(xd, xd_scales, offsets, w_gate, w_up, w_gate_scales=None, w_
     nbI = -(-I // FP8_BLOCK)
     fp8 = act == MOE_FP8_E4M3
     _check_ffn(xd, xd_scales, offsets, cap_per_expert, E_loc, H, cap, act,
-               w_up=(w_up, tuple(w_gate.shape)), h=(h, cap * I),
+               w_gate=(w_gate, None), w_up=(w_up, tuple(w_gate.shape)), h=(h, cap * I),
                h_scales=(h_scales if fp8 else None, cap * nbI),
                w_gate_scales=_w_scales(act, w_gate_scales, E_loc, I, H),
                w_up_scales=_w_scales(act, w_up_scales, E_loc, I, H))
@@ -651,7 +657,7 @@ def moe_ffn_down(h, h_scales, offsets, w_down, w_down_scales=None, y=None, y_dty
     y_dtype = _y_dtype_for(act) if y_dtype is None else y_dtype
     if y is None:
         y = _new((cap, H), y_dtype, h.device, stream)
-    _check_ffn(h, h_scales, offsets, cap_per_expert, E_loc, I, cap, act, y=(y, cap * H),
+    _check_ffn(h, h_scales, offsets, cap_per_expert, E_loc, I, cap, act, w_down=(w_down, None), y=(y, cap * H),
                w_down_scales=_w_scales(act, w_down_scales, E_loc, H, I))
     fn = lib().moe_ffn_down if cap_per_expert is None else lib().moe_ffn_down_masked
     _call(fn, h, stream, _ptr(h), _ptr(h_scales), _ptr(offsets), E_loc, third, H, I, act,
@@ -680,10 +686,9 @@ def moe_grouped_ffn(xd, xd_scales, offsets, w_gate, w_up, w_down, w_gate_scales=
     need = moe_ffn_workspace_bytes(cap, I, act)
     if ws is None:
         ws = _new(max(need, 256), torch.uint8, xd.device, stream)
-    _dev(ws, "ws")
     _check_ffn(xd, xd_scales, offsets, cap_per_expert, E_loc, H, cap, act,
-               w_up=(w_up, tuple(w_gate.shape)), w_down=(w_down, (E_loc, H, w_down.shape[2])),
-               y=(y, cap * H),
+               w_gate=(w_gate, None), w_up=(w_up, tuple(w_gate.shape)), w_down=(w_down, (E_loc, H, w_down.shape[2])),
+               y=(y, cap * H), ws=(ws, None),
                w_gate_scales=_w_scales(act, w_gate_scales, E_loc, I, H),
                w_up_scales=_w_scales(act, w_up_scales, E_loc, I, H),
                w_down_scales=_w_scales(act, w_down_scales, E_loc, H, I))
@@ -722,8 +727,9 @@ def moe_combine(y, row_of, topk_w, out=None, out_dtype=None, stream=None):
     _dev(out, "out")
     _need(topk_w, "topk_w", shape=(B, K))
     _need(out, "out", numel=B * H)
-    _check(lib().moe_combine(_ptr(y), _DT[y.dtype], y.shape[0], _ptr(row_of), _ptr(topk_w), B, K, H,
-                             _ptr(out), _DT[out.dtype], _stream(stream)))
+    _same_device(y, "y", row_of, topk_w, out)
+    _call(lib().moe_combine, y, stream, _ptr(y), _DT[y.dtype], y.shape[0], _ptr(row_of), _ptr(topk_w), B, K, H,
+          _ptr(out), _DT[out.dtype])
     return out
 
 

@@ -221,7 +221,7 @@ class MicroBatchedLayer:
     def forward(self, x_segments, logits, w):
         """Enqueue both micro-batches; returns (out_a, out_b) (token order: A then B)."""
         (xa, la), (xb, lb) = self.split_inputs(x_segments, logits)
-        main = torch.cuda.current_stream()
+        main = torch.cuda.current_stream(self.side.device)
         self._ev_start.record(main)
         self.side.wait_event(self._ev_start)
         a, b = self.a, self.b

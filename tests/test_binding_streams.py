@@ -82,3 +82,76 @@ def test_what_a_call_makes_belongs_to_the_stream_it_is_given(recorder, monkeypat
         call(stream=stream)
         assert got == [stream] * made
         assert [args[-1] for _, args in recorder.launched] == [stream]
+
+
+class Devices:
+    """Two devices, the first one current; every tensor says it is on `where`."""
+
+    def __init__(self, monkeypatch, where):
+        self.current = 0
+        monkeypatch.setattr(torch.Tensor, "get_device", lambda t: where())
+        monkeypatch.setattr(torch.cuda, "current_device", lambda: self.current)
+        monkeypatch.setattr(m, "_raw_stream", lambda index: 1000 + index)
+        devices = self
+
+        class device:
+            def __init__(self, index):
+                self.index = index
+
+            def __enter__(self):
+                self.before, devices.current = devices.current, self.index
+
+            def __exit__(self, *exc):
+                devices.current = self.before
+
+        monkeypatch.setattr(torch.cuda, "device", device)
+
+
+@pytest.fixture
+def on_host(monkeypatch):
+    r = Recorder(m.lib())
+    monkeypatch.setattr(m, "lib", lambda: r)
+    monkeypatch.setattr(m, "_dev", lambda t, *a, **k: t)
+    return r
+
+
+@pytest.mark.parametrize("name", CALLS)
+def test_the_tensors_device_is_current_during_a_call(on_host, monkeypatch, name):
+    """Launches go to the tensors' device, on that device's current stream."""
+    d = Devices(monkeypatch, lambda: 1)
+    during = []
+    monkeypatch.setattr(m, "_check", lambda status: during.append(d.current))
+    CALLS[name][0]()
+    assert during == [1] and d.current == 0
+    assert [args[-1] for _, args in on_host.launched] == [1001]
+    # the current device needs no switch
+    monkeypatch.setattr(torch.Tensor, "get_device", lambda t: 0)
+    monkeypatch.setattr(torch.cuda, "device", lambda index: pytest.fail("device switched"))
+    CALLS[name][0]()
+    assert during == [1, 0] and on_host.launched[1][1][-1] == 1000
+
+
+@pytest.mark.parametrize("name", CALLS)
+def test_tensors_of_two_devices_are_refused(on_host, monkeypatch, name):
+    """A kernel would read the other device's memory, or fault on it."""
+    seen = []
+    Devices(monkeypatch, lambda: seen.append(0) or min(len(seen) - 1, 1))
+    with pytest.raises(ValueError, match="all tensors must be on"):
+        CALLS[name][0]()
+    assert not on_host.launched
+
+
+@pytest.mark.parametrize("name", CALLS)
+def test_a_stream_of_another_device_is_refused(on_host, monkeypatch, name):
+    class Stream:
+        def __init__(self, index):
+            self.device_index, self.cuda_stream = index, 500 + index
+
+    Devices(monkeypatch, lambda: 1)
+    monkeypatch.setattr(torch.cuda, "Stream", Stream)
+    monkeypatch.setattr(m, "_new", lambda shape, dtype, device, stream: torch.empty(shape, dtype=dtype))
+    CALLS[name][0](stream=Stream(1))
+    assert [args[-1] for _, args in on_host.launched] == [501]
+    with pytest.raises(ValueError, match="stream must be"):
+        CALLS[name][0](stream=Stream(0))
+    assert len(on_host.launched) == 1
