@@ -137,16 +137,21 @@ def _call(fn, t, stream, *args):
             _check(fn(*args, _stream(stream)))
 
 
-def _new(shape, dtype, device, stream):
-    """An output or workspace the caller did not give, allocated for the stream that uses
-    it: memory of another stream may still be in use there, and a workspace freed on return
-    would go to that stream's next allocation while the call is still running."""
+def _new(shape, dtype, device, stream, scratch=False):
+    """An output or workspace (scratch) the caller did not give, allocated for the stream
+    that uses it: memory of another stream may still be in use there, and a workspace freed
+    on return would go to that stream's next allocation while the call is still running.
+    For an output the current stream, where the caller goes on, is noted as a user too: what
+    it still reads when the tensor is dropped is not written by the given stream's next call."""
     if stream is None:
         return torch.empty(shape, dtype=dtype, device=device)
     if not isinstance(stream, torch.cuda.Stream):
         stream = torch.cuda.ExternalStream(int(stream), device=device)
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=device)
+        t = torch.empty(shape, dtype=dtype, device=device)
+    if not scratch:
+        t.record_stream(torch.cuda.current_stream(device))
+    return t
 
 
 def _dev(t, name, dtype=None, ndim=None):
@@ -328,7 +333,7 @@ def moe_layout(topk_ids, E: int, e_begin: int, e_end: int, cap_rows: int, counts
     src_of = _new(max(cap_rows, 1), torch.int32, dev, stream) if src_of is None else src_of
     need = moe_layout_workspace_bytes(B, K, E)
     if ws is None:
-        ws = _new(max(need, 256), torch.uint8, dev, stream)
+        ws = _new(max(need, 256), torch.uint8, dev, stream, scratch=True)
     for n, t in (("counts", counts), ("offsets", offsets), ("row_of", row_of), ("src_of", src_of)):
         _dev(t, n, torch.int32)
     _check_layout_outputs(B, K, E, E_loc, cap_rows, counts, offsets, row_of, src_of)
@@ -381,7 +386,7 @@ def moe_layout_masked(topk_ids, E: int, e_begin: int, e_end: int, cap_per_expert
         src_of = _new(max(E_loc * cap_per_expert, 1), torch.int32, dev, stream)
     need = moe_layout_workspace_bytes(B, K, E)
     if ws is None:
-        ws = _new(max(need, 256), torch.uint8, dev, stream)
+        ws = _new(max(need, 256), torch.uint8, dev, stream, scratch=True)
     for n, t in (("counts", counts), ("m", m), ("row_of", row_of), ("src_of", src_of)):
         _dev(t, n, torch.int32)
     _need(counts, "counts", numel=E)
@@ -685,7 +690,7 @@ def moe_grouped_ffn(xd, xd_scales, offsets, w_gate, w_up, w_down, w_gate_scales=
         y = _new((cap, H), y_dtype, xd.device, stream)
     need = moe_ffn_workspace_bytes(cap, I, act)
     if ws is None:
-        ws = _new(max(need, 256), torch.uint8, xd.device, stream)
+        ws = _new(max(need, 256), torch.uint8, xd.device, stream, scratch=True)
     _check_ffn(xd, xd_scales, offsets, cap_per_expert, E_loc, H, cap, act,
                w_gate=(w_gate, None), w_up=(w_up, tuple(w_gate.shape)), w_down=(w_down, (E_loc, H, w_down.shape[2])),
                y=(y, cap * H), ws=(ws, None),

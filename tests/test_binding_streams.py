@@ -70,7 +70,7 @@ def test_what_a_call_makes_belongs_to_the_stream_it_is_given(recorder, monkeypat
     call, made = CALLS[name]
     empty, got = torch.empty, []
 
-    def new(shape, dtype, device, stream):
+    def new(shape, dtype, device, stream, scratch=False):
         got.append(stream)
         return empty(shape, dtype=dtype, device=device)
 
@@ -149,7 +149,7 @@ def test_a_stream_of_another_device_is_refused(on_host, monkeypatch, name):
 
     Devices(monkeypatch, lambda: 1)
     monkeypatch.setattr(torch.cuda, "Stream", Stream)
-    monkeypatch.setattr(m, "_new", lambda shape, dtype, device, stream: torch.empty(shape, dtype=dtype))
+    monkeypatch.setattr(m, "_new", lambda shape, dtype, *a, **k: torch.empty(shape, dtype=dtype))
     CALLS[name][0](stream=Stream(1))
     assert [args[-1] for _, args in on_host.launched] == [501]
     with pytest.raises(ValueError, match="stream must be"):

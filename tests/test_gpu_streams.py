@@ -9,10 +9,10 @@ from harness import has_gpu
 pytestmark = [pytest.mark.gpu, pytest.mark.skipif(not has_gpu(), reason="needs a GPU")]
 
 
-def _busy():
-    """A few milliseconds of work on the current stream."""
+def _busy(products=8):
+    """Milliseconds of work on the current stream."""
     big = torch.full((2048, 2048), 2.0**-6, device="cuda")
-    for _ in range(8):
+    for _ in range(products):
         big = big @ big
     return big
 
@@ -79,3 +79,78 @@ def test_layer_calls_on_a_side_stream():
         torch.cuda.synchronize()
         assert torch.equal(early, ref.cpu()) and torch.equal(out, ref)
         del keep
+
+
+@pytest.mark.parametrize("raw", [False, True])
+def test_a_dropped_output_is_not_reused_while_the_current_stream_reads_it(raw):
+    """The output of a call on a side stream belongs to that stream; the current stream
+    waits for it, reads it late and drops it.  The side stream's next call waits for
+    nothing, so it has to get other memory."""
+    import combine_grouped_gemm_amd as m
+    rows, cols = 3000, 512
+    x = [torch.full((rows, cols), v, dtype=torch.bfloat16, device="cuda") for v in (1.0, -1.0)]
+    side = torch.cuda.Stream()
+    stream = side.cuda_stream if raw else side
+    torch.cuda.synchronize()
+    for _ in range(4):
+        q, s = m.moe_quant_rows(x[0], stream=stream)
+        side.synchronize()
+        keep = _busy()
+        read = q.clone()                                   # late, on the current stream
+        at = q.data_ptr()
+        del q, s
+        again, _ = m.moe_quant_rows(x[1], stream=stream)
+        assert again.data_ptr() != at
+        torch.cuda.synchronize()
+        assert bool((read == 127).all()) and bool((again == -127).all())
+        del keep, read, again, _
+
+
+def test_workspaces_of_a_side_stream_are_reused_while_the_current_stream_is_busy():
+    """The current stream never reads a workspace, so it does not hold one up."""
+    import combine_grouped_gemm_amd as m
+    T, K, E = 20000, 8, 1024
+    ids = torch.rand(T, E, generator=torch.Generator().manual_seed(1)).topk(K, 1).indices.to(torch.int32).cuda()
+    out = m.moe_layout(ids, E, 0, E, T * K)
+    side = torch.cuda.Stream()
+    _busy(2)
+    m.moe_layout(ids, E, 0, E, T * K, **out, stream=side)
+    torch.cuda.synchronize()
+    before, need = torch.cuda.memory_reserved(), m.moe_layout_workspace_bytes(T, K, E)
+    keep = _busy(200)
+    for _ in range(100):
+        m.moe_layout(ids, E, 0, E, T * K, **out, stream=side)
+    assert torch.cuda.memory_reserved() - before < 50 * need
+    torch.cuda.synchronize()
+    del keep
+
+
+def test_a_captured_graph_with_a_forked_stream():
+    """Outputs made inside a capture, on a stream that forks from it, and dropped there."""
+    import combine_grouped_gemm_amd as m
+    x = torch.randn(700, 256, device="cuda")
+    main, side, g = torch.cuda.Stream(), torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    m.moe_quant_rows(x)
+    main.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.graph(g, stream=main):
+        side.wait_stream(main)
+        q, s = m.moe_quant_rows(x, stream=side)
+        main.wait_stream(side)
+        a = q.to(torch.float32) * s[:, None]
+        del q, s
+        side.wait_stream(main)
+        q, s = m.moe_quant_rows(a, stream=side)
+        main.wait_stream(side)
+        b = q.to(torch.float32) * s[:, None]
+        del q, s
+    for _ in range(4):
+        x.copy_(torch.randn(700, 256, device="cuda"))
+        a.zero_()
+        b.zero_()
+        torch.cuda.synchronize()
+        g.replay()
+        torch.cuda.synchronize()
+        q, s = m.moe_quant_rows(x)
+        want = q.to(torch.float32) * s[:, None]
+        q, s = m.moe_quant_rows(want)
+        assert torch.equal(a, want) and torch.equal(b, q.to(torch.float32) * s[:, None])
