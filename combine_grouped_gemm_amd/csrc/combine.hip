@@ -113,11 +113,8 @@ __global__ __launch_bounds__(kCombThreads) void combine_kernel(
     combine_token<KIND, ALL_LANES>(y, row_of, w, blockIdx.x, K, H, cap, c, c < H / 8, threadIdx.x % kWave, out);
 }
 
-}  // namespace
-
-hipError_t launch_combine(const void* y, int kind, const int32_t* row_of, const float* w, int B,
-                          int K, int H, void* out, int cap, hipStream_t stream) {
-    if (B == 0) return hipSuccess;
+hipError_t launch_tokens(const void* y, int kind, const int32_t* row_of, const float* w, int B,
+                         int K, int H, void* out, int cap, hipStream_t stream) {
     // slices of at most kCombThreads vectors, balanced (a 360-vector row is two
     // slices of 180, not 256 + 104), in whole waves
     const int nvec = H / 8;
@@ -131,6 +128,17 @@ hipError_t launch_combine(const void* y, int kind, const int32_t* row_of, const 
     else if (kind == 1) small ? go(combine_kernel<1, false>) : go(combine_kernel<1, true>);
     else small ? go(combine_kernel<2, false>) : go(combine_kernel<2, true>);
     return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_combine(const void* y, int kind, const int32_t* row_of, const float* w, int B,
+                          int K, int H, void* out, int cap, hipStream_t stream) {
+    const size_t row_bytes = (size_t)H * (kind == 1 ? 2 : 4);     // of out
+    return launch_in_parts(B, [&](size_t b0, int n) {
+        return launch_tokens(y, kind, row_of + b0 * K, w + b0 * K, n, K, H, static_cast<char*>(out) + b0 * row_bytes,
+                             cap, stream);
+    });
 }
 
 }  // namespace moeep

@@ -139,11 +139,8 @@ __global__ __launch_bounds__(kDispThreads) void dispatch_fp8_kernel(
     }
 }
 
-}  // namespace
-
-hipError_t launch_dispatch(const SegTable& seg, int B, int H, int kind, const int32_t* row_of,
-                           int K, void* xd, float* xd_scales, int cap, hipStream_t stream) {
-    if (B == 0) return hipSuccess;
+hipError_t launch_tokens(const SegTable& seg, int B, int H, int kind, const int32_t* row_of,
+                         int K, void* xd, float* xd_scales, int cap, hipStream_t stream) {
     if (kind == 0 || kind == 1) {
         const size_t row_bytes = (size_t)H * (kind == 0 ? 4 : 2);
         const int nvec = (int)(row_bytes / 16);
@@ -158,6 +155,15 @@ hipError_t launch_dispatch(const SegTable& seg, int B, int H, int kind, const in
                            row_of, K, cap, static_cast<uint8_t*>(xd), xd_scales);
     }
     return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_dispatch(const SegTable& seg, int B, int H, int kind, const int32_t* row_of,
+                           int K, void* xd, float* xd_scales, int cap, hipStream_t stream) {
+    return launch_in_parts(B, [&](size_t b0, int n) {
+        return launch_tokens(seg.from(b0), n, H, kind, row_of + b0 * K, K, xd, xd_scales, cap, stream);
+    });
 }
 
 }  // namespace moeep

@@ -9,14 +9,24 @@
 
 namespace moeep {
 
+// Tokens of one launch of a kernel with up to 512 threads a token: a grid of 2^32
+// threads or more is cut short without an error, so longer batches take several.
+constexpr int kMostTokens = 1 << 22;
+
+// part(first token, tokens) for each of the launches that B tokens take.
+template <typename Part>
+hipError_t launch_in_parts(int B, Part part) {
+    for (long long b0 = 0; b0 < B; b0 += kMostTokens) {
+        const hipError_t e = part((size_t)b0, B - b0 < kMostTokens ? (int)(B - b0) : kMostTokens);
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
+}
+
 // route.hip (map: optional (E) device table logical -> physical expert id; n_shared
 // always-on slots appended to each output row, ids E.., gate 1)
 hipError_t launch_route(const float* logits, int B, int E, int K, int32_t* ids, float* w,
                         const int32_t* map, int n_shared, hipStream_t stream);
-
-// Tokens of one launch of a kernel with up to 512 threads a token: a grid of 2^32
-// threads or more is cut short without an error, so longer batches take several.
-constexpr int kMostTokens = 1 << 22;
 
 // route_scored.hip
 struct RouteScoredArgs {
@@ -57,6 +67,13 @@ struct SegTable {
     const void* ptr[kMaxSeg];
     int start[kMaxSeg + 1];   // prefix sums of segment rows
     int n;
+
+    // the same segments with tokens counted from b0 (earlier ones start below 0)
+    SegTable from(size_t b0) const {
+        SegTable t = *this;
+        for (int s = 0; s <= n; ++s) t.start[s] -= (int)b0;
+        return t;
+    }
 };
 // kind: 0 = f32 copy, 1 = bf16 copy, 2 = bf16 -> fp8 quantise
 hipError_t launch_dispatch(const SegTable& seg, int B, int H, int kind, const int32_t* row_of,

@@ -369,16 +369,12 @@ hipError_t launch_quant_any(const QuantArgs& a, hipStream_t stream) {
 hipError_t launch_dispatch_i8(const SegTable& seg, int B, int H, bool f32, const int32_t* row_of, int K, void* xd,
                               float* xd_scales, int cap, hipStream_t stream) {
     uint8_t* q = static_cast<uint8_t*>(xd);
-    for (long long b0 = 0; b0 < B; b0 += kMostTokens) {
-        SegTable part = seg;                                      // its tokens counted from b0
-        for (int s = 0; s <= seg.n; ++s) part.start[s] -= (int)b0;
-        const int n = B - b0 < kMostTokens ? (int)(B - b0) : kMostTokens;
+    return launch_in_parts(B, [&](size_t b0, int n) {
+        const SegTable part = seg.from(b0);
         const int32_t* rows = row_of + b0 * K;
-        const hipError_t e = f32 ? launch_dispatch_any<true>(part, n, H, rows, K, q, xd_scales, cap, stream)
-                                 : launch_dispatch_any<false>(part, n, H, rows, K, q, xd_scales, cap, stream);
-        if (e != hipSuccess) return e;
-    }
-    return hipSuccess;
+        return f32 ? launch_dispatch_any<true>(part, n, H, rows, K, q, xd_scales, cap, stream)
+                   : launch_dispatch_any<false>(part, n, H, rows, K, q, xd_scales, cap, stream);
+    });
 }
 
 hipError_t launch_quant_rows(const QuantArgs& a, bool f32, hipStream_t stream) {

@@ -129,13 +129,13 @@ hipError_t launch_epl(const float* logits, int B, int E, int K, int32_t* ids, fl
 
 hipError_t launch_route(const float* logits, int B, int E, int K, int32_t* ids, float* w,
                         const int32_t* map, int n_shared, hipStream_t stream) {
-    if (B == 0) return hipSuccess;
     const int epl = (E + kWave - 1) / kWave;
-    if (epl <= 1) return launch_epl<1>(logits, B, E, K, ids, w, map, n_shared, stream);
-    if (epl <= 2) return launch_epl<2>(logits, B, E, K, ids, w, map, n_shared, stream);
-    if (epl <= 4) return launch_epl<4>(logits, B, E, K, ids, w, map, n_shared, stream);
-    if (epl <= 8) return launch_epl<8>(logits, B, E, K, ids, w, map, n_shared, stream);
-    return launch_epl<16>(logits, B, E, K, ids, w, map, n_shared, stream);
+    const auto launch = epl <= 1 ? launch_epl<1> : epl <= 2 ? launch_epl<2> : epl <= 4 ? launch_epl<4>
+                      : epl <= 8 ? launch_epl<8> : launch_epl<16>;
+    return launch_in_parts(B, [&](size_t b0, int n) {
+        const size_t at = b0 * (K + n_shared);
+        return launch(logits + b0 * E, n, E, K, ids + at, w + at, map, n_shared, stream);
+    });
 }
 
 }  // namespace moeep

@@ -575,16 +575,14 @@ hipError_t launch_tokens(const RouteScoredArgs& a, hipStream_t stream) {
 
 hipError_t launch_route_scored(const RouteScoredArgs& a, hipStream_t stream) {
     const int ld = a.K + a.n_shared;
-    for (long long b0 = 0; b0 < a.B; b0 += kMostTokens) {
+    return launch_in_parts(a.B, [&](size_t b0, int n) {
         RouteScoredArgs part = a;
-        part.B = a.B - b0 < kMostTokens ? (int)(a.B - b0) : kMostTokens;
+        part.B = n;
         part.logits = static_cast<const char*>(a.logits) + b0 * a.E * (a.bf16 ? 2 : 4);
         part.ids = a.ids + b0 * ld;
         part.w = a.w + b0 * ld;
-        const hipError_t e = launch_tokens(part, stream);
-        if (e != hipSuccess) return e;
-    }
-    return hipSuccess;
+        return launch_tokens(part, stream);
+    });
 }
 
 }  // namespace moeep
