@@ -182,15 +182,17 @@ __global__ __launch_bounds__(kWave) void layout_rank_kernel(
         if (in) row_of[s] = row;
         __syncthreads();
     }
-    // padding rows of src_of
+    // padding rows of src_of (rows up to 2^31 - 1: unsigned, so that a step past them,
+    // or R plus the first one, does not wrap to a negative row)
+    const uint32_t first = blockIdx.x * kWave + lane, stride = gridDim.x * kWave;
     if (MASKED) {
-        for (int r = blockIdx.x * kWave + lane; r < E_loc * cap; r += gridDim.x * kWave) {
-            const int j = r / cap, q = r - j * cap;
+        for (uint32_t r = first; r < (uint32_t)(E_loc * cap); r += stride) {
+            const uint32_t j = r / (uint32_t)cap, q = r - j * (uint32_t)cap;
             const int n = counts[e_begin + j];
-            if (q >= n) src_of[r] = -1;
+            if (q >= (uint32_t)n) src_of[r] = -1;
         }
     } else {
-        for (int r = R + blockIdx.x * kWave + lane; r < cap; r += gridDim.x * kWave) src_of[r] = -1;
+        for (uint32_t r = (uint32_t)R + first; r < (uint32_t)cap; r += stride) src_of[r] = -1;
     }
 }
 
@@ -287,14 +289,14 @@ __global__ __launch_bounds__(kFusedThreads) void layout_fused_kernel(
         }
         __syncthreads();                               // s_wc is read above before the next chunk clears it
     }
-    // padding rows of src_of
+    // padding rows of src_of (unsigned: see layout_rank_kernel)
     if (MASKED) {
-        for (int r = tid; r < E_loc * cap; r += kFusedThreads) {
-            const int j = r / cap, q = r - j * cap;
-            if (q >= s_cnt[e_begin + j]) src_of[r] = -1;
+        for (uint32_t r = tid; r < (uint32_t)(E_loc * cap); r += kFusedThreads) {
+            const uint32_t j = r / (uint32_t)cap, q = r - j * (uint32_t)cap;
+            if (q >= (uint32_t)s_cnt[e_begin + j]) src_of[r] = -1;
         }
     } else {
-        for (int r = R + tid; r < cap; r += kFusedThreads) src_of[r] = -1;
+        for (uint32_t r = (uint32_t)R + tid; r < (uint32_t)cap; r += kFusedThreads) src_of[r] = -1;
     }
 }
 

@@ -90,3 +90,27 @@ def test_combine(ydt, odt, K):
         bar += 2.0**-8 * (ref.abs() + bar)
     assert bool(((out[:64].cpu().double() - ref).abs() <= bar).all())
     assert _same_everywhere(out, out[:64])
+
+
+@pytest.mark.parametrize("masked", [False, True])
+@pytest.mark.parametrize("T", [3, 3000])
+def test_layout_of_a_buffer_of_two_to_the_31_rows(T, masked):
+    """One launch and three; the padding of the last rows, whose number plus the grid's
+    step passes 2^31."""
+    import combine_grouped_gemm_amd as m
+    cap, E, K = 2**31 - 1, 4, 2
+    ids = torch.rand(T, E, generator=_gen(4)).topk(K, 1).indices.to(torch.int32)
+    src = torch.full((cap,), 5, dtype=torch.int32, device="cuda")
+    if masked:                                             # the second expert's block is the whole buffer
+        ref = oracle.layout_masked(ids.numpy(), E, 1, 2, 4 * T)
+        lay = m.moe_layout_masked(ids.cuda(), E, 1, 2, cap, src_of=src)
+        n = int(ref["m"][0])
+        assert lay["m"].tolist() == [n]
+    else:
+        ref = oracle.layout(ids.numpy(), E, 0, E, T * K)
+        lay = m.moe_layout(ids.cuda(), E, 0, E, cap, src_of=src)
+        n = T * K
+        np.testing.assert_array_equal(lay["offsets"].cpu().numpy(), ref["offsets"])
+    np.testing.assert_array_equal(lay["row_of"].cpu().numpy(), ref["row_of"])
+    np.testing.assert_array_equal(src[:n].cpu().numpy(), ref["src_of"][:n])
+    assert bool((src[n:] == -1).all())
