@@ -184,7 +184,8 @@ moe_status_t ffn_gate_up(const void* xd, const float* xd_scales, Rows rows,
     REQUIRE(w_gate && w_up && (h || cap_rows == 0), "null weight or h pointer");
     REQUIRE(aligned16(w_gate) && aligned16(w_up) && aligned16(h), "weights and h must be 16-byte aligned");
     if (act_dt == MOE_FP8_E4M3)
-        REQUIRE(xd_scales && w_gate_scales && w_up_scales && h_scales, "fp8 needs all scale pointers");
+        REQUIRE(((xd_scales && h_scales) || cap_rows == 0) && w_gate_scales && w_up_scales,
+                "fp8 needs all scale pointers");
     if (act_dt == MOE_INT8)
         REQUIRE((xd_scales || cap_rows == 0) && w_gate_scales && w_up_scales,
                 "int8 needs the row and channel scale pointers");
@@ -204,7 +205,8 @@ moe_status_t ffn_down(const void* h, const float* h_scales, Rows rows, int E_loc
     if (s != MOE_OK) return s;
     REQUIRE(w_down && (y || cap_rows == 0), "null weight or y pointer");
     REQUIRE(aligned16(w_down) && aligned16(y), "weights and y must be 16-byte aligned");
-    if (act_dt == MOE_FP8_E4M3) REQUIRE(h_scales && w_down_scales, "fp8 needs all scale pointers");
+    if (act_dt == MOE_FP8_E4M3)
+        REQUIRE((h_scales || cap_rows == 0) && w_down_scales, "fp8 needs all scale pointers");
     if (act_dt == MOE_INT8)
         REQUIRE((h_scales || cap_rows == 0) && w_down_scales, "int8 needs the row and channel scale pointers");
     auto f = ffn_args(h, h_scales, rows, E_local, cap_rows, I, H, w_down, nullptr, w_down_scales,
@@ -494,10 +496,10 @@ moe_status_t moe_dispatch(const void* const* seg_x, const int32_t* seg_rows, int
         seg.start[i + 1] = (int)B;
     }
     if (B > 0) {
-        REQUIRE(row_of && xd, "null row_of or xd");
+        REQUIRE(row_of && (xd || cap_rows == 0), "null row_of or xd");
         REQUIRE(aligned16(xd), "xd must be 16-byte aligned");
-        if (kind == 2) REQUIRE(xd_scales, "fp8 dispatch needs xd_scales");
-        if (kind == 3) REQUIRE(xd_scales, "int8 dispatch needs xd_scales");
+        if (kind == 2) REQUIRE(xd_scales || cap_rows == 0, "fp8 dispatch needs xd_scales");
+        if (kind == 3) REQUIRE(xd_scales || cap_rows == 0, "int8 dispatch needs xd_scales");
     }
     if (kind == 3)
         return launched(moeep::launch_dispatch_i8(seg, (int)B, H, x_dt == MOE_F32, row_of, K, xd, xd_scales, cap_rows,
@@ -647,7 +649,7 @@ moe_status_t moe_combine(const void* y, moe_dtype_t y_dt, int cap_rows, const in
     else if (y_dt == MOE_BF16 && out_dt == MOE_F32) kind = 2;
     else return fail(MOE_ERR_UNSUPPORTED, "unsupported combine (y_dt, out_dt) = (%d, %d)", y_dt, out_dt);
     if (B > 0) {
-        REQUIRE(y && row_of && topk_w && out, "null pointer argument");
+        REQUIRE((y || cap_rows == 0) && row_of && topk_w && out, "null pointer argument");
         REQUIRE(aligned16(y) && aligned16(out), "y and out must be 16-byte aligned");
     }
     return launched(moeep::launch_combine(y, kind, row_of, topk_w, B, K, H, out, cap_rows, stream),

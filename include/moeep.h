@@ -30,6 +30,9 @@
  *   - Sizes: 1 <= K <= E <= 1024; 0 <= e_begin < e_end <= E; B >= 0;
  *     H and I multiples of 8 (of 16 when activations are fp8 or int8); row
  *     base pointers 16-byte aligned.
+ *   - A buffer of cap_rows = 0 rows (xd, h, y and their scales) may be NULL in
+ *     the dispatch, quantisation, FFN and combine calls: it is neither read nor
+ *     written, and moe_combine writes zeros.
  *   - Calls on one stream run in order; calls that share output or
  *     workspace buffers on different streams race.
  *   - Expert ids outside [0, E) in topk_ids are treated as unrouted slots.
