@@ -447,25 +447,33 @@ def _scale_cols(code, cols):
     return -(-cols // FP8_BLOCK) if code == MOE_FP8_E4M3 else 1
 
 
-def moe_quant_rows(x, rows=None, cap_per_expert=None, q=None, scales=None, stream=None):
+def moe_quant_rows(x, rows=None, cap_per_expert=None, q=None, scales=None, stream=None, E_loc=None):
     """int8 codes (cap_rows, cols) and a scale (cap_rows,) for each valid row of x
     (fp32 or bf16).  rows: the contiguous layout's offsets (E_loc + 1), or with
     cap_per_expert the masked layout's m (E_loc) (moe_quant_rows_masked); None
     quantises every row, e.g. weight rows (a scale for each output channel).
+    E_loc: the local experts, when rows is a longer buffer (default: as many as it
+    describes; the FFN calls take them from the weights).
     Other rows of given q and scales are left as they were."""
     _dev(x, "x", None, 2)
     if x.dtype not in (torch.float32, torch.bfloat16):
         raise ValueError(f"x must be float32 or bfloat16 (got {x.dtype})")
     cap, cols = x.shape
-    E_loc, third = 0, cap
+    third = cap
     if rows is None:
         if cap_per_expert is not None:
             raise ValueError("cap_per_expert needs the masked layout's m")
+        if E_loc is not None:
+            raise ValueError("E_loc needs the layout's offsets or m")
+        E_loc = 0
     else:
-        name = "offsets" if cap_per_expert is None else "m"
+        name, last = ("offsets", 1) if cap_per_expert is None else ("m", 0)
         _dev(rows, name, torch.int32, 1)
-        _need(rows, name, numel=2 if cap_per_expert is None else 1)    # an empty tensor's null pointer means all rows
-        E_loc = rows.numel() - 1 if cap_per_expert is None else rows.numel()
+        if E_loc is None:
+            E_loc = max(rows.numel() - last, 1)       # an empty tensor's null pointer would mean all rows
+        if E_loc < 1:
+            raise ValueError(f"E_loc must be positive (got {E_loc})")
+        _need(rows, name, numel=E_loc + last)
         third = _rows_arg(rows, cap_per_expert, E_loc, cap)
     if q is None:
         q = _new((cap, cols), torch.int8, x.device, stream)

@@ -145,7 +145,7 @@ class MoELayer:
     def quant_h(self, stream=None):
         """int8 only: gate/up's bf16 h to int8 rows and their scales."""
         moe_quant_rows(self.h_act, self.rows, cap_per_expert=self.cap_e, q=self.h, scales=self.h_scales,
-                       stream=stream)
+                       stream=stream, E_loc=self.E_loc)
 
     def down(self, w, stream=None):
         moe_ffn_down(self.h, self.h_scales, self.rows, w["down"], w.get("down_scale"), self.y,
