@@ -28,13 +28,13 @@ hipError_t launch_wide(const FfnArgs& a, hipStream_t stream) {
 }
 
 // The weights' cache policy.  Read with the non-temporal hint they leave L2 at
-// once: 5% faster where each line is read by one tile (T = 64 decode 857 against
-// 887 us, EP share 209 against 219).  Rows that are no whole number of 128-byte
-// lines need each line in two k-steps (H = I = 2880: 300 us without the hint,
-// 342 with it), and experts with more rows than a tile have their weights read
-// again by the next tile (256 rows prefill 2085 us without, 2133 with it; 64-row
-// tiles on 100 rows 3-8% faster without, on 600 rows 9-18%; on 40 rows, one tile,
-// 5-9% slower).
+// once: faster where each line is read by one tile (2 rows per expert of the
+// DeepSeek-shaped layer, gate/up 944 us against 1062; EP share, 115 rows, 179
+// against 188; 64-row tiles on 10-60 rows 1-3%).  Rows that are no whole number of
+// 128-byte lines need each line in two k-steps (H = I = 2880, 128 rows: 284 us
+// without the hint, 337 with it), and experts with more rows than a tile have their
+// weights read again by the next tile (256 rows 2188 us without, 2201 with; 64-row
+// tiles on 100 rows 6-14% faster without, on 600 rows 11-14%).
 template <int BM, int BN, int S>
 hipError_t launch_out(const FfnArgs& a, bool gated, hipStream_t stream) {
     const bool nt = a.ldw % 128 == 0 && a.rows_hint < BM * 3 / 4;
@@ -45,25 +45,27 @@ hipError_t launch_out(const FfnArgs& a, bool gated, hipStream_t stream) {
 
 }  // namespace
 
-// Tile shape.  Few rows per expert: 64 x 128 tiles, two workgroups per CU (T = 128
-// decode gate/up 1003 us against 1022 us with 256 x 256, down 524 against 538; 16
-// rows per expert at H = I = 2880: 447 against 475).  Many: 256 x 256 (64 rows per
-// expert: 1285 us against 1663; 256: 2120 against 5180).  They meet at about 32
-// (1194 against 1257 at H = 7168, 482 against 487 at 2880); 128 x 128 tiles were
-// never better than both by more than 1.5%.  However many rows there are, large
-// tiles that leave CUs without one lose to small ones that all run at once: 8
-// experts of 180 rows, 768 columns of 7168, 24 large tiles 64 us, 144 small 33;
-// 250 rows, 2048 columns, 64 large 79, 512 small 57; 100 rows, gate and up of 2048
-// columns, 128 large 72.5, 512 small 68.  Past one round of small tiles: 16 such
-// experts 84 against 129.
+// Tile shape.  Few rows per expert: 64 x 128 tiles in three stages, two workgroups
+// per CU (4 rows, all 256 experts with some: gate/up 1061 us against 1088 with 256 x
+// 256, down 569 against 599; 16 rows at H = I = 2880: gate/up 399 against 409).
+// Many: 256 x 256 (64 rows: 1337 us against 1648; 256: 2147 against 3646).  They meet
+// at about 32 (1197 against 1201 at H = 7168, down 735 against 721; 432 against 437 at
+// 2880).  However many rows there are, large tiles that leave CUs without one lose to
+// small ones that all run at once: 8 experts of 180 rows, 768 columns of 7168, 24
+// large tiles 72 us, 144 small 34; 250 rows, 2048 columns, 64 large 89, 512 small 58;
+// where the large ones number half the CUs they are even (100 rows, gate and up of
+// 2048 columns, 128 large 64 us, 512 small 67).  Past one round of small tiles: 16
+// such experts 81 against 119.
+// Two stages instead of three under the small tile gain 0.1-0.2 us of 5 where
+// fewer than some 200 tiles take one or two steps each, and lose 5-25% where more do
+// (256 experts of 512 columns, K = 144: 12.7 us, 15.2 with two).
 hipError_t launch_ffn_i8(const FfnArgs& a, bool gated, hipStream_t stream) {
     constexpr int BM = 64, BN = 128;
     const int cols = gated ? BN / 2 : BN;
     const long long row_tiles = ((long long)a.rows_hint + BM - 1) / BM;
     const long long small = a.E_loc * row_tiles * ((a.N + cols - 1) / cols);
     if (a.rows_hint >= 32 && small > 2 * device_cu_count()) return launch_out<256, 256, 2>(a, gated, stream);
-    // two steps have nothing for a third stage (31 experts, K = 144, 14.7 us against 16.6)
-    return a.Kdim > 2 * widei8::BK ? launch_out<BM, BN, 3>(a, gated, stream) : launch_out<BM, BN, 2>(a, gated, stream);
+    return launch_out<BM, BN, 3>(a, gated, stream);
 }
 
 }  // namespace moeep
