@@ -509,7 +509,10 @@ __global__ __launch_bounds__(kRowWaves * kWave) void route_scored_kernel(RouteSc
         const double kth = -row_max(pick ? -c : -(double)INFINITY);
         ok = ok && kth > key_bound(last);
     }
-    ok = ok && ((ballot64(odd) >> (row * 16)) & 0xffffu) == 0;
+    // every lane votes, whatever its ok: a NaN among the candidates makes kth, and so
+    // ok, differ between the lanes of a row
+    const bool strange = ((ballot64(odd) >> (row * 16)) & 0xffffu) != 0;
+    ok = ok & !strange;
 
     const double total = row_sum(pick ? s : 0.0);
     const int ld = p.K + p.n_shared;
