@@ -112,14 +112,16 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
-# the current stream of a device as an integer: torch.cuda.current_stream() builds an
-# object for it, which costs as much as the rest of a call
+# the current device, and the current stream of a device as an integer:
+# torch.cuda.current_stream() builds an object for it, which costs as much as the rest
+# of a call
+_current_device = torch._C._cuda_getDevice
 _raw_stream = torch._C._cuda_getCurrentRawStream
 
 
 def _stream(stream):
     if stream is None:
-        return _raw_stream(torch.cuda.current_device())
+        return _raw_stream(_current_device())
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
     return int(stream)
@@ -128,13 +130,17 @@ def _stream(stream):
 def _call(fn, t, stream, *args):
     """One library call with t's device current, on `stream` (None: that device's current stream)."""
     index = t.get_device()
-    if isinstance(stream, torch.cuda.Stream) and stream.device_index != index:
-        raise ValueError(f"stream must be of the tensors' device {t.device} (got one of cuda:{stream.device_index})")
-    if index == torch.cuda.current_device():
-        _check(fn(*args, _raw_stream(index) if stream is None else _stream(stream)))
-    else:
+    if index != _current_device():
         with torch.cuda.device(index):
-            _check(fn(*args, _stream(stream)))
+            return _call(fn, t, stream, *args)
+    if stream is None:
+        status = fn(*args, _raw_stream(index))
+    else:
+        if isinstance(stream, torch.cuda.Stream) and stream.device_index != index:
+            raise ValueError(f"stream must be of the tensors' device {t.device} (got one of cuda:{stream.device_index})")
+        status = fn(*args, _stream(stream))
+    if status != MOE_OK:
+        _check(status)
 
 
 def _new(shape, dtype, device, stream, scratch=False):
@@ -143,14 +149,23 @@ def _new(shape, dtype, device, stream, scratch=False):
     on return would go to that stream's next allocation while the call is still running.
     For an output the current stream, where the caller goes on, is noted as a user too: what
     it still reads when the tensor is dropped is not written by the given stream's next call."""
-    if stream is None:
+    if stream is None or _stream(stream) == _raw_stream(device.index):
         return torch.empty(shape, dtype=dtype, device=device)
     if not isinstance(stream, torch.cuda.Stream):
         stream = torch.cuda.ExternalStream(int(stream), device=device)
-    with torch.cuda.stream(stream):
-        t = torch.empty(shape, dtype=dtype, device=device)
+    current = torch.cuda.current_stream(device)
+    if device.index == _current_device():
+        # what torch.cuda.stream() does, at a third of its time
+        torch.cuda.set_stream(stream)
+        try:
+            t = torch.empty(shape, dtype=dtype, device=device)
+        finally:
+            torch.cuda.set_stream(current)
+    else:
+        with torch.cuda.stream(stream):
+            t = torch.empty(shape, dtype=dtype, device=device)
     if not scratch:
-        t.record_stream(torch.cuda.current_stream(device))
+        t.record_stream(current)
     return t
 
 
@@ -561,10 +576,10 @@ def _rows_arg(rows, cap_per_expert, E_loc, n_rows):
     return int(cap_per_expert)
 
 
-def _check_ffn(a, a_scales, rows, cap_per_expert, E_loc, Kdim, cap, act, **tensors):
+def _check_ffn(a, a_scales, rows, cap_per_expert, E_loc, Kdim, cap, act, also, **tensors):
     """Shapes of the FFN operands: the activation rows (cap, Kdim) [+ fp8 or
     int8 scales], the row description (offsets E_loc + 1, or m E_loc), and each
-    named (tensor, shape or minimum element count or None) pair; one device for all."""
+    named (tensor, shape or minimum element count) pair; one device for all, `also` too."""
     if a.shape[1] != Kdim:
         raise ValueError(f"activations must have {Kdim} columns (got {a.shape[1]})")
     _need(rows, "offsets" if cap_per_expert is None else "m",
@@ -581,16 +596,18 @@ def _check_ffn(a, a_scales, rows, cap_per_expert, E_loc, Kdim, cap, act, **tenso
                 if t is None:
                     raise ValueError(f"int8 weights need {name}")
                 _dev(t, name, torch.float32)
+    _same_device(a, "activations", a_scales if act in (MOE_FP8_E4M3, MOE_INT8) else None, rows, *also)
+    index = a.get_device()
     for name, (t, want) in tensors.items():
         if t is None:
             continue
         _dev(t, name)
+        if t.get_device() != index:
+            _same_device(a, "activations", t)
         if isinstance(want, tuple):
             _need(t, name, shape=want)
         else:
             _need(t, name, numel=want)
-    _same_device(a, "activations", a_scales if act in (MOE_FP8_E4M3, MOE_INT8) else None, rows,
-                 *(t for t, _ in tensors.values()))
 
 
 def _w_scales(act, scales, E_loc, rows, cols):
@@ -639,8 +656,8 @@ def moe_ffn_gate_up(xd, xd_scales, offsets, w_gate, w_up, w_gate_scales=None, w_
         raise ValueError(f"h must be {_h_dtype_for(xd)} (got {h.dtype})")
     nbI = -(-I // FP8_BLOCK)
     fp8 = act == MOE_FP8_E4M3
-    _check_ffn(xd, xd_scales, offsets, cap_per_expert, E_loc, H, cap, act,
-               w_gate=(w_gate, None), w_up=(w_up, tuple(w_gate.shape)), h=(h, cap * I),
+    _check_ffn(xd, xd_scales, offsets, cap_per_expert, E_loc, H, cap, act, (w_gate,),
+               w_up=(w_up, tuple(w_gate.shape)), h=(h, cap * I),
                h_scales=(h_scales if fp8 else None, cap * nbI),
                w_gate_scales=_w_scales(act, w_gate_scales, E_loc, I, H),
                w_up_scales=_w_scales(act, w_up_scales, E_loc, I, H))
@@ -670,7 +687,7 @@ def moe_ffn_down(h, h_scales, offsets, w_down, w_down_scales=None, y=None, y_dty
     y_dtype = _y_dtype_for(act) if y_dtype is None else y_dtype
     if y is None:
         y = _new((cap, H), y_dtype, h.device, stream)
-    _check_ffn(h, h_scales, offsets, cap_per_expert, E_loc, I, cap, act, w_down=(w_down, None), y=(y, cap * H),
+    _check_ffn(h, h_scales, offsets, cap_per_expert, E_loc, I, cap, act, (w_down,), y=(y, cap * H),
                w_down_scales=_w_scales(act, w_down_scales, E_loc, H, I))
     fn = lib().moe_ffn_down if cap_per_expert is None else lib().moe_ffn_down_masked
     _call(fn, h, stream, _ptr(h), _ptr(h_scales), _ptr(offsets), E_loc, third, H, I, act,
@@ -699,9 +716,10 @@ def moe_grouped_ffn(xd, xd_scales, offsets, w_gate, w_up, w_down, w_gate_scales=
     need = moe_ffn_workspace_bytes(cap, I, act)
     if ws is None:
         ws = _new(max(need, 256), torch.uint8, xd.device, stream, scratch=True)
-    _check_ffn(xd, xd_scales, offsets, cap_per_expert, E_loc, H, cap, act,
-               w_gate=(w_gate, None), w_up=(w_up, tuple(w_gate.shape)), w_down=(w_down, (E_loc, H, w_down.shape[2])),
-               y=(y, cap * H), ws=(ws, None),
+    _dev(ws, "ws")
+    _check_ffn(xd, xd_scales, offsets, cap_per_expert, E_loc, H, cap, act, (w_gate, ws),
+               w_up=(w_up, tuple(w_gate.shape)), w_down=(w_down, (E_loc, H, w_down.shape[2])),
+               y=(y, cap * H),
                w_gate_scales=_w_scales(act, w_gate_scales, E_loc, I, H),
                w_up_scales=_w_scales(act, w_up_scales, E_loc, I, H),
                w_down_scales=_w_scales(act, w_down_scales, E_loc, H, I))

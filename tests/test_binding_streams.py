@@ -12,12 +12,17 @@ class Recorder:
     """Stands for the loaded library: host queries answer, launches are written down."""
 
     def __init__(self, real):
-        self.real, self.launched = real, []
+        self.real, self.launched, self.on_launch = real, [], lambda: None
 
     def __getattr__(self, name):
         if name in HOST_QUERIES:
             return getattr(self.real, name)
-        return lambda *args: self.launched.append((name, args)) or 0
+        return lambda *args: self.launch(name, args)
+
+    def launch(self, name, args):
+        self.launched.append((name, args))
+        self.on_launch()
+        return m.MOE_OK
 
 
 i32 = lambda *s: torch.zeros(s, dtype=torch.int32)
@@ -90,7 +95,7 @@ class Devices:
     def __init__(self, monkeypatch, where):
         self.current = 0
         monkeypatch.setattr(torch.Tensor, "get_device", lambda t: where())
-        monkeypatch.setattr(torch.cuda, "current_device", lambda: self.current)
+        monkeypatch.setattr(m, "_current_device", lambda: self.current)
         monkeypatch.setattr(m, "_raw_stream", lambda index: 1000 + index)
         devices = self
 
@@ -120,7 +125,7 @@ def test_the_tensors_device_is_current_during_a_call(on_host, monkeypatch, name)
     """Launches go to the tensors' device, on that device's current stream."""
     d = Devices(monkeypatch, lambda: 1)
     during = []
-    monkeypatch.setattr(m, "_check", lambda status: during.append(d.current))
+    on_host.on_launch = lambda: during.append(d.current)
     CALLS[name][0]()
     assert during == [1] and d.current == 0
     assert [args[-1] for _, args in on_host.launched] == [1001]
