@@ -33,12 +33,17 @@
 // Other shapes (E > 512, K > 12, a G that does not divide 16) go through that
 // 64-bit routine, one wave a token, keys in LDS.
 //
-// Measured (MI355X, in a graph): one token of 256 experts, 8 groups, 5.2 us;
-// 8192 of them 7.6-8.8 us (bound by the VALU: some 1800 instructions a wave, two
-// waves a SIMD; reading the logits would take 2 us); 4093 tokens of 128 experts,
-// softmax, bf16, 4.0-4.4 us; 8192 of 512 13.8 us (24.0 with logits read one by
-// one), of 384, softmax, 15.0 (21.5), of 60 in 4 groups 6.4 (14 by the 64-bit
-// routine).  That routine alone: 14.7 and 36.5 us on the first two.
+// Measured (MI355X, in a graph): one token of 256 experts, 8 groups, 5.3 us;
+// 8192 of them 7.6-8.8 us (9.2 alone by the profiler; reading the logits would take
+// 2 us).  Bound by the VALU: 1300 instructions a wave by the counter, two waves a
+// SIMD, issuing 61% of the CUs' busy cycles, with little to hide the rest behind.
+// 4093 tokens of 128 experts, softmax, bf16, 4.0-4.4 us (5.0 by the profiler).  More
+// than 256 experts mean 32 keys a lane (149 VGPRs, scalars spilled, three waves a
+// SIMD): 8192 tokens of 512 12.7-13.8 us (24.0 with logits read one by one), of 384,
+// softmax, 13.1-15.0; 60 in 4 groups 5.5-6.4 (14 by the 64-bit routine).  The 64-bit
+// routine costs four to five times as much: 256 experts with K = 12 7.5 us, K = 13
+// 26.0, K = 22 37.1 (one token 5.2, 10.7, 15.6); 513 experts 42.5, 1024 95; 96 in 3
+// groups 19.6; 512 with K = 22 71.9.
 #include "device_common.hpp"
 #include "launch.hpp"
 
