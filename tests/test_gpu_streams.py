@@ -154,3 +154,21 @@ def test_a_captured_graph_with_a_forked_stream():
         want = q.to(torch.float32) * s[:, None]
         q, s = m.moe_quant_rows(want)
         assert torch.equal(a, want) and torch.equal(b, q.to(torch.float32) * s[:, None])
+
+
+def test_streams_given_by_number():
+    """The null stream and another one by their handles, from inside either."""
+    import combine_grouped_gemm_amd as m
+    lg = torch.randn(50, 16, device="cuda")
+    want = m.moe_route(lg, 2)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    for stream in (0, side.cuda_stream, side, torch.cuda.default_stream()):
+        for inside in (torch.cuda.default_stream(), side):
+            with torch.cuda.stream(inside):
+                got = m.moe_route(lg, 2, stream=stream)
+                lay = m.moe_layout(got[0], 16, 0, 16, 100, stream=stream)
+                assert torch.cuda.current_stream() == inside
+            torch.cuda.synchronize()
+            assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+            assert int(lay["offsets"][-1]) == 100
