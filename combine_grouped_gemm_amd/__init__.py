@@ -22,16 +22,21 @@ __all__ = ["MoeError", "lib", "library_path", "moe_version", "moe_route",
            "moe_grouped_ffn", "moe_combine", "moe_layout_masked", "moe_ffn_gate_up_masked",
            "moe_ffn_down_masked", "moe_grouped_ffn_masked", "moe_route_mapped", "moe_eplb_place", "moe_route_shared",
            "moe_route_scored", "moe_quant_rows", "moe_quant_rows_masked",
+           "moe_checkpoint_rows", "moe_checkpoint_values", "moe_ffn_gate_up_train", "moe_swiglu_backward",
+           "moe_ffn_dgrad", "moe_ffn_wgrad", "moe_route_backward",
            "moe_weight_ld", "moe_packed_weight_bytes", "moe_pack_weights",
-           "MOE_F32", "MOE_BF16", "MOE_FP8_E4M3", "MOE_FP8_E4M3_PO2", "MOE_INT8", "MOE_W_PACKED",
-           "MOE_SCORE_SOFTMAX", "MOE_SCORE_SIGMOID",
+           "MOE_F32", "MOE_BF16", "MOE_FP8_E4M3", "MOE_FP8_E4M3_PO2", "MOE_INT8", "MOE_CKPT8", "MOE_W_PACKED",
+           "MOE_SCORE_SOFTMAX", "MOE_SCORE_SIGMOID", "MOE_SCORE_PICKS",
+           "MOE_GATHER_NONE", "MOE_GATHER_X", "MOE_GATHER_DY",
            "MoELayer"]
 
 MOE_OK, MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED, MOE_ERR_HIP = 0, 1, 2, 3
-MOE_F32, MOE_BF16, MOE_FP8_E4M3, MOE_FP8_E4M3_PO2, MOE_INT8 = 0, 1, 2, 3, 4
-MOE_SCORE_SOFTMAX, MOE_SCORE_SIGMOID = 0, 1
+MOE_F32, MOE_BF16, MOE_FP8_E4M3, MOE_FP8_E4M3_PO2, MOE_INT8, MOE_CKPT8 = 0, 1, 2, 3, 4, 5
+MOE_SCORE_SOFTMAX, MOE_SCORE_SIGMOID, MOE_SCORE_PICKS = 0, 1, 2
+MOE_GATHER_NONE, MOE_GATHER_X, MOE_GATHER_DY = 0, 1, 2
 MOE_W_PACKED = 0x100
 FP8_BLOCK = 128
+CKPT_BLOCK = 128             # columns of a row that share a scale in an 8-bit checkpoint
 MAX_SEGMENTS = 64
 INT8_MAX_COLS = 131056       # largest H and I of int8 operands (exact int32 sums)
 
@@ -88,6 +93,13 @@ def lib() -> ctypes.CDLL:
         "moe_route_scored": ([P, I, P, I, I, I, I, I, I, I, I, F, P, I, P, P, P], S),
         "moe_quant_rows": ([P, I, P, I, I, I, P, P, P], S),
         "moe_quant_rows_masked": ([P, I, P, I, I, I, P, P, P], S),
+        "moe_checkpoint_rows": ([P, I, P, I, I, I, P, P, P], S),
+        "moe_checkpoint_values": ([P, P, P, I, I, I, P, I, P], S),
+        "moe_ffn_gate_up_train": ([P, P, I, I, I, I, I, P, P, I, P, P, P, P, P, I, P], S),
+        "moe_swiglu_backward": ([P, I, P, P, P, P, I, I, P, P, I, I, P, P, P, P, P], S),
+        "moe_ffn_dgrad": ([P, P, P, I, I, P, I, I, I, I, I, P, P, I, P, I, P], S),
+        "moe_ffn_wgrad": ([P, P, P, I, P, P, I, I, I, P, I, I, I, I, I, P, P, P, P, I, I, P], S),
+        "moe_route_backward": ([P, I, P, P, I, I, I, I, I, F, P, I, P, P], S),
         "moe_weight_ld": ([I, I], I),
         "moe_packed_weight_bytes": ([I, I, I, I], Z),
         "moe_pack_weights": ([P, I, I, I, I, P, P], S),
@@ -762,6 +774,255 @@ def moe_combine(y, row_of, topk_w, out=None, out_dtype=None, stream=None):
     _call(lib().moe_combine, y, stream, _ptr(y), _DT[y.dtype], y.shape[0], _ptr(row_of), _ptr(topk_w), B, K, H,
           _ptr(out), _DT[out.dtype])
     return out
+
+
+# ----------------------------------------------------------------------------
+# training step (contiguous layout, fp32 or bf16)
+# ----------------------------------------------------------------------------
+def _blocks(cols):
+    """Scales of a checkpointed row."""
+    return -(-cols // CKPT_BLOCK)
+
+
+def _train_type(t, name):
+    if t.dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError(f"{name} must be float32 or bfloat16 (got {t.dtype})")
+
+
+def _offsets(offsets, E_loc):
+    """Local experts of the contiguous layout's offsets (all rows: 0)."""
+    if offsets is None:
+        if E_loc is not None:
+            raise ValueError("E_loc needs the layout's offsets")
+        return 0
+    _dev(offsets, "offsets", torch.int32, 1)
+    E_loc = max(offsets.numel() - 1, 1) if E_loc is None else E_loc
+    if E_loc < 1:
+        raise ValueError(f"E_loc must be positive (got {E_loc})")
+    _need(offsets, "offsets", numel=E_loc + 1)
+    return E_loc
+
+
+def _output(t, name, shape, dtype, like, stream):
+    """The caller's tensor after its checks, or a new one."""
+    if t is None:
+        return _new(shape, dtype, like.device, stream)
+    _dev(t, name, dtype)
+    _need(t, name, shape=shape)
+    return t
+
+
+def moe_checkpoint_rows(x, offsets=None, q=None, scales=None, stream=None, E_loc=None):
+    """8-bit checkpoint of the rows of x (fp32 or bf16): int8 codes (cap_rows, cols)
+    and a power-of-two scale for each 128 columns of a row, (cap_rows,
+    ceil(cols/128)).  offsets: the contiguous layout's (E_loc + 1), None for all rows;
+    other rows of given q and scales are left as they were.  E_loc: as in
+    moe_quant_rows."""
+    _dev(x, "x", None, 2)
+    _train_type(x, "x")
+    cap, cols = x.shape
+    E_loc = _offsets(offsets, E_loc)
+    q = _output(q, "q", (cap, cols), torch.int8, x, stream)
+    scales = _output(scales, "scales", (cap, _blocks(cols)), torch.float32, x, stream)
+    _same_device(x, "x", offsets, q, scales)
+    _call(lib().moe_checkpoint_rows, x, stream, _ptr(x), _DT[x.dtype], _ptr(offsets), E_loc, cap, cols, _ptr(q),
+          _ptr(scales))
+    return q, scales
+
+
+def moe_checkpoint_values(q, scales, offsets=None, out=None, out_dtype=torch.bfloat16, stream=None, E_loc=None):
+    """The values (cap_rows, cols) that a checkpoint stands for, exact in bf16 and fp32;
+    offsets and E_loc as in moe_checkpoint_rows."""
+    _dev(q, "q", torch.int8, 2)
+    cap, cols = q.shape
+    _dev(scales, "scales", torch.float32)
+    _need(scales, "scales", shape=(cap, _blocks(cols)))
+    E_loc = _offsets(offsets, E_loc)
+    out = _output(out, "out", (cap, cols), out_dtype if out is None else out.dtype, q, stream)
+    _train_type(out, "out")
+    _same_device(q, "q", scales, offsets, out)
+    _call(lib().moe_checkpoint_values, q, stream, _ptr(q), _ptr(scales), _ptr(offsets), E_loc, cap, cols, _ptr(out),
+          _DT[out.dtype])
+    return out
+
+
+def moe_ffn_gate_up_train(xd, offsets, w_gate, w_up, h=None, gate_q=None, gate_scales=None, up_q=None, up_scales=None,
+                          expected_rows=0, stream=None):
+    """moe_ffn_gate_up (fp32 or bf16) that also leaves gate and up, before SwiGLU, as
+    8-bit checkpoints -> h (cap_rows, I), (gate_q, gate_scales), (up_q, up_scales)."""
+    _dev(xd, "xd", ndim=2)
+    _train_type(xd, "xd")
+    _dev(w_gate, "w_gate", xd.dtype, 3)
+    _dev(w_up, "w_up", xd.dtype, 3)
+    E_loc, I, H, cap = w_gate.shape[0], w_gate.shape[1], xd.shape[1], xd.shape[0]
+    act = _DT[xd.dtype]
+    packed = _pack_flag(_w_packed(w_gate, H, act, "w_gate"))
+    _need(w_up, "w_up", shape=tuple(w_gate.shape))
+    _dev(offsets, "offsets", torch.int32, 1)
+    _need(offsets, "offsets", numel=E_loc + 1)
+    h = _output(h, "h", (cap, I), xd.dtype, xd, stream)
+    gate_q = _output(gate_q, "gate_q", (cap, I), torch.int8, xd, stream)
+    up_q = _output(up_q, "up_q", (cap, I), torch.int8, xd, stream)
+    gate_scales = _output(gate_scales, "gate_scales", (cap, _blocks(I)), torch.float32, xd, stream)
+    up_scales = _output(up_scales, "up_scales", (cap, _blocks(I)), torch.float32, xd, stream)
+    _same_device(xd, "xd", offsets, w_gate, w_up, h, gate_q, gate_scales, up_q, up_scales)
+    _call(lib().moe_ffn_gate_up_train, xd, stream, _ptr(xd), _ptr(offsets), E_loc, cap, H, I, act, _ptr(w_gate),
+          _ptr(w_up), act | packed, _ptr(h), _ptr(gate_q), _ptr(gate_scales), _ptr(up_q), _ptr(up_scales),
+          int(expected_rows))
+    return h, (gate_q, gate_scales), (up_q, up_scales)
+
+
+def moe_swiglu_backward(dh, gate_q, gate_scales, up_q, up_scales, row_of, topk_w, dgate=None, dup=None, hw=None,
+                        dtopk_w=None, stream=None):
+    """From dh (cap_rows, I), the gradient of h before the routing weights, and the
+    checkpoints of gate and up: dgate, dup, hw = topk_w * h (cap_rows, I) and dtopk_w
+    (B, K).  Rows that no slot of row_of names are left as they were."""
+    _dev(dh, "dh", ndim=2)
+    _train_type(dh, "dh")
+    cap, I = dh.shape
+    for name, t in (("gate_q", gate_q), ("up_q", up_q)):
+        _dev(t, name, torch.int8)
+        _need(t, name, shape=(cap, I))
+    for name, t in (("gate_scales", gate_scales), ("up_scales", up_scales)):
+        _dev(t, name, torch.float32)
+        _need(t, name, shape=(cap, _blocks(I)))
+    _dev(row_of, "row_of", torch.int32, 2)
+    B, K = row_of.shape
+    _dev(topk_w, "topk_w", torch.float32)
+    _need(topk_w, "topk_w", shape=(B, K))
+    dgate = _output(dgate, "dgate", (cap, I), dh.dtype, dh, stream)
+    dup = _output(dup, "dup", (cap, I), dh.dtype, dh, stream)
+    hw = _output(hw, "hw", (cap, I), dh.dtype, dh, stream)
+    dtopk_w = _output(dtopk_w, "dtopk_w", (B, K), torch.float32, dh, stream)
+    _same_device(dh, "dh", gate_q, gate_scales, up_q, up_scales, row_of, topk_w, dgate, dup, hw, dtopk_w)
+    _call(lib().moe_swiglu_backward, dh, stream, _ptr(dh), _DT[dh.dtype], _ptr(gate_q), _ptr(gate_scales), _ptr(up_q),
+          _ptr(up_scales), cap, I, _ptr(row_of), _ptr(topk_w), B, K, _ptr(dgate), _ptr(dup), _ptr(hw), _ptr(dtopk_w))
+    return dgate, dup, hw, dtopk_w
+
+
+def moe_ffn_dgrad(dy, offsets, w, dy2=None, w2=None, src_of=None, slots_per_token=1, dx=None, in_dim=None,
+                  expected_rows=0, stream=None):
+    """dx[r] = dy[r] W_j (+ dy2[r] W2_j) for the rows of every local expert -> (cap_rows,
+    in_dim); w, w2 (E_loc, out_dim, in_dim), or packed (E_loc, out_dim, pitch) with
+    in_dim given (or dx).  src_of (cap_rows,): row r reads dy's row src_of[r] //
+    slots_per_token (a token's gradient); None: row r itself."""
+    _dev(dy, "dy", ndim=2)
+    _train_type(dy, "dy")
+    _dev(w, "w", dy.dtype, 3)
+    E_loc, out_dim = w.shape[0], w.shape[1]
+    if dy.shape[1] != out_dim:
+        raise ValueError(f"dy must have {out_dim} columns (got {dy.shape[1]})")
+    _dev(offsets, "offsets", torch.int32, 1)
+    _need(offsets, "offsets", numel=E_loc + 1)
+    if (dy2 is None) != (w2 is None):
+        raise ValueError("dy2 and w2 come together")
+    if dy2 is not None:
+        _dev(dy2, "dy2", dy.dtype)
+        _need(dy2, "dy2", shape=tuple(dy.shape))
+        _dev(w2, "w2", dy.dtype)
+        _need(w2, "w2", shape=tuple(w.shape))
+    if in_dim is None:
+        in_dim = w.shape[2] if dx is None else dx.shape[-1]
+    act = _DT[dy.dtype]
+    packed = _pack_flag(_w_packed(w, in_dim, act, "w"))
+    if src_of is None:
+        cap = dy.shape[0]
+    else:
+        _dev(src_of, "src_of", torch.int32, 1)
+        cap = src_of.numel() if dx is None else dx.shape[0]
+        _need(src_of, "src_of", numel=cap)
+    dx = _output(dx, "dx", (cap, in_dim), dy.dtype, dy, stream)
+    _same_device(dy, "dy", offsets, w, dy2, w2, src_of, dx)
+    _call(lib().moe_ffn_dgrad, dy, stream, _ptr(dy), _ptr(dy2), _ptr(src_of), int(slots_per_token), dy.shape[0],
+          _ptr(offsets), E_loc, cap, out_dim, in_dim, act, _ptr(w), _ptr(w2), act | packed, _ptr(dx),
+          int(expected_rows))
+    return dx
+
+
+_GATHER = {None: MOE_GATHER_NONE, "x": MOE_GATHER_X, "dy": MOE_GATHER_DY}
+
+
+def moe_ffn_wgrad(dy, x, offsets, x_scales=None, dy2=None, src_of=None, slots_per_token=1, gather=None, base=None,
+                  base2=None, dw=None, dw2=None, dw_dtype=torch.float32, expected_rows=0, stream=None, E_loc=None):
+    """dw_j = base_j + sum over expert j's rows of dy[r]^T x[r] -> (E_loc, out_dim, in_dim)
+    fp32, or bf16 beside bf16 activations; with dy2 a pair (dw, dw2) that shares x.
+    x: dy's type, or the int8 codes of a checkpoint with x_scales.  gather 'x' or
+    'dy': that operand holds tokens, and row r reads its row src_of[r] //
+    slots_per_token.  base may be dw itself (accumulation over micro-batches)."""
+    _dev(dy, "dy", ndim=2)
+    _train_type(dy, "dy")
+    _dev(x, "x", ndim=2)
+    out_dim, in_dim = dy.shape[1], x.shape[1]
+    if x.dtype not in (dy.dtype, torch.int8):
+        raise ValueError(f"x must be {dy.dtype} or a checkpoint's int8 (got {x.dtype})")
+    if (x.dtype == torch.int8) != (x_scales is not None):
+        raise ValueError("x_scales belong to a checkpoint's int8 x")
+    if x_scales is not None:
+        _dev(x_scales, "x_scales", torch.float32)
+        _need(x_scales, "x_scales", shape=(x.shape[0], _blocks(in_dim)))
+    if dy2 is not None:
+        _dev(dy2, "dy2", dy.dtype)
+        _need(dy2, "dy2", shape=tuple(dy.shape))
+    elif dw2 is not None or base2 is not None:
+        raise ValueError("dw2 and base2 belong to dy2")
+    if gather not in _GATHER:
+        raise ValueError(f"gather must be None, 'x' or 'dy' (got {gather!r})")
+    _dev(offsets, "offsets", torch.int32, 1)
+    E_loc = _offsets(offsets, (dw.shape[0] if dw is not None and dw.dim() == 3 else None) if E_loc is None else E_loc)
+    cap, src_rows = (x.shape[0], dy.shape[0]) if gather == "dy" else (dy.shape[0], x.shape[0])
+    if gather is None:
+        if src_rows != cap:
+            raise ValueError(f"dy and x must have the same rows (got {cap} and {src_rows})")
+    else:
+        if src_of is None:
+            raise ValueError("a gathered operand needs src_of")
+        _dev(src_of, "src_of", torch.int32, 1)
+        _need(src_of, "src_of", numel=cap)
+    shape = (E_loc, out_dim, in_dim)
+    dt = dw_dtype if dw is None else dw.dtype
+    dw = _output(dw, "dw", shape, dt, dy, stream)
+    if dy2 is not None:
+        dw2 = _output(dw2, "dw2", shape, dt, dy, stream)
+    for name, t in (("base", base), ("base2", base2)):
+        if t is not None:
+            _dev(t, name, dt)
+            _need(t, name, shape=shape)
+    _same_device(dy, "dy", x, offsets, x_scales, dy2, src_of if gather else None, base, base2, dw, dw2)
+    _call(lib().moe_ffn_wgrad, dy, stream, _ptr(dy), _ptr(dy2), _ptr(x),
+          MOE_CKPT8 if x.dtype == torch.int8 else _DT[x.dtype], _ptr(x_scales), _ptr(src_of) if gather else None,
+          int(slots_per_token), src_rows, _GATHER[gather], _ptr(offsets), E_loc, cap, out_dim, in_dim, _DT[dy.dtype],
+          _ptr(base), _ptr(base2), _ptr(dw), _ptr(dw2), _DT.get(dw.dtype, -1), int(expected_rows))
+    return dw if dy2 is None else (dw, dw2)
+
+
+_BACK_SCORES = {"picks": MOE_SCORE_PICKS, **_SCORES}
+
+
+def moe_route_backward(logits, topk_ids, dtopk_w, score: str = "picks", renorm: bool = True, scale: float = 1.0,
+                       phys_of_logical=None, n_shared: int = 0, dlogits=None, stream=None):
+    """dlogits (B, E) fp32 from the gradient dtopk_w (B, K + n_shared) of the routing
+    weights.  score 'picks': moe_route and its variants; 'sigmoid' or 'softmax':
+    moe_route_scored with its renorm, scale, placement map and shared slots."""
+    _dev(logits, "logits", None, 2)
+    if logits.dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError(f"logits must be float32 or bfloat16 (got {logits.dtype})")
+    if score not in _BACK_SCORES:
+        raise ValueError(f"score must be one of {sorted(_BACK_SCORES)} (got {score!r})")
+    B, E = logits.shape
+    _dev(topk_ids, "topk_ids", torch.int32, 2)
+    Kt = topk_ids.shape[1]
+    _need(topk_ids, "topk_ids", shape=(B, Kt))
+    _dev(dtopk_w, "dtopk_w", torch.float32)
+    _need(dtopk_w, "dtopk_w", shape=(B, Kt))
+    if phys_of_logical is not None:
+        _dev(phys_of_logical, "phys_of_logical", torch.int32, 1)
+        _need(phys_of_logical, "phys_of_logical", shape=(E,))
+    dlogits = _output(dlogits, "dlogits", (B, E), torch.float32, logits, stream)
+    _same_device(logits, "logits", topk_ids, dtopk_w, phys_of_logical, dlogits)
+    _call(lib().moe_route_backward, logits, stream, _ptr(logits), _DT[logits.dtype], _ptr(topk_ids), _ptr(dtopk_w), B, E,
+          Kt - int(n_shared), _BACK_SCORES[score], 1 if renorm else 0, scale, _ptr(phys_of_logical), int(n_shared),
+          _ptr(dlogits))
+    return dlogits
 
 
 from .layer import MoELayer  # noqa: E402  (uses the functions above)

@@ -73,8 +73,9 @@ struct Rows {
     int cap_e;
 };
 
+// names: whether the two sizes are H and I (else those of a weight, out and in)
 moe_status_t check_ffn_common(const void* a, Rows rows, int E_local, int cap_rows,
-                              int H, int I, moe_dtype_t act_dt, moe_dtype_t w_dt) {
+                              int H, int I, moe_dtype_t act_dt, moe_dtype_t w_dt, bool names = true) {
     // a buffer of no rows has no address to give
     REQUIRE((a || cap_rows == 0) && (rows.offsets || rows.m), "null activation or row-count pointer");
     REQUIRE(E_local >= 1 && E_local <= 1024, "E_local must be in [1, 1024] (got %d)", E_local);
@@ -82,7 +83,9 @@ moe_status_t check_ffn_common(const void* a, Rows rows, int E_local, int cap_row
     // rows move in 16-byte pieces: 8 elements (bf16, fp32), 16 for fp8 and int8
     const int q = act_dt == MOE_FP8_E4M3 || act_dt == MOE_INT8 ? 16 : 8;
     REQUIRE(H >= q && H % q == 0 && I >= q && I % q == 0,
-            "H and I must be positive multiples of %d for this dtype (got H=%d, I=%d)", q, H, I);
+            names ? "H and I must be positive multiples of %d for this dtype (got H=%d, I=%d)"
+                  : "out_dim and in_dim must be positive multiples of %d (got %d, %d)",
+            q, H, I);
     REQUIRE((long long)cap_rows * (H > I ? H : I) <= 0x7fffffffLL * 4LL, "cap_rows * H too large");
     REQUIRE(aligned16(a), "activation pointer must be 16-byte aligned");
     const bool ok = (act_dt == MOE_F32 && w_dt == MOE_F32) || (act_dt == MOE_BF16 && w_dt == MOE_BF16) ||
@@ -111,6 +114,12 @@ moeep::FfnArgs ffn_args(const void* a, const float* a_scales, Rows rows, int E_l
     moeep::FfnArgs f;
     f.w_scales_pow2 = w_dt == MOE_FP8_E4M3_PO2;
     f.out_f32 = false;
+    f.gate_q = f.up_q = nullptr;
+    f.gate_s = f.up_s = nullptr;
+    f.a2 = nullptr;
+    f.src_of = nullptr;
+    f.per = 1;
+    f.src_rows = 0;
     f.ldw = ldw;
     f.a = a;
     f.a_scales = a_scales;
@@ -243,6 +252,57 @@ moe_status_t quant_rows(const void* x, moe_dtype_t x_dt, Rows rows, int E_local,
     a.q = q;
     a.scales = scales;
     return launched(moeep::launch_quant_rows(a, x_dt == MOE_F32, stream), "moe_quant_rows");
+}
+
+// ---- training step ---------------------------------------------------------------
+moe_status_t check_train_dtype(moe_dtype_t act_dt, moe_dtype_t w_dt) {
+    if ((act_dt != MOE_F32 && act_dt != MOE_BF16) || w_dt != act_dt)
+        return fail(MOE_ERR_UNSUPPORTED, "unsupported (act_dt, w_dt) = (%d, %d): training takes F32 or BF16", act_dt, w_dt);
+    return MOE_OK;
+}
+
+moe_status_t check_gather(bool gathers, int slots_per_token, int src_rows) {
+    if (!gathers) return MOE_OK;
+    REQUIRE(slots_per_token >= 1 && slots_per_token <= 1024, "slots_per_token must be in [1, 1024] (got %d)",
+            slots_per_token);
+    REQUIRE(src_rows >= 0, "src_rows must be >= 0 (got %d)", src_rows);
+    return MOE_OK;
+}
+
+// whether two buffers share no byte (a null one shares none)
+bool apart(const void* a, size_t na, const void* b, size_t nb) {
+    const char *p = static_cast<const char*>(a), *q = static_cast<const char*>(b);
+    return !p || !q || p + na <= q || q + nb <= p;
+}
+
+// checkpoints of rows: x to q and scales, or back
+moe_status_t checkpoint(void* x, moe_dtype_t x_dt, const int32_t* offsets, int E_local, int cap_rows, int cols,
+                        int8_t* q, float* scales, bool write, hipStream_t stream) {
+    if (x_dt != MOE_F32 && x_dt != MOE_BF16)
+        return fail(MOE_ERR_UNSUPPORTED, "unsupported %s %d", write ? "x_dt" : "out_dt", x_dt);
+    REQUIRE(cap_rows >= 0, "cap_rows must be >= 0");
+    REQUIRE(cols >= 8 && cols % 8 == 0 && cols <= (1 << 24), "cols must be a positive multiple of 8, at most %d (got %d)",
+            1 << 24, cols);
+    if (offsets) REQUIRE(E_local >= 1 && E_local <= 1024, "E_local must be in [1, 1024] (got %d)", E_local);
+    if (cap_rows > 0) {
+        REQUIRE(x && q && scales, "null %s, q or scales pointer", write ? "x" : "out");
+        // (rows of codes are whole 8-byte pieces: a range of rows of a checkpoint is one too)
+        REQUIRE(aligned16(x), "%s must be 16-byte aligned", write ? "x" : "out");
+        REQUIRE((reinterpret_cast<uintptr_t>(q) & 7u) == 0, "q must be 8-byte aligned");
+        const size_t n = (size_t)cap_rows * cols;
+        REQUIRE(apart(x, n * elem_size(x_dt), q, n), "%s and q must not overlap", write ? "x" : "out");
+    }
+    moeep::CkptArgs a;
+    a.x = x;
+    a.offsets = offsets;
+    a.E_loc = E_local;
+    a.cap = cap_rows;
+    a.cols = cols;
+    a.q = q;
+    a.scales = scales;
+    const bool f32 = x_dt == MOE_F32;
+    if (write) return launched(moeep::launch_checkpoint_rows(a, f32, stream), "moe_checkpoint_rows");
+    return launched(moeep::launch_checkpoint_values(a, f32, stream), "moe_checkpoint_values");
 }
 
 moe_status_t grouped_ffn(const void* xd, const float* xd_scales, Rows rows,
@@ -634,6 +694,212 @@ moe_status_t moe_grouped_ffn_masked(const void* xd, const float* xd_scales, cons
     return grouped_ffn(xd, xd_scales, Rows{nullptr, m, cap_per_expert}, E_local,
                        E_local * cap_per_expert, H, I, act_dt, w_gate, w_up, w_down, w_gate_scales,
                        w_up_scales, w_down_scales, w_dt, y, y_dt, ws, ws_bytes, expected_rows, stream);
+}
+
+moe_status_t moe_checkpoint_rows(const void* x, moe_dtype_t x_dt, const int32_t* offsets, int E_local, int cap_rows,
+                                 int cols, int8_t* q, float* scales, hipStream_t stream) {
+    return checkpoint(const_cast<void*>(x), x_dt, offsets, E_local, cap_rows, cols, q, scales, true, stream);
+}
+
+moe_status_t moe_checkpoint_values(const int8_t* q, const float* scales, const int32_t* offsets, int E_local,
+                                   int cap_rows, int cols, void* out, moe_dtype_t out_dt, hipStream_t stream) {
+    return checkpoint(out, out_dt, offsets, E_local, cap_rows, cols, const_cast<int8_t*>(q),
+                      const_cast<float*>(scales), false, stream);
+}
+
+moe_status_t moe_ffn_gate_up_train(const void* xd, const int32_t* offsets, int E_local, int cap_rows, int H, int I,
+                                   moe_dtype_t act_dt, const void* w_gate, const void* w_up, moe_dtype_t w_dt,
+                                   void* h, int8_t* gate_q, float* gate_scales, int8_t* up_q, float* up_scales,
+                                   int expected_rows, hipStream_t stream) {
+    const WType wt = split_w(w_dt);
+    moe_status_t s = check_train_dtype(act_dt, wt.dt);
+    if (s != MOE_OK) return s;
+    s = check_ffn_common(xd, Rows{offsets, nullptr, 0}, E_local, cap_rows, H, I, act_dt, wt.dt);
+    if (s != MOE_OK) return s;
+    REQUIRE(w_gate && w_up, "null weight pointer");
+    REQUIRE((h && gate_q && gate_scales && up_q && up_scales) || cap_rows == 0, "null h or checkpoint pointer");
+    REQUIRE(aligned16(w_gate) && aligned16(w_up) && aligned16(h) && aligned16(gate_q) && aligned16(up_q),
+            "weights, h and codes must be 16-byte aligned");
+    auto f = ffn_args(xd, nullptr, Rows{offsets, nullptr, 0}, E_local, cap_rows, H, I, w_gate, w_up, nullptr, nullptr,
+                      h, nullptr, expected_rows, wt.dt, weight_ld(wt, H));
+    f.gate_q = gate_q;
+    f.up_q = up_q;
+    f.gate_s = gate_scales;
+    f.up_s = up_scales;
+    hipError_t e = hipSuccess;
+    if (cap_rows > 0) e = act_dt == MOE_F32 ? moeep::launch_ffn_ckpt_f32(f, stream) : moeep::launch_ffn_ckpt_bf16(f, stream);
+    return launched(e, "moe_ffn_gate_up_train");
+}
+
+moe_status_t moe_swiglu_backward(const void* dh, moe_dtype_t act_dt, const int8_t* gate_q, const float* gate_scales,
+                                 const int8_t* up_q, const float* up_scales, int cap_rows, int I,
+                                 const int32_t* row_of, const float* topk_w, int B, int K, void* dgate, void* dup,
+                                 void* hw, float* dtopk_w, hipStream_t stream) {
+    moe_status_t s = check_train_dtype(act_dt, act_dt);
+    if (s != MOE_OK) return s;
+    REQUIRE(B >= 0 && K >= 1 && K <= 1024, "need B >= 0 and 1 <= K <= 1024");
+    REQUIRE((long long)B * K <= 0x7fffffffLL, "B*K must fit in int32");
+    REQUIRE(cap_rows >= 0, "cap_rows must be >= 0");
+    REQUIRE(I >= 8 && I % 8 == 0, "I must be a positive multiple of 8 (got %d)", I);
+    if (cap_rows > 0) {
+        REQUIRE(dh && gate_q && gate_scales && up_q && up_scales && dgate && dup && hw, "null pointer argument");
+        REQUIRE(aligned16(dh) && aligned16(gate_q) && aligned16(up_q) && aligned16(dgate) && aligned16(dup) &&
+                    aligned16(hw),
+                "dh, codes, dgate, dup and hw must be 16-byte aligned");
+        const size_t n = (size_t)cap_rows * I, nf = n * elem_size(act_dt);
+        REQUIRE(apart(dgate, nf, dup, nf) && apart(dgate, nf, hw, nf) && apart(dup, nf, hw, nf),
+                "dgate, dup and hw must not overlap");
+        for (const void* o : {dgate, dup, hw})
+            REQUIRE(apart(o, nf, dh, nf) && apart(o, nf, gate_q, n) && apart(o, nf, up_q, n),
+                    "dgate, dup and hw must not overlap dh or the codes");
+    }
+    if (B > 0) REQUIRE(row_of && topk_w && dtopk_w, "null row_of, topk_w or dtopk_w");
+    moeep::SwigluBwdArgs a;
+    a.dh = dh;
+    a.gate_q = gate_q;
+    a.up_q = up_q;
+    a.gate_s = gate_scales;
+    a.up_s = up_scales;
+    a.row_of = row_of;
+    a.topk_w = topk_w;
+    a.dgate = dgate;
+    a.dup = dup;
+    a.hw = hw;
+    a.dtopk_w = dtopk_w;
+    a.cap = cap_rows;
+    a.I = I;
+    a.slots = (long long)B * K;
+    return launched(moeep::launch_swiglu_backward(a, act_dt == MOE_F32, stream), "moe_swiglu_backward");
+}
+
+moe_status_t moe_ffn_dgrad(const void* dy, const void* dy2, const int32_t* src_of, int slots_per_token, int src_rows,
+                           const int32_t* offsets, int E_local, int cap_rows, int out_dim, int in_dim,
+                           moe_dtype_t act_dt, const void* w, const void* w2, moe_dtype_t w_dt, void* dx,
+                           int expected_rows, hipStream_t stream) {
+    const WType wt = split_w(w_dt);
+    moe_status_t s = check_train_dtype(act_dt, wt.dt);
+    if (s != MOE_OK) return s;
+    s = check_gather(src_of != nullptr, slots_per_token, src_rows);
+    if (s != MOE_OK) return s;
+    REQUIRE(w && (dx || cap_rows == 0), "null weight or dx pointer");
+    s = check_ffn_common(dx, Rows{offsets, nullptr, 0}, E_local, cap_rows, out_dim, in_dim, act_dt, wt.dt, false);
+    if (s != MOE_OK) return s;
+    // a buffer of no rows may be null; where src_of names none of no rows, every row of dx is zero
+    const bool none = cap_rows == 0 || (src_of && src_rows == 0);
+    REQUIRE(dy || none, "null dy");
+    REQUIRE((w2 != nullptr) == (dy2 != nullptr) || none, "dy2 and w2 come together");
+    REQUIRE(aligned16(dy) && aligned16(dy2) && aligned16(w) && aligned16(w2) && aligned16(dx),
+            "dy, weights and dx must be 16-byte aligned");
+    const size_t esz = elem_size(act_dt), dy_bytes = (size_t)(src_of ? src_rows : cap_rows) * out_dim * esz,
+                 dx_bytes = (size_t)cap_rows * in_dim * esz;
+    REQUIRE(apart(dx, dx_bytes, dy, dy_bytes) && apart(dx, dx_bytes, dy2, dy_bytes), "dx must not overlap dy or dy2");
+    auto f = ffn_args(dy, nullptr, Rows{offsets, nullptr, 0}, E_local, cap_rows, out_dim, in_dim, w, w2, nullptr,
+                      nullptr, dx, nullptr, expected_rows, wt.dt, weight_ld(wt, in_dim));
+    f.a2 = w2 ? dy2 : nullptr;
+    f.src_of = src_of;
+    f.per = slots_per_token;
+    f.src_rows = src_rows;
+    hipError_t e = hipSuccess;
+    if (cap_rows > 0) e = act_dt == MOE_F32 ? moeep::launch_dgrad_f32(f, stream) : moeep::launch_dgrad_bf16(f, stream);
+    return launched(e, "moe_ffn_dgrad");
+}
+
+moe_status_t moe_ffn_wgrad(const void* dy, const void* dy2, const void* x, moe_dtype_t x_dt, const float* x_scales,
+                           const int32_t* src_of, int slots_per_token, int src_rows, moe_gather_t gather,
+                           const int32_t* offsets, int E_local, int cap_rows, int out_dim, int in_dim,
+                           moe_dtype_t act_dt, const void* base, const void* base2, void* dw, void* dw2,
+                           moe_dtype_t dw_dt, int expected_rows, hipStream_t stream) {
+    moe_status_t s = check_train_dtype(act_dt, act_dt);
+    if (s != MOE_OK) return s;
+    if (x_dt != act_dt && x_dt != MOE_CKPT8)
+        return fail(MOE_ERR_UNSUPPORTED, "unsupported (act_dt, x_dt) = (%d, %d)", act_dt, x_dt);
+    if (!(dw_dt == MOE_F32 || (dw_dt == MOE_BF16 && act_dt == MOE_BF16)))
+        return fail(MOE_ERR_UNSUPPORTED, "unsupported (act_dt, dw_dt) = (%d, %d)", act_dt, dw_dt);
+    REQUIRE(gather == MOE_GATHER_NONE || gather == MOE_GATHER_X || gather == MOE_GATHER_DY, "unknown gather %d", gather);
+    const bool gathers = gather != MOE_GATHER_NONE;
+    REQUIRE(!gathers || src_of || cap_rows == 0, "a gathered operand needs src_of");
+    s = check_gather(gathers, slots_per_token, src_rows);
+    if (s != MOE_OK) return s;
+    const int dy_rows = gather == MOE_GATHER_DY ? src_rows : cap_rows, x_rows = gather == MOE_GATHER_X ? src_rows : cap_rows;
+    REQUIRE(dw, "null dw");
+    s = check_ffn_common(dw, Rows{offsets, nullptr, 0}, E_local, cap_rows, out_dim, in_dim, act_dt, act_dt, false);
+    if (s != MOE_OK) return s;
+    const bool none = dy_rows == 0 || x_rows == 0;
+    REQUIRE((dy && x) || none, "null dy or x");
+    REQUIRE((dw2 != nullptr) == (dy2 != nullptr) || none, "dy2 and dw2 come together");
+    REQUIRE(!base2 || dw2, "base2 needs dw2");
+    if (x_dt == MOE_CKPT8) REQUIRE(x_scales || none, "a checkpoint x needs its scales");
+    REQUIRE(aligned16(dy) && aligned16(dy2) && aligned16(x) && aligned16(base) && aligned16(base2) && aligned16(dw) &&
+                aligned16(dw2),
+            "dy, x, base and dw must be 16-byte aligned");
+    const size_t dw_bytes = (size_t)E_local * out_dim * in_dim * elem_size(dw_dt);
+    REQUIRE(!dw2 || apart(dw, dw_bytes, dw2, dw_bytes), "dw and dw2 must not overlap");
+    for (const void* b : {base, base2})
+        for (const void* d : {static_cast<const void*>(dw), static_cast<const void*>(dw2)})
+            REQUIRE(!b || !d || (b == d && (d == dw) == (b == base)) || apart(b, dw_bytes, d, dw_bytes),
+                    "a base must be its own dw or lie apart from both");
+    const size_t dy_bytes = (size_t)dy_rows * out_dim * elem_size(act_dt),
+                 x_bytes = (size_t)x_rows * in_dim * (x_dt == MOE_CKPT8 ? 1 : elem_size(act_dt));
+    for (const void* d : {static_cast<const void*>(dw), static_cast<const void*>(dw2)})
+        REQUIRE(apart(d, dw_bytes, dy, dy_bytes) && apart(d, dw_bytes, dy2, dy_bytes) && apart(d, dw_bytes, x, x_bytes),
+                "dw must not overlap dy, dy2 or x");
+    moeep::WgradArgs a;
+    a.dy[0] = dy;
+    a.dy[1] = dw2 ? dy2 : nullptr;
+    a.x = x;
+    a.x_scales = x_dt == MOE_CKPT8 ? x_scales : nullptr;
+    a.src_of = gathers ? src_of : nullptr;
+    a.per = slots_per_token;
+    a.src_rows = src_rows;
+    a.gather_x = gather == MOE_GATHER_X;
+    a.gather_dy = gather == MOE_GATHER_DY;
+    a.offsets = offsets;
+    a.E_loc = E_local;
+    // no rows on one side: sums of none
+    a.cap = none ? 0 : cap_rows;
+    a.N = out_dim;
+    a.M = in_dim;
+    a.base[0] = base;
+    a.base[1] = base2;
+    a.dw[0] = dw;
+    a.dw[1] = dw2;
+    a.dw_f32 = dw_dt == MOE_F32;
+    a.rows_hint = expected_rows > 0 ? expected_rows : cap_rows / E_local;
+    return launched(act_dt == MOE_F32 ? moeep::launch_wgrad_f32(a, stream) : moeep::launch_wgrad_bf16(a, stream),
+                    "moe_ffn_wgrad");
+}
+
+moe_status_t moe_route_backward(const void* logits, moe_dtype_t logits_dt, const int32_t* topk_ids,
+                                const float* dtopk_w, int B, int E, int K, moe_score_t score, int renorm, float scale,
+                                const int32_t* phys_of_logical, int n_shared, float* dlogits, hipStream_t stream) {
+    moe_status_t s = check_route_shape(B, E, K);
+    if (s != MOE_OK) return s;
+    if (logits_dt != MOE_F32 && logits_dt != MOE_BF16)
+        return fail(MOE_ERR_UNSUPPORTED, "unsupported logits_dt %d", logits_dt);
+    if (score != MOE_SCORE_SOFTMAX && score != MOE_SCORE_SIGMOID && score != MOE_SCORE_PICKS)
+        return fail(MOE_ERR_UNSUPPORTED, "unsupported score %d", score);
+    if (score == MOE_SCORE_PICKS && logits_dt != MOE_F32)
+        return fail(MOE_ERR_UNSUPPORTED, "moe_route takes fp32 logits (got logits_dt %d)", logits_dt);
+    REQUIRE(std::isfinite(scale), "scale must be finite");
+    REQUIRE(score != MOE_SCORE_PICKS || scale == 1.0f, "moe_route's weights have no scale (got %g)", (double)scale);
+    REQUIRE(n_shared >= 0 && n_shared <= 1024 - E, "need 0 <= n_shared and E + n_shared <= 1024");
+    REQUIRE((long long)B * (K + n_shared) <= 0x7fffffffLL, "B*(K+n_shared) must fit in int32");
+    if (B > 0) REQUIRE(logits && topk_ids && dtopk_w && dlogits, "null pointer argument");
+    moeep::RouteBwdArgs a;
+    a.logits = logits;
+    a.ids = topk_ids;
+    a.dw = dtopk_w;
+    a.map = phys_of_logical;
+    a.dlogits = dlogits;
+    a.scale = scale;
+    a.B = B;
+    a.E = E;
+    a.K = K;
+    a.Kt = K + n_shared;
+    a.score = score;
+    a.bf16 = logits_dt == MOE_BF16;
+    a.renorm = renorm != 0;
+    return launched(moeep::launch_route_backward(a, stream), "moe_route_backward");
 }
 
 moe_status_t moe_combine(const void* y, moe_dtype_t y_dt, int cap_rows, const int32_t* row_of,

@@ -115,12 +115,90 @@ struct FfnArgs {
     int rows_hint;            // cap / E_loc, picks the tile shape
     bool w_scales_pow2;       // fp8: every weight scale is a power of two
     bool out_f32;             // int8 down: fp32 outputs instead of bf16
+    // gate/up of a training step: 8-bit checkpoints of g and u beside h
+    int8_t* gate_q;           // (cap, N)
+    int8_t* up_q;
+    float* gate_s;            // (cap, ceil(N/128))
+    float* up_s;
+    // input gradients: out = a w0 + a2 w1 over the weights' rows (Kdim of them, N
+    // columns at pitch ldw); with src_of row r of a is a's row src_of[r] / per
+    const void* a2;
+    const int32_t* src_of;    // (cap), or nullptr: row r itself
+    int per, src_rows;
 };
 
 hipError_t launch_ffn_f32(const FfnArgs& a, bool gated, hipStream_t stream);   // ffn_f32.hip
 hipError_t launch_ffn_bf16(const FfnArgs& a, bool gated, hipStream_t stream);  // ffn_bf16.hip
 hipError_t launch_ffn_fp8(const FfnArgs& a, bool gated, hipStream_t stream);   // ffn_fp8.hip
 hipError_t launch_ffn_i8(const FfnArgs& a, bool gated, hipStream_t stream);    // ffn_i8.hip
+
+// the same with 8-bit checkpoints of g and u (gate_q ... up_s)
+hipError_t launch_ffn_ckpt_f32(const FfnArgs& a, hipStream_t stream);          // grad_f32.hip
+hipError_t launch_ffn_ckpt_bf16(const FfnArgs& a, hipStream_t stream);         // ffn_bf16.hip
+
+// input gradients (a2, w1 may be null: one product)
+hipError_t launch_dgrad_f32(const FfnArgs& a, hipStream_t stream);             // grad_f32.hip
+hipError_t launch_dgrad_bf16(const FfnArgs& a, hipStream_t stream);            // dgrad_bf16.hip
+
+// weight gradients: dw_j = base_j + sum over expert j's rows r of dy[r]^T x[r], for one
+// or two dy that share x
+struct WgradArgs {
+    const void* dy[2];        // (rows, N); dy[1] may be null
+    const void* x;            // (rows, M)
+    const float* x_scales;    // checkpoint x: (rows, ceil(M/128)); else nullptr
+    const int32_t* src_of;    // (cap): the gathered operand's row of r is src_of[r] / per
+    int per, src_rows;        // src_rows: rows of the gathered operand
+    bool gather_x, gather_dy;
+    const int32_t* offsets;   // (E_loc + 1)
+    int E_loc, cap, N, M;
+    const void* base[2];      // (E_loc, N, M) or null; may be dw itself
+    void* dw[2];
+    bool dw_f32;
+    int rows_hint;
+};
+hipError_t launch_wgrad_f32(const WgradArgs& a, hipStream_t stream);           // grad_f32.hip
+hipError_t launch_wgrad_bf16(const WgradArgs& a, hipStream_t stream);          // wgrad_bf16.hip
+
+// ckpt.hip
+struct CkptArgs {
+    void* x;                  // (cap, cols) fp32 or bf16: read by the packing, written by the reading
+    const int32_t* offsets;   // (E_loc + 1), or nullptr: all rows
+    int E_loc, cap, cols;
+    int8_t* q;                // (cap, cols)
+    float* scales;            // (cap, ceil(cols/128))
+};
+hipError_t launch_checkpoint_rows(const CkptArgs& a, bool f32, hipStream_t stream);
+hipError_t launch_checkpoint_values(const CkptArgs& a, bool f32, hipStream_t stream);
+
+struct SwigluBwdArgs {
+    const void* dh;           // (cap, I)
+    const int8_t* gate_q;     // (cap, I)
+    const int8_t* up_q;
+    const float* gate_s;      // (cap, ceil(I/128))
+    const float* up_s;
+    const int32_t* row_of;    // (slots)
+    const float* topk_w;      // (slots)
+    void* dgate;              // (cap, I)
+    void* dup;
+    void* hw;
+    float* dtopk_w;           // (slots)
+    int cap, I;
+    long long slots;
+};
+hipError_t launch_swiglu_backward(const SwigluBwdArgs& a, bool f32, hipStream_t stream);
+
+// route_bwd.hip
+struct RouteBwdArgs {
+    const void* logits;       // (B, E) fp32 or bf16
+    const int32_t* ids;       // (B, Kt)
+    const float* dw;          // (B, Kt)
+    const int32_t* map;       // (E) logical -> physical id, or nullptr
+    float* dlogits;           // (B, E)
+    float scale;
+    int B, E, K, Kt, score;   // score: moe_score_t
+    bool bf16, renorm;
+};
+hipError_t launch_route_backward(const RouteBwdArgs& a, hipStream_t stream);
 
 int device_cu_count();   // api.hip: compute units of the current device (cached)
 

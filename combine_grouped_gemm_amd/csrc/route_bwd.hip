@@ -1,0 +1,204 @@
+// Gradient of the routing weights back to the logits, for moe_route and
+// moe_route_scored.
+//
+// With picks P of a token, dw the gradient of its weights w and s the scores:
+//   softmax over the picks     dl_e = w_e (dw_e - sum_P w dw)               e in P
+//   scored                     a_e = scale / S (dw_e - sum_P (s / S) dw)    renormalised, S = sum_P s (0 if S is 0)
+//                              a_e = scale dw_e                             otherwise
+//     sigmoid                  dl_e = a_e s_e (1 - s_e)                     e in P
+//     softmax over all         dl_e = s_e ([e in P] a_e - sum_P s a)        every e that is not masked
+// The choice itself is a step and passes no gradient, so neither does the bias.
+//
+// A wave takes a token.  Lane k holds pick k (picks beyond 64 in further
+// registers' turns of a loop) and works on its own logit; the row of dlogits is
+// then written once, each lane finding its experts among the picks (K compares an
+// expert, by lane reads), so that no store depends on another.  1 - s of the
+// sigmoid comes from e^-|l|, which does not cancel.
+#include "device_common.hpp"
+#include "launch.hpp"
+#include "moeep.h"
+
+namespace moeep {
+namespace {
+
+constexpr int kWaves = 4;
+constexpr int kMaxE = 1024;
+// logits at or below the lowest finite bf16 value take their expert out
+constexpr float kLow = -3.38953138925153547590470800371487866880e38f;
+
+__device__ __forceinline__ float wave_sum(float v) {
+#pragma unroll
+    for (int d = 32; d > 0; d >>= 1) v += __shfl_xor(v, d, kWave);
+    return v;
+}
+__device__ __forceinline__ float wave_max(float v) {
+#pragma unroll
+    for (int d = 32; d > 0; d >>= 1) v = fmaxf(v, __shfl_xor(v, d, kWave));
+    return v;
+}
+
+template <bool BF16>
+__device__ __forceinline__ float logit(const void* l, size_t i) {
+    if constexpr (BF16) return __uint_as_float((uint32_t) static_cast<const uint16_t*>(l)[i] << 16);
+    else return static_cast<const float*>(l)[i];
+}
+
+// s and 1 - s of the sigmoid
+__device__ __forceinline__ void sigmoid2(float l, float& s, float& rest) {
+    const float e = expf(-fabsf(l)), big = 1.0f / (1.0f + e), small = e * big;
+    s = l >= 0.0f ? big : small;
+    rest = l >= 0.0f ? small : big;
+}
+
+// NP: picks a lane (K <= 64 NP)
+template <bool BF16, int SCORE, int NP>
+__global__ __launch_bounds__(kWaves * kWave) void route_backward_kernel(RouteBwdArgs p) {
+    __shared__ int s_inv[kMaxE];              // expert of a physical id, -1: none
+    const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
+    const int E = p.E, K = p.K;
+    if (p.map != nullptr) {
+        for (int e = threadIdx.x; e < E; e += kWaves * kWave) s_inv[e] = -1;
+        __syncthreads();
+        for (int e = threadIdx.x; e < E; e += kWaves * kWave) {
+            const int q = p.map[e];
+            if (q >= 0 && q < E) s_inv[q] = e;
+        }
+        __syncthreads();
+    }
+    for (long long t = (long long)blockIdx.x * kWaves + wave; t < p.B; t += (long long)gridDim.x * kWaves) {
+        const size_t row = (size_t)t * E;
+        // softmax over all: the row's maximum and sum
+        float top = -INFINITY, total = 0.0f;
+        if constexpr (SCORE == MOE_SCORE_SOFTMAX) {
+            for (int e = lane; e < E; e += kWave) {
+                const float l = logit<BF16>(p.logits, row + e);
+                if (l > kLow) top = fmaxf(top, l);
+            }
+            top = wave_max(top);
+            for (int e = lane; e < E; e += kWave) {
+                const float l = logit<BF16>(p.logits, row + e);
+                if (l > kLow) total += expf(l - top);
+            }
+            total = wave_sum(total);
+        }
+        // the picks
+        int at[NP];
+        float s[NP], rest[NP], dw[NP];
+#pragma unroll
+        for (int i = 0; i < NP; ++i) {
+            const int k = i * kWave + lane;
+            int e = -1;
+            float l = 0.0f;
+            dw[i] = 0.0f;
+            if (k < K) {
+                e = p.ids[(size_t)t * p.Kt + k];
+                e = e >= 0 && e < E ? e : -1;
+                if (p.map != nullptr && e >= 0) e = s_inv[e];
+                if (e >= 0) {
+                    l = logit<BF16>(p.logits, row + e);
+                    if (SCORE != MOE_SCORE_PICKS && l <= kLow) e = -1;
+                }
+                if (e >= 0) dw[i] = p.dw[(size_t)t * p.Kt + k];
+            }
+            at[i] = e;
+            s[i] = l;                          // the score follows
+            rest[i] = 0.0f;
+        }
+        if constexpr (SCORE == MOE_SCORE_PICKS) {
+            float m = -INFINITY, z = 0.0f;
+#pragma unroll
+            for (int i = 0; i < NP; ++i) m = fmaxf(m, at[i] >= 0 ? s[i] : -INFINITY);
+            m = wave_max(m);
+#pragma unroll
+            for (int i = 0; i < NP; ++i) {
+                s[i] = at[i] >= 0 ? expf(s[i] - m) : 0.0f;
+                z += s[i];
+            }
+            z = wave_sum(z);
+#pragma unroll
+            for (int i = 0; i < NP; ++i) s[i] = at[i] >= 0 ? s[i] / z : 0.0f;
+        } else {
+#pragma unroll
+            for (int i = 0; i < NP; ++i) {
+                if constexpr (SCORE == MOE_SCORE_SIGMOID) sigmoid2(s[i], s[i], rest[i]);
+                else s[i] = expf(s[i] - top) / total;
+                if (at[i] < 0) s[i] = 0.0f;
+            }
+        }
+        // a: the gradient of the scores (picks: of the logits)
+        float a[NP], sum = 0.0f;
+        if constexpr (SCORE == MOE_SCORE_PICKS) {
+#pragma unroll
+            for (int i = 0; i < NP; ++i) sum += s[i] * dw[i];
+            sum = wave_sum(sum);
+#pragma unroll
+            for (int i = 0; i < NP; ++i) a[i] = s[i] * (dw[i] - sum);
+        } else if (p.renorm) {
+            float S = 0.0f;
+#pragma unroll
+            for (int i = 0; i < NP; ++i) S += s[i];
+            S = wave_sum(S);
+#pragma unroll
+            for (int i = 0; i < NP; ++i) sum += S > 0.0f ? s[i] / S * dw[i] : 0.0f;
+            sum = wave_sum(sum);
+#pragma unroll
+            for (int i = 0; i < NP; ++i) a[i] = S > 0.0f ? p.scale / S * (dw[i] - sum) : 0.0f;
+        } else {
+#pragma unroll
+            for (int i = 0; i < NP; ++i) a[i] = p.scale * dw[i];
+        }
+        float all = 0.0f;                      // softmax over all: sum_P s a
+        if constexpr (SCORE == MOE_SCORE_SIGMOID) {
+#pragma unroll
+            for (int i = 0; i < NP; ++i) a[i] *= s[i] * rest[i];
+        } else if constexpr (SCORE == MOE_SCORE_SOFTMAX) {
+#pragma unroll
+            for (int i = 0; i < NP; ++i) all += at[i] >= 0 ? s[i] * a[i] : 0.0f;
+            all = wave_sum(all);
+        }
+        for (int e = lane; e - lane < E; e += kWave) {
+            float v = 0.0f;
+#pragma unroll
+            for (int i = 0; i < NP; ++i) {
+                const int n = min(kWave, K - i * kWave);
+                for (int k = 0; k < n; ++k) {
+                    const int q = __builtin_amdgcn_readlane(at[i], k);
+                    const float x = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(a[i]), k));
+                    v += q == e ? x : 0.0f;
+                }
+            }
+            if (e < E) {
+                if constexpr (SCORE == MOE_SCORE_SOFTMAX) {
+                    const float l = logit<BF16>(p.logits, row + e);
+                    v = l > kLow ? expf(l - top) / total * (v - all) : 0.0f;
+                }
+                p.dlogits[row + e] = v;
+            }
+        }
+    }
+}
+
+template <bool BF16, int SCORE>
+hipError_t launch_as(const RouteBwdArgs& a, hipStream_t stream) {
+    const int need = (int)(((long long)a.B + kWaves - 1) / kWaves), most = device_cu_count() * 8;
+    const dim3 grid(need < most ? need : most), block(kWaves * kWave);
+    if (a.K <= 64) hipLaunchKernelGGL((route_backward_kernel<BF16, SCORE, 1>), grid, block, 0, stream, a);
+    else hipLaunchKernelGGL((route_backward_kernel<BF16, SCORE, 16>), grid, block, 0, stream, a);
+    return hipGetLastError();
+}
+
+template <int SCORE>
+hipError_t launch_type(const RouteBwdArgs& a, hipStream_t stream) {
+    return a.bf16 ? launch_as<true, SCORE>(a, stream) : launch_as<false, SCORE>(a, stream);
+}
+
+}  // namespace
+
+hipError_t launch_route_backward(const RouteBwdArgs& a, hipStream_t stream) {
+    if (a.B == 0) return hipSuccess;
+    if (a.score == MOE_SCORE_PICKS) return launch_type<MOE_SCORE_PICKS>(a, stream);
+    if (a.score == MOE_SCORE_SIGMOID) return launch_type<MOE_SCORE_SIGMOID>(a, stream);
+    return launch_type<MOE_SCORE_SOFTMAX>(a, stream);
+}
+
+}  // namespace moeep

@@ -5,7 +5,11 @@ asks of an EP decode step).
 
     route -> layout -> dispatch -> gate/up (+SwiGLU) -> down -> combine
 
-(with int8 experts a quantisation of h between gate/up and down).
+(with int8 experts a quantisation of h between gate/up and down).  A layer made
+for training also keeps 8-bit checkpoints on the way and has the backward pass:
+
+    dgrad of down -> SwiGLU backwards -> wgrad of down -> dgrad of gate/up ->
+    wgrad of gate/up -> combine of the rows' gradients -> route backwards
 Every stage is one call into libmoeep; this class only owns the buffers
 and orders the calls on one stream.
 """
@@ -13,9 +17,10 @@ from __future__ import annotations
 
 import torch
 
-from . import (FP8_BLOCK, moe_combine, moe_dispatch, moe_ffn_down, moe_ffn_gate_up,
-               moe_layout, moe_layout_masked, moe_layout_workspace_bytes, moe_quant_rows, moe_route,
-               moe_route_mapped, moe_route_scored, moe_route_shared)
+from . import (CKPT_BLOCK, FP8_BLOCK, moe_checkpoint_rows, moe_combine, moe_dispatch, moe_ffn_dgrad, moe_ffn_down,
+               moe_ffn_gate_up, moe_ffn_gate_up_train, moe_ffn_wgrad, moe_layout, moe_layout_masked,
+               moe_layout_workspace_bytes, moe_quant_rows, moe_route, moe_route_backward, moe_route_mapped,
+               moe_route_scored, moe_route_shared, moe_swiglu_backward)
 
 _TORCH = {"f32": torch.float32, "bf16": torch.bfloat16, "fp8": torch.float8_e4m3fn, "int8": torch.int8}
 
@@ -41,11 +46,15 @@ class MoELayer:
     topk_groups, group_top, renorm, scale) routes by that call, with the
     balance bias (E,) in self.router_bias when set.  moe_route_scored takes a
     placement map beside shared experts; the map then covers the routed ids.
+    train: forward keeps 8-bit checkpoints of x (a row a token) and of the gate and
+    up products, and backward() gives the gradients; 'f32' or 'bf16' storage, the
+    contiguous layout.  The checkpoints, the routing and the layout of the last
+    forward are what backward() works from.
     """
 
     def __init__(self, seg_rows, E, K, H, I, e_begin, e_end, act_dtype, y_dtype, out_dtype,
                  device="cuda", cap_rows=None, layout="contiguous", cap_per_expert=None, n_shared=0,
-                 router=None):
+                 router=None, train=False):
         self.router = None if router is None else dict(router)
         if self.router is not None:
             unknown = set(self.router) - {"score", "n_groups", "topk_groups", "group_top", "renorm", "scale"}
@@ -65,6 +74,9 @@ class MoELayer:
         if layout not in ("contiguous", "masked"):
             raise ValueError(f"unknown layout {layout!r}")
         self.masked = layout == "masked"
+        self.train = bool(train)
+        if self.train and (act_dtype not in ("f32", "bf16") or self.masked):
+            raise ValueError("training needs f32 or bf16 storage and the contiguous layout")
         self.cap_e = (max(self.T, 1) if cap_per_expert is None else int(cap_per_expert)) if self.masked else None
         if self.masked:
             self.cap = self.E_loc * self.cap_e
@@ -101,6 +113,22 @@ class MoELayer:
         self.expert_map = None
         # balance bias (E,) fp32 on the device for the scored router (None: no bias)
         self.router_bias = None
+        if self.train:
+            f32 = dict(dtype=torch.float32, device=dev)
+            i8 = dict(dtype=torch.int8, device=dev)
+            rows = dict(dtype=act, device=dev)
+            self.x_q = torch.empty((T, H), **i8)
+            self.x_s = torch.empty((T, -(-H // CKPT_BLOCK)), **f32)
+            self.gate_q, self.up_q = torch.empty((cap, I), **i8), torch.empty((cap, I), **i8)
+            self.gate_s = torch.empty((cap, -(-I // CKPT_BLOCK)), **f32)
+            self.up_s = torch.empty_like(self.gate_s)
+            self.dh, self.dgate = torch.empty((cap, I), **rows), torch.empty((cap, I), **rows)
+            self.dup, self.hw = torch.empty((cap, I), **rows), torch.empty((cap, I), **rows)
+            self.dxd = torch.empty((cap, H), **rows)
+            self.dx = torch.empty((T, H), **rows)
+            self.dtopk_w = torch.empty((T, K), **f32)
+            self.dlogits = torch.empty((T, self.E_routed), **f32)
+            self._ones = torch.ones((T, K), **f32)
 
     # individual stages (each one library call) ---------------------------------
     def route(self, logits, stream=None):
@@ -135,8 +163,18 @@ class MoELayer:
     def dispatch(self, x_segments, stream=None):
         moe_dispatch(x_segments, self.row_of, self.cap, self.act_dtype, self.xd, self.xd_scales,
                      stream=stream)
+        if self.train:
+            t = 0
+            for x in [x_segments] if isinstance(x_segments, torch.Tensor) else x_segments:
+                part = slice(t, t + x.shape[0])
+                moe_checkpoint_rows(x, q=self.x_q[part], scales=self.x_s[part], stream=stream)
+                t = part.stop
 
     def gate_up(self, w, stream=None):
+        if self.train:
+            moe_ffn_gate_up_train(self.xd, self.rows, w["gate"], w["up"], self.h, self.gate_q, self.gate_s, self.up_q,
+                                  self.up_s, expected_rows=self.expected_rows, stream=stream)
+            return
         moe_ffn_gate_up(self.xd, self.xd_scales, self.rows, w["gate"], w["up"],
                         w.get("gate_scale"), w.get("up_scale"), self.h if self.h_act is None else self.h_act,
                         self.h_scales if self.h_act is None else None, expected_rows=self.expected_rows, stream=stream, cap_per_expert=self.cap_e,
@@ -170,6 +208,68 @@ class MoELayer:
         for _, run in self.stages(x_segments, logits, w):
             run(stream)
         return self.out
+
+    # the backward pass ----------------------------------------------------------
+    def dgrad_down(self, dout, w, stream=None):
+        moe_ffn_dgrad(dout, self.offsets, w["down"], src_of=self.src_of, slots_per_token=self.K, dx=self.dh,
+                      expected_rows=self.expected_rows, stream=stream)
+
+    def swiglu_backward(self, stream=None):
+        moe_swiglu_backward(self.dh, self.gate_q, self.gate_s, self.up_q, self.up_s, self.row_of, self.topk_w,
+                            self.dgate, self.dup, self.hw, self.dtopk_w, stream=stream)
+
+    def wgrad_down(self, dout, grads, accumulate=False, stream=None):
+        moe_ffn_wgrad(dout, self.hw, self.offsets, src_of=self.src_of, slots_per_token=self.K, gather="dy",
+                      base=grads["down"] if accumulate else None, dw=grads["down"],
+                      expected_rows=self.expected_rows, stream=stream)
+
+    def dgrad_gate_up(self, w, stream=None):
+        moe_ffn_dgrad(self.dgate, self.offsets, w["gate"], dy2=self.dup, w2=w["up"], dx=self.dxd,
+                      expected_rows=self.expected_rows, stream=stream)
+
+    def wgrad_gate_up(self, grads, accumulate=False, stream=None):
+        moe_ffn_wgrad(self.dgate, self.x_q, self.offsets, x_scales=self.x_s, dy2=self.dup, src_of=self.src_of,
+                      slots_per_token=self.K, gather="x", base=grads["gate"] if accumulate else None,
+                      base2=grads["up"] if accumulate else None, dw=grads["gate"], dw2=grads["up"],
+                      expected_rows=self.expected_rows, stream=stream)
+
+    def route_backward(self, logits, stream=None):
+        kw = dict(score="picks")
+        if self.router is not None:
+            kw = dict(score=self.router.get("score", "sigmoid"), renorm=self.router.get("renorm", True),
+                      scale=self.router.get("scale", 1.0))
+        moe_route_backward(logits, self.topk_ids, self.dtopk_w, phys_of_logical=self.expert_map,
+                           n_shared=self.n_shared, dlogits=self.dlogits, stream=stream, **kw)
+
+    def backward_stages(self, dout, logits, w, grads, accumulate=False):
+        """(name, thunk) pairs of the seven calls, in order."""
+        if not self.train:
+            raise ValueError("backward needs a layer made with train=True")
+        return [("dgrad_down", lambda s=None: self.dgrad_down(dout, w, s)),
+                ("swiglu_backward", lambda s=None: self.swiglu_backward(s)),
+                ("wgrad_down", lambda s=None: self.wgrad_down(dout, grads, accumulate, s)),
+                ("dgrad_gate_up", lambda s=None: self.dgrad_gate_up(w, s)),
+                ("wgrad_gate_up", lambda s=None: self.wgrad_gate_up(grads, accumulate, s)),
+                ("combine_backward", lambda s=None: moe_combine(self.dxd, self.row_of, self._ones, self.dx, stream=s)),
+                ("route_backward", lambda s=None: self.route_backward(logits, s))]
+
+    def new_grads(self, dtype=torch.float32):
+        """Buffers for the weights' gradients: fp32, or bf16 for a bf16 layer."""
+        kw = dict(dtype=dtype, device=self.out.device)
+        return {"gate": torch.empty((self.E_loc, self.I, self.H), **kw),
+                "up": torch.empty((self.E_loc, self.I, self.H), **kw),
+                "down": torch.empty((self.E_loc, self.H, self.I), **kw)}
+
+    def backward(self, dout, logits, w, grads, accumulate=False, stream=None):
+        """Gradients of the last forward for dout (T, H), the loss gradient of its out in
+        the storage type.  logits and w as forward took them; grads from new_grads():
+        the weights' gradients are written there (accumulate: added).  Returns dx (T, H)
+        and dlogits (T, E), the layer's own buffers; dtopk_w holds the gradient of the
+        routing weights.  dx is that of the experts; the router's projection, outside
+        the layer, adds its own from dlogits."""
+        for _, run in self.backward_stages(dout, logits, w, grads, accumulate):
+            run(stream)
+        return self.dx, self.dlogits
 
 
 class MicroBatchedLayer:

@@ -73,9 +73,11 @@ enum {
                                   of two 2^e, e in [-127, 127] (the E8M0 scale convention of
                                   the microscaling formats); the matrix cores apply such
                                   scales, and only a scale's exponent field is read */
-    MOE_INT8 = 4               /* two's complement codes with one fp32 scale per row: per token
+    MOE_INT8 = 4,              /* two's complement codes with one fp32 scale per row: per token
                                   for activations, per output channel for weights; a code c
                                   stands for c * scale */
+    MOE_CKPT8 = 5              /* 8-bit checkpoint of a row: two's complement codes with one fp32
+                                  power-of-two scale per 128 columns (moe_checkpoint_rows) */
 };
 
 /* Largest H and I of int8 operands: sums of this many products of two codes
@@ -86,13 +88,24 @@ enum {
 typedef int32_t moe_score_t;
 enum {
     MOE_SCORE_SOFTMAX = 0,     /* softmax over all E logits */
-    MOE_SCORE_SIGMOID = 1      /* 1 / (1 + exp(-logit)) */
+    MOE_SCORE_SIGMOID = 1,     /* 1 / (1 + exp(-logit)) */
+    MOE_SCORE_PICKS = 2        /* moe_route_backward only: moe_route's softmax over the K picks */
+};
+
+/* Operand of moe_ffn_wgrad whose rows are looked up through src_of. */
+typedef int32_t moe_gather_t;
+enum {
+    MOE_GATHER_NONE = 0,
+    MOE_GATHER_X = 1,
+    MOE_GATHER_DY = 2
 };
 
 /* Largest number of simulated source segments moe_dispatch accepts. */
 #define MOE_MAX_SEGMENTS 64
 /* fp8 scale block length along the contraction (row) dimension. */
 #define MOE_FP8_BLOCK 128
+/* Block length of 8-bit checkpoints along a row. */
+#define MOE_CKPT_BLOCK 128
 
 const char* moe_status_string(moe_status_t status);
 const char* moe_last_error(void);
@@ -463,6 +476,129 @@ moe_status_t moe_grouped_ffn_masked(const void* xd, const float* xd_scales, cons
 moe_status_t moe_combine(const void* y, moe_dtype_t y_dt, int cap_rows, const int32_t* row_of,
                          const float* topk_w, int B, int K, int H,
                          void* out, moe_dtype_t out_dt, hipStream_t stream);
+
+/*
+ * Training step.  The calls below and the forward ones make the layer's
+ * backward pass, over the contiguous layout, in F32 or BF16 (act_dt = w_dt).
+ * For the loss gradient dout (B, H) of moe_combine's out:
+ *   dh    = moe_ffn_dgrad(dout, src_of, w_down)            gradient of h before the weights
+ *   dgate, dup, hw, dtopk_w = moe_swiglu_backward(dh, checkpoints, row_of, topk_w)
+ *   dw_down = moe_ffn_wgrad(dout gathered, hw)
+ *   dxd   = moe_ffn_dgrad(dgate, dup, w_gate, w_up)
+ *   dw_gate, dw_up = moe_ffn_wgrad(dgate, dup, x gathered)
+ *   dx    = moe_combine(dxd, row_of, ones)
+ *   dlogits = moe_route_backward(logits, topk_ids, dtopk_w)
+ * y need not be kept: the gradient of slot (t, k)'s weight, <dout[t], y[row]>, is
+ * <dh[row], h[row]>.  What is kept from the forward pass is the routing, x (B, H)
+ * and the gate and up products of every row, the last three as 8-bit checkpoints.
+ * Sums are held in fp32; each result is rounded once to its type.  Results do not
+ * depend on expected_rows beyond the order of fp32 sums, and are the same from
+ * run to run.
+ *
+ * moe_checkpoint_rows -- an 8-bit checkpoint (MOE_CKPT8) of the rows of x.
+ *   x       (cap_rows, cols) F32 or BF16; cols a multiple of 8, at most 2^24.
+ *   Valid rows: as in moe_quant_rows (offsets NULL: all).  Other rows of q and
+ *   scales are not written.
+ *   q       (cap_rows, cols) int8 out, 8-byte aligned, not overlapping x.
+ *   scales  (cap_rows, ceil(cols/128)) fp32 out: the smallest 2^e, -126 <= e <=
+ *           121, with max |v| <= 127 * 2^e over the block; 1 for a block of zeros.
+ *   code = v / scale to the nearest integer, ties to even, within +-127.  A block
+ *   with a NaN or an infinity gets scale NaN and codes 0.  bf16 holds every
+ *   code * scale exactly.
+ * moe_checkpoint_values -- the values back: out (cap_rows, cols) of out_dt (F32 or
+ *   BF16) = code * scale on the valid rows; out does not overlap q.
+ */
+moe_status_t moe_checkpoint_rows(const void* x, moe_dtype_t x_dt, const int32_t* offsets, int E_local, int cap_rows,
+                                 int cols, int8_t* q, float* scales, hipStream_t stream);
+moe_status_t moe_checkpoint_values(const int8_t* q, const float* scales, const int32_t* offsets, int E_local,
+                                   int cap_rows, int cols, void* out, moe_dtype_t out_dt, hipStream_t stream);
+
+/*
+ * moe_ffn_gate_up_train -- moe_ffn_gate_up for F32 and BF16 (w_dt may carry
+ * MOE_W_PACKED) that also leaves g and u, before SwiGLU, as 8-bit checkpoints
+ * taken from their fp32 sums:
+ *   gate_q, up_q (cap_rows, I) int8, gate_scales, up_scales (cap_rows,
+ *   ceil(I/128)) fp32 out.
+ * Rows past offsets[E_local] of the outputs are not written.
+ */
+moe_status_t moe_ffn_gate_up_train(const void* xd, const int32_t* offsets, int E_local, int cap_rows, int H, int I,
+                                   moe_dtype_t act_dt, const void* w_gate, const void* w_up, moe_dtype_t w_dt,
+                                   void* h, int8_t* gate_q, float* gate_scales, int8_t* up_q, float* up_scales,
+                                   int expected_rows, hipStream_t stream);
+
+/*
+ * moe_swiglu_backward -- from dh to the gradients of gate and up.  For the row r =
+ * row_of[t,k] of every slot, g and u the values of its checkpoints, w =
+ * topk_w[t,k], sg = 1 / (1 + exp(-g)) and h = g sg u:
+ *   dgate[r] = w dh[r] u sg (1 + g (1 - sg)),  dup[r] = w dh[r] g sg,
+ *   hw[r] = w h,  dtopk_w[t,k] = sum_i dh[r,i] h_i.
+ *   dh (cap_rows, I), dgate, dup, hw (cap_rows, I) of act_dt (F32 or BF16), the
+ *   outputs overlapping neither each other nor the inputs; row_of, topk_w, dtopk_w
+ *   (B, K).
+ * Slots whose row lies outside [0, cap_rows) get dtopk_w 0; rows that no slot
+ * names are not written.  Two slots must not name one row.
+ */
+moe_status_t moe_swiglu_backward(const void* dh, moe_dtype_t act_dt, const int8_t* gate_q, const float* gate_scales,
+                                 const int8_t* up_q, const float* up_scales, int cap_rows, int I,
+                                 const int32_t* row_of, const float* topk_w, int B, int K, void* dgate, void* dup,
+                                 void* hw, float* dtopk_w, hipStream_t stream);
+
+/*
+ * moe_ffn_dgrad -- input gradients of a grouped product y = x W^T.  For every row
+ * r of local expert j:
+ *   dx[r] = dy[r] W_j (+ dy2[r] W2_j)
+ *   dy, dy2 (rows, out_dim) of act_dt; w, w2 (E_local, out_dim, in_dim) of w_dt
+ *   (may carry MOE_W_PACKED: pitch moe_weight_ld(in_dim)); dx (cap_rows, in_dim)
+ *   out.  dy2 and w2 NULL: one product.
+ *   src_of NULL: row r of dy is r, and dy has cap_rows rows.  Else (cap_rows) from
+ *   moe_layout: row r reads dy's row src_of[r] / slots_per_token of src_rows (a
+ *   token's gradient, sent back to all of its rows); rows that name none of them
+ *   read zeros.  src_rows and slots_per_token are unused without src_of.
+ * Rows past offsets[E_local] of dx are not written; dx overlaps neither dy nor dy2.
+ */
+moe_status_t moe_ffn_dgrad(const void* dy, const void* dy2, const int32_t* src_of, int slots_per_token, int src_rows,
+                           const int32_t* offsets, int E_local, int cap_rows, int out_dim, int in_dim,
+                           moe_dtype_t act_dt, const void* w, const void* w2, moe_dtype_t w_dt, void* dx,
+                           int expected_rows, hipStream_t stream);
+
+/*
+ * moe_ffn_wgrad -- weight gradients of grouped products y = x W^T.  For every
+ * local expert j, over its rows r:
+ *   dw_j = base_j + sum_r dy[r]^T x[r]   (and dw2_j = base2_j + sum_r dy2[r]^T x[r])
+ *   dy, dy2 (rows, out_dim) of act_dt; x (rows, in_dim) of act_dt, or MOE_CKPT8
+ *   codes with x_scales (rows, ceil(in_dim/128)); base, base2, dw, dw2 (E_local,
+ *   out_dim, in_dim) of dw_dt: F32, or BF16 with BF16 activations.
+ *   base NULL: zeros.  base may be dw itself (gradients accumulated over
+ *   micro-batches), else it must not overlap dw or dw2.  dy2 and dw2 NULL: one
+ *   product.  dw overlaps none of dy, dy2, x.
+ *   gather: the operand (x; dy and dy2) whose row of r is src_of[r] /
+ *   slots_per_token of src_rows; rows that name none of them add nothing.  The
+ *   other has cap_rows rows.  MOE_GATHER_NONE: both do; src_of, slots_per_token
+ *   and src_rows are unused.
+ * An expert without rows gets its base.
+ */
+moe_status_t moe_ffn_wgrad(const void* dy, const void* dy2, const void* x, moe_dtype_t x_dt, const float* x_scales,
+                           const int32_t* src_of, int slots_per_token, int src_rows, moe_gather_t gather,
+                           const int32_t* offsets, int E_local, int cap_rows, int out_dim, int in_dim,
+                           moe_dtype_t act_dt, const void* base, const void* base2, void* dw, void* dw2,
+                           moe_dtype_t dw_dt, int expected_rows, hipStream_t stream);
+
+/*
+ * moe_route_backward -- gradient of the routing weights back to the logits.
+ *   logits, scale, renorm, phys_of_logical, n_shared as the forward call took them:
+ *   MOE_SCORE_PICKS for moe_route and its variants (F32 logits, scale 1, renorm
+ *   unused), else moe_route_scored's score.
+ *   topk_ids (B, K + n_shared) as it wrote them, dtopk_w (B, K + n_shared) fp32; the
+ *   shared slots' weights are constant, their columns are not read.
+ *   dlogits (B, E) fp32 out, every entry written: 0 for experts that the weights
+ *   do not depend on (softmax over all: for masked ones only).  Slots with id -1
+ *   add nothing.
+ * The choice of experts is piecewise constant and passes no gradient; neither
+ * does the balance bias.  Weights renormalised by a sum of zero pass none.
+ */
+moe_status_t moe_route_backward(const void* logits, moe_dtype_t logits_dt, const int32_t* topk_ids,
+                                const float* dtopk_w, int B, int E, int K, moe_score_t score, int renorm, float scale,
+                                const int32_t* phys_of_logical, int n_shared, float* dlogits, hipStream_t stream);
 
 #ifdef __cplusplus
 }

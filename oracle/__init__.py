@@ -34,12 +34,14 @@ Parity status of each function (what pins it, in tests/test_oracle_*.py):
   expert_ffn     pinned: dense SwiGLU via torch CPU, pure-Python brute force.
   numerics       pinned: exhaustive bf16 / e4m3 casts against torch; int8 rows
                  against rational arithmetic.
+  train          pinned: fp64 automatic differentiation, central differences of the
+                 oracle's forward pass, rational arithmetic for the checkpoints.
   fp8 block geometry and scale rule: parity unpinned by the pages (a reading
   both sides implement); its properties are checked.
 """
-from . import eplb, numerics
+from . import eplb, numerics, train
 from .moe import (route, route_scored, route_shared, layout, layout_masked, dispatch, silu, expert_ffn, grouped_ffn,
                   grouped_ffn_masked, combine, layer)
 
-__all__ = ["eplb", "numerics", "route", "route_scored", "route_shared", "layout", "layout_masked", "dispatch", "silu", "expert_ffn",
+__all__ = ["eplb", "numerics", "train", "route", "route_scored", "route_shared", "layout", "layout_masked", "dispatch", "silu", "expert_ffn",
            "grouped_ffn", "grouped_ffn_masked", "combine", "layer"]
