@@ -119,6 +119,7 @@ moeep::FfnArgs ffn_args(const void* a, const float* a_scales, Rows rows, int E_l
     f.a2 = nullptr;
     f.src_of = nullptr;
     f.per = 1;
+    f.per_div = moeep::divisor_of(1);
     f.src_rows = 0;
     f.ldw = ldw;
     f.a = a;
@@ -797,7 +798,8 @@ moe_status_t moe_ffn_dgrad(const void* dy, const void* dy2, const int32_t* src_o
                       nullptr, dx, nullptr, expected_rows, wt.dt, weight_ld(wt, in_dim));
     f.a2 = w2 ? dy2 : nullptr;
     f.src_of = src_of;
-    f.per = slots_per_token;
+    f.per = src_of ? slots_per_token : 1;
+    f.per_div = moeep::divisor_of(f.per);
     f.src_rows = src_rows;
     hipError_t e = hipSuccess;
     if (cap_rows > 0) e = act_dt == MOE_F32 ? moeep::launch_dgrad_f32(f, stream) : moeep::launch_dgrad_bf16(f, stream);
@@ -849,7 +851,8 @@ moe_status_t moe_ffn_wgrad(const void* dy, const void* dy2, const void* x, moe_d
     a.x = x;
     a.x_scales = x_dt == MOE_CKPT8 ? x_scales : nullptr;
     a.src_of = gathers ? src_of : nullptr;
-    a.per = slots_per_token;
+    a.per = gathers ? slots_per_token : 1;
+    a.per_div = moeep::divisor_of(a.per);
     a.src_rows = src_rows;
     a.gather_x = gather == MOE_GATHER_X;
     a.gather_dy = gather == MOE_GATHER_DY;

@@ -269,10 +269,6 @@ hipError_t launch_dgrad_f32(const FfnArgs& a, hipStream_t stream) {
     static int per_cu = 0;
     return launch_persistent(dgrad_kernel<float>, kThreads, a, stream, &per_cu);
 }
-hipError_t launch_dgrad_bf16(const FfnArgs& a, hipStream_t stream) {
-    static int per_cu = 0;
-    return launch_persistent(dgrad_kernel<uint16_t>, kThreads, a, stream, &per_cu);
-}
 hipError_t launch_wgrad_f32(const WgradArgs& a, hipStream_t stream) { return wgrad<float>(a, stream); }
 hipError_t launch_wgrad_bf16(const WgradArgs& a, hipStream_t stream) { return wgrad<uint16_t>(a, stream); }
 

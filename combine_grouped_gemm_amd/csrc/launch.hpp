@@ -97,6 +97,21 @@ hipError_t launch_quant_rows(const QuantArgs& a, bool f32, hipStream_t stream);
 hipError_t launch_combine(const void* y, int kind, const int32_t* row_of, const float* w,
                           int B, int K, int H, void* out, int cap, hipStream_t stream);
 
+// Division of a slot (below 2^31) by the slots of a token: q = umulhi(slot, mul) >> shift
+// with l = ceil(log2 d), mul = floor(2^(31 + l) / d) + 1 and shift = l - 1: the multiplier
+// is above 2^(31 + l) / d by at most 1, which moves the quotient by less than slot / 2^(31
+// + l) < 1 / d, too little to reach the next integer.  d = 1: shift -1, the slot itself.
+struct Divisor {
+    uint32_t mul;
+    int shift;
+};
+inline Divisor divisor_of(int d) {
+    if (d <= 1) return Divisor{0, -1};
+    int l = 1;
+    while ((1 << l) < d) ++l;
+    return Divisor{(uint32_t)((1ull << (31 + l)) / (unsigned)d + 1), l - 1};
+}
+
 // ffn kernels: shared argument block
 struct FfnArgs {
     const void* a;            // activations (cap, Kdim)
@@ -125,6 +140,7 @@ struct FfnArgs {
     const void* a2;
     const int32_t* src_of;    // (cap), or nullptr: row r itself
     int per, src_rows;
+    Divisor per_div;          // by per
 };
 
 hipError_t launch_ffn_f32(const FfnArgs& a, bool gated, hipStream_t stream);   // ffn_f32.hip
@@ -148,6 +164,7 @@ struct WgradArgs {
     const float* x_scales;    // checkpoint x: (rows, ceil(M/128)); else nullptr
     const int32_t* src_of;    // (cap): the gathered operand's row of r is src_of[r] / per
     int per, src_rows;        // src_rows: rows of the gathered operand
+    Divisor per_div;          // by per
     bool gather_x, gather_dy;
     const int32_t* offsets;   // (E_loc + 1)
     int E_loc, cap, N, M;
