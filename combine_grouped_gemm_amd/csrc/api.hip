@@ -834,6 +834,7 @@ moe_status_t moe_ffn_wgrad(const void* dy, const void* dy2, const void* x, moe_d
     REQUIRE(aligned16(dy) && aligned16(dy2) && aligned16(x) && aligned16(base) && aligned16(base2) && aligned16(dw) &&
                 aligned16(dw2),
             "dy, x, base and dw must be 16-byte aligned");
+    REQUIRE((long long)out_dim * in_dim <= (1ll << 38) / E_local, "dw is too large");
     const size_t dw_bytes = (size_t)E_local * out_dim * in_dim * elem_size(dw_dt);
     REQUIRE(!dw2 || apart(dw, dw_bytes, dw2, dw_bytes), "dw and dw2 must not overlap");
     for (const void* b : {base, base2})

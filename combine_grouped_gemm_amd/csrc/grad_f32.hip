@@ -270,6 +270,5 @@ hipError_t launch_dgrad_f32(const FfnArgs& a, hipStream_t stream) {
     return launch_persistent(dgrad_kernel<float>, kThreads, a, stream, &per_cu);
 }
 hipError_t launch_wgrad_f32(const WgradArgs& a, hipStream_t stream) { return wgrad<float>(a, stream); }
-hipError_t launch_wgrad_bf16(const WgradArgs& a, hipStream_t stream) { return wgrad<uint16_t>(a, stream); }
 
 }  // namespace moeep
