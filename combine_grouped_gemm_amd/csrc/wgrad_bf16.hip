@@ -29,14 +29,64 @@ namespace {
 using namespace cols;
 
 constexpr int kPieceRows = 1024;             // rows listed at a time
+// Offsets out of range: kOutOfRange for a row, this for a column.  A sum of the two, or of
+// either and an offset below kReach, stays below 2^32 and at or above kReach, which every
+// extent stays under.
+constexpr uint32_t kNoColumn = 0x7fff0000u;
+constexpr unsigned long long kReach = kNoColumn;
+
 #define INLINE __attribute__((always_inline))
 
-// what a lane of a 64-bit gathered load reads where there is no row
+// what a lane of a 64-bit load reads where there is nothing to read
 __device__ uint4 g_zeros;
 
-// TN, TM: tile of dw (out x in).  8 waves, 2 (out) x 4 (in).  FAR: a gathered operand of
-// 2 GiB or more, which a buffer resource's 32-bit offsets do not reach: 64-bit addresses.
-template <int TN, int TM, bool CKPT, bool FAR>
+__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+__device__ __forceinline__ uint4 buf_load16(rsrc_t r, uint32_t off) {
+#if defined(__HIP_DEVICE_COMPILE__)
+    return __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(r, (int)off, 0, 0));
+#else
+    return make_uint4(0, 0, 0, 0);
+#endif
+}
+__device__ __forceinline__ uint2 buf_load8(rsrc_t r, uint32_t off) {
+#if defined(__HIP_DEVICE_COMPILE__)
+    return __builtin_bit_cast(uint2, __builtin_amdgcn_raw_buffer_load_b64(r, (int)off, 0, 0));
+#else
+    return make_uint2(0, 0);
+#endif
+}
+__device__ __forceinline__ float buf_load4(rsrc_t r, uint32_t off) {
+#if defined(__HIP_DEVICE_COMPILE__)
+    return __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(r, (int)off, 0, 0));
+#else
+    return 0.0f;
+#endif
+}
+__device__ __forceinline__ void buf_store16(rsrc_t r, uint32_t off, floatx4 v) {
+#if defined(__HIP_DEVICE_COMPILE__)
+    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, v), r, (int)off, 0, 0);
+#endif
+}
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ void buf_store8(rsrc_t r, uint32_t off, floatx4 v) {
+#if defined(__HIP_DEVICE_COMPILE__)
+    __builtin_amdgcn_raw_buffer_store_b64(u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])}, r, (int)off, 0, 0);
+#endif
+}
+// base values of four neighbouring columns, as they are in memory
+__device__ __forceinline__ floatx4 base_values(uint4 t) { return __builtin_bit_cast(floatx4, t); }
+__device__ __forceinline__ floatx4 base_values(uint2 t) {
+    return floatx4{bf16_lo(t.x), bf16_hi(t.x), bf16_lo(t.y), bf16_hi(t.y)};
+}
+
+// a piece of work: rows [row0, row0 + rows) of a tile's expert
+struct Piece {
+    int tile, j, q, n0, m0, row0, rows, end;     // end: the expert's last row, exclusive
+};
+
+// TN, TM: tile of dw (out x in); 8 waves, 2 (out) x 4 (in).  FAR: an operand, or a tile's
+// rows of dw, that 32-bit offsets do not reach: 64-bit addresses.
+template <int TN, int TM, bool CKPT, bool F32, bool FAR>
 __global__ __launch_bounds__(512, 1) void wgrad_kernel(WgradArgs p, int tiles_n, int tiles_m, int tiles) {
     constexpr int NT = 512, NW = 8;
     constexpr int FN = TN / 2 / 16, FM = TM / 4 / 16;        // fragments of a wave
@@ -45,39 +95,40 @@ __global__ __launch_bounds__(512, 1) void wgrad_kernel(WgradArgs p, int tiles_n,
     constexpr int C_ITERS = BK * TM / 1024 / NW;             // checkpoint: 16-code loads of a lane
     constexpr int YR = 512 / TN, XR = 512 / TM;              // rows of a direct load
     constexpr int CR = 1024 / TM;                            // rows of a wave's code load
-    static_assert(Y_ITERS >= 1 && X_ITERS >= 1 && C_ITERS >= 1, "tile shape");
+    constexpr int LOADS = Y_ITERS + (CKPT ? 0 : X_ITERS);
+    constexpr int STORES = FN * FM;                          // of a wave and tile, whatever its borders
+    static_assert(Y_ITERS >= 1 && X_ITERS >= 1 && C_ITERS >= 1 && STORES < 64, "tile shape");
 
+    // each stage an object of its own: the compiler sees that reads of one do not
+    // depend on the loads in flight into the other
     __shared__ uint4 sy0[BK * TN / 8];
     __shared__ uint4 sx0[BK * TM / 8];
     __shared__ uint4 sy1[BK * TN / 8];
     __shared__ uint4 sx1[BK * TM / 8];
     __shared__ int s_tok[2][kPieceRows];
 
-    auto y_base = [&](auto I) -> char* {
+    auto y_base = [&](auto I) INLINE -> char* {
         if constexpr (decltype(I)::value == 0) return reinterpret_cast<char*>(sy0);
         else return reinterpret_cast<char*>(sy1);
     };
-    auto x_base = [&](auto I) -> char* {
+    auto x_base = [&](auto I) INLINE -> char* {
         if constexpr (decltype(I)::value == 0) return reinterpret_cast<char*>(sx0);
         else return reinterpret_cast<char*>(sx1);
     };
 
     const int tid = threadIdx.x, lane = tid % kWave;
-    const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
+    const int wave = uniform(tid / kWave);
     const int wn = wave / 4, wm = wave % 4;
-    const int N = p.N, M = p.M;
+    const int N = p.N, M = p.M, G = gridDim.x;
     const int nb = (M + kCkptBlock - 1) / kCkptBlock;
     const bool gathers = p.src_of != nullptr;
 
-    // a piece of work: rows [row0, row0 + rows) of a tile's expert
-    struct Piece {
-        int tile;
-        int j, q, n0, m0, row0, rows, end;      // end: the expert's last row, exclusive
-    };
     auto open_tile = [&](int tau, Piece& w) INLINE {
         w.tile = tau;
+        w.row0 = w.rows = w.end = 0;
         if (tau >= tiles) return;
-        // the tiles of one expert's one dw, columns (in) slowest: tiles that run together share both operands
+        // out columns fastest, then the pair, then the in columns, then the expert: tiles that run
+        // together share both operands in L2
         unsigned rest = (unsigned)tau;
         w.n0 = (int)(rest % (unsigned)tiles_n) * TN;
         rest /= (unsigned)tiles_n;
@@ -85,18 +136,14 @@ __global__ __launch_bounds__(512, 1) void wgrad_kernel(WgradArgs p, int tiles_n,
         w.q = (int)(rest % pairs);
         rest /= pairs;
         w.m0 = (int)(rest % (unsigned)tiles_m) * TM;
-        w.j = (int)(rest / (unsigned)tiles_m);
-        w.row0 = clampi(p.offsets[w.j], 0, p.cap);
-        w.end = clampi(p.offsets[w.j + 1], w.row0, p.cap);
-        w.n0 = __builtin_amdgcn_readfirstlane(w.n0);
-        w.q = __builtin_amdgcn_readfirstlane(w.q);
-        w.m0 = __builtin_amdgcn_readfirstlane(w.m0);
-        w.j = __builtin_amdgcn_readfirstlane(w.j);
-        w.row0 = __builtin_amdgcn_readfirstlane(w.row0);
-        w.end = __builtin_amdgcn_readfirstlane(w.end);
+        w.j = uniform((int)(rest / (unsigned)tiles_m));
+        w.n0 = uniform(w.n0);
+        w.q = uniform(w.q);
+        w.m0 = uniform(w.m0);
+        w.row0 = uniform(clampi(p.offsets[w.j], 0, p.cap));
+        w.end = uniform(clampi(p.offsets[w.j + 1], w.row0, p.cap));
         w.rows = min(w.end - w.row0, kPieceRows);
     };
-    const int G = gridDim.x;
     auto after = [&](const Piece& w) INLINE {
         Piece n = w;
         if (w.row0 + w.rows < w.end) {
@@ -107,19 +154,20 @@ __global__ __launch_bounds__(512, 1) void wgrad_kernel(WgradArgs p, int tiles_n,
         }
         return n;
     };
-    // the slots of a piece's rows, and the list of the rows that a gathered operand reads for them
+    // the slots of a piece's rows, and the list of the rows that a gathered operand reads for
+    // them (-1: none, also behind the last row)
     constexpr int LIST = kPieceRows / NT;
     int listed[LIST];
     auto load_list = [&](const Piece& w) INLINE {
-        if (!gathers || w.tile >= tiles) return;
+        if (!gathers) return;
 #pragma unroll
         for (int i = 0; i < LIST; ++i) {
             const int r = i * NT + tid;
             listed[i] = r < w.rows ? p.src_of[w.row0 + r] : -1;
         }
     };
-    auto store_list = [&](const Piece& w, int* tok) INLINE {
-        if (!gathers || w.tile >= tiles) return;
+    auto store_list = [&](int* tok) INLINE {
+        if (!gathers) return;
 #pragma unroll
         for (int i = 0; i < LIST; ++i) {
             const int t = listed[i] < 0 ? -1 : token_of(listed[i], p.per_div);
@@ -127,61 +175,77 @@ __global__ __launch_bounds__(512, 1) void wgrad_kernel(WgradArgs p, int tiles_n,
         }
     };
 
-    // direct load i of an operand's step: `i0` first row of the step within the piece
-    auto row_at = [&](const Piece& w, const int* tok, bool gathered, int i) INLINE -> int {
-        if (i >= w.rows) return -1;
-        return gathered ? tok[i] : w.row0 + i;
+    // What a step of piece w that starts at its row i0 loads.  Lane offsets of the direct
+    // loads: a gathered row lies anywhere in its operand, another is counted from the step's
+    // first one and the extent ends with the piece's rows.
+    uint32_t yoff[Y_ITERS], xoff[X_ITERS];
+    int yrow[Y_ITERS], xrow[X_ITERS];                         // FAR: the rows themselves
+    auto operand_rows = [&](auto iters, auto rows_of, bool gathered, int pitch, int c0, int width, const Piece& w,
+                            const int* tok, int i0, uint32_t* off, int* row) INLINE {
+        constexpr int ITERS = decltype(iters)::value, R = decltype(rows_of)::value, T = 512 / R;
+#pragma unroll
+        for (int i = 0; i < ITERS; ++i) {
+            const int k = (i * NW + wave) * R + lane / (64 / R);
+            const int col = c0 + ((lane % (64 / R)) ^ swz_row<T>(k)) * 8;
+            const uint32_t cb = col < width ? (uint32_t)col * 2 : kNoColumn;
+            int r = k;
+            if (gathered) r = tok[i0 + k];
+            if constexpr (FAR) {
+                row[i] = gathered ? r : (i0 + k < w.rows ? w.row0 + i0 + k : -1);
+                off[i] = cb;
+            } else {
+                off[i] = (r >= 0 ? (uint32_t)r * (uint32_t)pitch : kOutOfRange) + cb;
+            }
+        }
     };
-    auto issue_y = [&](auto I, const Piece& w, const int* tok, int i0, int i) INLINE {
-        const int blk = i * NW + wave, k = blk * YR + lane / (64 / YR);
-        const int c = (lane % (64 / YR)) ^ swz_row<TN>(k);
-        const int col = w.n0 + c * 8;
-        const int r = row_at(w, tok, p.gather_dy, i0 + k);
-        // gathered rows lie anywhere, others within the expert's
-        const char* base = static_cast<const char*>(w.q == 0 ? p.dy[0] : p.dy[1]) +
-                           (p.gather_dy ? (size_t)0 : (size_t)w.row0 * N * 2);
-        const int rel = p.gather_dy ? r : i0 + k;
-        const uint32_t bytes = (uint32_t)(p.gather_dy ? p.src_rows : w.rows) * (uint32_t)(N * 2);
-        const bool here = r >= 0 && col < N;
-        char* dst = y_base(I) + blk * 1024;
+    struct Source {
+        rsrc_t y, x;
+        const char *ybase, *xbase;
+    };
+    auto issue_y = [&](auto I, const Source& s, int i) INLINE {
+        char* dst = y_base(I) + (i * NW + wave) * 1024;
         if constexpr (FAR)
-            lds_dma16<0>(here ? base + (size_t)rel * N * 2 + col * 2 : reinterpret_cast<const char*>(&g_zeros), dst);
+            lds_dma16<0>(yrow[i] >= 0 && yoff[i] != kNoColumn ? s.ybase + (size_t)yrow[i] * N * 2 + yoff[i]
+                                                             : reinterpret_cast<const char*>(&g_zeros), dst);
         else
-            lds_buf16<0>(make_rsrc(base, bytes), dst, here ? (uint32_t)rel * (uint32_t)(N * 2) + (uint32_t)col * 2 : kOutOfRange, 0);
+            lds_buf16<0>(s.y, dst, yoff[i], 0);
     };
-    auto issue_x = [&](auto I, const Piece& w, const int* tok, int i0, int i) INLINE {
-        const int blk = i * NW + wave, k = blk * XR + lane / (64 / XR);
-        const int c = (lane % (64 / XR)) ^ swz_row<TM>(k);
-        const int col = w.m0 + c * 8;
-        const int r = row_at(w, tok, p.gather_x, i0 + k);
-        const char* base = static_cast<const char*>(p.x) + (p.gather_x ? (size_t)0 : (size_t)w.row0 * M * 2);
-        const int rel = p.gather_x ? r : i0 + k;
-        const uint32_t bytes = (uint32_t)(p.gather_x ? p.src_rows : w.rows) * (uint32_t)(M * 2);
-        const bool here = r >= 0 && col < M;
-        char* dst = x_base(I) + blk * 1024;
+    auto issue_x = [&](auto I, const Source& s, int i) INLINE {
+        char* dst = x_base(I) + (i * NW + wave) * 1024;
         if constexpr (FAR)
-            lds_dma16<0>(here ? base + (size_t)rel * M * 2 + col * 2 : reinterpret_cast<const char*>(&g_zeros), dst);
+            lds_dma16<0>(xrow[i] >= 0 && xoff[i] != kNoColumn ? s.xbase + (size_t)xrow[i] * M * 2 + xoff[i]
+                                                             : reinterpret_cast<const char*>(&g_zeros), dst);
         else
-            lds_buf16<0>(make_rsrc(base, bytes), dst, here ? (uint32_t)rel * (uint32_t)(M * 2) + (uint32_t)col * 2 : kOutOfRange, 0);
+            lds_buf16<0>(s.x, dst, xoff[i], 0);
     };
-    // 16 codes of a row and their scale (zeros where there is no row)
+    // 16 codes of a row and their scale; zeros where there is no row.  A row that ends with 8
+    // codes reads 8 of the next one, in columns that dw does not have.
     uint4 code[C_ITERS];
     float cscale[C_ITERS];
     auto load_codes = [&](const Piece& w, const int* tok, int i0) INLINE {
+        const int rows = p.gather_x ? p.src_rows : p.cap;
 #pragma unroll
         for (int i = 0; i < C_ITERS; ++i) {
             const int k = (i * NW + wave) * CR + lane / (TM / 16);
             const int col = w.m0 + (lane % (TM / 16)) * 16;
-            const int r = row_at(w, tok, p.gather_x, i0 + k);
-            code[i] = make_uint4(0, 0, 0, 0);
-            cscale[i] = 0.0f;
-            if (r >= 0 && col < M) {
-                const int8_t* row = static_cast<const int8_t*>(p.x) + (size_t)r * M + col;
-                const uint2 lo = *reinterpret_cast<const uint2*>(row);
-                uint2 hi = make_uint2(0, 0);
-                if (col + 8 < M) hi = *reinterpret_cast<const uint2*>(row + 8);
-                code[i] = make_uint4(lo.x, lo.y, hi.x, hi.y);
-                cscale[i] = p.x_scales[(size_t)r * nb + col / kCkptBlock];
+            int r = i0 + k < w.rows ? w.row0 + i0 + k : -1;
+            if (p.gather_x) r = tok[i0 + k];
+            const bool here = r >= 0 && col < M;
+            if constexpr (FAR) {
+                code[i] = make_uint4(0, 0, 0, 0);
+                cscale[i] = 0.0f;
+                if (here) {
+                    const int8_t* row = static_cast<const int8_t*>(p.x) + (size_t)r * M + col;
+                    const uint2 lo = *reinterpret_cast<const uint2*>(row);
+                    const uint2 hi = col + 8 < M ? *reinterpret_cast<const uint2*>(row + 8) : make_uint2(0, 0);
+                    code[i] = make_uint4(lo.x, lo.y, hi.x, hi.y);
+                    cscale[i] = p.x_scales[(size_t)r * nb + col / kCkptBlock];
+                }
+            } else {
+                code[i] = buf_load16(make_rsrc(p.x, (uint32_t)rows * (uint32_t)M),
+                                     here ? (uint32_t)r * (uint32_t)M + (uint32_t)col : kOutOfRange);
+                cscale[i] = buf_load4(make_rsrc(p.x_scales, (uint32_t)rows * (uint32_t)nb * 4u),
+                                      here ? ((uint32_t)r * (uint32_t)nb + (uint32_t)(col / kCkptBlock)) * 4u : kOutOfRange);
             }
         }
     };
@@ -203,12 +267,30 @@ __global__ __launch_bounds__(512, 1) void wgrad_kernel(WgradArgs p, int tiles_n,
             d[1] = make_uint4(o[4], o[5], o[6], o[7]);
         }
     };
+    // everything that precedes the direct loads of a step
+    auto prepare = [&](const Piece& w, const int* tok, int i0, bool live) INLINE {
+        Source s;
+        if constexpr (CKPT) load_codes(w, tok, i0);
+        operand_rows(ic<Y_ITERS>{}, ic<YR>{}, p.gather_dy, N * 2, w.n0, N, w, tok, i0, yoff, yrow);
+        if constexpr (!CKPT) operand_rows(ic<X_ITERS>{}, ic<XR>{}, p.gather_x, M * 2, w.m0, M, w, tok, i0, xoff, xrow);
+        const char* dy = static_cast<const char*>(w.q == 0 ? p.dy[0] : p.dy[1]);
+        if constexpr (FAR) {
+            s.ybase = dy;
+            s.xbase = static_cast<const char*>(p.x);
+        } else {
+            const uint32_t left = live ? (uint32_t)(w.rows - i0) : 0u, all = live ? (uint32_t)p.src_rows : 0u;
+            s.y = p.gather_dy ? make_rsrc(dy, all * (uint32_t)(N * 2))
+                              : make_rsrc(dy + (size_t)(w.row0 + i0) * N * 2, left * (uint32_t)(N * 2));
+            if constexpr (!CKPT) {
+                const char* x = static_cast<const char*>(p.x);
+                s.x = p.gather_x ? make_rsrc(x, all * (uint32_t)(M * 2))
+                                 : make_rsrc(x + (size_t)(w.row0 + i0) * M * 2, left * (uint32_t)(M * 2));
+            }
+        }
+        return s;
+    };
 
-    uint32_t yfrag[FN], xfrag[FM];
-#pragma unroll
-    for (int f = 0; f < FN; ++f) yfrag[f] = frag_offset<TN>(lane, wn * (FN * 16) + f * 16);
-#pragma unroll
-    for (int f = 0; f < FM; ++f) xfrag[f] = frag_offset<TM>(lane, wm * (FM * 16) + f * 16);
+    const uint32_t yfrag0 = frag_offset<TN>(lane, wn * (FN * 16)), xfrag0 = frag_offset<TM>(lane, wm * (FM * 16));
 
     floatx4 acc[FN][FM];
     auto clear = [&]() INLINE {
@@ -219,107 +301,142 @@ __global__ __launch_bounds__(512, 1) void wgrad_kernel(WgradArgs p, int tiles_n,
     };
     clear();
 
-    // dw of a finished tile: lane l has row n = l % 16 and columns 4 (l / 16) .. + 3 of every fragment
-    auto write_tile = [&](const Piece& w) INLINE {
-        const size_t mat = (size_t)w.j * N * M;
+    // dw of a finished tile: lane l has row n = l % 16 and columns 4 (l / 16) .. + 3 of every
+    // fragment.  All stores go out, those past the borders to an offset out of range, so that
+    // their number is known to the wait of the next step.  A base is read one row of fragments
+    // ahead of the stores.
+    auto write_as = [&](const Piece& w, auto type, bool based) INLINE {
+        typedef decltype(type) Raw;                           // four columns in memory
+        constexpr int SIZE = sizeof(Raw) / 4;
+        const size_t at = ((size_t)w.j * N + w.n0) * M * SIZE;
         const void* base = w.q == 0 ? p.base[0] : p.base[1];
-        void* dw = w.q == 0 ? p.dw[0] : p.dw[1];
+        char* dw = static_cast<char*>(w.q == 0 ? p.dw[0] : p.dw[1]) + at;
+        const int m = w.m0 + wm * (FM * 16) + (lane >> 4) * 4, n = wn * (FN * 16) + (lane & 15);
+        if constexpr (FAR) {
 #pragma unroll
-        for (int a = 0; a < FN; ++a) {
-            const int n = w.n0 + wn * (FN * 16) + a * 16 + (lane & 15);
-            const size_t row = mat + (size_t)n * M;
-            floatx4 b[FM];
+            for (int a = 0; a < FN; ++a)
 #pragma unroll
-            for (int f = 0; f < FM; ++f) {
-                const int m = w.m0 + wm * (FM * 16) + f * 16 + (lane >> 4) * 4;
-                b[f] = floatx4{0.f, 0.f, 0.f, 0.f};
-                if (base != nullptr && n < N && m < M) {
-                    if (p.dw_f32) {
-                        const float4 t = *reinterpret_cast<const float4*>(static_cast<const float*>(base) + row + m);
-                        b[f] = floatx4{t.x, t.y, t.z, t.w};
-                    } else {
-                        const uint2 t = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(base) + row + m);
-                        b[f] = floatx4{bf16_lo(t.x), bf16_hi(t.x), bf16_lo(t.y), bf16_hi(t.y)};
-                    }
+                for (int f = 0; f < FM; ++f) {
+                    if (w.n0 + n + a * 16 >= N || m + f * 16 >= M) continue;
+                    const size_t o = ((size_t)(n + a * 16) * M + m + f * 16) * SIZE;
+                    floatx4 v = acc[a][f];
+                    if (based) v += base_values(*reinterpret_cast<const Raw*>(static_cast<const char*>(base) + at + o));
+                    if constexpr (SIZE == 4) *reinterpret_cast<floatx4*>(dw + o) = v;
+                    else *reinterpret_cast<uint2*>(dw + o) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+                }
+        } else {
+            const uint32_t bytes = (uint32_t)min(TN, N - w.n0) * (uint32_t)M * SIZE;
+            const rsrc_t rw = make_rsrc(dw, bytes), rb = make_rsrc(static_cast<const char*>(base) + at, based ? bytes : 0u);
+            uint32_t col[FM];
+#pragma unroll
+            for (int f = 0; f < FM; ++f)
+                col[f] = (m + f * 16 < M ? (uint32_t)(m + f * 16) * SIZE : kNoColumn) + (uint32_t)n * (uint32_t)M * SIZE;
+            const uint32_t pitch = 16u * (uint32_t)M * SIZE;
+            Raw b[2][FM];
+            auto load_base = [&](int a) INLINE {
+#pragma unroll
+                for (int f = 0; f < FM; ++f) {
+                    if constexpr (SIZE == 4) b[a & 1][f] = buf_load16(rb, col[f] + a * pitch);
+                    else b[a & 1][f] = buf_load8(rb, col[f] + a * pitch);
+                }
+            };
+            if (based) load_base(0);
+#pragma unroll
+            for (int a = 0; a < FN; ++a) {
+                if (based && a + 1 < FN) load_base(a + 1);
+#pragma unroll
+                for (int f = 0; f < FM; ++f) {
+                    const floatx4 v = based ? acc[a][f] + base_values(b[a & 1][f]) : acc[a][f];
+                    if constexpr (SIZE == 4) buf_store16(rw, col[f] + a * pitch, v);
+                    else buf_store8(rw, col[f] + a * pitch, v);
                 }
             }
-#pragma unroll
-            for (int f = 0; f < FM; ++f) {
-                const int m = w.m0 + wm * (FM * 16) + f * 16 + (lane >> 4) * 4;
-                if (n >= N || m >= M) continue;
-                const floatx4 s = acc[a][f] + b[f];
-                if (p.dw_f32)
-                    *reinterpret_cast<float4*>(static_cast<float*>(dw) + row + m) = make_float4(s[0], s[1], s[2], s[3]);
-                else
-                    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(dw) + row + m) =
-                        make_uint2(pack_bf16x2(s[0], s[1]), pack_bf16x2(s[2], s[3]));
-            }
         }
+    };
+    auto write_tile = [&](const Piece& w) INLINE {
+        typedef std::conditional_t<F32, uint4, uint2> Raw;
+        if ((w.q == 0 ? p.base[0] : p.base[1]) != nullptr) write_as(w, Raw{}, true);
+        else write_as(w, Raw{}, false);
     };
 
-    // the sequence of steps: `cur` is computed, `nxt` loaded
-    Piece cur, nxt;
+    // the sequence of steps: `cur` is computed, `nxt` comes after it; s_tok[slot] lists cur's rows
+    Piece cur, nxt, then;
+    cur.j = cur.q = cur.n0 = cur.m0 = 0;
     open_tile(xcd_block_order(), cur);
     if (cur.tile >= tiles) return;
-    int slot = 0;                                            // s_tok of cur's piece; the next one's is the other
     load_list(cur);
-    store_list(cur, s_tok[0]);
+    store_list(s_tok[0]);
     nxt = after(cur);
     load_list(nxt);
-    store_list(nxt, s_tok[1]);
+    store_list(s_tok[1]);
     __syncthreads();
-    auto issue_step = [&](auto I, const Piece& w, const int* tok, int i0) INLINE {
-        if constexpr (CKPT) load_codes(w, tok, i0);
+    {
+        const Source s = prepare(cur, s_tok[0], 0, true);
 #pragma unroll
-        for (int i = 0; i < Y_ITERS; ++i) issue_y(I, w, tok, i0, i);
-        if constexpr (!CKPT) {
+        for (int i = 0; i < Y_ITERS; ++i) issue_y(ic<0>{}, s, i);
+        if constexpr (CKPT) store_codes(ic<0>{});
+        else {
 #pragma unroll
-            for (int i = 0; i < X_ITERS; ++i) issue_x(I, w, tok, i0, i);
+            for (int i = 0; i < X_ITERS; ++i) issue_x(ic<0>{}, s, i);
         }
-    };
-    issue_step(ic<0>{}, cur, s_tok[0], 0);
-    if constexpr (CKPT) store_codes(ic<0>{});
-    int i0 = 0;                                              // first row of cur's step
+    }
+    int slot = 0, i0 = 0;                        // i0: first row of cur's step
+    bool draining = false;                                   // a tile's stores are the last things issued
 
     // one step; false after the last one of all
     auto step = [&](auto I) INLINE -> bool {
-        constexpr auto other = ic<1 - decltype(I)::value>{};
-        wait_vmcnt<0>();
+        // this step's loads have landed; a tile's stores issued after them may still be on their way
+        if (draining) wait_vmcnt<STORES>();
+        else wait_vmcnt<0>();
+        draining = false;
         wait_lgkm0();
         block_barrier();
         // what comes next: another step of this piece, or the first of the next piece
-        const bool same = __builtin_amdgcn_readfirstlane(i0 + BK < cur.rows ? 1 : 0) != 0;
-        const bool more = __builtin_amdgcn_readfirstlane(same || nxt.tile < tiles ? 1 : 0) != 0;
-        const bool turn = !same && more;
-        Piece then = nxt;
+        const bool same = uniform(i0 + BK < cur.rows ? 1 : 0) != 0;
+        const bool more = uniform(same || nxt.tile < tiles ? 1 : 0) != 0;
+        const bool turn = uniform(!same && more ? 1 : 0) != 0;
         if (turn) {
             then = after(nxt);
             load_list(then);
         }
-        if (more) {
-            if (same) issue_step(other, cur, s_tok[slot], i0 + BK);
-            else issue_step(other, nxt, s_tok[slot ^ 1], 0);
-        }
-        const char* yb = y_base(I);
-        const char* xb = x_base(I);
+        {
+            constexpr auto other = ic<1 - decltype(I)::value>{};
+            const Piece& w = same ? cur : nxt;
+            // (past the last step nothing is read, but the loads go out)
+            const Source s = prepare(w, s_tok[same ? slot : slot ^ 1], same ? i0 + BK : 0, more);
+            const char* yb = y_base(I);
+            const char* xb = x_base(I);
+            uint32_t y0 = yfrag0, x0 = xfrag0;
+            asm volatile("" : "+v"(y0), "+v"(x0));           // keeps the offsets below from living across steps
 #pragma unroll
-        for (int kk = 0; kk < 2; ++kk) {
-            bf16x8 xf[FM];
+            for (int kk = 0; kk < 2; ++kk) {
+                bf16x8 xf[FM];
 #pragma unroll
-            for (int f = 0; f < FM; ++f) xf[f] = read_frag<TM>(xb, xfrag[f], kk);
+                for (int f = 0; f < FM; ++f) xf[f] = read_frag<TM>(xb, x0 ^ (f << 5), kk);
+                bf16x8 yf = read_frag<TN>(yb, y0, kk);
 #pragma unroll
-            for (int a = 0; a < FN; ++a) {
-                const bf16x8 yf = read_frag<TN>(yb, yfrag[a], kk);
+                for (int a = 0; a < FN; ++a) {
+                    bf16x8 yn;
+                    if (a + 1 < FN) yn = read_frag<TN>(yb, y0 ^ ((a + 1) << 5), kk);
 #pragma unroll
-                for (int f = 0; f < FM; ++f)
-                    acc[a][f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xf[f], yf, acc[a][f], 0, 0, 0);
+                    for (int f = 0; f < FM; ++f)
+                        acc[a][f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xf[f], yf, acc[a][f], 0, 0, 0);
+                    const int q = kk * FN + a;
+                    if (q < Y_ITERS) issue_y(other, s, q);
+                    else if (q < LOADS) issue_x(other, s, q - Y_ITERS);
+                    if (a + 1 < FN) yf = yn;
+                    __builtin_amdgcn_sched_barrier(0);
+                }
             }
-        }
-        if constexpr (CKPT) {
-            if (more) store_codes(other);
+#pragma unroll
+            for (int q = 2 * FN; q < LOADS; ++q) {
+                if (q < Y_ITERS) issue_y(other, s, q);
+                else issue_x(other, s, q - Y_ITERS);
+            }
+            if constexpr (CKPT) store_codes(other);
         }
         // cur's list was last read for this step's loads, ahead of the barrier above
-        if (turn) store_list(then, s_tok[slot]);
+        if (turn) store_list(s_tok[slot]);
         if (same) {
             i0 += BK;
             return true;
@@ -327,6 +444,7 @@ __global__ __launch_bounds__(512, 1) void wgrad_kernel(WgradArgs p, int tiles_n,
         if (cur.row0 + cur.rows >= cur.end) {
             write_tile(cur);
             clear();
+            draining = !FAR;
         }
         if (!more) return false;
         cur = nxt;
@@ -339,39 +457,43 @@ __global__ __launch_bounds__(512, 1) void wgrad_kernel(WgradArgs p, int tiles_n,
         if (!step(ic<0>{})) break;
         if (!step(ic<1>{})) break;
     }
+    wait_vmcnt<0>();                                         // the loads past the last step have landed
 }
 
-template <int TN, int TM, bool CKPT, bool FAR>
+template <int TN, int TM, bool CKPT, bool F32, bool FAR>
 hipError_t launch_tiles(const WgradArgs& a, hipStream_t stream) {
     static int per_cu = 0;
     if (per_cu == 0) {
         int n = 0;
-        if (hipOccupancyMaxActiveBlocksPerMultiprocessor(&n, wgrad_kernel<TN, TM, CKPT, FAR>, 512, 0) != hipSuccess || n < 1) n = 1;
+        if (hipOccupancyMaxActiveBlocksPerMultiprocessor(&n, wgrad_kernel<TN, TM, CKPT, F32, FAR>, 512, 0) != hipSuccess || n < 1) n = 1;
         per_cu = n;
     }
     const int tn = (a.N + TN - 1) / TN, tm = (a.M + TM - 1) / TM;
     const int tiles = a.E_loc * (a.dy[1] != nullptr ? 2 : 1) * tn * tm;      // (api.hip bounds dw)
     const int most = device_cu_count() * per_cu;
-    hipLaunchKernelGGL((wgrad_kernel<TN, TM, CKPT, FAR>), dim3(tiles < most ? tiles : most), dim3(512), 0, stream, a, tn, tm,
+    hipLaunchKernelGGL((wgrad_kernel<TN, TM, CKPT, F32, FAR>), dim3(tiles < most ? tiles : most), dim3(512), 0, stream, a, tn, tm,
                        tiles);
     return hipGetLastError();
 }
 
-template <bool CKPT>
+template <bool CKPT, bool F32>
 hipError_t launch_any(const WgradArgs& a, hipStream_t stream) {
-    // direct loads reach an operand's gathered rows, or a piece's, by 32-bit offsets below kOutOfRange
-    const unsigned long long y_rows = a.gather_dy ? a.src_rows : kPieceRows, x_rows = a.gather_x ? a.src_rows : kPieceRows;
-    const bool far = y_rows * a.N * 2 >= (1ull << 31) || (!CKPT && x_rows * a.M * 2 >= (1ull << 31));
-    if (far) return launch_tiles<256, 256, CKPT, true>(a, stream);
+    // 32-bit offsets reach an operand's gathered rows (others: a piece's), all codes and scales,
+    // and a tile's rows of dw
+    const unsigned long long y_rows = a.gather_dy ? a.src_rows : kPieceRows;
+    const unsigned long long x_rows = a.gather_x ? a.src_rows : CKPT ? a.cap : kPieceRows;
+    const bool far = y_rows * a.N * 2 >= kReach || x_rows * a.M * (CKPT ? 1 : 2) >= kReach || 256ull * a.M * 4 >= kReach;
+    if (far) return launch_tiles<256, 256, CKPT, F32, true>(a, stream);
     const long long large = (long long)a.E_loc * (a.dy[1] != nullptr ? 2 : 1) * ((a.N + 255) / 256) * ((a.M + 255) / 256);
-    if (large >= device_cu_count()) return launch_tiles<256, 256, CKPT, false>(a, stream);
-    return launch_tiles<128, 128, CKPT, false>(a, stream);
+    if (large >= device_cu_count()) return launch_tiles<256, 256, CKPT, F32, false>(a, stream);
+    return launch_tiles<128, 128, CKPT, F32, false>(a, stream);
 }
 
 }  // namespace
 
 hipError_t launch_wgrad_bf16(const WgradArgs& a, hipStream_t stream) {
-    return a.x_scales != nullptr ? launch_any<true>(a, stream) : launch_any<false>(a, stream);
+    if (a.dw_f32) return a.x_scales != nullptr ? launch_any<true, true>(a, stream) : launch_any<false, true>(a, stream);
+    return a.x_scales != nullptr ? launch_any<true, false>(a, stream) : launch_any<false, false>(a, stream);
 }
 
 }  // namespace moeep
