@@ -41,18 +41,12 @@ constexpr unsigned long long kReach = kNoColumn;
 __device__ uint4 g_zeros;
 
 __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+template <int CPOL>
 __device__ __forceinline__ uint4 buf_load16(rsrc_t r, uint32_t off) {
 #if defined(__HIP_DEVICE_COMPILE__)
-    return __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(r, (int)off, 0, 0));
+    return __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(r, (int)off, 0, CPOL));
 #else
     return make_uint4(0, 0, 0, 0);
-#endif
-}
-__device__ __forceinline__ uint2 buf_load8(rsrc_t r, uint32_t off) {
-#if defined(__HIP_DEVICE_COMPILE__)
-    return __builtin_bit_cast(uint2, __builtin_amdgcn_raw_buffer_load_b64(r, (int)off, 0, 0));
-#else
-    return make_uint2(0, 0);
 #endif
 }
 __device__ __forceinline__ float buf_load4(rsrc_t r, uint32_t off) {
@@ -62,21 +56,29 @@ __device__ __forceinline__ float buf_load4(rsrc_t r, uint32_t off) {
     return 0.0f;
 #endif
 }
-__device__ __forceinline__ void buf_store16(rsrc_t r, uint32_t off, floatx4 v) {
+template <int CPOL>
+__device__ __forceinline__ void buf_store16(rsrc_t r, uint32_t off, uint4 v) {
 #if defined(__HIP_DEVICE_COMPILE__)
-    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, v), r, (int)off, 0, 0);
+    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, v), r, (int)off, 0, CPOL);
 #endif
 }
-typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
-__device__ __forceinline__ void buf_store8(rsrc_t r, uint32_t off, floatx4 v) {
-#if defined(__HIP_DEVICE_COMPILE__)
-    __builtin_amdgcn_raw_buffer_store_b64(u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])}, r, (int)off, 0, 0);
-#endif
+
+// Of two fragments' results (lane n of 16 has row n of each): a becomes rows 0..7 of both, the
+// second's in lanes 8..15, b rows 8..15, the first's in lanes 0..7.
+__device__ __forceinline__ void exchange_rows(float& a, float& b) {
+    const int x = __float_as_int(a), y = __float_as_int(b);
+    constexpr int kRor8 = 0x128;
+    a = __int_as_float(__builtin_amdgcn_update_dpp(x, y, kRor8, 0xf, 0xc, false));
+    b = __int_as_float(__builtin_amdgcn_update_dpp(y, x, kRor8, 0xf, 0x3, false));
 }
-// base values of four neighbouring columns, as they are in memory
-__device__ __forceinline__ floatx4 base_values(uint4 t) { return __builtin_bit_cast(floatx4, t); }
-__device__ __forceinline__ floatx4 base_values(uint2 t) {
-    return floatx4{bf16_lo(t.x), bf16_hi(t.x), bf16_lo(t.y), bf16_hi(t.y)};
+// Of two values of every lane, by groups of 16 lanes: even groups keep a and get the next
+// group's a beside it, odd groups keep b behind the group before's b.
+__device__ __forceinline__ void exchange_groups(float& a, float& b) {
+#if defined(__HIP_DEVICE_COMPILE__)
+    const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(a), __float_as_uint(b), false, false);
+    a = __uint_as_float(r[0]);
+    b = __uint_as_float(r[1]);
+#endif
 }
 
 // a piece of work: rows [row0, row0 + rows) of a tile's expert
@@ -96,7 +98,9 @@ __global__ __launch_bounds__(512, 1) void wgrad_kernel(WgradArgs p, int tiles_n,
     constexpr int YR = 512 / TN, XR = 512 / TM;              // rows of a direct load
     constexpr int CR = 1024 / TM;                            // rows of a wave's code load
     constexpr int LOADS = Y_ITERS + (CKPT ? 0 : X_ITERS);
-    constexpr int STORES = FN * FM;                          // of a wave and tile, whatever its borders
+    // dw in 16-byte units: 4 columns of fp32, 8 of bf16
+    constexpr int SIZE = F32 ? 4 : 2, WIDE = 16 / SIZE, UNITS = FM * 4 / WIDE;
+    constexpr int STORES = FN * UNITS;                       // of a wave and tile, whatever its borders
     static_assert(Y_ITERS >= 1 && X_ITERS >= 1 && C_ITERS >= 1 && STORES < 64, "tile shape");
 
     // each stage an object of its own: the compiler sees that reads of one do not
@@ -242,7 +246,7 @@ __global__ __launch_bounds__(512, 1) void wgrad_kernel(WgradArgs p, int tiles_n,
                     cscale[i] = p.x_scales[(size_t)r * nb + col / kCkptBlock];
                 }
             } else {
-                code[i] = buf_load16(make_rsrc(p.x, (uint32_t)rows * (uint32_t)M),
+                code[i] = buf_load16<0>(make_rsrc(p.x, (uint32_t)rows * (uint32_t)M),
                                      here ? (uint32_t)r * (uint32_t)M + (uint32_t)col : kOutOfRange);
                 cscale[i] = buf_load4(make_rsrc(p.x_scales, (uint32_t)rows * (uint32_t)nb * 4u),
                                       here ? ((uint32_t)r * (uint32_t)nb + (uint32_t)(col / kCkptBlock)) * 4u : kOutOfRange);
@@ -301,62 +305,102 @@ __global__ __launch_bounds__(512, 1) void wgrad_kernel(WgradArgs p, int tiles_n,
     };
     clear();
 
-    // dw of a finished tile: lane l has row n = l % 16 and columns 4 (l / 16) .. + 3 of every
-    // fragment.  All stores go out, those past the borders to an offset out of range, so that
-    // their number is known to the wait of the next step.  A base is read one row of fragments
-    // ahead of the stores.
-    auto write_as = [&](const Piece& w, auto type, bool based) INLINE {
-        typedef decltype(type) Raw;                           // four columns in memory
-        constexpr int SIZE = sizeof(Raw) / 4;
+    // dw of a finished tile.  Lane l of a fragment has row n = l % 16 and columns 4 (l / 16) ..
+    // + 3.  Lanes exchange values so that a unit is 16 bytes and a store covers whole 128-byte
+    // lines (8 rows of them; bf16 in 128-column tiles half lines): such stores can be
+    // non-temporal, and dw, 56 MB a pair at 2048 x 7168, does not push the operands out of L2.
+    // (Half lines, kept in L2: EP share 1509 us; whole ones, not kept, 1238 us.)  All stores go
+    // out, those past the borders to an offset out of range, so that their number is known to
+    // the wait of the next step.  A base is read one row of fragments ahead of the stores.
+    const int g = lane >> 4, n8 = lane & 7, upper = (lane >> 3) & 1;
+    auto unit_row = [&](int u) INLINE { return n8 + (F32 ? (u & 1) * 8 : FM == 4 ? u * 8 : (g & 1) * 8); };
+    auto unit_col = [&](int u) INLINE {
+        return upper * 16 + (F32 ? (u >> 1) * 32 + g * 4 : (FM == 4 ? (g & 1) * 32 : 0) + (g >> 1) * 8);
+    };
+    auto units_of = [&](int a, float (&v)[UNITS][WIDE]) INLINE {
+        float t[FM][4];
+#pragma unroll
+        for (int f = 0; f < FM; f += 2)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                t[f][e] = acc[a][f][e];
+                t[f + 1][e] = acc[a][f + 1][e];
+                exchange_rows(t[f][e], t[f + 1][e]);
+            }
+#pragma unroll
+        for (int u = 0; u < UNITS; ++u)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                if constexpr (F32) v[u][e] = t[u][e];
+                else {
+                    // rows 8 u .. + 7 of both column pairs; of the only pair, rows 0..7 and 8..15
+                    float x = t[u][e], y = t[FM == 4 ? u + 2 : 1][e];
+                    exchange_groups(x, y);
+                    v[u][e] = x;
+                    v[u][4 + e] = y;
+                }
+            }
+    };
+    auto write_as = [&](const Piece& w, bool based) INLINE {
         const size_t at = ((size_t)w.j * N + w.n0) * M * SIZE;
-        const void* base = w.q == 0 ? p.base[0] : p.base[1];
+        const char* base = static_cast<const char*>(w.q == 0 ? p.base[0] : p.base[1]) + at;
         char* dw = static_cast<char*>(w.q == 0 ? p.dw[0] : p.dw[1]) + at;
-        const int m = w.m0 + wm * (FM * 16) + (lane >> 4) * 4, n = wn * (FN * 16) + (lane & 15);
-        if constexpr (FAR) {
+        const int m = w.m0 + wm * (FM * 16), n = wn * (FN * 16);
+        const uint32_t bytes = FAR ? 0u : (uint32_t)min(TN, N - w.n0) * (uint32_t)M * SIZE, pitch = (uint32_t)M * SIZE;
+        const rsrc_t rw = make_rsrc(dw, bytes), rb = make_rsrc(base, based ? bytes : 0u);
+        uint32_t off[UNITS];
 #pragma unroll
-            for (int a = 0; a < FN; ++a)
+        for (int u = 0; u < UNITS; ++u) {
+            const int col = m + unit_col(u);
+            off[u] = (col < M ? (uint32_t)col * SIZE : kNoColumn) + (uint32_t)(n + unit_row(u)) * pitch;
+        }
+        constexpr int CPOL = F32 || FM == 4 ? kNonTemporal : 0;
+        uint4 b[2][UNITS];
+        auto load_base = [&](int a) INLINE {
 #pragma unroll
-                for (int f = 0; f < FM; ++f) {
-                    if (w.n0 + n + a * 16 >= N || m + f * 16 >= M) continue;
-                    const size_t o = ((size_t)(n + a * 16) * M + m + f * 16) * SIZE;
-                    floatx4 v = acc[a][f];
-                    if (based) v += base_values(*reinterpret_cast<const Raw*>(static_cast<const char*>(base) + at + o));
-                    if constexpr (SIZE == 4) *reinterpret_cast<floatx4*>(dw + o) = v;
-                    else *reinterpret_cast<uint2*>(dw + o) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+            for (int u = 0; u < UNITS; ++u) b[a & 1][u] = buf_load16<CPOL>(rb, off[u] + a * 16 * pitch);
+        };
+        if (!FAR && based) load_base(0);
+#pragma unroll
+        for (int a = 0; a < FN; ++a) {
+            if (!FAR && based && a + 1 < FN) load_base(a + 1);
+            float v[UNITS][WIDE];
+            units_of(a, v);
+#pragma unroll
+            for (int u = 0; u < UNITS; ++u) {
+                const int row = n + a * 16 + unit_row(u), col = m + unit_col(u);
+                const bool here = w.n0 + row < N && col < M;
+                const size_t o = ((size_t)row * M + col) * SIZE;
+                if (based) {
+                    if constexpr (FAR) b[a & 1][u] = here ? *reinterpret_cast<const uint4*>(base + o) : make_uint4(0, 0, 0, 0);
+                    const uint32_t t[4] = {b[a & 1][u].x, b[a & 1][u].y, b[a & 1][u].z, b[a & 1][u].w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        if constexpr (F32) v[u][e] += __uint_as_float(t[e]);
+                        else {
+                            v[u][2 * e] += bf16_lo(t[e]);
+                            v[u][2 * e + 1] += bf16_hi(t[e]);
+                        }
+                    }
                 }
-        } else {
-            const uint32_t bytes = (uint32_t)min(TN, N - w.n0) * (uint32_t)M * SIZE;
-            const rsrc_t rw = make_rsrc(dw, bytes), rb = make_rsrc(static_cast<const char*>(base) + at, based ? bytes : 0u);
-            uint32_t col[FM];
-#pragma unroll
-            for (int f = 0; f < FM; ++f)
-                col[f] = (m + f * 16 < M ? (uint32_t)(m + f * 16) * SIZE : kNoColumn) + (uint32_t)n * (uint32_t)M * SIZE;
-            const uint32_t pitch = 16u * (uint32_t)M * SIZE;
-            Raw b[2][FM];
-            auto load_base = [&](int a) INLINE {
-#pragma unroll
-                for (int f = 0; f < FM; ++f) {
-                    if constexpr (SIZE == 4) b[a & 1][f] = buf_load16(rb, col[f] + a * pitch);
-                    else b[a & 1][f] = buf_load8(rb, col[f] + a * pitch);
-                }
-            };
-            if (based) load_base(0);
-#pragma unroll
-            for (int a = 0; a < FN; ++a) {
-                if (based && a + 1 < FN) load_base(a + 1);
-#pragma unroll
-                for (int f = 0; f < FM; ++f) {
-                    const floatx4 v = based ? acc[a][f] + base_values(b[a & 1][f]) : acc[a][f];
-                    if constexpr (SIZE == 4) buf_store16(rw, col[f] + a * pitch, v);
-                    else buf_store8(rw, col[f] + a * pitch, v);
+                uint4 t;
+                if constexpr (F32)
+                    t = make_uint4(__float_as_uint(v[u][0]), __float_as_uint(v[u][1]), __float_as_uint(v[u][2]),
+                                   __float_as_uint(v[u][3]));
+                else
+                    t = make_uint4(pack_bf16x2(v[u][0], v[u][1]), pack_bf16x2(v[u][2], v[u][3]),
+                                   pack_bf16x2(v[u][4], v[u][5]), pack_bf16x2(v[u][6], v[u][7]));
+                if constexpr (FAR) {
+                    if (here) *reinterpret_cast<uint4*>(dw + o) = t;
+                } else {
+                    buf_store16<CPOL>(rw, off[u] + a * 16 * pitch, t);
                 }
             }
         }
     };
     auto write_tile = [&](const Piece& w) INLINE {
-        typedef std::conditional_t<F32, uint4, uint2> Raw;
-        if ((w.q == 0 ? p.base[0] : p.base[1]) != nullptr) write_as(w, Raw{}, true);
-        else write_as(w, Raw{}, false);
+        if ((w.q == 0 ? p.base[0] : p.base[1]) != nullptr) write_as(w, true);
+        else write_as(w, false);
     };
 
     // the sequence of steps: `cur` is computed, `nxt` comes after it; s_tok[slot] lists cur's rows
