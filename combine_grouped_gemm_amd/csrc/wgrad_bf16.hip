@@ -35,6 +35,8 @@ constexpr int kPieceRows = 1024;             // rows listed at a time
 constexpr uint32_t kNoColumn = 0x7fff0000u;
 constexpr unsigned long long kReach = kNoColumn;
 
+constexpr int kGroup = 4;                    // tiles along the in columns that are done together
+
 #define INLINE __attribute__((always_inline))
 
 // what a lane of a 64-bit load reads where there is nothing to read
@@ -131,19 +133,20 @@ __global__ __launch_bounds__(512, 1) void wgrad_kernel(WgradArgs p, int tiles_n,
         w.tile = tau;
         w.row0 = w.rows = w.end = 0;
         if (tau >= tiles) return;
-        // out columns fastest, then the pair, then the in columns, then the expert: tiles that run
-        // together share both operands in L2
-        unsigned rest = (unsigned)tau;
-        w.n0 = (int)(rest % (unsigned)tiles_n) * TN;
-        rest /= (unsigned)tiles_n;
-        const unsigned pairs = p.dy[1] != nullptr ? 2 : 1;
-        w.q = (int)(rest % pairs);
-        rest /= pairs;
-        w.m0 = (int)(rest % (unsigned)tiles_m) * TM;
-        w.j = uniform((int)(rest / (unsigned)tiles_m));
-        w.n0 = uniform(w.n0);
-        w.q = uniform(w.q);
-        w.m0 = uniform(w.m0);
+        // Groups of kGroup tiles along the in columns, within them all tiles along the out
+        // columns, then the pair: the 32 tiles that run together on an XCD share 8 + 4 operand
+        // columns of tiles in its L2, and the next ones go on with the 4.
+        const unsigned pairs = p.dy[1] != nullptr ? 2 : 1, per = (unsigned)tiles_n * (unsigned)tiles_m * pairs;
+        w.j = uniform((int)((unsigned)tau / per));
+        unsigned rest = (unsigned)tau - (unsigned)w.j * per;
+        const unsigned band = (unsigned)tiles_n * kGroup * pairs, b = rest / band;
+        rest -= b * band;
+        const unsigned wide = min((unsigned)tiles_m - b * kGroup, (unsigned)kGroup), one = (unsigned)tiles_n * wide;
+        w.q = uniform(rest >= one ? 1 : 0);
+        rest -= w.q ? one : 0u;
+        const unsigned n = rest / wide;
+        w.n0 = uniform((int)n * TN);
+        w.m0 = uniform((int)(b * kGroup + rest - n * wide) * TM);
         w.row0 = uniform(clampi(p.offsets[w.j], 0, p.cap));
         w.end = uniform(clampi(p.offsets[w.j + 1], w.row0, p.cap));
         w.rows = min(w.end - w.row0, kPieceRows);
