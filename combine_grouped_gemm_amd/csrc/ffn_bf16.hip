@@ -35,8 +35,11 @@ namespace {
 
 constexpr int BK = 64;            // bf16 per k-step
 
-template <int BM, int BN, int WMW, int WNW, bool GATED>
+// CKPT (gate/up with BN = 256: a tile's 128 columns of g and of u are a checkpoint block
+// each): g and u also leave as 8-bit checkpoints, as in gemm_wide.hpp.
+template <int BM, int BN, int WMW, int WNW, bool GATED, bool CKPT = false>
 __global__ __launch_bounds__(64 * WMW * WNW) void grouped_gemm_bf16_kernel(FfnArgs p) {
+    static_assert(!CKPT || (GATED && BN == 256), "checkpoint blocks");
     constexpr int NT = 64 * WMW * WNW;
     constexpr int FM = BM / 16 / WMW;          // m-fragments per wave
     constexpr int WN = BN / WNW;               // B-tile rows per wave
@@ -206,30 +209,84 @@ __global__ __launch_bounds__(64 * WMW * WNW) void grouped_gemm_bf16_kernel(FfnAr
                 }
             }
         }
+        if constexpr (CKPT) {
+            __shared__ uint2 s_max[BM][WNW];
+            const int nb = (N + kCkptBlock - 1) / kCkptBlock;
+#pragma unroll
+            for (int i = 0; i < FM; ++i)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    uint32_t g = 0, u = 0;      // (columns past N hold zeros)
+#pragma unroll
+                    for (int f = 0; f < FN / 2; ++f) {
+                        g = max(g, __float_as_uint(acc[i][f][e]) & 0x7fffffffu);
+                        u = max(u, __float_as_uint(acc[i][f + FN / 2][e]) & 0x7fffffffu);
+                    }
+                    g = row16_max_u32(g);
+                    u = row16_max_u32(u);
+                    if ((lane & 15) == 0) s_max[(wm + WMW * i) * 16 + (lane >> 4) * 4 + e][wn] = make_uint2(g, u);
+                }
+            __syncthreads();                    // (the next write is behind the next tile's k-loop barriers)
+#pragma unroll
+            for (int i = 0; i < FM; ++i)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int r = (wm + WMW * i) * 16 + (lane >> 4) * 4 + e;
+                    if (r >= nvalid) continue;
+                    uint2 m = s_max[r][0];
+#pragma unroll
+                    for (int w = 1; w < WNW; ++w) m = make_uint2(max(m.x, s_max[r][w].x), max(m.y, s_max[r][w].y));
+                    const float gs = ckpt_scale(m.x), us = ckpt_scale(m.y), grs = ckpt_recip(gs), urs = ckpt_recip(us);
+                    const size_t row = (size_t)(row0 + r);
+                    if (wn == 0 && (lane & 15) == 0) {
+                        p.gate_s[row * nb + tc.nt] = gs;
+                        p.up_s[row * nb + tc.nt] = us;
+                    }
+#pragma unroll
+                    for (int f = 0; f < FN / 2; ++f) {
+                        const int col = fcol(f) + (lane & 15);
+                        if (col >= N) continue;
+                        p.gate_q[row * N + col] = gs == gs ? (int8_t)ckpt_code(acc[i][f][e], grs) : (int8_t)0;
+                        p.up_q[row * N + col] = us == us ? (int8_t)ckpt_code(acc[i][f + FN / 2][e], urs) : (int8_t)0;
+                    }
+                }
+        }
     }
 }
 
-template <int BM, int BN, int WMW, int WNW, bool GATED>
+template <int BM, int BN, int WMW, int WNW, bool GATED, bool CKPT = false>
 hipError_t launch_cfg(const FfnArgs& a, hipStream_t stream) {
     static int per_cu = 0;
-    return launch_persistent(grouped_gemm_bf16_kernel<BM, BN, WMW, WNW, GATED>, 64 * WMW * WNW, a,
+    return launch_persistent(grouped_gemm_bf16_kernel<BM, BN, WMW, WNW, GATED, CKPT>, 64 * WMW * WNW, a,
                              stream, &per_cu);
 }
 
-template <int BM, bool GATED>
+template <int BM, bool GATED, bool CKPT = false>
 hipError_t launch_wide(const FfnArgs& a, hipStream_t stream) {
     static int per_cu = 0;
-    return launch_persistent(wide::grouped_gemm_bf16_wide_kernel<BM, GATED>, 512, a, stream, &per_cu);
+    return launch_persistent(wide::grouped_gemm_bf16_wide_kernel<BM, GATED, CKPT>, 512, a, stream, &per_cu);
+}
+
+// see launch_ffn_bf16
+bool wide_reaches(const FfnArgs& a) {
+    return (unsigned long long)a.N * a.ldw * 2 < (1ull << 31) && (unsigned long long)320 * (a.Kdim + 64) * 2 < (1ull << 31);
 }
 
 }  // namespace
+
+hipError_t launch_ffn_ckpt_bf16(const FfnArgs& a, hipStream_t stream) {
+    const bool wide_ok = wide_reaches(a);
+    if (wide_ok && a.rows_hint >= 192) return launch_wide<320, true, true>(a, stream);
+    if (wide_ok && a.rows_hint >= 64) return launch_wide<256, true, true>(a, stream);
+    if (a.rows_hint < 24) return launch_cfg<16, 256, 1, 4, true, true>(a, stream);
+    return launch_cfg<64, 256, 1, 4, true, true>(a, stream);
+}
 
 hipError_t launch_ffn_bf16(const FfnArgs& a, bool gated, hipStream_t stream) {
     // the wide kernels address one expert's weight matrix with 32-bit offsets
     // and keep every resource extent (plus the k-step offset) below 2^31, so
     // that an out-of-range lane offset exists
-    const bool wide_ok = (unsigned long long)a.N * a.ldw * 2 < (1ull << 31) &&
-                         (unsigned long long)320 * (a.Kdim + 64) * 2 < (1ull << 31);
+    const bool wide_ok = wide_reaches(a);
     if (wide_ok && a.rows_hint >= 192)   // ~256-row experts: one 320-row tile holds nearly all
         return gated ? launch_wide<320, true>(a, stream) : launch_wide<320, false>(a, stream);
     if (wide_ok && a.rows_hint >= 64)

@@ -44,6 +44,7 @@
 
 #include <type_traits>
 
+#include "ckpt_common.hpp"
 #include "grouped_tiles.hpp"
 
 namespace moeep {
@@ -156,8 +157,13 @@ __device__ __forceinline__ uint32_t lds_addr(const void* p) {
 // 8 waves laid out 2 (rows) x 4 (weight rows).  A wave owns the interleaved
 // 16-row fragments {wm, wm + 2, ...} (so a short tile still spreads its valid
 // rows over both row-waves) and 64 weight rows.
-template <int BM, bool GATED>
+//
+// CKPT (gate/up only): g and u also leave as 8-bit checkpoints.  A tile's 128 gate and
+// 128 up rows are one checkpoint block each, its columns spread over four waves: the
+// epilogue joins the waves' row maxima in LDS and stages the codes as it does h.
+template <int BM, bool GATED, bool CKPT = false>
 __global__ __launch_bounds__(512, 1) void grouped_gemm_bf16_wide_kernel(FfnArgs p) {
+    static_assert(!CKPT || GATED, "checkpoints belong to gate/up");
     constexpr int WMW = 2, WNW = 4, NT = 512, NW = 8;
     constexpr int A_BLOCKS = BM * CPR / 64;          // 1 KiB blocks of a row stage
     constexpr int BLOCKS = (BM + BN) * CPR / 64;
@@ -536,6 +542,77 @@ __global__ __launch_bounds__(512, 1) void grouped_gemm_bf16_wide_kernel(FfnArgs 
                     if (i < NF && trow < nvalid && col < N) {
                         const uint4 v = *reinterpret_cast<const uint4*>(region + lrow * OPITCH + ch * 16);
                         *reinterpret_cast<uint4*>(out_bytes + ((size_t)(row0 + trow) * N + col) * 2) = v;
+                    }
+                }
+            }
+            if constexpr (CKPT) {
+                int ln = lane;
+                asm volatile("" : "+v"(ln));                    // keeps what depends on it out of the k-loop's registers
+                // row maxima of this wave's 32 columns, [row][wave column][g, u], behind the regions of sb0
+                constexpr int kMax = 2 * RSZ;
+                static_assert(kMax + BM * WNW * 8 <= BN * ROWB && FO == 2, "row maxima fit behind the regions");
+                char* maxima = reinterpret_cast<char*>(sb0) + kMax;
+#pragma unroll
+                for (int i = 0; i < NF; ++i)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        uint32_t m[2];
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            const uint32_t a = __float_as_uint(acc[i][2 * h][e]) & 0x7fffffffu;
+                            const uint32_t b = __float_as_uint(acc[i][2 * h + 1][e]) & 0x7fffffffu;
+                            m[h] = row16_max_u32(a > b ? a : b);
+                        }
+                        const int trow = (wm + WMW * i) * 16 + (ln >> 4) * 4 + e;
+                        if ((ln & 15) == 0)
+                            *reinterpret_cast<uint2*>(maxima + (trow * WNW + wn) * 8) = make_uint2(m[0], m[1]);
+                        __builtin_amdgcn_sched_barrier(0);       // (all rows at once would spill)
+                    }
+                wait_lgkm0();
+                block_barrier();
+                const int nb = (N + kCkptBlock - 1) / kCkptBlock;
+                constexpr int CPITCH = 32 + 16;                 // staged codes of a row: 32 bytes, padded
+                constexpr int CPF = PF * OPITCH / (2 * CPITCH); // fragments a pass, g and u
+                static_assert(CPF >= 1, "staged codes fit in a region");
+#pragma unroll
+                for (int p0 = 0; p0 < NF; p0 += CPF) {
+#pragma unroll
+                    for (int ii = 0; ii < CPF; ++ii) {
+                        const int i = p0 + ii;
+                        if (i < NF) {
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                const int trow = (wm + WMW * i) * 16 + (ln >> 4) * 4 + e;
+                                const uint4 a = *reinterpret_cast<const uint4*>(maxima + trow * WNW * 8);
+                                const uint4 b = *reinterpret_cast<const uint4*>(maxima + trow * WNW * 8 + 16);
+                                const float gs = ckpt_scale(max(max(a.x, a.z), max(b.x, b.z)));
+                                const float us = ckpt_scale(max(max(a.y, a.w), max(b.y, b.w)));
+                                const float grs = ckpt_recip(gs), urs = ckpt_recip(us);
+                                if (wn == 0 && (ln & 15) == 0 && trow < nvalid) {
+                                    p.gate_s[(size_t)(row0 + trow) * nb + tc.nt] = gs;
+                                    p.up_s[(size_t)(row0 + trow) * nb + tc.nt] = us;
+                                }
+                                char* at = region + (ii * 16 + (ln >> 4) * 4 + e) * 2 * CPITCH + (ln & 15);
+#pragma unroll
+                                for (int f = 0; f < 2; ++f) {
+                                    at[f * 16] = gs == gs ? (char)ckpt_code(acc[i][f][e], grs) : (char)0;
+                                    at[CPITCH + f * 16] = us == us ? (char)ckpt_code(acc[i][f + 2][e], urs) : (char)0;
+                                }
+                                __builtin_amdgcn_sched_barrier(0);
+                            }
+                        }
+                    }
+                    // out in 8-byte pieces: 4 of a row's 32 bytes of g, then 4 of u
+#pragma unroll
+                    for (int q = 0; q < CPF * 16 * 8 / 64; ++q) {
+                        const int piece = q * 64 + ln, lrow = piece / 8, half = (piece / 4) & 1, ch = piece & 3;
+                        const int i = p0 + lrow / 16;
+                        const int trow = (wm + WMW * i) * 16 + lrow % 16;
+                        const int col = colbase + ch * 8;
+                        if (i < NF && trow < nvalid && col < N) {
+                            const uint2 v = *reinterpret_cast<const uint2*>(region + lrow * 2 * CPITCH + half * CPITCH + ch * 8);
+                            *reinterpret_cast<uint2*>((half ? p.up_q : p.gate_q) + (size_t)(row0 + trow) * N + col) = v;
+                        }
                     }
                 }
             }

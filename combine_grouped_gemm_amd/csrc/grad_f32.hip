@@ -261,10 +261,6 @@ hipError_t launch_ffn_ckpt_f32(const FfnArgs& a, hipStream_t stream) {
     static int per_cu = 0;
     return launch_persistent(gate_up_ckpt_kernel<float>, kThreads, a, stream, &per_cu);
 }
-hipError_t launch_ffn_ckpt_bf16(const FfnArgs& a, hipStream_t stream) {
-    static int per_cu = 0;
-    return launch_persistent(gate_up_ckpt_kernel<uint16_t>, kThreads, a, stream, &per_cu);
-}
 hipError_t launch_dgrad_f32(const FfnArgs& a, hipStream_t stream) {
     static int per_cu = 0;
     return launch_persistent(dgrad_kernel<float>, kThreads, a, stream, &per_cu);
