@@ -789,8 +789,29 @@ def _train_type(t, name):
         raise ValueError(f"{name} must be float32 or bfloat16 (got {t.dtype})")
 
 
-def _offsets(offsets, E_loc):
-    """Local experts of the contiguous layout's offsets (all rows: 0)."""
+def _is(t, name, dtype, shape, first, index):
+    """t is a device tensor of this type and shape on the device (index) of the call's first
+    tensor (a name).  One expression for what holds as a rule: the single checks and
+    their messages cost a call of ten small tensors as much as its launch."""
+    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.get_device() == index
+            and t.is_contiguous()):
+        return
+    _dev(t, name, dtype, len(shape))
+    _need(t, name, shape=shape)
+    if t.get_device() != index:
+        raise ValueError(f"all tensors must be on {first}'s device cuda:{index} (got {t.device})")
+
+
+def _out(t, name, dtype, shape, like, first, index, stream):
+    """The caller's tensor after its checks, or a new one."""
+    if t is None:
+        return _new(shape, dtype, like.device, stream)
+    _is(t, name, dtype, shape, first, index)
+    return t
+
+
+def _offsets(offsets, E_loc, first, index):
+    """Local experts of the contiguous layout's offsets (None, all rows: 0)."""
     if offsets is None:
         if E_loc is not None:
             raise ValueError("E_loc needs the layout's offsets")
@@ -800,16 +821,9 @@ def _offsets(offsets, E_loc):
     if E_loc < 1:
         raise ValueError(f"E_loc must be positive (got {E_loc})")
     _need(offsets, "offsets", numel=E_loc + 1)
+    if offsets.get_device() != index:
+        raise ValueError(f"all tensors must be on {first}'s device cuda:{index} (got {offsets.device})")
     return E_loc
-
-
-def _output(t, name, shape, dtype, like, stream):
-    """The caller's tensor after its checks, or a new one."""
-    if t is None:
-        return _new(shape, dtype, like.device, stream)
-    _dev(t, name, dtype)
-    _need(t, name, shape=shape)
-    return t
 
 
 def moe_checkpoint_rows(x, offsets=None, q=None, scales=None, stream=None, E_loc=None):
@@ -821,12 +835,12 @@ def moe_checkpoint_rows(x, offsets=None, q=None, scales=None, stream=None, E_loc
     _dev(x, "x", None, 2)
     _train_type(x, "x")
     cap, cols = x.shape
-    E_loc = _offsets(offsets, E_loc)
-    q = _output(q, "q", (cap, cols), torch.int8, x, stream)
-    scales = _output(scales, "scales", (cap, _blocks(cols)), torch.float32, x, stream)
-    _same_device(x, "x", offsets, q, scales)
-    _call(lib().moe_checkpoint_rows, x, stream, _ptr(x), _DT[x.dtype], _ptr(offsets), E_loc, cap, cols, _ptr(q),
-          _ptr(scales))
+    index = x.get_device()
+    E_loc = _offsets(offsets, E_loc, "x", index)
+    q = _out(q, "q", torch.int8, (cap, cols), x, "x", index, stream)
+    scales = _out(scales, "scales", torch.float32, (cap, _blocks(cols)), x, "x", index, stream)
+    _call(lib().moe_checkpoint_rows, x, stream, x.data_ptr(), _DT[x.dtype], _ptr(offsets), E_loc, cap, cols, q.data_ptr(),
+          scales.data_ptr())
     return q, scales
 
 
@@ -835,14 +849,13 @@ def moe_checkpoint_values(q, scales, offsets=None, out=None, out_dtype=torch.bfl
     offsets and E_loc as in moe_checkpoint_rows."""
     _dev(q, "q", torch.int8, 2)
     cap, cols = q.shape
-    _dev(scales, "scales", torch.float32)
-    _need(scales, "scales", shape=(cap, _blocks(cols)))
-    E_loc = _offsets(offsets, E_loc)
-    out = _output(out, "out", (cap, cols), out_dtype if out is None else out.dtype, q, stream)
+    index = q.get_device()
+    _is(scales, "scales", torch.float32, (cap, _blocks(cols)), "q", index)
+    E_loc = _offsets(offsets, E_loc, "q", index)
+    out = _out(out, "out", out_dtype if out is None else out.dtype, (cap, cols), q, "q", index, stream)
     _train_type(out, "out")
-    _same_device(q, "q", scales, offsets, out)
-    _call(lib().moe_checkpoint_values, q, stream, _ptr(q), _ptr(scales), _ptr(offsets), E_loc, cap, cols, _ptr(out),
-          _DT[out.dtype])
+    _call(lib().moe_checkpoint_values, q, stream, q.data_ptr(), scales.data_ptr(), _ptr(offsets), E_loc, cap, cols,
+          out.data_ptr(), _DT[out.dtype])
     return out
 
 
@@ -852,20 +865,19 @@ def moe_ffn_gate_up_train(xd, offsets, w_gate, w_up, h=None, gate_q=None, gate_s
     8-bit checkpoints -> h (cap_rows, I), (gate_q, gate_scales), (up_q, up_scales)."""
     _dev(xd, "xd", ndim=2)
     _train_type(xd, "xd")
-    _dev(w_gate, "w_gate", xd.dtype, 3)
-    _dev(w_up, "w_up", xd.dtype, 3)
-    E_loc, I, H, cap = w_gate.shape[0], w_gate.shape[1], xd.shape[1], xd.shape[0]
-    act = _DT[xd.dtype]
+    index, dt = xd.get_device(), xd.dtype
+    _dev(w_gate, "w_gate", dt, 3)
+    (E_loc, I, _), (cap, H) = w_gate.shape, xd.shape
+    _is(w_gate, "w_gate", dt, w_gate.shape, "xd", index)
+    _is(w_up, "w_up", dt, w_gate.shape, "xd", index)
+    act = _DT[dt]
     packed = _pack_flag(_w_packed(w_gate, H, act, "w_gate"))
-    _need(w_up, "w_up", shape=tuple(w_gate.shape))
-    _dev(offsets, "offsets", torch.int32, 1)
-    _need(offsets, "offsets", numel=E_loc + 1)
-    h = _output(h, "h", (cap, I), xd.dtype, xd, stream)
-    gate_q = _output(gate_q, "gate_q", (cap, I), torch.int8, xd, stream)
-    up_q = _output(up_q, "up_q", (cap, I), torch.int8, xd, stream)
-    gate_scales = _output(gate_scales, "gate_scales", (cap, _blocks(I)), torch.float32, xd, stream)
-    up_scales = _output(up_scales, "up_scales", (cap, _blocks(I)), torch.float32, xd, stream)
-    _same_device(xd, "xd", offsets, w_gate, w_up, h, gate_q, gate_scales, up_q, up_scales)
+    _offsets(offsets, E_loc, "xd", index)
+    h = _out(h, "h", dt, (cap, I), xd, "xd", index, stream)
+    gate_q = _out(gate_q, "gate_q", torch.int8, (cap, I), xd, "xd", index, stream)
+    up_q = _out(up_q, "up_q", torch.int8, (cap, I), xd, "xd", index, stream)
+    gate_scales = _out(gate_scales, "gate_scales", torch.float32, (cap, _blocks(I)), xd, "xd", index, stream)
+    up_scales = _out(up_scales, "up_scales", torch.float32, (cap, _blocks(I)), xd, "xd", index, stream)
     _call(lib().moe_ffn_gate_up_train, xd, stream, _ptr(xd), _ptr(offsets), E_loc, cap, H, I, act, _ptr(w_gate),
           _ptr(w_up), act | packed, _ptr(h), _ptr(gate_q), _ptr(gate_scales), _ptr(up_q), _ptr(up_scales),
           int(expected_rows))
@@ -879,24 +891,24 @@ def moe_swiglu_backward(dh, gate_q, gate_scales, up_q, up_scales, row_of, topk_w
     (B, K).  Rows that no slot of row_of names are left as they were."""
     _dev(dh, "dh", ndim=2)
     _train_type(dh, "dh")
-    cap, I = dh.shape
-    for name, t in (("gate_q", gate_q), ("up_q", up_q)):
-        _dev(t, name, torch.int8)
-        _need(t, name, shape=(cap, I))
-    for name, t in (("gate_scales", gate_scales), ("up_scales", up_scales)):
-        _dev(t, name, torch.float32)
-        _need(t, name, shape=(cap, _blocks(I)))
+    index, dt, rows = dh.get_device(), dh.dtype, dh.shape
+    cap, I = rows
+    blocks = (cap, _blocks(I))
+    _is(gate_q, "gate_q", torch.int8, rows, "dh", index)
+    _is(up_q, "up_q", torch.int8, rows, "dh", index)
+    _is(gate_scales, "gate_scales", torch.float32, blocks, "dh", index)
+    _is(up_scales, "up_scales", torch.float32, blocks, "dh", index)
     _dev(row_of, "row_of", torch.int32, 2)
-    B, K = row_of.shape
-    _dev(topk_w, "topk_w", torch.float32)
-    _need(topk_w, "topk_w", shape=(B, K))
-    dgate = _output(dgate, "dgate", (cap, I), dh.dtype, dh, stream)
-    dup = _output(dup, "dup", (cap, I), dh.dtype, dh, stream)
-    hw = _output(hw, "hw", (cap, I), dh.dtype, dh, stream)
-    dtopk_w = _output(dtopk_w, "dtopk_w", (B, K), torch.float32, dh, stream)
-    _same_device(dh, "dh", gate_q, gate_scales, up_q, up_scales, row_of, topk_w, dgate, dup, hw, dtopk_w)
-    _call(lib().moe_swiglu_backward, dh, stream, _ptr(dh), _DT[dh.dtype], _ptr(gate_q), _ptr(gate_scales), _ptr(up_q),
-          _ptr(up_scales), cap, I, _ptr(row_of), _ptr(topk_w), B, K, _ptr(dgate), _ptr(dup), _ptr(hw), _ptr(dtopk_w))
+    slots = row_of.shape
+    _is(row_of, "row_of", torch.int32, slots, "dh", index)
+    _is(topk_w, "topk_w", torch.float32, slots, "dh", index)
+    dgate = _out(dgate, "dgate", dt, rows, dh, "dh", index, stream)
+    dup = _out(dup, "dup", dt, rows, dh, "dh", index, stream)
+    hw = _out(hw, "hw", dt, rows, dh, "dh", index, stream)
+    dtopk_w = _out(dtopk_w, "dtopk_w", torch.float32, slots, dh, "dh", index, stream)
+    _call(lib().moe_swiglu_backward, dh, stream, dh.data_ptr(), _DT[dt], gate_q.data_ptr(), gate_scales.data_ptr(),
+          up_q.data_ptr(), up_scales.data_ptr(), cap, I, row_of.data_ptr(), topk_w.data_ptr(), slots[0], slots[1],
+          dgate.data_ptr(), dup.data_ptr(), hw.data_ptr(), dtopk_w.data_ptr())
     return dgate, dup, hw, dtopk_w
 
 
@@ -908,22 +920,21 @@ def moe_ffn_dgrad(dy, offsets, w, dy2=None, w2=None, src_of=None, slots_per_toke
     slots_per_token (a token's gradient); None: row r itself."""
     _dev(dy, "dy", ndim=2)
     _train_type(dy, "dy")
-    _dev(w, "w", dy.dtype, 3)
+    index, dt = dy.get_device(), dy.dtype
+    _dev(w, "w", dt, 3)
+    _is(w, "w", dt, w.shape, "dy", index)
     E_loc, out_dim = w.shape[0], w.shape[1]
     if dy.shape[1] != out_dim:
         raise ValueError(f"dy must have {out_dim} columns (got {dy.shape[1]})")
-    _dev(offsets, "offsets", torch.int32, 1)
-    _need(offsets, "offsets", numel=E_loc + 1)
+    _offsets(offsets, E_loc, "dy", index)
     if (dy2 is None) != (w2 is None):
         raise ValueError("dy2 and w2 come together")
     if dy2 is not None:
-        _dev(dy2, "dy2", dy.dtype)
-        _need(dy2, "dy2", shape=tuple(dy.shape))
-        _dev(w2, "w2", dy.dtype)
-        _need(w2, "w2", shape=tuple(w.shape))
+        _is(dy2, "dy2", dt, dy.shape, "dy", index)
+        _is(w2, "w2", dt, w.shape, "dy", index)
     if in_dim is None:
         in_dim = w.shape[2] if dx is None else dx.shape[-1]
-    act = _DT[dy.dtype]
+    act = _DT[dt]
     packed = _pack_flag(_w_packed(w, in_dim, act, "w"))
     if src_of is None:
         cap = dy.shape[0]
@@ -931,8 +942,8 @@ def moe_ffn_dgrad(dy, offsets, w, dy2=None, w2=None, src_of=None, slots_per_toke
         _dev(src_of, "src_of", torch.int32, 1)
         cap = src_of.numel() if dx is None else dx.shape[0]
         _need(src_of, "src_of", numel=cap)
-    dx = _output(dx, "dx", (cap, in_dim), dy.dtype, dy, stream)
-    _same_device(dy, "dy", offsets, w, dy2, w2, src_of, dx)
+        _is(src_of, "src_of", torch.int32, src_of.shape, "dy", index)
+    dx = _out(dx, "dx", dt, (cap, in_dim), dy, "dy", index, stream)
     _call(lib().moe_ffn_dgrad, dy, stream, _ptr(dy), _ptr(dy2), _ptr(src_of), int(slots_per_token), dy.shape[0],
           _ptr(offsets), E_loc, cap, out_dim, in_dim, act, _ptr(w), _ptr(w2), act | packed, _ptr(dx),
           int(expected_rows))
@@ -951,24 +962,26 @@ def moe_ffn_wgrad(dy, x, offsets, x_scales=None, dy2=None, src_of=None, slots_pe
     slots_per_token.  base may be dw itself (accumulation over micro-batches)."""
     _dev(dy, "dy", ndim=2)
     _train_type(dy, "dy")
+    index, dt = dy.get_device(), dy.dtype
     _dev(x, "x", ndim=2)
+    _is(x, "x", x.dtype, x.shape, "dy", index)
     out_dim, in_dim = dy.shape[1], x.shape[1]
-    if x.dtype not in (dy.dtype, torch.int8):
-        raise ValueError(f"x must be {dy.dtype} or a checkpoint's int8 (got {x.dtype})")
+    if x.dtype not in (dt, torch.int8):
+        raise ValueError(f"x must be {dt} or a checkpoint's int8 (got {x.dtype})")
     if (x.dtype == torch.int8) != (x_scales is not None):
         raise ValueError("x_scales belong to a checkpoint's int8 x")
     if x_scales is not None:
-        _dev(x_scales, "x_scales", torch.float32)
-        _need(x_scales, "x_scales", shape=(x.shape[0], _blocks(in_dim)))
+        _is(x_scales, "x_scales", torch.float32, (x.shape[0], _blocks(in_dim)), "dy", index)
     if dy2 is not None:
-        _dev(dy2, "dy2", dy.dtype)
-        _need(dy2, "dy2", shape=tuple(dy.shape))
+        _is(dy2, "dy2", dt, dy.shape, "dy", index)
     elif dw2 is not None or base2 is not None:
         raise ValueError("dw2 and base2 belong to dy2")
     if gather not in _GATHER:
         raise ValueError(f"gather must be None, 'x' or 'dy' (got {gather!r})")
-    _dev(offsets, "offsets", torch.int32, 1)
-    E_loc = _offsets(offsets, (dw.shape[0] if dw is not None and dw.dim() == 3 else None) if E_loc is None else E_loc)
+    if offsets is None:
+        raise ValueError("offsets must be a torch.Tensor")
+    E_loc = _offsets(offsets, (dw.shape[0] if dw is not None and dw.dim() == 3 else None) if E_loc is None else E_loc,
+                     "dy", index)
     cap, src_rows = (x.shape[0], dy.shape[0]) if gather == "dy" else (dy.shape[0], x.shape[0])
     if gather is None:
         if src_rows != cap:
@@ -978,19 +991,17 @@ def moe_ffn_wgrad(dy, x, offsets, x_scales=None, dy2=None, src_of=None, slots_pe
             raise ValueError("a gathered operand needs src_of")
         _dev(src_of, "src_of", torch.int32, 1)
         _need(src_of, "src_of", numel=cap)
+        _is(src_of, "src_of", torch.int32, src_of.shape, "dy", index)
     shape = (E_loc, out_dim, in_dim)
-    dt = dw_dtype if dw is None else dw.dtype
-    dw = _output(dw, "dw", shape, dt, dy, stream)
+    dw = _out(dw, "dw", dw_dtype if dw is None else dw.dtype, shape, dy, "dy", index, stream)
     if dy2 is not None:
-        dw2 = _output(dw2, "dw2", shape, dt, dy, stream)
+        dw2 = _out(dw2, "dw2", dw.dtype, shape, dy, "dy", index, stream)
     for name, t in (("base", base), ("base2", base2)):
         if t is not None:
-            _dev(t, name, dt)
-            _need(t, name, shape=shape)
-    _same_device(dy, "dy", x, offsets, x_scales, dy2, src_of if gather else None, base, base2, dw, dw2)
+            _is(t, name, dw.dtype, shape, "dy", index)
     _call(lib().moe_ffn_wgrad, dy, stream, _ptr(dy), _ptr(dy2), _ptr(x),
           MOE_CKPT8 if x.dtype == torch.int8 else _DT[x.dtype], _ptr(x_scales), _ptr(src_of) if gather else None,
-          int(slots_per_token), src_rows, _GATHER[gather], _ptr(offsets), E_loc, cap, out_dim, in_dim, _DT[dy.dtype],
+          int(slots_per_token), src_rows, _GATHER[gather], _ptr(offsets), E_loc, cap, out_dim, in_dim, _DT[dt],
           _ptr(base), _ptr(base2), _ptr(dw), _ptr(dw2), _DT.get(dw.dtype, -1), int(expected_rows))
     return dw if dy2 is None else (dw, dw2)
 
@@ -1009,19 +1020,17 @@ def moe_route_backward(logits, topk_ids, dtopk_w, score: str = "picks", renorm: 
     if score not in _BACK_SCORES:
         raise ValueError(f"score must be one of {sorted(_BACK_SCORES)} (got {score!r})")
     B, E = logits.shape
+    index = logits.get_device()
     _dev(topk_ids, "topk_ids", torch.int32, 2)
     Kt = topk_ids.shape[1]
-    _need(topk_ids, "topk_ids", shape=(B, Kt))
-    _dev(dtopk_w, "dtopk_w", torch.float32)
-    _need(dtopk_w, "dtopk_w", shape=(B, Kt))
+    _is(topk_ids, "topk_ids", torch.int32, (B, Kt), "logits", index)
+    _is(dtopk_w, "dtopk_w", torch.float32, (B, Kt), "logits", index)
     if phys_of_logical is not None:
-        _dev(phys_of_logical, "phys_of_logical", torch.int32, 1)
-        _need(phys_of_logical, "phys_of_logical", shape=(E,))
-    dlogits = _output(dlogits, "dlogits", (B, E), torch.float32, logits, stream)
-    _same_device(logits, "logits", topk_ids, dtopk_w, phys_of_logical, dlogits)
-    _call(lib().moe_route_backward, logits, stream, _ptr(logits), _DT[logits.dtype], _ptr(topk_ids), _ptr(dtopk_w), B, E,
-          Kt - int(n_shared), _BACK_SCORES[score], 1 if renorm else 0, scale, _ptr(phys_of_logical), int(n_shared),
-          _ptr(dlogits))
+        _is(phys_of_logical, "phys_of_logical", torch.int32, (E,), "logits", index)
+    dlogits = _out(dlogits, "dlogits", torch.float32, (B, E), logits, "logits", index, stream)
+    _call(lib().moe_route_backward, logits, stream, logits.data_ptr(), _DT[logits.dtype], topk_ids.data_ptr(),
+          dtopk_w.data_ptr(), B, E, Kt - n_shared, _BACK_SCORES[score], 1 if renorm else 0, scale,
+          _ptr(phys_of_logical), n_shared, dlogits.data_ptr())
     return dlogits
 
 

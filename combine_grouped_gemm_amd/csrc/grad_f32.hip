@@ -1,9 +1,16 @@
 // The training step's grouped products in fp32 (the toy EP layer): gate/up with
 // 8-bit checkpoints, input gradients, weight gradients.
 //
-// Sizes are small, so these are FMA kernels with LDS tiles on a persistent grid.
-// Every sum runs in ascending order of its contraction index, so a result does
-// not depend on the tile it falls into.
+// Sizes are small, so one tile shape each: 64 x 64 of a gradient, 32 rows x 128 columns
+// of both gate and up (a checkpoint block), four waves, 32-deep contraction chunks that go
+// through registers into LDS while the chunk before is multiplied.  The products are
+// v_mfma_f32_16x16x4_f32: fp32 operands, fp32 sums; lane l feeds row (column) l % 16 with
+// k = l / 16 and receives rows 4 (l / 16) + e, column l % 16.
+//
+// Operands lie in LDS as they do in memory.  Contraction along the row ([r][k], pitch 36):
+// the 16 rows x 4 k of an operand read fall into 64 different banks (36 r mod 64 takes
+// every multiple of 4).  Contraction over rows ([k][c], pitch 80): 4 rows of 16 columns,
+// 16 banks apart.
 #include "ckpt_common.hpp"
 #include "grouped_tiles.hpp"
 
@@ -11,129 +18,14 @@ namespace moeep {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kK = 16;                       // contraction steps of a chunk
-
-template <typename T>
-__device__ __forceinline__ float value(const T* p, size_t i) {
-    if constexpr (sizeof(T) == 2) return __uint_as_float((uint32_t)p[i] << 16);
-    else return p[i];
-}
-template <typename T>
-__device__ __forceinline__ void put(void* p, size_t i, float v) {
-    if constexpr (sizeof(T) == 2) static_cast<uint16_t*>(p)[i] = (uint16_t)f32_to_bf16_bits(v);
-    else static_cast<float*>(p)[i] = v;
-}
-
-// ---- gate/up with checkpoints: 32 rows x 128 columns (one checkpoint block) of
-// both products.  Thread (tx, ty) owns rows ty + 8 i and columns tx + 32 j, so the
-// amax of a row's block is over 32 consecutive lanes.
-constexpr int kRows = 32, kCols = 128;
-
-template <typename T>
-__global__ __launch_bounds__(kThreads) void gate_up_ckpt_kernel(FfnArgs p) {
-    __shared__ float sA[kRows][kK + 1], sG[kCols][kK + 1], sU[kCols][kK + 1];
-    __shared__ int s_pre[kMaxExperts + 1];
-    __shared__ int s_tmp[kThreads / kWave];
-    const int tid = threadIdx.x, tx = tid % 32, ty = tid / 32;
-    const int Kdim = p.Kdim, N = p.N, ldw = p.ldw, nb = (N + kCkptBlock - 1) / kCkptBlock;
-    build_tile_prefix<kThreads, kRows>(p, s_pre, s_tmp);
-    const int n_tiles = (N + kCols - 1) / kCols, total = n_tiles * s_pre[p.E_loc];
-    const T* A = static_cast<const T*>(p.a);
-    for (int tau = blockIdx.x; tau < total; tau += gridDim.x) {
-        const TileCoord tc = decode_tile<kRows>(tau, n_tiles, s_pre, p);
-        const int col0 = tc.nt * kCols;
-        const T* wg = static_cast<const T*>(p.w0) + (size_t)tc.j * N * ldw;
-        const T* wu = static_cast<const T*>(p.w1) + (size_t)tc.j * N * ldw;
-        float g[4][4] = {}, u[4][4] = {};
-        for (int k0 = 0; k0 < Kdim; k0 += kK) {
-            __syncthreads();
-            for (int i = tid; i < kRows * kK; i += kThreads) {
-                const int r = i / kK, k = i % kK;
-                sA[r][k] = r < tc.nvalid && k0 + k < Kdim ? value(A, (size_t)(tc.row0 + r) * Kdim + k0 + k) : 0.0f;
-            }
-            for (int i = tid; i < kCols * kK; i += kThreads) {
-                const int c = i / kK, k = i % kK;
-                const bool in = col0 + c < N && k0 + k < Kdim;
-                const size_t at = (size_t)(col0 + c) * ldw + k0 + k;
-                sG[c][k] = in ? value(wg, at) : 0.0f;
-                sU[c][k] = in ? value(wu, at) : 0.0f;
-            }
-            __syncthreads();
-#pragma unroll
-            for (int k = 0; k < kK; ++k) {
-                float a[4], wgv[4], wuv[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) a[i] = sA[ty + 8 * i][k];
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    wgv[j] = sG[tx + 32 * j][k];
-                    wuv[j] = sU[tx + 32 * j][k];
-                }
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        g[i][j] = fmaf(a[i], wgv[j], g[i][j]);
-                        u[i][j] = fmaf(a[i], wuv[j], u[i][j]);
-                    }
-            }
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int r = ty + 8 * i;
-            uint32_t mg = 0, mu = 0;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {       // columns past N hold zeros
-                mg = max(mg, __float_as_uint(g[i][j]) & 0x7fffffffu);
-                mu = max(mu, __float_as_uint(u[i][j]) & 0x7fffffffu);
-            }
-#pragma unroll
-            for (int d = 16; d > 0; d >>= 1) {
-                mg = max(mg, (uint32_t)__shfl_xor((int)mg, d, kWave));
-                mu = max(mu, (uint32_t)__shfl_xor((int)mu, d, kWave));
-            }
-            if (r >= tc.nvalid) continue;
-            const float gs = ckpt_scale(mg), us = ckpt_scale(mu), grs = ckpt_recip(gs), urs = ckpt_recip(us);
-            const size_t row = (size_t)(tc.row0 + r);
-            if (tx == 0) {
-                p.gate_s[row * nb + tc.nt] = gs;
-                p.up_s[row * nb + tc.nt] = us;
-            }
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int c = col0 + tx + 32 * j;
-                if (c >= N) continue;
-                p.gate_q[row * N + c] = gs == gs ? (int8_t)ckpt_code(g[i][j], grs) : (int8_t)0;
-                p.up_q[row * N + c] = us == us ? (int8_t)ckpt_code(u[i][j], urs) : (int8_t)0;
-                put<T>(p.out, row * N + c, g[i][j] / (1.0f + expf(-g[i][j])) * u[i][j]);
-            }
-        }
-    }
-}
-
-// ---- 64 x 64 tiles of the gradients: thread (tx, ty) owns rows ty + 16 i and
-// columns tx + 16 j
+constexpr int kK = 32;                       // contraction steps of a chunk
+constexpr int kPitchK = 36;                  // floats, [r][k]
+constexpr int kPitchC = 80;                  // floats, [k][64 columns]
 constexpr int kTile = 64;
 
-struct Tile {
-    float a[kK][kTile + 1], b[kK][kTile + 1];
-
-    __device__ __forceinline__ void multiply(float (&acc)[4][4], int tx, int ty) const {
-#pragma unroll
-        for (int k = 0; k < kK; ++k) {
-            float av[4], bv[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                av[i] = a[k][ty + 16 * i];
-                bv[i] = b[k][tx + 16 * i];
-            }
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(av[i], bv[j], acc[i][j]);
-        }
-    }
-};
+__device__ __forceinline__ floatx4 mma(float a, float b, floatx4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x4f32(a, b, c, 0, 0, 0);
+}
 
 // the operand row that the expert row r reads, -1 if src_of names none of src_rows
 __device__ __forceinline__ int gathered(const int32_t* src_of, int per, int src_rows, int r) {
@@ -143,128 +35,277 @@ __device__ __forceinline__ int gathered(const int32_t* src_of, int per, int src_
     return t < src_rows ? t : -1;
 }
 
-template <typename T>
+__device__ __forceinline__ float4 zero4() { return make_float4(0.0f, 0.0f, 0.0f, 0.0f); }
+
+// ---- gate/up with checkpoints: wave w has columns 32 w .. + 31 of both products
+constexpr int kRows = 32, kCols = 128;
+
+__global__ __launch_bounds__(kThreads) void gate_up_ckpt_kernel(FfnArgs p) {
+    __shared__ __align__(16) float sA[kRows * kPitchK], sG[kCols * kPitchK], sU[kCols * kPitchK];
+    __shared__ uint2 s_max[kRows][4];
+    __shared__ int s_pre[kMaxExperts + 1];
+    __shared__ int s_tmp[kThreads / kWave];
+    const int tid = threadIdx.x, lane = tid % kWave, wave = tid / kWave, r16 = lane & 15, g4 = lane >> 4;
+    const int Kdim = p.Kdim, N = p.N, ldw = p.ldw, nb = (N + kCkptBlock - 1) / kCkptBlock;
+    build_tile_prefix<kThreads, kRows>(p, s_pre, s_tmp);
+    const int n_tiles = (N + kCols - 1) / kCols, total = n_tiles * s_pre[p.E_loc];
+    const float* A = static_cast<const float*>(p.a);
+    float* Out = static_cast<float*>(p.out);
+    const int lr = tid / 8, lk = (tid % 8) * 4;              // row and first k of a thread's pieces
+    for (int tau = blockIdx.x; tau < total; tau += gridDim.x) {
+        const TileCoord tc = decode_tile<kRows>(tau, n_tiles, s_pre, p);
+        const int col0 = tc.nt * kCols;
+        const float* wg = static_cast<const float*>(p.w0) + (size_t)tc.j * N * ldw;
+        const float* wu = static_cast<const float*>(p.w1) + (size_t)tc.j * N * ldw;
+        float4 ra, rg[4], ru[4];
+        auto load = [&](int k0) {
+            const int k = k0 + lk;
+            ra = lr < tc.nvalid && k < Kdim ? *reinterpret_cast<const float4*>(A + (size_t)(tc.row0 + lr) * Kdim + k) : zero4();
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int c = col0 + i * 32 + lr;
+                const bool in = c < N && k < Kdim;
+                rg[i] = in ? *reinterpret_cast<const float4*>(wg + (size_t)c * ldw + k) : zero4();
+                ru[i] = in ? *reinterpret_cast<const float4*>(wu + (size_t)c * ldw + k) : zero4();
+            }
+        };
+        floatx4 g[2][2] = {}, u[2][2] = {};
+        load(0);
+        for (int k0 = 0; k0 < Kdim; k0 += kK) {
+            __syncthreads();
+            *reinterpret_cast<float4*>(sA + lr * kPitchK + lk) = ra;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                *reinterpret_cast<float4*>(sG + (i * 32 + lr) * kPitchK + lk) = rg[i];
+                *reinterpret_cast<float4*>(sU + (i * 32 + lr) * kPitchK + lk) = ru[i];
+            }
+            __syncthreads();
+            if (k0 + kK < Kdim) load(k0 + kK);
+#pragma unroll
+            for (int k = 0; k < kK; k += 4) {
+                float a[2], b[2], c[2];
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    a[i] = sA[(i * 16 + r16) * kPitchK + k + g4];
+                    b[i] = sG[(wave * 32 + i * 16 + r16) * kPitchK + k + g4];
+                    c[i] = sU[(wave * 32 + i * 16 + r16) * kPitchK + k + g4];
+                }
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        g[i][j] = mma(a[i], b[j], g[i][j]);
+                        u[i][j] = mma(a[i], c[j], u[i][j]);
+                    }
+            }
+        }
+        // each row's largest magnitudes over the block's 128 columns (those past N hold zeros)
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const uint32_t mg = row16_max_u32(max(__float_as_uint(g[i][0][e]) & 0x7fffffffu,
+                                                      __float_as_uint(g[i][1][e]) & 0x7fffffffu));
+                const uint32_t mu = row16_max_u32(max(__float_as_uint(u[i][0][e]) & 0x7fffffffu,
+                                                      __float_as_uint(u[i][1][e]) & 0x7fffffffu));
+                if (r16 == 0) s_max[i * 16 + g4 * 4 + e][wave] = make_uint2(mg, mu);
+            }
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int r = i * 16 + g4 * 4 + e;
+                if (r >= tc.nvalid) continue;
+                uint2 m = s_max[r][0];
+#pragma unroll
+                for (int w = 1; w < 4; ++w) m = make_uint2(max(m.x, s_max[r][w].x), max(m.y, s_max[r][w].y));
+                const float gs = ckpt_scale(m.x), us = ckpt_scale(m.y), grs = ckpt_recip(gs), urs = ckpt_recip(us);
+                const size_t row = (size_t)(tc.row0 + r);
+                if (wave == 0 && r16 == 0) {
+                    p.gate_s[row * nb + tc.nt] = gs;
+                    p.up_s[row * nb + tc.nt] = us;
+                }
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const int c = col0 + wave * 32 + j * 16 + r16;
+                    if (c >= N) continue;
+                    const float gv = g[i][j][e], uv = u[i][j][e];
+                    p.gate_q[row * N + c] = gs == gs ? (int8_t)ckpt_code(gv, grs) : (int8_t)0;
+                    p.up_q[row * N + c] = us == us ? (int8_t)ckpt_code(uv, urs) : (int8_t)0;
+                    Out[row * N + c] = gv / (1.0f + expf(-gv)) * uv;
+                }
+            }
+    }
+}
+
+// ---- gradients: wave (wr, wc) of 2 x 2 has a 32 x 32 quarter
 __global__ __launch_bounds__(kThreads) void dgrad_kernel(FfnArgs p) {
-    __shared__ Tile s;
+    __shared__ __align__(16) float sA[kTile * kPitchK], sB[kK * kPitchC];
     __shared__ int s_row[kTile];
     __shared__ int s_pre[kMaxExperts + 1];
     __shared__ int s_tmp[kThreads / kWave];
-    const int tid = threadIdx.x, tx = tid % 16, ty = tid / 16;
+    const int tid = threadIdx.x, lane = tid % kWave, wave = tid / kWave, r16 = lane & 15, g4 = lane >> 4;
+    const int wr = wave / 2 * 32, wc = wave % 2 * 32;
     const int Kdim = p.Kdim, N = p.N, ldw = p.ldw;
     build_tile_prefix<kThreads, kTile>(p, s_pre, s_tmp);
     const int n_tiles = (N + kTile - 1) / kTile, total = n_tiles * s_pre[p.E_loc];
+    float* Out = static_cast<float*>(p.out);
     for (int tau = blockIdx.x; tau < total; tau += gridDim.x) {
         const TileCoord tc = decode_tile<kTile>(tau, n_tiles, s_pre, p);
         const int col0 = tc.nt * kTile;
         __syncthreads();
         if (tid < kTile) s_row[tid] = tid < tc.nvalid ? gathered(p.src_of, p.per, p.src_rows, tc.row0 + tid) : -1;
-        float acc[4][4] = {};
+        __syncthreads();
+        floatx4 acc[2][2] = {};
         for (int q = 0; q < 2; ++q) {
-            const T* A = static_cast<const T*>(q == 0 ? p.a : p.a2);
+            const float* A = static_cast<const float*>(q == 0 ? p.a : p.a2);
             if (A == nullptr) break;
-            const T* W = static_cast<const T*>(q == 0 ? p.w0 : p.w1) + (size_t)tc.j * Kdim * ldw;
+            const float* W = static_cast<const float*>(q == 0 ? p.w0 : p.w1) + (size_t)tc.j * Kdim * ldw;
+            float4 ra[2], rb[2];
+            auto load = [&](int k0) {
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int row = s_row[i * 32 + tid / 8], k = k0 + (tid % 8) * 4;
+                    ra[i] = row >= 0 && k < Kdim ? *reinterpret_cast<const float4*>(A + (size_t)row * Kdim + k) : zero4();
+                    const int kb = k0 + i * 16 + tid / 16, c = col0 + (tid % 16) * 4;
+                    rb[i] = kb < Kdim && c < N ? *reinterpret_cast<const float4*>(W + (size_t)kb * ldw + c) : zero4();
+                }
+            };
+            load(0);
             for (int k0 = 0; k0 < Kdim; k0 += kK) {
                 __syncthreads();
-                for (int i = tid; i < kTile * kK; i += kThreads) {
-                    const int r = i / kK, k = i % kK, row = s_row[r];
-                    s.a[k][r] = row >= 0 && k0 + k < Kdim ? value(A, (size_t)row * Kdim + k0 + k) : 0.0f;
-                }
-                for (int i = tid; i < kTile * kK; i += kThreads) {
-                    const int k = i / kTile, c = i % kTile;
-                    s.b[k][c] = k0 + k < Kdim && col0 + c < N ? value(W, (size_t)(k0 + k) * ldw + col0 + c) : 0.0f;
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    *reinterpret_cast<float4*>(sA + (i * 32 + tid / 8) * kPitchK + (tid % 8) * 4) = ra[i];
+                    *reinterpret_cast<float4*>(sB + (i * 16 + tid / 16) * kPitchC + (tid % 16) * 4) = rb[i];
                 }
                 __syncthreads();
-                s.multiply(acc, tx, ty);
+                if (k0 + kK < Kdim) load(k0 + kK);
+#pragma unroll
+                for (int k = 0; k < kK; k += 4) {
+                    float a[2], b[2];
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        a[i] = sA[(wr + i * 16 + r16) * kPitchK + k + g4];
+                        b[i] = sB[(k + g4) * kPitchC + wc + i * 16 + r16];
+                    }
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) acc[i][j] = mma(a[i], b[j], acc[i][j]);
+                }
             }
         }
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < 2; ++i)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int r = ty + 16 * i, c = col0 + tx + 16 * j;
-                if (r < tc.nvalid && c < N) put<T>(p.out, (size_t)(tc.row0 + r) * N + c, acc[i][j]);
-            }
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int r = wr + i * 16 + g4 * 4 + e, c = col0 + wc + j * 16 + r16;
+                    if (r < tc.nvalid && c < N) Out[(size_t)(tc.row0 + r) * N + c] = acc[i][j][e];
+                }
     }
 }
 
-template <typename T>
-__global__ __launch_bounds__(kThreads) void wgrad_kernel(WgradArgs p, long long tiles) {
-    __shared__ Tile s;
-    __shared__ int s_dy[kK], s_x[kK];
-    const int tid = threadIdx.x, tx = tid % 16, ty = tid / 16;
+__global__ __launch_bounds__(kThreads) void wgrad_kernel(WgradArgs p, int tiles) {
+    __shared__ __align__(16) float sY[kK * kPitchC], sX[kK * kPitchC];
+    const int tid = threadIdx.x, lane = tid % kWave, wave = tid / kWave, r16 = lane & 15, g4 = lane >> 4;
+    const int wr = wave / 2 * 32, wc = wave % 2 * 32, lc = (tid % 16) * 4;
     const int N = p.N, M = p.M, tm = (M + kTile - 1) / kTile, tn = (N + kTile - 1) / kTile;
     const int nb = (M + kCkptBlock - 1) / kCkptBlock;
-    for (long long tau = blockIdx.x; tau < tiles; tau += gridDim.x) {
-        long long rest = tau;
-        const int m0 = (int)(rest % tm) * kTile;
+    for (int tau = blockIdx.x; tau < tiles; tau += gridDim.x) {
+        int rest = tau;
+        const int m0 = rest % tm * kTile;
         rest /= tm;
-        const int n0 = (int)(rest % tn) * kTile;
+        const int n0 = rest % tn * kTile;
         rest /= tn;
-        const int pairs = p.dy[1] != nullptr ? 2 : 1, q = (int)(rest % pairs), j = (int)(rest / pairs);
-        const T* dy = static_cast<const T*>(p.dy[q]);
+        const int pairs = p.dy[1] != nullptr ? 2 : 1, q = rest % pairs, j = rest / pairs;
+        const float* dy = static_cast<const float*>(p.dy[q]);
         const int r0 = clampi(p.offsets[j], 0, p.cap), r1 = clampi(p.offsets[j + 1], r0, p.cap);
-        float acc[4][4] = {};
+        float4 ry[2], rx[2];
+        auto load = [&](int first) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int r = first + i * 16 + tid / 16;
+                int a = r < r1 ? r : -1, b = a;
+                if (p.src_of != nullptr && a >= 0) {
+                    const int t = gathered(p.src_of, p.per, p.src_rows, r);
+                    (p.gather_dy ? a : b) = t;
+                }
+                ry[i] = a >= 0 && n0 + lc < N ? *reinterpret_cast<const float4*>(dy + (size_t)a * N + n0 + lc) : zero4();
+                rx[i] = zero4();
+                if (b >= 0 && m0 + lc < M) {
+                    const size_t at = (size_t)b * M + m0 + lc;
+                    if (p.x_scales != nullptr) {
+                        const uint32_t c = *reinterpret_cast<const uint32_t*>(static_cast<const int8_t*>(p.x) + at);
+                        const float s = p.x_scales[(size_t)b * nb + (m0 + lc) / kCkptBlock];
+                        rx[i] = make_float4(code_value<0>(c) * s, code_value<1>(c) * s, code_value<2>(c) * s,
+                                            code_value<3>(c) * s);
+                    } else {
+                        rx[i] = *reinterpret_cast<const float4*>(static_cast<const float*>(p.x) + at);
+                    }
+                }
+            }
+        };
+        floatx4 acc[2][2] = {};
+        load(r0);
         for (int r = r0; r < r1; r += kK) {
             __syncthreads();
-            if (tid < kK) {
-                const int g = r + tid < r1 ? gathered(p.src_of, p.per, p.src_rows, r + tid) : -1;
-                const int own = r + tid < r1 ? r + tid : -1;
-                s_dy[tid] = p.gather_dy ? g : own;
-                s_x[tid] = p.gather_x ? g : own;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                *reinterpret_cast<float4*>(sY + (i * 16 + tid / 16) * kPitchC + lc) = ry[i];
+                *reinterpret_cast<float4*>(sX + (i * 16 + tid / 16) * kPitchC + lc) = rx[i];
             }
             __syncthreads();
-            for (int i = tid; i < kTile * kK; i += kThreads) {
-                const int k = i / kTile, c = i % kTile, a = s_dy[k], b = s_x[k];
-                s.a[k][c] = a >= 0 && n0 + c < N ? value(dy, (size_t)a * N + n0 + c) : 0.0f;
-                float x = 0.0f;
-                if (b >= 0 && m0 + c < M) {
-                    const size_t at = (size_t)b * M + m0 + c;
-                    if (p.x_scales != nullptr)
-                        x = (float)static_cast<const int8_t*>(p.x)[at] * p.x_scales[(size_t)b * nb + (m0 + c) / kCkptBlock];
-                    else x = value(static_cast<const T*>(p.x), at);
+            if (r + kK < r1) load(r + kK);
+#pragma unroll
+            for (int k = 0; k < kK; k += 4) {
+                float a[2], b[2];
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    a[i] = sY[(k + g4) * kPitchC + wr + i * 16 + r16];
+                    b[i] = sX[(k + g4) * kPitchC + wc + i * 16 + r16];
                 }
-                s.b[k][c] = x;
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+#pragma unroll
+                    for (int jj = 0; jj < 2; ++jj) acc[i][jj] = mma(a[i], b[jj], acc[i][jj]);
             }
-            __syncthreads();
-            s.multiply(acc, tx, ty);
         }
-        const size_t w0 = (size_t)j * N * M;
+        const float* base = static_cast<const float*>(p.base[q]);
+        float* dw = static_cast<float*>(p.dw[q]);
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < 2; ++i)
 #pragma unroll
-            for (int jj = 0; jj < 4; ++jj) {
-                const int n = n0 + ty + 16 * i, m = m0 + tx + 16 * jj;
-                if (n >= N || m >= M) continue;
-                const size_t at = w0 + (size_t)n * M + m;
-                float v = acc[i][jj];
-                if (p.base[q] != nullptr)
-                    v += p.dw_f32 ? static_cast<const float*>(p.base[q])[at]
-                                  : value(static_cast<const uint16_t*>(p.base[q]), at);
-                if (p.dw_f32) put<float>(p.dw[q], at, v);
-                else put<uint16_t>(p.dw[q], at, v);
-            }
+            for (int jj = 0; jj < 2; ++jj)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int n = n0 + wr + i * 16 + g4 * 4 + e, m = m0 + wc + jj * 16 + r16;
+                    if (n >= N || m >= M) continue;
+                    const size_t at = ((size_t)j * N + n) * M + m;
+                    dw[at] = base != nullptr ? acc[i][jj][e] + base[at] : acc[i][jj][e];
+                }
     }
-}
-
-template <typename T>
-hipError_t wgrad(const WgradArgs& a, hipStream_t stream) {
-    const long long tiles = (long long)a.E_loc * (a.dy[1] != nullptr ? 2 : 1) * ((a.N + kTile - 1) / kTile) *
-                            ((a.M + kTile - 1) / kTile);
-    const int most = device_cu_count() * 8;
-    hipLaunchKernelGGL(wgrad_kernel<T>, dim3(tiles < most ? (int)tiles : most), dim3(kThreads), 0, stream, a, tiles);
-    return hipGetLastError();
 }
 
 }  // namespace
 
 hipError_t launch_ffn_ckpt_f32(const FfnArgs& a, hipStream_t stream) {
     static int per_cu = 0;
-    return launch_persistent(gate_up_ckpt_kernel<float>, kThreads, a, stream, &per_cu);
+    return launch_persistent(gate_up_ckpt_kernel, kThreads, a, stream, &per_cu);
 }
 hipError_t launch_dgrad_f32(const FfnArgs& a, hipStream_t stream) {
     static int per_cu = 0;
-    return launch_persistent(dgrad_kernel<float>, kThreads, a, stream, &per_cu);
+    return launch_persistent(dgrad_kernel, kThreads, a, stream, &per_cu);
 }
-hipError_t launch_wgrad_f32(const WgradArgs& a, hipStream_t stream) { return wgrad<float>(a, stream); }
+hipError_t launch_wgrad_f32(const WgradArgs& a, hipStream_t stream) {
+    // (api.hip bounds dw)
+    const int tiles = a.E_loc * (a.dy[1] != nullptr ? 2 : 1) * ((a.N + kTile - 1) / kTile) * ((a.M + kTile - 1) / kTile);
+    const int most = device_cu_count() * 8;
+    hipLaunchKernelGGL(wgrad_kernel, dim3(tiles < most ? tiles : most), dim3(kThreads), 0, stream, a, tiles);
+    return hipGetLastError();
+}
 
 }  // namespace moeep
