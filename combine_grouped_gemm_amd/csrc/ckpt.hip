@@ -158,64 +158,95 @@ __global__ __launch_bounds__(kWaves * kWave) void checkpoint_values_kernel(CkptA
 //   dgate = w dh u sg (1 + g (1 - sg)), dup = w dh g sg, hw = w h, dw = <dh, h>
 // dh is the gradient of the unweighted expert output's h, so <dh, h> is the
 // gradient of the slot's weight w.  1 - sg comes from e^-g itself and does not
-// cancel.  A wave takes `chunk` consecutive slots: it reads their rows at once,
-// writes zeros for those without one, and walks the others.
+// cancel.
+//
+// A block takes `per` consecutive slots (4 to 64).  Its first wave reads their rows, writes the
+// zeros of those that have none and lists the others in LDS; the waves share the list a row
+// each.  So ranks that hold an eighth of the slots keep their waves busy alike (8192 of
+// 65536 slots, 2048 columns: a wave that walked its own 8 slots 54 us), and a wave has all loads of
+// 2048 columns in flight.
+constexpr int kSlots = 64;
+
 template <bool F32>
-__global__ __launch_bounds__(kWaves * kWave) void swiglu_backward_kernel(SwigluBwdArgs p, int chunk) {
-    const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
+__global__ __launch_bounds__(kWaves * kWave) void swiglu_backward_kernel(SwigluBwdArgs p, int per) {
+    __shared__ int s_row[kSlots], s_slot[kSlots], s_n;
+    __shared__ float s_w[kSlots];
+    const int tid = threadIdx.x, lane = tid % kWave, wave = tid / kWave;
     const int nb = (p.I + kCkptBlock - 1) / kCkptBlock;
     constexpr int kSize = F32 ? 4 : 2;
-    for (long long s0 = ((long long)blockIdx.x * kWaves + wave) * chunk; s0 < p.slots;
-         s0 += (long long)gridDim.x * kWaves * chunk) {
-        int my = -1;
-        float my_w = 0.0f;
-        const bool mine = lane < chunk && s0 + lane < p.slots;
-        if (mine) {
-            const int r = p.row_of[s0 + lane];
-            my = r >= 0 && r < p.cap ? r : -1;
-            my_w = p.topk_w[s0 + lane];
+    for (long long s0 = (long long)blockIdx.x * per; s0 < p.slots; s0 += (long long)gridDim.x * per) {
+        __syncthreads();                             // the list before is used up
+        if (tid < kWave) {
+            int r = -1;
+            const bool mine = lane < per && s0 + lane < p.slots;
+            if (mine) {
+                r = p.row_of[s0 + lane];
+                if (r < 0 || r >= p.cap) {
+                    r = -1;
+                    p.dtopk_w[s0 + lane] = 0.0f;
+                }
+            }
+            const uint64_t local = ballot64(r >= 0);
+            if (r >= 0) {
+                const int at = popc64(local & lanemask_lt());
+                s_row[at] = r;
+                s_slot[at] = lane;
+                s_w[at] = p.topk_w[s0 + lane];
+            }
+            if (lane == 0) s_n = popc64(local);
         }
-        uint64_t todo = ballot64(my >= 0);
-        float my_dw = 0.0f;
-        while (todo != 0) {
-            const int k = __builtin_ctzll(todo);
-            todo &= todo - 1;
-            const int r = __builtin_amdgcn_readlane(my, k);
-            const float w = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(my_w), k));
+        __syncthreads();
+        const int n = s_n;
+        for (int i = wave; i < n; i += kWaves) {
+            const int r = __builtin_amdgcn_readfirstlane(s_row[i]);
+            const float w = s_w[i];
             const size_t at = (size_t)r * p.I, sat = (size_t)r * nb;
             const char* dh_row = static_cast<const char*>(p.dh) + at * kSize;
             float sum = 0.0f;
-#pragma unroll 2
-            for (int c = lane * 8; c < p.I; c += 512) {
-                Eight<F32> d;
-                d.load(dh_row + (size_t)c * kSize);
-                const uint2 gq = *reinterpret_cast<const uint2*>(p.gate_q + at + c);
-                const uint2 uq = *reinterpret_cast<const uint2*>(p.up_q + at + c);
-                float g[8], u[8], dh[8], dg[8], du[8], hw[8];
-                code_values(gq, p.gate_s[sat + c / kCkptBlock], g);
-                code_values(uq, p.up_s[sat + c / kCkptBlock], u);
-                d.values(dh);
+            for (int c0 = 0; c0 < p.I; c0 += kPieceCols) {
+                Eight<F32> d[kPiece];
+                uint2 gq[kPiece], uq[kPiece];
+                float gs[kPiece], us[kPiece];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    // e^-g overflows for g < -88: sg = 0, 1 - sg = 1
-                    const float e = F32 ? expf(-g[i]) : __expf(-g[i]);
-                    const float sg = F32 ? 1.0f / (1.0f + e) : __builtin_amdgcn_rcpf(1.0f + e);
-                    const float rest = e < 3e38f ? e * sg : 1.0f;                // 1 - sg
-                    const float act = g[i] * sg, wd = w * dh[i], h = act * u[i];
-                    dg[i] = wd * u[i] * fmaf(act, rest, sg);
-                    du[i] = wd * act;
-                    hw[i] = w * h;
-                    sum = fmaf(dh[i], h, sum);
+                for (int k = 0; k < kPiece; ++k) {
+                    const int c = c0 + k * 512 + lane * 8;
+                    if (c < p.I) {
+                        d[k].load(dh_row + (size_t)c * kSize);
+                        gq[k] = *reinterpret_cast<const uint2*>(p.gate_q + at + c);
+                        uq[k] = *reinterpret_cast<const uint2*>(p.up_q + at + c);
+                        gs[k] = p.gate_s[sat + c / kCkptBlock];
+                        us[k] = p.up_s[sat + c / kCkptBlock];
+                    }
                 }
-                Eight<F32>::store(static_cast<char*>(p.dgate) + (at + c) * kSize, dg);
-                Eight<F32>::store(static_cast<char*>(p.dup) + (at + c) * kSize, du);
-                Eight<F32>::store(static_cast<char*>(p.hw) + (at + c) * kSize, hw);
+#pragma unroll
+                for (int k = 0; k < kPiece; ++k) {
+                    const int c = c0 + k * 512 + lane * 8;
+                    if (c >= p.I) continue;
+                    float g[8], u[8], dh[8], dg[8], du[8], hw[8];
+                    code_values(gq[k], gs[k], g);
+                    code_values(uq[k], us[k], u);
+                    d[k].values(dh);
+#pragma unroll
+                    for (int e8 = 0; e8 < 8; ++e8) {
+                        // e^-g overflows for g < -88: sg = 0, 1 - sg = 1
+                        const float e = F32 ? expf(-g[e8]) : __expf(-g[e8]);
+                        const float sg = F32 ? 1.0f / (1.0f + e) : __builtin_amdgcn_rcpf(1.0f + e);
+                        const float rest = e < 3e38f ? e * sg : 1.0f;                // 1 - sg
+                        const float act = g[e8] * sg, wd = w * dh[e8], h = act * u[e8];
+                        dg[e8] = wd * u[e8] * fmaf(act, rest, sg);
+                        du[e8] = wd * act;
+                        hw[e8] = w * h;
+                        sum = fmaf(dh[e8], h, sum);
+                    }
+                    Eight<F32>::store(static_cast<char*>(p.dgate) + (at + c) * kSize, dg);
+                    Eight<F32>::store(static_cast<char*>(p.dup) + (at + c) * kSize, du);
+                    Eight<F32>::store(static_cast<char*>(p.hw) + (at + c) * kSize, hw);
+                }
             }
 #pragma unroll
             for (int d = 32; d > 0; d >>= 1) sum += __shfl_xor(sum, d, kWave);
-            if (lane == k) my_dw = sum;
+            if (lane == 0) p.dtopk_w[s0 + s_slot[i]] = sum;
         }
-        if (mine) p.dtopk_w[s0 + lane] = my_dw;
     }
 }
 
@@ -245,14 +276,14 @@ hipError_t launch_checkpoint_values(const CkptArgs& a, bool f32, hipStream_t str
 
 hipError_t launch_swiglu_backward(const SwigluBwdArgs& a, bool f32, hipStream_t stream) {
     if (a.slots == 0) return hipSuccess;
+    // a slot a wave while there are few; a list long enough to share once they fill the device
     const int most = device_cu_count() * 8;
-    // one slot a wave while there are few, up to 16 when a launch has many
-    int chunk = 1;
-    while (chunk < 16 && a.slots > (long long)most * kWaves * chunk) chunk *= 2;
-    const long long need = (a.slots + (long long)kWaves * chunk - 1) / ((long long)kWaves * chunk);
+    int per = kWaves;
+    while (per < kSlots && a.slots > (long long)device_cu_count() * 4 * per) per *= 2;
+    const long long need = (a.slots + per - 1) / per;
     const dim3 grid(need < most ? (int)need : most), block(kWaves * kWave);
-    if (f32) hipLaunchKernelGGL(swiglu_backward_kernel<true>, grid, block, 0, stream, a, chunk);
-    else hipLaunchKernelGGL(swiglu_backward_kernel<false>, grid, block, 0, stream, a, chunk);
+    if (f32) hipLaunchKernelGGL(swiglu_backward_kernel<true>, grid, block, 0, stream, a, per);
+    else hipLaunchKernelGGL(swiglu_backward_kernel<false>, grid, block, 0, stream, a, per);
     return hipGetLastError();
 }
 
