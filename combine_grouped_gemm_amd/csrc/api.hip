@@ -741,7 +741,7 @@ moe_status_t moe_swiglu_backward(const void* dh, moe_dtype_t act_dt, const int8_
     REQUIRE(B >= 0 && K >= 1 && K <= 1024, "need B >= 0 and 1 <= K <= 1024");
     REQUIRE((long long)B * K <= 0x7fffffffLL, "B*K must fit in int32");
     REQUIRE(cap_rows >= 0, "cap_rows must be >= 0");
-    REQUIRE(I >= 8 && I % 8 == 0, "I must be a positive multiple of 8 (got %d)", I);
+    REQUIRE(I >= 8 && I % 8 == 0 && I <= (1 << 24), "I must be a positive multiple of 8, at most %d (got %d)", 1 << 24, I);
     if (cap_rows > 0) {
         REQUIRE(dh && gate_q && gate_scales && up_q && up_scales && dgate && dup && hw, "null pointer argument");
         REQUIRE(aligned16(dh) && aligned16(gate_q) && aligned16(up_q) && aligned16(dgate) && aligned16(dup) &&

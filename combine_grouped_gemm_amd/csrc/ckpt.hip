@@ -160,15 +160,15 @@ __global__ __launch_bounds__(kWaves * kWave) void checkpoint_values_kernel(CkptA
 // gradient of the slot's weight w.  1 - sg comes from e^-g itself and does not
 // cancel.
 //
-// A block takes `per` consecutive slots (4 to 64).  Its first wave reads their rows, writes the
+// A block takes `per` consecutive slots (4 to 32).  Its first wave reads their rows, writes the
 // zeros of those that have none and lists the others in LDS; the waves share the list a row
 // each.  So ranks that hold an eighth of the slots keep their waves busy alike (8192 of
 // 65536 slots, 2048 columns: a wave that walked its own 8 slots 54 us), and a wave has all loads of
 // 2048 columns in flight.
-constexpr int kSlots = 64;
+constexpr int kSlots = 32;
 
 template <bool F32>
-__global__ __launch_bounds__(kWaves * kWave) void swiglu_backward_kernel(SwigluBwdArgs p, int per) {
+__global__ __launch_bounds__(kWaves * kWave, 4) void swiglu_backward_kernel(SwigluBwdArgs p, int per) {
     __shared__ int s_row[kSlots], s_slot[kSlots], s_n;
     __shared__ float s_w[kSlots];
     const int tid = threadIdx.x, lane = tid % kWave, wave = tid / kWave;
@@ -252,7 +252,7 @@ __global__ __launch_bounds__(kWaves * kWave) void swiglu_backward_kernel(SwigluB
 
 dim3 row_grid(const CkptArgs& a) {
     const int pieces = (a.cols + kPieceCols - 1) / kPieceCols;
-    const int need = (a.cap + kWaves - 1) / kWaves, most = (device_cu_count() * 8 + pieces - 1) / pieces;
+    const int need = a.cap / kWaves + (a.cap % kWaves != 0), most = (device_cu_count() * 8 + pieces - 1) / pieces;
     return dim3(need < most ? need : most, pieces);
 }
 

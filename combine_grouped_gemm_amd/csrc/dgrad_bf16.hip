@@ -35,7 +35,6 @@ __global__ __launch_bounds__(512, 1) void dgrad_wide_kernel(FfnArgs p) {
     constexpr int LPS = A_ITERS + B_ITERS;
     constexpr int FM = BM / 16 / WMW, FN = BN / WNW / 16;
     constexpr bool LOOK = BM <= 256;
-    constexpr int WROW = BN * 2;                     // bytes of a weight row in LDS
     static_assert(BM % 64 == 0 && B_ITERS == 4 && FN == 4, "tile shape");
 
     __shared__ uint4 sa0[BM * CPR];
@@ -155,8 +154,8 @@ __global__ __launch_bounds__(512, 1) void dgrad_wide_kernel(FfnArgs p) {
                 for (int f = 0; f < FN; ++f) ad[f] = bb + wfrag[f];
                 bf16x8 bfr[2][FN];
                 if constexpr (LOOK) {
-                    read_frags4<0, 4 * WROW>(bfr[0], ad);
-                    read_frags4<32 * WROW, 4 * WROW>(bfr[1], ad);
+                    read_frags<BN, 0>(bfr[0], ad);
+                    read_frags<BN, 1>(bfr[1], ad);
                     block_barrier();                     // every wave holds this step's weight fragments
                 }
                 auto issue_slot = [&](int q) {
@@ -166,9 +165,9 @@ __global__ __launch_bounds__(512, 1) void dgrad_wide_kernel(FfnArgs p) {
 #pragma unroll
                 for (int kk = 0; kk < 2; ++kk) {
                     if constexpr (!LOOK) {
-                        if (kk == 0) read_frags4<0, 4 * WROW>(bfr[0], ad);
+                        if (kk == 0) read_frags<BN, 0>(bfr[0], ad);
                         else {
-                            read_frags4<32 * WROW, 4 * WROW>(bfr[1], ad);
+                            read_frags<BN, 1>(bfr[1], ad);
                             block_barrier();
                         }
                     }

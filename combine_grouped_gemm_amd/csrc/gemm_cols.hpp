@@ -59,11 +59,10 @@ __device__ __forceinline__ bf16x8 read_frag(const char* stage, uint32_t off, int
 #endif
 }
 
-// Four fragments of one half, read and waited for in one block (as lds_read16x4): ad
-// holds the LDS addresses of their first reads.  OFF: byte offset of the half, OFF2 of
-// the second reads.
-template <int OFF, int OFF2>
-__device__ __forceinline__ void read_frags4(bf16x8 (&f)[4], const uint32_t (&ad)[4]) {
+// Fragments of one 32-row half of a [64][TW] stage, read and waited for in one block (as
+// lds_read16x4): ad holds the LDS addresses of their first reads in the first half.
+template <int TW, int HALF>
+__device__ __forceinline__ void read_frags(bf16x8 (&f)[4], const uint32_t (&ad)[4]) {
     uint2 t[8];
     asm volatile(
         "ds_read_b64_tr_b16 %0, %8 offset:%12\n\t"
@@ -76,10 +75,25 @@ __device__ __forceinline__ void read_frags4(bf16x8 (&f)[4], const uint32_t (&ad)
         "ds_read_b64_tr_b16 %7, %11 offset:%13\n\t"
         "s_waitcnt lgkmcnt(0)"
         : "=&v"(t[0]), "=&v"(t[1]), "=&v"(t[2]), "=&v"(t[3]), "=&v"(t[4]), "=&v"(t[5]), "=&v"(t[6]), "=&v"(t[7])
-        : "v"(ad[0]), "v"(ad[1]), "v"(ad[2]), "v"(ad[3]), "n"(OFF), "n"(OFF + OFF2)
+        : "v"(ad[0]), "v"(ad[1]), "v"(ad[2]), "v"(ad[3]), "n"(HALF * 32 * TW * 2), "n"((HALF * 32 + 4) * TW * 2)
         : "memory");
 #pragma unroll
     for (int i = 0; i < 4; ++i) f[i] = join_frag(t[2 * i], t[2 * i + 1]);
+}
+template <int TW, int HALF>
+__device__ __forceinline__ void read_frags(bf16x8 (&f)[2], const uint32_t (&ad)[2]) {
+    uint2 t[4];
+    asm volatile(
+        "ds_read_b64_tr_b16 %0, %4 offset:%6\n\t"
+        "ds_read_b64_tr_b16 %1, %4 offset:%7\n\t"
+        "ds_read_b64_tr_b16 %2, %5 offset:%6\n\t"
+        "ds_read_b64_tr_b16 %3, %5 offset:%7\n\t"
+        "s_waitcnt lgkmcnt(0)"
+        : "=&v"(t[0]), "=&v"(t[1]), "=&v"(t[2]), "=&v"(t[3])
+        : "v"(ad[0]), "v"(ad[1]), "n"(HALF * 32 * TW * 2), "n"((HALF * 32 + 4) * TW * 2)
+        : "memory");
+#pragma unroll
+    for (int i = 0; i < 2; ++i) f[i] = join_frag(t[2 * i], t[2 * i + 1]);
 }
 
 // quotient of a slot by the slots of a token, exact for slots below 2^31: the host's

@@ -112,6 +112,7 @@ __global__ __launch_bounds__(512, 1) void wgrad_kernel(WgradArgs p, int tiles_n,
     __shared__ uint4 sy1[BK * TN / 8];
     __shared__ uint4 sx1[BK * TM / 8];
     __shared__ int s_tok[2][kPieceRows];
+    __shared__ int s_off[kMaxExperts + 1];                   // the experts' offsets, within the buffer
 
     auto y_base = [&](auto I) INLINE -> char* {
         if constexpr (decltype(I)::value == 0) return reinterpret_cast<char*>(sy0);
@@ -147,8 +148,8 @@ __global__ __launch_bounds__(512, 1) void wgrad_kernel(WgradArgs p, int tiles_n,
         const unsigned n = rest / wide;
         w.n0 = uniform((int)n * TN);
         w.m0 = uniform((int)(b * kGroup + rest - n * wide) * TM);
-        w.row0 = uniform(clampi(p.offsets[w.j], 0, p.cap));
-        w.end = uniform(clampi(p.offsets[w.j + 1], w.row0, p.cap));
+        w.row0 = uniform(s_off[w.j]);
+        w.end = uniform(max(s_off[w.j + 1], w.row0));
         w.rows = min(w.end - w.row0, kPieceRows);
     };
     auto after = [&](const Piece& w) INLINE {
@@ -406,6 +407,10 @@ __global__ __launch_bounds__(512, 1) void wgrad_kernel(WgradArgs p, int tiles_n,
         else write_as(w, false);
     };
 
+    // (read here once: a load in the sequence of steps would wait for the stores before it)
+    for (int j = tid; j <= p.E_loc; j += NT) s_off[j] = clampi(p.offsets[j], 0, p.cap);
+    __syncthreads();
+
     // the sequence of steps: `cur` is computed, `nxt` comes after it; s_tok[slot] lists cur's rows
     Piece cur, nxt, then;
     cur.j = cur.q = cur.n0 = cur.m0 = 0;
@@ -451,28 +456,34 @@ __global__ __launch_bounds__(512, 1) void wgrad_kernel(WgradArgs p, int tiles_n,
             const Piece& w = same ? cur : nxt;
             // (past the last step nothing is read, but the loads go out)
             const Source s = prepare(w, s_tok[same ? slot : slot ^ 1], same ? i0 + BK : 0, more);
-            const char* yb = y_base(I);
-            const char* xb = x_base(I);
-            uint32_t y0 = yfrag0, x0 = xfrag0;
-            asm volatile("" : "+v"(y0), "+v"(x0));           // keeps the offsets below from living across steps
+            // fragments come in blocks of four, read and waited for together: the compiler, left to
+            // place the waits, lets a read wait for every load and store in flight
+            uint32_t ya[FN], xa[FM];
+#pragma unroll
+            for (int a = 0; a < FN; ++a) ya[a] = lds_addr(y_base(I)) + (yfrag0 ^ (a << 5));
+#pragma unroll
+            for (int f = 0; f < FM; ++f) xa[f] = lds_addr(x_base(I)) + (xfrag0 ^ (f << 5));
 #pragma unroll
             for (int kk = 0; kk < 2; ++kk) {
                 bf16x8 xf[FM];
+                if (kk == 0) read_frags<TM, 0>(xf, xa);
+                else read_frags<TM, 1>(xf, xa);
 #pragma unroll
-                for (int f = 0; f < FM; ++f) xf[f] = read_frag<TM>(xb, x0 ^ (f << 5), kk);
-                bf16x8 yf = read_frag<TN>(yb, y0, kk);
+                for (int a0 = 0; a0 < FN; a0 += 4) {
+                    bf16x8 yf[4];
+                    const uint32_t ad[4] = {ya[a0], ya[a0 + 1], ya[a0 + 2], ya[a0 + 3]};
+                    if (kk == 0) read_frags<TN, 0>(yf, ad);
+                    else read_frags<TN, 1>(yf, ad);
 #pragma unroll
-                for (int a = 0; a < FN; ++a) {
-                    bf16x8 yn;
-                    if (a + 1 < FN) yn = read_frag<TN>(yb, y0 ^ ((a + 1) << 5), kk);
+                    for (int a = 0; a < 4; ++a) {
 #pragma unroll
-                    for (int f = 0; f < FM; ++f)
-                        acc[a][f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xf[f], yf, acc[a][f], 0, 0, 0);
-                    const int q = kk * FN + a;
-                    if (q < Y_ITERS) issue_y(other, s, q);
-                    else if (q < LOADS) issue_x(other, s, q - Y_ITERS);
-                    if (a + 1 < FN) yf = yn;
-                    __builtin_amdgcn_sched_barrier(0);
+                        for (int f = 0; f < FM; ++f)
+                            acc[a0 + a][f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xf[f], yf[a], acc[a0 + a][f], 0, 0, 0);
+                        const int q = kk * FN + a0 + a;
+                        if (q < Y_ITERS) issue_y(other, s, q);
+                        else if (q < LOADS) issue_x(other, s, q - Y_ITERS);
+                        __builtin_amdgcn_sched_barrier(0);
+                    }
                 }
             }
 #pragma unroll

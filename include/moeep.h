@@ -532,7 +532,7 @@ moe_status_t moe_ffn_gate_up_train(const void* xd, const int32_t* offsets, int E
  * topk_w[t,k], sg = 1 / (1 + exp(-g)) and h = g sg u:
  *   dgate[r] = w dh[r] u sg (1 + g (1 - sg)),  dup[r] = w dh[r] g sg,
  *   hw[r] = w h,  dtopk_w[t,k] = sum_i dh[r,i] h_i.
- *   dh (cap_rows, I), dgate, dup, hw (cap_rows, I) of act_dt (F32 or BF16), the
+ *   dh (cap_rows, I), dgate, dup, hw (cap_rows, I) of act_dt (F32 or BF16; I a multiple of 8, at most 2^24), the
  *   outputs overlapping neither each other nor the inputs; row_of, topk_w, dtopk_w
  *   (B, K).
  * Slots whose row lies outside [0, cap_rows) get dtopk_w 0; rows that no slot

@@ -688,6 +688,14 @@ def test_rows_past_4_gib():
     for j, (a, b) in enumerate(((0, 1), (1, 4))):
         ref, mag = dy[a:b].double().t() @ xv[a:b], dy[a:b].double().abs().t() @ xv[a:b].abs()
         _near(got[j], ref, HALF[torch.float32] * ref.abs() + 4 * 2.0**-23 * mag, "dw")
+    # the same tokens in bf16, and as gathered gradients
+    for y, z, side in ((dy, x, "x"), (x, dy, "dy")):
+        for dt in TYPES:
+            got = m.moe_ffn_wgrad(y, z, _offsets([1, 3]), src_of=src, gather=side, dw_dtype=dt)
+            a_, b_ = (v[src.long()] if v is x else v for v in (y, z))
+            for j, (a, b) in enumerate(((0, 1), (1, 4))):
+                ref, mag = a_[a:b].double().t() @ b_[a:b].double(), a_[a:b].double().abs().t() @ b_[a:b].double().abs()
+                _near(got[j], ref, HALF[dt] * ref.abs() + 4 * 2.0**-23 * mag, f"dw, {side} gathered")
     wt = _weights(2, cols, 72, 5, torch.bfloat16)
     for hint in (1, 300):
         dx = m.moe_ffn_dgrad(x, _offsets([1, 3]), wt, src_of=src, expected_rows=hint)
@@ -695,3 +703,84 @@ def test_rows_past_4_gib():
             d = x[src[a:b].long()].double()
             ref, mag = d @ wt[j].double(), d.abs() @ wt[j].double().abs()
             _near(dx[a:b], ref, HALF[torch.bfloat16] * ref.abs() + cols * 2.0**-23 * mag, "dx")
+
+
+@pytest.mark.parametrize("ckpt", [False, True])
+@pytest.mark.parametrize("base", [False, True])
+def test_wgrad_of_very_wide_rows(base, ckpt):
+    """256 rows of dw that together pass 2^31 bytes; the last columns are 8 codes."""
+    import combine_grouped_gemm_amd as m
+    N, M = 16, 2**21 + 8
+    dy = _values(5, N, 1, torch.bfloat16)
+    x, xs = _codes(5, M, 2) if ckpt else (_values(5, M, 2, torch.bfloat16), None)
+    b = torch.ones(2, N, M, device="cuda") if base else None
+    dw = m.moe_ffn_wgrad(dy, x, _offsets([2, 3]), x_scales=xs, base=b)
+    xv = _decoded(x, xs) if ckpt else x.double()
+    for j, (r0, r1) in enumerate(((0, 2), (2, 5))):
+        ref, mag = dy[r0:r1].double().t() @ xv[r0:r1] + base, dy[r0:r1].double().abs().t() @ xv[r0:r1].abs() + base
+        _near(dw[j], ref, HALF[torch.float32] * ref.abs() + 4 * 2.0**-23 * mag, "dw")
+
+
+def test_layer_of_no_tokens():
+    import combine_grouped_gemm_amd as m
+    layer, x, lg, w, dout = _train_layer(m, 0, 4, 2, 64, 72, 0, 4, torch.bfloat16)
+    grads = layer.new_grads()
+    layer.forward(x, lg, w)
+    dx, dlogits = layer.backward(dout, lg, w, grads)
+    assert dx.shape == (0, 64) and dlogits.shape == (0, 4)
+    assert all(not bool(g.any()) for g in grads.values())
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_layer_that_drops_rows(dtype):
+    """A buffer shorter than the batch's rows: the dropped slots pass no gradient."""
+    import combine_grouped_gemm_amd as m
+    name = {torch.float32: "f32", torch.bfloat16: "bf16"}[dtype]
+    T, E, K, H, I = 60, 6, 2, 72, 136
+    _, x, lg, w, dout = _train_layer(m, T, E, K, H, I, 0, E, dtype, seed=11)
+    layer = m.MoELayer([T], E, K, H, I, 0, E, name, name, name, cap_rows=70, train=True)
+    grads = layer.new_grads()
+    layer.forward(x, lg, w)
+    dx, _ = layer.backward(dout, lg, w, grads)
+    row_of = layer.row_of.cpu().numpy()
+    assert (row_of < 0).sum() == T * K - 70
+    assert bool((layer.dtopk_w[layer.row_of < 0] == 0).all())
+    off = np.minimum(layer.offsets.cpu().numpy(), 70)
+    src = layer.src_of.cpu().numpy()
+    dh = to_np(layer.dh)
+    g, u = (to_np(_decoded(q, s)) for q, s in ((layer.gate_q, layer.gate_s), (layer.up_q, layer.up_s)))
+    dg, du, hw, dw = tr.swiglu_backward(dh, g, u, row_of, layer.topk_w.cpu().numpy())
+    bar = 1e-2 if dtype == torch.bfloat16 else 1e-5
+    xt, dt = tr.token_rows(to_np(_decoded(layer.x_q, layer.x_s)), src, K), tr.token_rows(to_np(dout), src, K)
+    dxd = tr.dgrad([(dg, to_np(w["gate"])), (du, to_np(w["up"]))], off, 70)
+    want = np.zeros((T, H))
+    for t in range(T):
+        for k in range(K):
+            if row_of[t, k] >= 0:
+                want[t] += dxd[row_of[t, k]]
+    for what, got, ref in (("dtopk_w", layer.dtopk_w, dw), ("gate", grads["gate"], tr.wgrad(dg, xt, off)),
+                           ("up", grads["up"], tr.wgrad(du, xt, off)), ("down", grads["down"], tr.wgrad(dt, hw, off)),
+                           ("dx", dx, want)):
+        assert np.linalg.norm(to_np(got) - ref) <= bar * np.linalg.norm(ref), what
+
+
+def test_micro_batches_add_up_to_the_batch():
+    """Two micro-batches on two streams, the second's gradients added to the first's."""
+    import combine_grouped_gemm_amd as m
+    from combine_grouped_gemm_amd.layer import MicroBatchedLayer
+    whole, x, lg, w, dout = _train_layer(m, 120, 8, 2, 136, 264, 0, 8, torch.bfloat16, seed=13, segs=2)
+    one = whole.new_grads()
+    whole.forward(x, lg, w)
+    dx, dlogits = whole.backward(dout, lg, w, one)
+    halves = MicroBatchedLayer(whole.seg_rows, 8, 2, 136, 264, 0, 8, "bf16", "bf16", "bf16", train=True)
+    (xa, la), (xb, lb) = halves.split_inputs(x, lg)
+    oa, ob = halves.forward(x, lg, w)
+    assert torch.equal(torch.cat([oa, ob]), whole.out)
+    two = halves.a.new_grads()
+    Ta = halves.a.T
+    dxa, dla = halves.a.backward(dout[:Ta], la, w, two)
+    dxb, dlb = halves.b.backward(dout[Ta:].contiguous(), lb, w, two, accumulate=True)
+    assert torch.equal(torch.cat([dxa, dxb]), dx) and torch.equal(torch.cat([dla, dlb]), dlogits)
+    for k in one:
+        # the same products in two sums: fp32 roundings of up to 120 terms each
+        _near(two[k], one[k], 2 * 121 * 2.0**-23 * (one[k].double().abs() + one[k].double().abs().amax()), k)
