@@ -62,14 +62,16 @@ __global__ __launch_bounds__(512, 1) void dgrad_wide_kernel(FfnArgs p) {
     const int nk1 = (Kdim + BK - 1) / BK, nk = p.a2 != nullptr ? 2 * nk1 : nk1;
     const int lane_k = swz(lane / 8, lane % 8) * 8;
 
-    build_tile_prefix_sorted<NT, BM>(p, s_pre, s_ord, reinterpret_cast<int*>(sa0), s_tmp);
+    build_tile_prefix_sorted<NT, BM, true>(p, s_pre, s_ord, reinterpret_cast<int*>(sa0), s_tmp);
     const int n_tiles_n = (N + BN - 1) / BN;
     const int total = n_tiles_n * s_pre[p.E_loc];
     const int G = gridDim.x;
     const int v = xcd_block_order();
     uint16_t* __restrict__ Out = static_cast<uint16_t*>(p.out);
 
-    for (int tau = v; tau < total; tau += G) {
+    for (int rnd = 0; rnd * (long long)G < total; ++rnd) {
+        const int tau = round_tile_back(rnd, v, G, total);
+        if (tau < 0) continue;                           // (an odd last round fills from the other end)
         const TileCoord tc = decode_tile<BM>(tau, n_tiles_n, s_pre, p, s_ord);
         const int j = tc.j, row0 = tc.row0, nvalid = tc.nvalid;
         const int col0 = tc.nt * BN;

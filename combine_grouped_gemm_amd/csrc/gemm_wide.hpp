@@ -218,7 +218,7 @@ __global__ __launch_bounds__(512, 1) void grouped_gemm_bf16_wide_kernel(FfnArgs 
     const int lane_k = swz(lane / 8, lane % 8) * 8;
 
     // largest experts' tiles first; the first row stage is free scratch until the first load
-    build_tile_prefix_sorted<NT, BM>(p, s_pre, s_ord, reinterpret_cast<int*>(sa0), s_tmp);
+    build_tile_prefix_sorted<NT, BM, CKPT>(p, s_pre, s_ord, reinterpret_cast<int*>(sa0), s_tmp);
     const int n_tiles_n = (N + BNO - 1) / BNO;
     const int total = n_tiles_n * s_pre[p.E_loc];
     const int G = gridDim.x;
@@ -229,7 +229,11 @@ __global__ __launch_bounds__(512, 1) void grouped_gemm_bf16_wide_kernel(FfnArgs 
     const uint16_t* __restrict__ W1 = static_cast<const uint16_t*>(p.w1);
     uint16_t* __restrict__ Out = static_cast<uint16_t*>(p.out);
 
-    for (int tau = v; tau < total; tau += G) {
+    for (int rnd = 0, tau = v; CKPT ? rnd * (long long)G < total : tau < total; ++rnd, tau += G) {
+        if constexpr (CKPT) {
+            tau = round_tile_back(rnd, v, G, total);
+            if (tau < 0) continue;
+        }
         const TileCoord tc = decode_tile<BM>(tau, n_tiles_n, s_pre, p, s_ord);
         const int j = tc.j, row0 = tc.row0, nvalid = tc.nvalid;
         const int col0 = tc.nt * BNO;
