@@ -173,8 +173,8 @@ __device__ __forceinline__ int round_tile(int r, int v, int b, int G, int total)
 
 // Tile of round r for position v of G when the tiles lie in decreasing cost: every other
 // round runs backwards, so that a block with a large tile of one round has a small one of
-// the next (-1: none).  Training share of a rank with 26 to 1131 rows an expert, 1.3 rounds: dh
-// 311 -> XXX us.
+// the next (-1: none).  A rank with 26 to 1131 rows an expert, 1.3 rounds of dgrad tiles: 309
+// -> 302 us; 2.6 rounds of gate/up with checkpoints: 607 -> 581.
 __device__ __forceinline__ int round_tile_back(int r, int v, int G, int total) {
     const long long tau = (long long)r * G + ((r & 1) != 0 ? G - 1 - v : v);
     return tau < total ? (int)tau : -1;
