@@ -837,10 +837,12 @@ moe_status_t moe_ffn_wgrad(const void* dy, const void* dy2, const void* x, moe_d
     REQUIRE((long long)out_dim * in_dim <= (1ll << 38) / E_local, "dw is too large");
     const size_t dw_bytes = (size_t)E_local * out_dim * in_dim * elem_size(dw_dt);
     REQUIRE(!dw2 || apart(dw, dw_bytes, dw2, dw_bytes), "dw and dw2 must not overlap");
-    for (const void* b : {base, base2})
-        for (const void* d : {static_cast<const void*>(dw), static_cast<const void*>(dw2)})
-            REQUIRE(!b || !d || (b == d && (d == dw) == (b == base)) || apart(b, dw_bytes, d, dw_bytes),
-                    "a base must be its own dw or lie apart from both");
+    const void* const bases[2] = {base, base2};
+    void* const dws[2] = {dw, dw2};
+    for (int j = 0; j < 2; ++j)
+        REQUIRE((bases[j] == dws[j] || apart(bases[j], dw_bytes, dws[j], dw_bytes)) &&
+                    apart(bases[j], dw_bytes, dws[1 - j], dw_bytes),
+                "a base must be its own dw or lie apart from both");
     const size_t dy_bytes = (size_t)dy_rows * out_dim * elem_size(act_dt),
                  x_bytes = (size_t)x_rows * in_dim * (x_dt == MOE_CKPT8 ? 1 : elem_size(act_dt));
     for (const void* d : {static_cast<const void*>(dw), static_cast<const void*>(dw2)})

@@ -133,7 +133,7 @@ BAD_WGRAD = [
     (dict(dw=NONE), ARG, "null dw"), (dict(dw2=NONE), ARG, "together"), (dict(dy2=NONE), ARG, "together"),
     (dict(x_dt=m.MOE_CKPT8), ARG, "scales"), (dict(dw2=NONE, dy2=NONE, base2=P), ARG, "base2"), (dict(dw=HALF8), ARG, "16-byte"),
     (dict(x=HALF8), ARG, "16-byte"), (dict(dw2=Q), ARG, "overlap"), (dict(dw2=V((1 << 30) + DW - 16)), ARG, "overlap"),
-    (dict(base=V((1 << 30) + 16)), ARG, "base"), (dict(base=S), ARG, "base"), (dict(base2=Q), ARG, "base"), (dict(dw=P), ARG, "overlap"),
+    (dict(base=V((1 << 30) + 16)), ARG, "base"), (dict(base=Q, base2=Q), ARG, "base"), (dict(base=S), ARG, "base"), (dict(base2=Q), ARG, "base"), (dict(dw=P), ARG, "overlap"),
 ]
 
 
