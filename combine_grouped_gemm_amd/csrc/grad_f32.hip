@@ -232,7 +232,8 @@ __global__ __launch_bounds__(kThreads) void wgrad_kernel(WgradArgs p, int tiles)
                 int a = r < r1 ? r : -1, b = a;
                 if (p.src_of != nullptr && a >= 0) {
                     const int t = gathered(p.src_of, p.per, p.src_rows, r);
-                    (p.gather_dy ? a : b) = t;
+                    if (t < 0) a = b = -1;                   // adds nothing, whatever the other row holds
+                    else (p.gather_dy ? a : b) = t;
                 }
                 ry[i] = a >= 0 && n0 + lc < N ? *reinterpret_cast<const float4*>(dy + (size_t)a * N + n0 + lc) : zero4();
                 rx[i] = zero4();

@@ -13,9 +13,11 @@
 //
 // The row of a gathered operand (src_of) is looked up once per piece of work (a tile, or
 // 1024 rows of one): the piece's rows are listed in LDS during the piece before, so that a
-// load's address is one LDS read away.  Rows past the expert's last one, and rows that
-// src_of names nowhere, get an offset outside the operand's extent, read nothing and land
-// zeros in both operands.
+// load's address is one LDS read away.  Rows past the expert's last one get an offset outside
+// the operand's extent, read nothing and land zeros in both operands.  So do rows of the gathered
+// operand that src_of names nowhere; a list says whether it has any, and then their rows of the
+// other operand are cleared in LDS, so that they add nothing whatever it holds.  (Without a word
+// of this EP share 1045 us, so 1063; with both operands' offsets from the list 1080.)
 //
 // A checkpoint x comes through registers: 16 codes a load, issued a step ahead as the
 // direct loads are, turned into the bf16 values they stand for (exact) after the step's
@@ -112,6 +114,7 @@ __global__ __launch_bounds__(512, 1) void wgrad_kernel(WgradArgs p, int tiles_n,
     __shared__ uint4 sy1[BK * TN / 8];
     __shared__ uint4 sx1[BK * TM / 8];
     __shared__ int s_tok[2][kPieceRows];
+    __shared__ uint2 s_holes[2];                             // whether a list has such a row (a byte a wave)
     __shared__ int s_off[kMaxExperts + 1];                   // the experts' offsets, within the buffer
 
     auto y_base = [&](auto I) INLINE -> char* {
@@ -174,13 +177,19 @@ __global__ __launch_bounds__(512, 1) void wgrad_kernel(WgradArgs p, int tiles_n,
             listed[i] = r < w.rows ? p.src_of[w.row0 + r] : -1;
         }
     };
-    auto store_list = [&](int* tok) INLINE {
+    auto store_list = [&](const Piece& w, int list) INLINE {
         if (!gathers) return;
+        bool hole = false;
 #pragma unroll
         for (int i = 0; i < LIST; ++i) {
-            const int t = listed[i] < 0 ? -1 : token_of(listed[i], p.per_div);
-            tok[i * NT + tid] = t < p.src_rows ? t : -1;
+            const int r = i * NT + tid;
+            int t = listed[i] < 0 ? -1 : token_of(listed[i], p.per_div);
+            t = t < p.src_rows ? t : -1;
+            s_tok[list][r] = t;
+            hole |= t < 0 && r < w.rows;
         }
+        const bool any = ballot64(hole) != 0;
+        if (lane == 0) reinterpret_cast<uint8_t*>(&s_holes[list])[wave] = any;
     };
 
     // What a step of piece w that starts at its row i0 loads.  Lane offsets of the direct
@@ -274,6 +283,18 @@ __global__ __launch_bounds__(512, 1) void wgrad_kernel(WgradArgs p, int tiles_n,
             d[0] = make_uint4(o[0], o[1], o[2], o[3]);
             d[1] = make_uint4(o[4], o[5], o[6], o[7]);
         }
+    };
+    // zeros in both operands' rows that src_of names nowhere, in a stage whose loads have landed
+    auto clear_holes = [&](auto I, const int* tok) INLINE {
+        for (int k = wave; k < BK; k += NW) {
+            if (uniform(tok[k]) >= 0) continue;
+            for (int c = lane; c < TN / 8; c += kWave)
+                reinterpret_cast<uint4*>(y_base(I))[k * (TN / 8) + c] = make_uint4(0, 0, 0, 0);
+            for (int c = lane; c < TM / 8; c += kWave)
+                reinterpret_cast<uint4*>(x_base(I))[k * (TM / 8) + c] = make_uint4(0, 0, 0, 0);
+        }
+        wait_lgkm0();
+        block_barrier();
     };
     // everything that precedes the direct loads of a step
     auto prepare = [&](const Piece& w, const int* tok, int i0, bool live) INLINE {
@@ -417,10 +438,10 @@ __global__ __launch_bounds__(512, 1) void wgrad_kernel(WgradArgs p, int tiles_n,
     open_tile(xcd_block_order(), cur);
     if (cur.tile >= tiles) return;
     load_list(cur);
-    store_list(s_tok[0]);
+    store_list(cur, 0);
     nxt = after(cur);
     load_list(nxt);
-    store_list(s_tok[1]);
+    store_list(nxt, 1);
     __syncthreads();
     {
         const Source s = prepare(cur, s_tok[0], 0, true);
@@ -437,12 +458,14 @@ __global__ __launch_bounds__(512, 1) void wgrad_kernel(WgradArgs p, int tiles_n,
 
     // one step; false after the last one of all
     auto step = [&](auto I) INLINE -> bool {
+        const uint2 holes = s_holes[slot];
         // this step's loads have landed; a tile's stores issued after them may still be on their way
         if (draining) wait_vmcnt<STORES>();
         else wait_vmcnt<0>();
         draining = false;
         wait_lgkm0();
         block_barrier();
+        if (gathers && uniform((int)(holes.x | holes.y)) != 0) clear_holes(I, s_tok[slot] + i0);
         // what comes next: another step of this piece, or the first of the next piece
         const bool same = uniform(i0 + BK < cur.rows ? 1 : 0) != 0;
         const bool more = uniform(same || nxt.tile < tiles ? 1 : 0) != 0;
@@ -494,7 +517,7 @@ __global__ __launch_bounds__(512, 1) void wgrad_kernel(WgradArgs p, int tiles_n,
             if constexpr (CKPT) store_codes(other);
         }
         // cur's list was last read for this step's loads, ahead of the barrier above
-        if (turn) store_list(s_tok[slot]);
+        if (turn) store_list(then, slot);
         if (same) {
             i0 += BK;
             return true;

@@ -409,6 +409,35 @@ def test_wgrad_bases_and_types(base, two, dw_dtype):
         _check_wgrad(m, COUNTS["mixed"], 72, 136, torch.float32, two, None, False, base, dw_dtype)
 
 
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("ckpt", [False, True])
+@pytest.mark.parametrize("gather", ["x", "dy"])
+def test_wgrad_rows_without_a_source_add_nothing_whatever_the_other_holds(gather, ckpt, dtype):
+    import combine_grouped_gemm_amd as m
+    counts, N, M, K, T = [70, 3], 72, 136, 2, 9
+    src = _routed(counts, T, K, 73, 4)
+    src[5], src[66], src[71] = -1, -1, 2**31 - 1
+    keep = [r for r in range(73) if r not in (5, 66, 71)]
+    dy = _values(T if gather == "dy" else 73, N, 1, dtype)
+    x, xs = _codes(T if gather == "x" else 73, M, 2) if ckpt else (_values(T if gather == "x" else 73, M, 2, dtype), None)
+    for r in (5, 66, 71):
+        if gather == "x":
+            dy[r] = float("nan")
+        elif ckpt:
+            xs[r] = float("nan")
+        else:
+            x[r] = float("inf")
+    kw = dict(gather=gather, slots_per_token=K, dw_dtype=torch.float32)
+    got = m.moe_ffn_wgrad(dy, x, _offsets(counts), x_scales=xs, src_of=src, **kw)
+    assert bool(torch.isfinite(got).all())
+    xv = (_decoded(x, xs) if ckpt else x.double()).cpu()
+    d, tok = dy.double().cpu(), (src.long() // K).cpu()
+    for j, rows in enumerate(([r for r in keep if r < 70], [r for r in keep if r >= 70])):
+        p, q = (d[tok[rows]], xv[rows]) if gather == "dy" else (d[rows], xv[tok[rows]])
+        ref, mag = p.t() @ q, p.abs().t() @ q.abs()
+        _near(got[j].cpu(), ref, 2.0**-24 * ref.abs() + (len(rows) + 1) * 2.0**-23 * mag, f"expert {j}")
+
+
 def test_wgrad_of_a_nan_stays_with_its_expert_and_column():
     import combine_grouped_gemm_amd as m
     counts = [40, 50, 3]
