@@ -276,14 +276,17 @@ bool apart(const void* a, size_t na, const void* b, size_t nb) {
     return !p || !q || p + na <= q || q + nb <= p;
 }
 
+// (columns are counted in ints, a tile's last ones past the end too)
+constexpr int kTrainCols = 1 << 24;
+
 // checkpoints of rows: x to q and scales, or back
 moe_status_t checkpoint(void* x, moe_dtype_t x_dt, const int32_t* offsets, int E_local, int cap_rows, int cols,
                         int8_t* q, float* scales, bool write, hipStream_t stream) {
     if (x_dt != MOE_F32 && x_dt != MOE_BF16)
         return fail(MOE_ERR_UNSUPPORTED, "unsupported %s %d", write ? "x_dt" : "out_dt", x_dt);
     REQUIRE(cap_rows >= 0, "cap_rows must be >= 0");
-    REQUIRE(cols >= 8 && cols % 8 == 0 && cols <= (1 << 24), "cols must be a positive multiple of 8, at most %d (got %d)",
-            1 << 24, cols);
+    REQUIRE(cols >= 8 && cols % 8 == 0 && cols <= kTrainCols, "cols must be a positive multiple of 8, at most %d (got %d)",
+            kTrainCols, cols);
     if (offsets) REQUIRE(E_local >= 1 && E_local <= 1024, "E_local must be in [1, 1024] (got %d)", E_local);
     if (cap_rows > 0) {
         REQUIRE(x && q && scales, "null %s, q or scales pointer", write ? "x" : "out");
@@ -717,10 +720,16 @@ moe_status_t moe_ffn_gate_up_train(const void* xd, const int32_t* offsets, int E
     if (s != MOE_OK) return s;
     s = check_ffn_common(xd, Rows{offsets, nullptr, 0}, E_local, cap_rows, H, I, act_dt, wt.dt);
     if (s != MOE_OK) return s;
+    REQUIRE(H <= kTrainCols && I <= kTrainCols, "H and I must be at most %d (got H=%d, I=%d)", kTrainCols, H, I);
     REQUIRE(w_gate && w_up, "null weight pointer");
     REQUIRE((h && gate_q && gate_scales && up_q && up_scales) || cap_rows == 0, "null h or checkpoint pointer");
     REQUIRE(aligned16(w_gate) && aligned16(w_up) && aligned16(h) && aligned16(gate_q) && aligned16(up_q),
             "weights, h and codes must be 16-byte aligned");
+    const size_t n = (size_t)cap_rows * I, esz = elem_size(act_dt);
+    REQUIRE(apart(h, n * esz, gate_q, n) && apart(h, n * esz, up_q, n) && apart(gate_q, n, up_q, n) &&
+                apart(h, n * esz, xd, (size_t)cap_rows * H * esz) && apart(gate_q, n, xd, (size_t)cap_rows * H * esz) &&
+                apart(up_q, n, xd, (size_t)cap_rows * H * esz),
+            "h and the codes must overlap neither each other nor xd");
     auto f = ffn_args(xd, nullptr, Rows{offsets, nullptr, 0}, E_local, cap_rows, H, I, w_gate, w_up, nullptr, nullptr,
                       h, nullptr, expected_rows, wt.dt, weight_ld(wt, H));
     f.gate_q = gate_q;
@@ -741,7 +750,7 @@ moe_status_t moe_swiglu_backward(const void* dh, moe_dtype_t act_dt, const int8_
     REQUIRE(B >= 0 && K >= 1 && K <= 1024, "need B >= 0 and 1 <= K <= 1024");
     REQUIRE((long long)B * K <= 0x7fffffffLL, "B*K must fit in int32");
     REQUIRE(cap_rows >= 0, "cap_rows must be >= 0");
-    REQUIRE(I >= 8 && I % 8 == 0 && I <= (1 << 24), "I must be a positive multiple of 8, at most %d (got %d)", 1 << 24, I);
+    REQUIRE(I >= 8 && I % 8 == 0 && I <= kTrainCols, "I must be a positive multiple of 8, at most %d (got %d)", kTrainCols, I);
     if (cap_rows > 0) {
         REQUIRE(dh && gate_q && gate_scales && up_q && up_scales && dgate && dup && hw, "null pointer argument");
         REQUIRE(aligned16(dh) && aligned16(gate_q) && aligned16(up_q) && aligned16(dgate) && aligned16(dup) &&
@@ -785,6 +794,8 @@ moe_status_t moe_ffn_dgrad(const void* dy, const void* dy2, const int32_t* src_o
     REQUIRE(w && (dx || cap_rows == 0), "null weight or dx pointer");
     s = check_ffn_common(dx, Rows{offsets, nullptr, 0}, E_local, cap_rows, out_dim, in_dim, act_dt, wt.dt, false);
     if (s != MOE_OK) return s;
+    REQUIRE(out_dim <= kTrainCols && in_dim <= kTrainCols, "out_dim and in_dim must be at most %d (got %d, %d)", kTrainCols,
+            out_dim, in_dim);
     // a buffer of no rows may be null; where src_of names none of no rows, every row of dx is zero
     const bool none = cap_rows == 0 || (src_of && src_rows == 0);
     REQUIRE(dy || none, "null dy");
@@ -826,6 +837,8 @@ moe_status_t moe_ffn_wgrad(const void* dy, const void* dy2, const void* x, moe_d
     REQUIRE(dw, "null dw");
     s = check_ffn_common(dw, Rows{offsets, nullptr, 0}, E_local, cap_rows, out_dim, in_dim, act_dt, act_dt, false);
     if (s != MOE_OK) return s;
+    REQUIRE(out_dim <= kTrainCols && in_dim <= kTrainCols, "out_dim and in_dim must be at most %d (got %d, %d)", kTrainCols,
+            out_dim, in_dim);
     const bool none = dy_rows == 0 || x_rows == 0;
     REQUIRE((dy && x) || none, "null dy or x");
     REQUIRE((dw2 != nullptr) == (dy2 != nullptr) || none, "dy2 and dw2 come together");
@@ -870,7 +883,7 @@ moe_status_t moe_ffn_wgrad(const void* dy, const void* dy2, const void* x, moe_d
     a.dw[0] = dw;
     a.dw[1] = dw2;
     a.dw_f32 = dw_dt == MOE_F32;
-    a.rows_hint = expected_rows > 0 ? expected_rows : cap_rows / E_local;
+    (void)expected_rows;        // the kernel is chosen by the size of dw
     return launched(act_dt == MOE_F32 ? moeep::launch_wgrad_f32(a, stream) : moeep::launch_wgrad_bf16(a, stream),
                     "moe_ffn_wgrad");
 }

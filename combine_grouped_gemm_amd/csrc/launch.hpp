@@ -171,7 +171,6 @@ struct WgradArgs {
     const void* base[2];      // (E_loc, N, M) or null; may be dw itself
     void* dw[2];
     bool dw_f32;
-    int rows_hint;
 };
 hipError_t launch_wgrad_f32(const WgradArgs& a, hipStream_t stream);           // grad_f32.hip
 hipError_t launch_wgrad_bf16(const WgradArgs& a, hipStream_t stream);          // wgrad_bf16.hip

@@ -492,11 +492,12 @@ moe_status_t moe_combine(const void* y, moe_dtype_t y_dt, int cap_rows, const in
  * <dh[row], h[row]>.  What is kept from the forward pass is the routing, x (B, H)
  * and the gate and up products of every row, the last three as 8-bit checkpoints.
  * Sums are held in fp32; each result is rounded once to its type.  Results do not
- * depend on expected_rows beyond the order of fp32 sums, and are the same from
- * run to run.
+ * depend on expected_rows beyond the order of fp32 sums (moe_ffn_wgrad's not at all),
+ * and are the same from run to run.  Columns of any operand: a multiple of 8, at most
+ * 2^24.
  *
  * moe_checkpoint_rows -- an 8-bit checkpoint (MOE_CKPT8) of the rows of x.
- *   x       (cap_rows, cols) F32 or BF16; cols a multiple of 8, at most 2^24.
+ *   x       (cap_rows, cols) F32 or BF16.
  *   Valid rows: as in moe_quant_rows (offsets NULL: all).  Other rows of q and
  *   scales are not written.
  *   q       (cap_rows, cols) int8 out, 8-byte aligned, not overlapping x.
@@ -518,7 +519,7 @@ moe_status_t moe_checkpoint_values(const int8_t* q, const float* scales, const i
  * MOE_W_PACKED) that also leaves g and u, before SwiGLU, as 8-bit checkpoints
  * taken from their fp32 sums:
  *   gate_q, up_q (cap_rows, I) int8, gate_scales, up_scales (cap_rows,
- *   ceil(I/128)) fp32 out.
+ *   ceil(I/128)) fp32 out.  h and the codes overlap neither each other nor xd.
  * Rows past offsets[E_local] of the outputs are not written.
  */
 moe_status_t moe_ffn_gate_up_train(const void* xd, const int32_t* offsets, int E_local, int cap_rows, int H, int I,
@@ -532,8 +533,8 @@ moe_status_t moe_ffn_gate_up_train(const void* xd, const int32_t* offsets, int E
  * topk_w[t,k], sg = 1 / (1 + exp(-g)) and h = g sg u:
  *   dgate[r] = w dh[r] u sg (1 + g (1 - sg)),  dup[r] = w dh[r] g sg,
  *   hw[r] = w h,  dtopk_w[t,k] = sum_i dh[r,i] h_i.
- *   dh (cap_rows, I), dgate, dup, hw (cap_rows, I) of act_dt (F32 or BF16; I a multiple of 8, at most 2^24), the
- *   outputs overlapping neither each other nor the inputs; row_of, topk_w, dtopk_w
+ *   dh (cap_rows, I), dgate, dup, hw (cap_rows, I) of act_dt, the outputs
+ *   overlapping neither each other nor dh and the codes; row_of, topk_w, dtopk_w
  *   (B, K).
  * Slots whose row lies outside [0, cap_rows) get dtopk_w 0; rows that no slot
  * names are not written.  Two slots must not name one row.

@@ -51,7 +51,7 @@ def test_checkpoints_of_no_rows_are_noops():
     assert values(x=NONE, q=NONE, s=NONE, cap=0) == m.MOE_OK
 
 
-def gate_up(xd=P, off=P, E=4, cap=8, H=64, I=64, dt=BF16, wg=P, wu=P, w_dt=None, h=Q, gq=Q, gs=Q, uq=Q, us=Q):
+def gate_up(xd=P, off=P, E=4, cap=8, H=64, I=64, dt=BF16, wg=P, wu=P, w_dt=None, h=Q, gq=V(1 << 31), gs=Q, uq=V(1 << 32), us=Q):
     return m.lib().moe_ffn_gate_up_train(xd, off, E, cap, H, I, dt, wg, wu, dt if w_dt is None else w_dt, h, gq, gs, uq,
                                          us, 0, None)
 
@@ -61,7 +61,9 @@ BAD_GATE_UP = [
     (dict(off=NONE), ARG, "null"), (dict(E=0), ARG, "E_local"), (dict(cap=-1), ARG, "cap_rows"), (dict(H=60), ARG, "multiples of 8"),
     (dict(I=0), ARG, "multiples of 8"), (dict(xd=NONE), ARG, "null"), (dict(wg=NONE), ARG, "null"), (dict(wu=NONE), ARG, "null"),
     (dict(h=NONE), ARG, "null"), (dict(gq=NONE), ARG, "null"), (dict(us=NONE), ARG, "null"), (dict(xd=HALF8), ARG, "16-byte"),
-    (dict(uq=HALF8), ARG, "16-byte"), (dict(h=ODD), ARG, "16-byte"),
+    (dict(uq=HALF8), ARG, "16-byte"), (dict(h=ODD), ARG, "16-byte"), (dict(H=(1 << 24) + 8), ARG, "at most"),
+    (dict(I=(1 << 24) + 8, cap=1), ARG, "at most"), (dict(h=P), ARG, "overlap"), (dict(gq=V((1 << 30) + 1008)), ARG, "overlap"),
+    (dict(uq=V((1 << 31) + 496)), ARG, "overlap"), (dict(uq=P), ARG, "overlap"),
 ]
 
 
@@ -103,7 +105,8 @@ BAD_DGRAD = [
     (dict(M=100), ARG, "multiples of 8"), (dict(dy=NONE), ARG, "null dy"), (dict(dy2=NONE), ARG, "together"),
     (dict(w2=NONE), ARG, "together"), (dict(w=NONE), ARG, "null"), (dict(dx=NONE), ARG, "null"), (dict(dx=HALF8), ARG, "16-byte"),
     (dict(w2=HALF8), ARG, "16-byte"), (dict(dx=P), ARG, "overlap"), (dict(dx=V((1 << 20) + 1008)), ARG, "overlap"),
-    (dict(cap=2**31 - 1, M=1 << 20), ARG, "too large"),
+    (dict(cap=2**31 - 1, M=1 << 20), ARG, "too large"), (dict(N=(1 << 24) + 8), ARG, "at most"),
+    (dict(M=(1 << 24) + 8), ARG, "at most"),
 ]
 
 
@@ -133,7 +136,7 @@ BAD_WGRAD = [
     (dict(dw=NONE), ARG, "null dw"), (dict(dw2=NONE), ARG, "together"), (dict(dy2=NONE), ARG, "together"),
     (dict(x_dt=m.MOE_CKPT8), ARG, "scales"), (dict(dw2=NONE, dy2=NONE, base2=P), ARG, "base2"), (dict(dw=HALF8), ARG, "16-byte"),
     (dict(x=HALF8), ARG, "16-byte"), (dict(dw2=Q), ARG, "overlap"), (dict(dw2=V((1 << 30) + DW - 16)), ARG, "overlap"),
-    (dict(base=V((1 << 30) + 16)), ARG, "base"), (dict(base=Q, base2=Q), ARG, "base"), (dict(base=S), ARG, "base"), (dict(base2=Q), ARG, "base"), (dict(dw=P), ARG, "overlap"),
+    (dict(N=(1 << 24) + 8), ARG, "at most"), (dict(M=(1 << 24) + 8), ARG, "at most"), (dict(base=V((1 << 30) + 16)), ARG, "base"), (dict(base=Q, base2=Q), ARG, "base"), (dict(base=S), ARG, "base"), (dict(base2=Q), ARG, "base"), (dict(dw=P), ARG, "overlap"),
 ]
 
 
