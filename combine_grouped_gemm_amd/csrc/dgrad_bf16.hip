@@ -14,6 +14,8 @@ namespace {
 
 using namespace cols;
 
+#define INLINE __attribute__((always_inline))
+
 // row of dy that expert row r reads (-1: none)
 __device__ __forceinline__ int dy_row(const FfnArgs& p, int r) {
     if (p.src_of == nullptr) return r;
@@ -23,36 +25,57 @@ __device__ __forceinline__ int dy_row(const FfnArgs& p, int r) {
     return t < p.src_rows ? t : -1;
 }
 
-// ---- row-rich experts: 8 waves 2 (rows) x 4 (columns), tiles of up to BM rows by 256
-// columns, two-stage ring.  Tiles of at most 256 rows keep both halves' weight fragments
-// of a step in registers and so release its weight stage to step k + 2 at once; 320-row
-// tiles release it half-way (gemm_wide.hpp has the reasons and what they measured).
-template <int BM>
+// ---- 8 waves 2 (rows) x 4 (columns), tiles of up to 320 rows by 256 columns.  A ring of
+// 64-row stages of the contraction; how deep is a matter of the tile's rows, for the LDS is
+// shared out in blocks of 64 rows of dy (8 KB), ten of them, and two stages of weights:
+//   193 to 320 rows  two row stages of five blocks, rows issued one step ahead
+//   129 to 192       three of three, rows two steps ahead
+//   up to 128        three of two, and the last four blocks are a third weight stage
+// Weights are issued as many steps ahead as they have stages (of tiles of more than 192 rows
+// the next ones only half-way through the step): up to 192 rows a wave holds both halves'
+// fragments of a step in registers, so that the stage is free before the step's matrix
+// instructions.
+// What bounds it, 32 experts of 7168 x 2048 (256 tiles, one a CU): up to 128 rows each the
+// stream of weights (16 rows 141 us, 128 rows 151: 6.7 and 6.2 TB/s; with two stages of each 150
+// and 160); from 192 rows on the matrix instructions beside it (256 rows 208 us, 1.15 PFLOP/s;
+// 640 rows 460 us, 1.31); of ragged experts the rounds that tiles of unlike cost do not fill (a
+// rank with 26 to 1131 rows an expert, 336 to 400 tiles: 300 us).  A pair at 2880 x 2880, 128
+// experts of 128 rows on average: 888 us, with two stages 980.
+constexpr int kBM = 320;
+
+// A tile's plan: MODE 0, 1, 2 as above with the row fragments NF of a wave
+template <int MODE>
+struct Plan {
+    static constexpr int A_ITERS = MODE == 0 ? 2 : MODE == 1 ? 3 : 5;    // 64-row blocks of a stage
+    static constexpr int AST = MODE == 2 ? 2 : 3, BST = MODE == 0 ? 3 : 2;
+    static constexpr int DA = AST - 1, DB = BST;                         // steps ahead that are issued
+    static constexpr int UNROLL = MODE == 0 ? 3 : MODE == 1 ? 6 : 2;
+    static constexpr bool LOOK = MODE < 2;
+};
+
 __global__ __launch_bounds__(512, 1) void dgrad_wide_kernel(FfnArgs p) {
     constexpr int WMW = 2, WNW = 4, NT = 512, NW = 8;
-    constexpr int A_ITERS = BM * CPR / 64 / NW;      // row loads of a wave per stage
+    constexpr int A_MAX = kBM / 64;                  // row loads of a wave per stage: 8 rows each
     constexpr int B_ITERS = BK * BN * 2 / 1024 / NW; // weight loads: 1 KiB is two rows of 256 columns
-    constexpr int LPS = A_ITERS + B_ITERS;
-    constexpr int FM = BM / 16 / WMW, FN = BN / WNW / 16;
-    constexpr bool LOOK = BM <= 256;
-    static_assert(BM % 64 == 0 && B_ITERS == 4 && FN == 4, "tile shape");
+    constexpr int FN = BN / WNW / 16;
+    constexpr int BLK = 64 * ROWB;                   // a block of 64 rows
+    static_assert(B_ITERS == 4 && FN == 4 && BLK == 8192, "tile shape");
 
-    __shared__ uint4 sa0[BM * CPR];
-    __shared__ uint4 sb0[BK * BN / 8];
-    __shared__ uint4 sa1[BM * CPR];
-    __shared__ uint4 sb1[BK * BN / 8];
+    // each block and stage an object of its own: the compiler sees that reads of one do not
+    // depend on the loads in flight into the others
+    __shared__ uint4 s_b0[BK * BN / 8], s_b1[BK * BN / 8];
+    __shared__ uint4 s_r0[BLK / 16], s_r1[BLK / 16], s_r2[BLK / 16], s_r3[BLK / 16], s_r4[BLK / 16], s_r5[BLK / 16];
+    __shared__ uint4 s_r6[4 * BLK / 16];             // blocks 6 to 9, or the third weight stage
     __shared__ int s_pre[kMaxExperts + 1];
     __shared__ uint16_t s_ord[kMaxExperts];
-    static_assert(sizeof(sa0) >= kMaxExperts * sizeof(int), "row counts fit in the first row stage");
+    static_assert(sizeof(s_b0) >= kMaxExperts * sizeof(int), "row counts fit in the first weight stage");
+    static_assert(sizeof(s_r6) == sizeof(s_b0), "a weight stage");
     __shared__ int s_tmp[NT / kWave];
 
-    auto a_base = [&](auto I) -> char* {
-        if constexpr (decltype(I)::value == 0) return reinterpret_cast<char*>(sa0);
-        else return reinterpret_cast<char*>(sa1);
-    };
-    auto b_base = [&](auto I) -> char* {
-        if constexpr (decltype(I)::value == 0) return reinterpret_cast<char*>(sb0);
-        else return reinterpret_cast<char*>(sb1);
+    auto block = [&](int b) INLINE -> char* {
+        uint4* q = b == 0 ? s_r0 : b == 1 ? s_r1 : b == 2 ? s_r2 : b == 3 ? s_r3 : b == 4 ? s_r4 : b == 5 ? s_r5
+                   : s_r6 + (b - 6) * (BLK / 16);
+        return reinterpret_cast<char*>(q);
     };
 
     const int tid = threadIdx.x, lane = tid % kWave;
@@ -62,17 +85,16 @@ __global__ __launch_bounds__(512, 1) void dgrad_wide_kernel(FfnArgs p) {
     const int nk1 = (Kdim + BK - 1) / BK, nk = p.a2 != nullptr ? 2 * nk1 : nk1;
     const int lane_k = swz(lane / 8, lane % 8) * 8;
 
-    build_tile_prefix_sorted<NT, BM, true>(p, s_pre, s_ord, reinterpret_cast<int*>(sa0), s_tmp);
+    build_tile_prefix_sorted<NT, kBM, true>(p, s_pre, s_ord, reinterpret_cast<int*>(s_b0), s_tmp);
     const int n_tiles_n = (N + BN - 1) / BN;
-    const int total = n_tiles_n * s_pre[p.E_loc];
+    const int total = __builtin_amdgcn_readfirstlane(n_tiles_n * s_pre[p.E_loc]);
     const int G = gridDim.x;
-    const int v = xcd_block_order();
-    uint16_t* __restrict__ Out = static_cast<uint16_t*>(p.out);
+    const int v = total <= G ? xcd_chunk_order() : xcd_block_order();
 
     for (int rnd = 0; rnd * (long long)G < total; ++rnd) {
         const int tau = round_tile_back(rnd, v, G, total);
         if (tau < 0) continue;                           // (an odd last round fills from the other end)
-        const TileCoord tc = decode_tile<BM>(tau, n_tiles_n, s_pre, p, s_ord);
+        const TileCoord tc = decode_tile<kBM>(tau, n_tiles_n, s_pre, p, s_ord);
         const int j = tc.j, row0 = tc.row0, nvalid = tc.nvalid;
         const int col0 = tc.nt * BN;
 
@@ -87,86 +109,109 @@ __global__ __launch_bounds__(512, 1) void dgrad_wide_kernel(FfnArgs p) {
         const uint32_t a_bytes = (uint32_t)(p.src_of != nullptr ? p.src_rows : nvalid) * (uint32_t)(Kdim * 2);
         const char* wbase[2] = {reinterpret_cast<const char*>(static_cast<const uint16_t*>(p.w0) + (size_t)j * Kdim * ldw),
                                 reinterpret_cast<const char*>(static_cast<const uint16_t*>(p.w1) + (size_t)j * Kdim * ldw)};
-        uint32_t off[LPS];
+        uint32_t aoff[A_MAX], boff[B_ITERS];
 #pragma unroll
-        for (int i = 0; i < LPS; ++i) {
-            if (i < A_ITERS) {
-                const int r = (i * NW + wave) * 8 + lane / 8;
-                int q = -1;
-                if (r < nvalid) q = p.src_of != nullptr ? dy_row(p, row0 + r) : r;
-                off[i] = q >= 0 ? (uint32_t)q * (uint32_t)(Kdim * 2) + (uint32_t)swz(r, lane % 8) * 16 : kOutOfRange;
-            } else {
-                const int k = ((i - A_ITERS) * NW + wave) * 2 + lane / 32;
-                const int c = (lane % 32) ^ swz_row<BN>(k);
-                off[i] = col0 + c * 8 < N ? (uint32_t)k * (uint32_t)(ldw * 2) + (uint32_t)(col0 + c * 8) * 2 : kOutOfRange;
-            }
+        for (int i = 0; i < A_MAX; ++i) {
+            const int r = (i * NW + wave) * 8 + lane / 8;
+            int q = -1;
+            if (r < nvalid) q = p.src_of != nullptr ? dy_row(p, row0 + r) : r;
+            aoff[i] = q >= 0 ? (uint32_t)q * (uint32_t)(Kdim * 2) + (uint32_t)swz(r, lane % 8) * 16 : kOutOfRange;
         }
-        auto issue_one = [&](auto I, int i, int kstep, bool live) {
-            const bool is_a = i < A_ITERS;
-            const bool second = kstep >= nk1;
-            const int ks = second ? kstep - nk1 : kstep;
-            if (is_a) {
-                const rsrc_t r = make_rsrc(second ? abase[1] : abase[0], live ? a_bytes : 0u);
-                const uint32_t vo = ks * BK + lane_k < Kdim ? off[i] : kOutOfRange;
-                lds_buf16<0>(r, a_base(I) + (i * NW + wave) * 1024, vo, ks * BK * 2);
-            } else {
-                const int left = Kdim - ks * BK < BK ? Kdim - ks * BK : BK;
-                const rsrc_t r = make_rsrc((second ? wbase[1] : wbase[0]) + (size_t)ks * BK * ldw * 2,
-                                           live ? (uint32_t)left * (uint32_t)(ldw * 2) : 0u);
-                lds_buf16<kNonTemporal>(r, b_base(I) + ((i - A_ITERS) * NW + wave) * 1024, off[i], 0);
-            }
-        };
+#pragma unroll
+        for (int i = 0; i < B_ITERS; ++i) {
+            const int k = (i * NW + wave) * 2 + lane / 32;
+            const int c = (lane % 32) ^ swz_row<BN>(k);
+            boff[i] = col0 + c * 8 < N ? (uint32_t)k * (uint32_t)(ldw * 2) + (uint32_t)(col0 + c * 8) * 2 : kOutOfRange;
+        }
 
         int lds_lane[2];
 #pragma unroll
         for (int kk = 0; kk < 2; ++kk)
-            lds_lane[kk] = (lane & 15) * ROWB + (((kk * 4 + (lane >> 4)) ^ (lane & 7)) * 16);
+            lds_lane[kk] = (wm * 16 + (lane & 15)) * ROWB + (((kk * 4 + (lane >> 4)) ^ (lane & 7)) * 16);
         uint32_t wfrag[FN];
 #pragma unroll
         for (int f = 0; f < FN; ++f) wfrag[f] = frag_offset<BN>(lane, wn * (FN * 16) + f * 16);
 
-        const int nf = __builtin_amdgcn_readfirstlane(
-            nvalid > wm * 16 ? min(FM, (nvalid - wm * 16 + 31) / 32) : 0);
-
-        // the previous tile's reads of both stages must be complete before new loads land
+        // the previous tile's reads of every stage must be complete before new loads land
         wait_lgkm0();
         block_barrier();
-#pragma unroll
-        for (int i = 0; i < LPS; ++i) issue_one(ic<0>{}, i, 0, true);
-        {
-            const bool l1 = __builtin_amdgcn_readfirstlane(nk > 1 ? 1 : 0) != 0;
-#pragma unroll
-            for (int i = A_ITERS; i < LPS; ++i) issue_one(ic<1>{}, i, 1, l1);
-        }
 
-        auto tile = [&](auto NFc) {
-            constexpr int NF = decltype(NFc)::value;
+        auto tile = [&](auto NFc, auto MODEc) INLINE {
+            constexpr int NF = decltype(NFc)::value, MODE = decltype(MODEc)::value;
+            using P = Plan<MODE>;
+            constexpr int A_ITERS = P::A_ITERS, LPS = A_ITERS + B_ITERS;
+            // step k's stages, by its index in the unrolled loop: row fragment i's, and the weights'
+            auto a_block = [&](auto I, int b) INLINE { return block(decltype(I)::value % P::AST * A_ITERS + b); };
+            auto b_base = [&](auto I) INLINE -> char* {
+                constexpr int s = decltype(I)::value % P::BST;
+                return reinterpret_cast<char*>(s == 0 ? s_b0 : s == 1 ? s_b1 : s_r6);
+            };
+            auto issue_a = [&](auto I, int i, int kstep, bool live) INLINE {
+                const bool second = kstep >= nk1;
+                const int ks = second ? kstep - nk1 : kstep;
+                const rsrc_t r = make_rsrc(second ? abase[1] : abase[0], live ? a_bytes : 0u);
+                const uint32_t vo = ks * BK + lane_k < Kdim ? aoff[i] : kOutOfRange;
+                lds_buf16<0>(r, a_block(I, i) + wave * 1024, vo, ks * BK * 2);
+            };
+            auto issue_b = [&](auto I, int i, int kstep, bool live) INLINE {
+                const bool second = kstep >= nk1;
+                const int ks = second ? kstep - nk1 : kstep;
+                const int left = Kdim - ks * BK < BK ? Kdim - ks * BK : BK;
+                const rsrc_t r = make_rsrc((second ? wbase[1] : wbase[0]) + (size_t)ks * BK * ldw * 2,
+                                           live ? (uint32_t)left * (uint32_t)(ldw * 2) : 0u);
+                lds_buf16<kNonTemporal>(r, b_base(I) + (i * NW + wave) * 1024, boff[i], 0);
+            };
+            auto live_step = [&](int k) INLINE { return __builtin_amdgcn_readfirstlane(k < nk ? 1 : 0) != 0; };
+            auto first_step = [&](auto I) INLINE {
+                constexpr int k = decltype(I)::value;
+                const bool live = live_step(k);
+                if constexpr (k < P::DA) {
+#pragma unroll
+                    for (int i = 0; i < A_ITERS; ++i) issue_a(I, i, k, live);
+                }
+                if constexpr (k < P::DB) {
+#pragma unroll
+                    for (int i = 0; i < B_ITERS; ++i) issue_b(I, i, k, live);
+                }
+            };
+            first_step(ic<0>{});
+            first_step(ic<1>{});
+            first_step(ic<2>{});
+
+            // the weights are the matrix instructions' row operand: a lane's four results are
+            // neighbouring columns of row l % 16
             floatx4 acc[NF > 0 ? NF : 1][FN];
 #pragma unroll
             for (int i = 0; i < NF; ++i)
 #pragma unroll
                 for (int f = 0; f < FN; ++f) acc[i][f] = floatx4{0.f, 0.f, 0.f, 0.f};
 
-            auto compute = [&](auto I, int k, bool liveA, bool liveB) {
-                const char* ab = a_base(I);
+            auto step = [&](auto I, int k) INLINE {
+                // rows and weights of step k were issued DA and DB steps ago, rows first
+                wait_vmcnt<(P::DA - 1) * LPS + (P::DB > P::DA ? B_ITERS : 0)>();
+                wait_lgkm0();
+                block_barrier();
+                const bool liveA = live_step(k + P::DA), liveB = live_step(k + P::DB);
+                auto issue_slot = [&](int q) INLINE {
+                    if (q < A_ITERS) issue_a(ic<decltype(I)::value + P::DA>{}, q, k + P::DA, liveA);
+                    else issue_b(I, q - A_ITERS, k + P::DB, liveB);
+                };
+                auto row_frag = [&](int kk, int i) INLINE {
+                    return *reinterpret_cast<const bf16x8*>(a_block(I, i / 2) + (i & 1) * (WMW * 16 * ROWB) + lds_lane[kk]);
+                };
                 const uint32_t bb = lds_addr(b_base(I));
-                constexpr auto nextbuf = ic<1 - decltype(I)::value>{};
                 uint32_t ad[FN];
 #pragma unroll
                 for (int f = 0; f < FN; ++f) ad[f] = bb + wfrag[f];
                 bf16x8 bfr[2][FN];
-                if constexpr (LOOK) {
+                if constexpr (P::LOOK) {
                     read_frags<BN, 0>(bfr[0], ad);
                     read_frags<BN, 1>(bfr[1], ad);
                     block_barrier();                     // every wave holds this step's weight fragments
                 }
-                auto issue_slot = [&](int q) {
-                    if (q < A_ITERS) issue_one(nextbuf, q, k + 1, liveA);
-                    else issue_one(I, q, k + 2, liveB);
-                };
 #pragma unroll
                 for (int kk = 0; kk < 2; ++kk) {
-                    if constexpr (!LOOK) {
+                    if constexpr (!P::LOOK) {
                         if (kk == 0) read_frags<BN, 0>(bfr[0], ad);
                         else {
                             read_frags<BN, 1>(bfr[1], ad);
@@ -174,17 +219,15 @@ __global__ __launch_bounds__(512, 1) void dgrad_wide_kernel(FfnArgs p) {
                         }
                     }
                     bf16x8 acur;
-                    if (NF > 0) acur = *reinterpret_cast<const bf16x8*>(ab + lds_lane[kk] + wm * 16 * ROWB);
+                    if (NF > 0) acur = row_frag(kk, 0);
 #pragma unroll
                     for (int i = 0; i < NF; ++i) {
                         bf16x8 anext;
-                        if (i + 1 < NF)
-                            anext = *reinterpret_cast<const bf16x8*>(
-                                ab + lds_lane[kk] + (wm + WMW * (i + 1)) * 16 * ROWB);
+                        if (i + 1 < NF) anext = row_frag(kk, i + 1);
 #pragma unroll
                         for (int f = 0; f < FN; ++f)
-                            acc[i][f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(acur, bfr[kk][f], acc[i][f], 0, 0, 0);
-                        if constexpr (LOOK) {
+                            acc[i][f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(bfr[kk][f], acur, acc[i][f], 0, 0, 0);
+                        if constexpr (P::LOOK) {
                             const int slot = kk * NF + i;
                             if (slot < LPS) issue_slot(slot);
                         } else {
@@ -194,91 +237,73 @@ __global__ __launch_bounds__(512, 1) void dgrad_wide_kernel(FfnArgs p) {
                         if (i + 1 < NF) acur = anext;
                         __builtin_amdgcn_sched_barrier(0);
                     }
-                    if constexpr (!LOOK) {
-                        if (kk == 0) {
-#pragma unroll
-                            for (int q = NF; q < A_ITERS; ++q) issue_slot(q);
-                        } else {
-#pragma unroll
-                            for (int q = NF; q < B_ITERS; ++q) issue_slot(A_ITERS + q);
-                        }
-                    }
                 }
-                if constexpr (LOOK) {
+                if constexpr (P::LOOK) {
 #pragma unroll
                     for (int q = 2 * NF; q < LPS; ++q) issue_slot(q);
+                } else {
+                    static_assert(NF >= A_ITERS && NF >= B_ITERS, "a slot for every load");
                 }
             };
-            auto step = [&](auto I, int k) {
-                wait_vmcnt<B_ITERS>();
-                wait_lgkm0();
-                block_barrier();
-                const bool l1 = __builtin_amdgcn_readfirstlane(k + 1 < nk ? 1 : 0) != 0;
-                const bool l2 = __builtin_amdgcn_readfirstlane(k + 2 < nk ? 1 : 0) != 0;
-                compute(I, k, l1, l2);
-            };
-            for (int k = 0; k < nk; k += 2) {
+            for (int k = 0; k < nk; k += P::UNROLL) {
                 step(ic<0>{}, k);
                 if (k + 1 < nk) step(ic<1>{}, k + 1);
-            }
-            wait_vmcnt<0>();                             // the last step's loads read nothing but count
-
-            // epilogue: PF fragments at a time through a private LDS region, out in 16-byte chunks
-            constexpr int OCOLS = FN * 16, OCH = OCOLS / 8, OPITCH = OCOLS * 2 + 16, PF = 5;
-            constexpr int RSZ = PF * 16 * OPITCH, RPI = 64 / OCH;
-            static_assert(2 * RSZ <= BK * BN * 2 && 2 * RSZ <= BM * ROWB, "two regions per stage buffer");
-            wait_lgkm0();
-            block_barrier();
-            char* region = (wave < 2 ? reinterpret_cast<char*>(sa0) : wave < 4 ? reinterpret_cast<char*>(sb0)
-                            : wave < 6 ? reinterpret_cast<char*>(sa1) : reinterpret_cast<char*>(sb1)) + (wave & 1) * RSZ;
-            const int colbase = col0 + wn * OCOLS;
-            char* out_bytes = reinterpret_cast<char*>(Out);
-#pragma unroll
-            for (int p0 = 0; p0 < NF; p0 += PF) {
-#pragma unroll
-                for (int ii = 0; ii < PF; ++ii) {
-                    const int i = p0 + ii;
-                    if (i < NF) {
-#pragma unroll
-                        for (int f = 0; f < FN; ++f)
-#pragma unroll
-                            for (int e = 0; e < 4; ++e)
-                                *reinterpret_cast<uint16_t*>(region + (ii * 16 + (lane >> 4) * 4 + e) * OPITCH +
-                                                             (f * 16 + (lane & 15)) * 2) =
-                                    (uint16_t)f32_to_bf16_bits(acc[i][f][e]);
-                    }
+                if constexpr (P::UNROLL > 2) {
+                    if (k + 2 < nk) step(ic<2>{}, k + 2);
                 }
+                if constexpr (P::UNROLL > 3) {
+                    if (k + 3 < nk) step(ic<3>{}, k + 3);
+                    if (k + 4 < nk) step(ic<4>{}, k + 4);
+                    if (k + 5 < nk) step(ic<5>{}, k + 5);
+                }
+            }
+            wait_vmcnt<0>();                             // the last steps' loads read nothing but count
+
+            // out: lanes exchange values so that each holds 16 bytes of a row, 8 lanes a
+            // whole line of the wave's 64 columns
+            int ln = lane;
+            asm volatile("" : "+v"(ln));                 // keeps what depends on it out of the k-loop's registers
+            uint16_t* Out = static_cast<uint16_t*>(p.out) + (size_t)row0 * N;
+            const int col = col0 + wn * (FN * 16) + unit_col(ln);
 #pragma unroll
-                for (int q = 0; q < PF * 16 / RPI; ++q) {
-                    const int lrow = q * RPI + lane / OCH, ch = lane % OCH;
-                    const int i = p0 + lrow / 16;
-                    const int trow = (wm + WMW * i) * 16 + lrow % 16;
-                    const int col = colbase + ch * 8;
-                    if (i < NF && trow < nvalid && col < N)
-                        *reinterpret_cast<uint4*>(out_bytes + ((size_t)(row0 + trow) * N + col) * 2) =
-                            *reinterpret_cast<const uint4*>(region + lrow * OPITCH + ch * 16);
+            for (int i = 0; i < NF; ++i) {
+                uint4 u[2];
+                units_of(acc[i], u);
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int r = (wm + WMW * i) * 16 + h * 8 + (ln & 7);
+                    if (r < nvalid && col < N) *reinterpret_cast<uint4*>(Out + (size_t)r * N + col) = u[h];
                 }
             }
         };
-        static_assert(FM <= 10, "one case per fragment count");
-        switch (nf) {
-            case 0: tile(ic<0>{}); break;
-            case 1: tile(ic<1>{}); break;
-            case 2: tile(ic<2>{}); break;
-            case 3: tile(ic<3>{}); break;
-            case 4: tile(ic<4>{}); break;
-            case 5: tile(ic<5>{}); break;
-            case 6: tile(ic<6>{}); break;
-            case 7: tile(ic<7>{}); break;
-            case 8: tile(ic<8>{}); break;
-            case 9: if constexpr (9 <= FM) tile(ic<9>{}); break;
-            case 10: if constexpr (10 <= FM) tile(ic<10>{}); break;
-            default: break;
+        const int nf = __builtin_amdgcn_readfirstlane(nvalid > wm * 16 ? (nvalid - wm * 16 + 31) / 32 : 0);
+        if (nvalid <= 128) {
+            switch (nf) {
+                case 0: tile(ic<0>{}, ic<0>{}); break;
+                case 1: tile(ic<1>{}, ic<0>{}); break;
+                case 2: tile(ic<2>{}, ic<0>{}); break;
+                case 3: tile(ic<3>{}, ic<0>{}); break;
+                default: tile(ic<4>{}, ic<0>{}); break;
+            }
+        } else if (nvalid <= 192) {
+            switch (nf) {
+                case 4: tile(ic<4>{}, ic<1>{}); break;
+                case 5: tile(ic<5>{}, ic<1>{}); break;
+                default: tile(ic<6>{}, ic<1>{}); break;
+            }
+        } else {
+            switch (nf) {
+                case 6: tile(ic<6>{}, ic<2>{}); break;
+                case 7: tile(ic<7>{}, ic<2>{}); break;
+                case 8: tile(ic<8>{}, ic<2>{}); break;
+                case 9: tile(ic<9>{}, ic<2>{}); break;
+                default: tile(ic<10>{}, ic<2>{}); break;
+            }
         }
     }
 }
 
-// ---- few rows: register-staged tiles of BM rows by 128 columns, as ffn_bf16.hip's
+// ---- register-staged tiles of BM rows by 128 columns, as ffn_bf16.hip's, with 64-bit addresses
 template <int BM, int WMW, int WNW>
 __global__ __launch_bounds__(64 * WMW * WNW) void dgrad_small_kernel(FfnArgs p) {
     constexpr int NT = 64 * WMW * WNW, TW = 128;
@@ -298,7 +323,7 @@ __global__ __launch_bounds__(64 * WMW * WNW) void dgrad_small_kernel(FfnArgs p) 
     build_tile_prefix<NT, BM>(p, s_pre, s_tmp);
     const int n_tiles_n = (N + TW - 1) / TW;
     const int total = n_tiles_n * s_pre[p.E_loc];
-    const int G = gridDim.x, v = xcd_block_order();
+    const int G = gridDim.x, v = total <= G ? xcd_chunk_order() : xcd_block_order();
     uint16_t* __restrict__ Out = static_cast<uint16_t*>(p.out);
     uint32_t wfrag[FN];
 #pragma unroll
@@ -390,10 +415,9 @@ __global__ __launch_bounds__(64 * WMW * WNW) void dgrad_small_kernel(FfnArgs p) 
     }
 }
 
-template <int BM>
 hipError_t launch_wide(const FfnArgs& a, hipStream_t stream) {
     static int per_cu = 0;
-    return launch_persistent(dgrad_wide_kernel<BM>, 512, a, stream, &per_cu);
+    return launch_persistent(dgrad_wide_kernel, 512, a, stream, &per_cu);
 }
 template <int BM, int WMW, int WNW>
 hipError_t launch_small(const FfnArgs& a, hipStream_t stream) {
@@ -409,10 +433,12 @@ hipError_t launch_dgrad_bf16(const FfnArgs& a, hipStream_t stream) {
     const unsigned long long reach = a.src_of != nullptr ? (unsigned long long)a.src_rows : 320;
     const bool wide_ok = (reach * a.Kdim + a.Kdim + 64) * 2 < (1ull << 31) &&
                          (unsigned long long)BK * a.ldw * 2 < (1ull << 31) && (a.src_of == nullptr || a.src_rows > 0);
-    if (wide_ok && a.rows_hint >= 192) return launch_wide<320>(a, stream);
-    if (wide_ok && a.rows_hint >= 64) return launch_wide<256>(a, stream);
-    if (a.rows_hint < 24) return launch_small<16, 1, 2>(a, stream);
-    return launch_small<128, 2, 2>(a, stream);
+    if (!wide_ok) return launch_small<128, 2, 2>(a, stream);
+    // a few rows and a short contraction: several small blocks a CU hide the rings' filling and
+    // the epilogue (64 experts of 2 rows, 512 x 512: 12.8 us, wide 17.3; at 1024 x 1024 they meet,
+    // 32 experts of 4 rows 21.6 and 20.2; 32 of 8 rows, 7168 x 2048: 266 and 144)
+    if (a.rows_hint < 24 && a.Kdim <= 1024) return launch_small<16, 1, 2>(a, stream);
+    return launch_wide(a, stream);
 }
 
 }  // namespace moeep

@@ -96,6 +96,49 @@ __device__ __forceinline__ void read_frags(bf16x8 (&f)[2], const uint32_t (&ad)[
     for (int i = 0; i < 2; ++i) f[i] = join_frag(t[2 * i], t[2 * i + 1]);
 }
 
+// Of two fragments' results (lane n of 16 has row n of each): a becomes rows 0..7 of both, the
+// second's in lanes 8..15, b rows 8..15, the first's in lanes 0..7.
+__device__ __forceinline__ void exchange_rows(float& a, float& b) {
+    const int x = __float_as_int(a), y = __float_as_int(b);
+    constexpr int kRor8 = 0x128;
+    a = __int_as_float(__builtin_amdgcn_update_dpp(x, y, kRor8, 0xf, 0xc, false));
+    b = __int_as_float(__builtin_amdgcn_update_dpp(y, x, kRor8, 0xf, 0x3, false));
+}
+// Of two values of every lane, by groups of 16 lanes: even groups keep a and get the next
+// group's a beside it, odd groups keep b behind the group before's b.
+__device__ __forceinline__ void exchange_groups(float& a, float& b) {
+#if defined(__HIP_DEVICE_COMPILE__)
+    const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(a), __float_as_uint(b), false, false);
+    a = __uint_as_float(r[0]);
+    b = __uint_as_float(r[1]);
+#endif
+}
+
+// 16 rows by 64 columns of a wave (four fragments, the columns as the matrix instructions' row
+// operand) as bf16 in two 16-byte units a lane: unit h is row 8 h + l % 8, columns unit_col(l) ..
+// + 7, so that 8 lanes hold a row's 128 bytes.
+__device__ __forceinline__ int unit_col(int lane) {
+    return ((lane >> 3) & 1) * 16 + ((lane >> 4) & 1) * 32 + (lane >> 5) * 8;
+}
+__device__ __forceinline__ void units_of(const floatx4 (&acc)[4], uint4 (&unit)[2]) {
+    float t[4][4];
+#pragma unroll
+    for (int f = 0; f < 4; f += 2)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            t[f][e] = acc[f][e];
+            t[f + 1][e] = acc[f + 1][e];
+            exchange_rows(t[f][e], t[f + 1][e]);
+        }
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) exchange_groups(t[h][e], t[h + 2][e]);
+        unit[h] = make_uint4(pack_bf16x2(t[h][0], t[h][1]), pack_bf16x2(t[h][2], t[h][3]),
+                             pack_bf16x2(t[h + 2][0], t[h + 2][1]), pack_bf16x2(t[h + 2][2], t[h + 2][3]));
+    }
+}
+
 // quotient of a slot by the slots of a token, exact for slots below 2^31: the host's
 // multiplier and shift (divisor_of in launch.hpp)
 __device__ __forceinline__ int token_of(int slot, const Divisor& d) {

@@ -222,7 +222,7 @@ __global__ __launch_bounds__(512, 1) void grouped_gemm_bf16_wide_kernel(FfnArgs 
     const int n_tiles_n = (N + BNO - 1) / BNO;
     const int total = n_tiles_n * s_pre[p.E_loc];
     const int G = gridDim.x;
-    const int v = xcd_block_order();
+    const int v = CKPT && total <= G ? xcd_chunk_order() : xcd_block_order();
 
     const uint16_t* __restrict__ A = static_cast<const uint16_t*>(p.a);
     const uint16_t* __restrict__ W0 = static_cast<const uint16_t*>(p.w0);

@@ -67,24 +67,6 @@ __device__ __forceinline__ void buf_store16(rsrc_t r, uint32_t off, uint4 v) {
 #endif
 }
 
-// Of two fragments' results (lane n of 16 has row n of each): a becomes rows 0..7 of both, the
-// second's in lanes 8..15, b rows 8..15, the first's in lanes 0..7.
-__device__ __forceinline__ void exchange_rows(float& a, float& b) {
-    const int x = __float_as_int(a), y = __float_as_int(b);
-    constexpr int kRor8 = 0x128;
-    a = __int_as_float(__builtin_amdgcn_update_dpp(x, y, kRor8, 0xf, 0xc, false));
-    b = __int_as_float(__builtin_amdgcn_update_dpp(y, x, kRor8, 0xf, 0x3, false));
-}
-// Of two values of every lane, by groups of 16 lanes: even groups keep a and get the next
-// group's a beside it, odd groups keep b behind the group before's b.
-__device__ __forceinline__ void exchange_groups(float& a, float& b) {
-#if defined(__HIP_DEVICE_COMPILE__)
-    const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(a), __float_as_uint(b), false, false);
-    a = __uint_as_float(r[0]);
-    b = __uint_as_float(r[1]);
-#endif
-}
-
 // a piece of work: rows [row0, row0 + rows) of a tile's expert
 struct Piece {
     int tile, j, q, n0, m0, row0, rows, end;     // end: the expert's last row, exclusive

@@ -319,6 +319,16 @@ def test_dgrad(name, N, M, hint, two, gather, dtype):
     _check_dgrad(m, COUNTS[name], N, M, dtype, hint, two, gather)
 
 
+@pytest.mark.parametrize("counts", [[128, 129, 192, 193, 16, 17, 144], [320, 321, 256, 257, 224, 33], [641, 96, 0, 384, 209]])
+@pytest.mark.parametrize("out_dim", [64, 136, 584, 832])
+def test_dgrad_tiles_of_every_row_count(counts, out_dim):
+    """Row counts at which a tile's rings and fragments change, contractions of one to thirteen steps."""
+    import combine_grouped_gemm_amd as m
+    print(f"[dgrad tiles] {counts} out_dim={out_dim}", flush=True)
+    _check_dgrad(m, counts, out_dim, 264, torch.bfloat16, 0, 0, False)
+    _check_dgrad(m, counts, out_dim, 512, torch.bfloat16, 200, 1, True)
+
+
 @pytest.mark.parametrize("hint", [1, 40, 100, 300])
 @pytest.mark.parametrize("two", [0, 1])
 def test_dgrad_packed(two, hint):
