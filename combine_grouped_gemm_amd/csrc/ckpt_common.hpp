@@ -46,6 +46,13 @@ __device__ __forceinline__ uint32_t pack_low_bytes(uint32_t a, uint32_t b, uint3
     return __builtin_amdgcn_perm(b, a, 0x0c0c0400u) | __builtin_amdgcn_perm(d, c, 0x04000c0cu);
 }
 
+// the codes of four neighbouring columns under scale s
+__device__ __forceinline__ uint32_t ckpt_codes4(const floatx4& v, float s) {
+    const float rs = ckpt_recip(s);
+    const uint32_t q = pack_low_bytes(ckpt_code(v[0], rs), ckpt_code(v[1], rs), ckpt_code(v[2], rs), ckpt_code(v[3], rs));
+    return s == s ? q : 0u;
+}
+
 // the value of byte k of w as a signed code
 template <int k>
 __device__ __forceinline__ float code_value(uint32_t w) {
@@ -60,6 +67,28 @@ __device__ __forceinline__ uint32_t row16_max_u32(uint32_t v) {
     v = most(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x141, 0xF, 0xF, true));
     v = most(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x140, 0xF, 0xF, true));
     return v;
+}
+
+// By groups of 16 lanes: even groups keep a and get the next group's a as b, odd groups get the
+// group before's b as a and keep b.
+__device__ __forceinline__ void exchange_groups_u32(uint32_t& a, uint32_t& b) {
+#if defined(__HIP_DEVICE_COMPILE__)
+    const auto r = __builtin_amdgcn_permlane16_swap(a, b, false, false);
+    a = r[0];
+    b = r[1];
+#endif
+}
+
+// Maxima over the four lanes l, l + 16, l + 32, l + 48: of a in lanes 0..31, of b in 32..63.
+__device__ __forceinline__ uint32_t lane_groups_max(uint32_t a, uint32_t b) {
+#if defined(__HIP_DEVICE_COMPILE__)
+    const auto r = __builtin_amdgcn_permlane32_swap(a, b, false, false);
+    const uint32_t m = r[0] > r[1] ? r[0] : r[1];
+    const auto q = __builtin_amdgcn_permlane16_swap(m, m, false, false);
+    return q[0] > q[1] ? q[0] : q[1];
+#else
+    return 0u;
+#endif
 }
 
 }  // namespace moeep

@@ -104,14 +104,11 @@ __device__ __forceinline__ void exchange_rows(float& a, float& b) {
     a = __int_as_float(__builtin_amdgcn_update_dpp(x, y, kRor8, 0xf, 0xc, false));
     b = __int_as_float(__builtin_amdgcn_update_dpp(y, x, kRor8, 0xf, 0x3, false));
 }
-// Of two values of every lane, by groups of 16 lanes: even groups keep a and get the next
-// group's a beside it, odd groups keep b behind the group before's b.
 __device__ __forceinline__ void exchange_groups(float& a, float& b) {
-#if defined(__HIP_DEVICE_COMPILE__)
-    const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(a), __float_as_uint(b), false, false);
-    a = __uint_as_float(r[0]);
-    b = __uint_as_float(r[1]);
-#endif
+    uint32_t x = __float_as_uint(a), y = __float_as_uint(b);
+    exchange_groups_u32(x, y);
+    a = __uint_as_float(x);
+    b = __uint_as_float(y);
 }
 
 // 16 rows by 64 columns of a wave (four fragments, the columns as the matrix instructions' row

@@ -160,7 +160,11 @@ __device__ __forceinline__ uint32_t lds_addr(const void* p) {
 //
 // CKPT (gate/up only): g and u also leave as 8-bit checkpoints.  A tile's 128 gate and
 // 128 up rows are one checkpoint block each, its columns spread over four waves: the
-// epilogue joins the waves' row maxima in LDS and stages the codes as it does h.
+// epilogue joins the waves' row maxima in LDS.  With the weights as the matrix instructions'
+// row operand a lane has its row's maxima and four neighbouring codes in registers, and nothing
+// else goes through LDS: 32 experts of 288 rows, 7168 -> 2048, 474 us (without checkpoints
+// 468; codes a byte at a time through LDS 470 beside 447 on another card, a ragged EP share 600
+// -> 582 with the values of both checkpoints).
 template <int BM, bool GATED, bool CKPT = false>
 __global__ __launch_bounds__(512, 1) void grouped_gemm_bf16_wide_kernel(FfnArgs p) {
     static_assert(!CKPT || GATED, "checkpoints belong to gate/up");
@@ -322,7 +326,12 @@ __global__ __launch_bounds__(512, 1) void grouped_gemm_bf16_wide_kernel(FfnArgs 
         // The tile for NF valid fragments: no branch inside a step.
         // v_mfma_f32_16x16x32_bf16: lane l feeds row (l % 16) with k-chunk (l / 16)
         // of the 32-wide step for both operands and receives rows 4*(l/16)+e,
-        // column l % 16 of the 16x16 result.
+        // column l % 16 of the 16x16 result.  CKPT takes the weights as the row operand:
+        // then a lane has columns 4*(l/16)+e of row l % 16, neighbours to pack.
+        auto mma = [](bf16x8 rows, bf16x8 weights, floatx4 c) {
+            if constexpr (CKPT) return __builtin_amdgcn_mfma_f32_16x16x32_bf16(weights, rows, c, 0, 0, 0);
+            else return __builtin_amdgcn_mfma_f32_16x16x32_bf16(rows, weights, c, 0, 0, 0);
+        };
         auto tile = [&](auto NFc) {
             constexpr int NF = decltype(NFc)::value;
             floatx4 acc[NF > 0 ? NF : 1][FN];
@@ -355,7 +364,7 @@ __global__ __launch_bounds__(512, 1) void grouped_gemm_bf16_wide_kernel(FfnArgs 
                                 ab + lds_lane[kk] + (wm + WMW * (i + 1)) * 16 * ROWB);
 #pragma unroll
                         for (int f = 0; f < FN; ++f)
-                            acc[i][f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(acur, bfr[f], acc[i][f], 0, 0, 0);
+                            acc[i][f] = mma(acur, bfr[f], acc[i][f]);
                         const int slot = kk * NF + i;
                         if (slot < LPS) issue_one(nextbuf, slot, knext, live);
                         if (i + 1 < NF) acur = anext;
@@ -411,7 +420,7 @@ __global__ __launch_bounds__(512, 1) void grouped_gemm_bf16_wide_kernel(FfnArgs 
                                 ab + lds_lane[kk] + (wm + WMW * (i + 1)) * 16 * ROWB);
 #pragma unroll
                         for (int f = 0; f < FN; ++f)
-                            acc[i][f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(acur, bfr[kk][f], acc[i][f], 0, 0, 0);
+                            acc[i][f] = mma(acur, bfr[kk][f], acc[i][f]);
                         const int slot = kk * NF + i;
                         if (slot < LPS) issue_slot(slot);
                         if (i + 1 < NF) acur = anext;
@@ -455,7 +464,7 @@ __global__ __launch_bounds__(512, 1) void grouped_gemm_bf16_wide_kernel(FfnArgs 
                                 ab + lds_lane[kk] + (wm + WMW * (i + 1)) * 16 * ROWB);
 #pragma unroll
                         for (int f = 0; f < FN; ++f)
-                            acc[i][f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(acur, bfr[f], acc[i][f], 0, 0, 0);
+                            acc[i][f] = mma(acur, bfr[f], acc[i][f]);
                         if (kk == 0 && i < A_ITERS) issue_one(nextbuf, i, k + 1, liveA);
                         if (kk == 1 && i < B_ITERS) issue_one(I, A_ITERS + i, k + 2, liveB);
                         if (i + 1 < NF) acur = anext;
@@ -500,6 +509,73 @@ __global__ __launch_bounds__(512, 1) void grouped_gemm_bf16_wide_kernel(FfnArgs 
             // the loads issued by the last step read nothing but still count
             wait_vmcnt<0>();
 
+            if constexpr (CKPT) {
+                // ---- epilogue with checkpoints: a lane holds row r16 of each fragment, columns 4 g + e
+                // of its 16.  Row maxima: over the lane's columns, over the four lane groups (g in the
+                // lower half, u in the upper), over the four waves in LDS.
+                int ln = lane;
+                asm volatile("" : "+v"(ln));                    // keeps what depends on it out of the k-loop's registers
+                const int r16 = ln & 15;
+                constexpr int FO = FN / 2;
+                static_assert(BM * WNW * 8 <= BN * ROWB && FO == 2, "row maxima [row][wave column][g, u] fit in a stage");
+                char* maxima = reinterpret_cast<char*>(sb0);
+                wait_lgkm0();
+                block_barrier();
+#pragma unroll
+                for (int i = 0; i < NF; ++i) {
+                    uint32_t m[2] = {0, 0};
+#pragma unroll
+                    for (int f = 0; f < FN; ++f)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) m[f / FO] = max(m[f / FO], __float_as_uint(acc[i][f][e]) & 0x7fffffffu);
+                    const uint32_t most = lane_groups_max(m[0], m[1]);
+                    const int trow = (wm + WMW * i) * 16 + r16;
+                    if ((ln & 16) == 0) *reinterpret_cast<uint32_t*>(maxima + (trow * WNW + wn) * 8 + (ln >> 5) * 4) = most;
+                    __builtin_amdgcn_sched_barrier(0);           // (all rows at once would spill)
+                }
+                wait_lgkm0();
+                block_barrier();
+                const int nb = (N + kCkptBlock - 1) / kCkptBlock;
+                // lanes of two groups exchange so that each has 8 neighbouring columns
+                const int col = fcol(0) + ((ln >> 4) & 1) * 16 + (ln >> 5) * 8;
+#pragma unroll
+                for (int i = 0; i < NF; ++i) {
+                    const int trow = (wm + WMW * i) * 16 + r16;
+                    const uint4 a = *reinterpret_cast<const uint4*>(maxima + trow * WNW * 8);
+                    const uint4 b = *reinterpret_cast<const uint4*>(maxima + trow * WNW * 8 + 16);
+                    const float gs = ckpt_scale(max(max(a.x, a.z), max(b.x, b.z)));
+                    const float us = ckpt_scale(max(max(a.y, a.w), max(b.y, b.w)));
+                    const size_t row = (size_t)(row0 + trow);
+                    if (wn == 0 && ln < 16 && trow < nvalid) {
+                        p.gate_s[row * nb + tc.nt] = gs;
+                        p.up_s[row * nb + tc.nt] = us;
+                    }
+                    uint32_t hv[FO][2];
+#pragma unroll
+                    for (int f = 0; f < FO; ++f)
+#pragma unroll
+                        for (int e = 0; e < 4; e += 2)
+                            hv[f][e / 2] = pack_bf16x2(silu(acc[i][f][e]) * acc[i][f + FO][e],
+                                                       silu(acc[i][f][e + 1]) * acc[i][f + FO][e + 1]);
+                    uint32_t gq[FO], uq[FO];
+#pragma unroll
+                    for (int f = 0; f < FO; ++f) {
+                        gq[f] = ckpt_codes4(acc[i][f], gs);
+                        uq[f] = ckpt_codes4(acc[i][f + FO], us);
+                    }
+                    exchange_groups_u32(hv[0][0], hv[1][0]);
+                    exchange_groups_u32(hv[0][1], hv[1][1]);
+                    exchange_groups_u32(gq[0], gq[1]);
+                    exchange_groups_u32(uq[0], uq[1]);
+                    if (trow < nvalid && col < N) {
+                        const size_t at = row * N + col;
+                        *reinterpret_cast<uint4*>(Out + at) = make_uint4(hv[0][0], hv[0][1], hv[1][0], hv[1][1]);
+                        *reinterpret_cast<uint2*>(p.gate_q + at) = make_uint2(gq[0], gq[1]);
+                        *reinterpret_cast<uint2*>(p.up_q + at) = make_uint2(uq[0], uq[1]);
+                    }
+                    __builtin_amdgcn_sched_barrier(0);
+                }
+            } else {
             // ---- epilogue: every wave stages its bf16 outputs in a private LDS
             // region (both stages are free once every wave is past the k-loop)
             // and stores whole 16-byte row chunks: 8 per 128-byte output row
@@ -549,76 +625,6 @@ __global__ __launch_bounds__(512, 1) void grouped_gemm_bf16_wide_kernel(FfnArgs 
                     }
                 }
             }
-            if constexpr (CKPT) {
-                int ln = lane;
-                asm volatile("" : "+v"(ln));                    // keeps what depends on it out of the k-loop's registers
-                // row maxima of this wave's 32 columns, [row][wave column][g, u], behind the regions of sb0
-                constexpr int kMax = 2 * RSZ;
-                static_assert(kMax + BM * WNW * 8 <= BN * ROWB && FO == 2, "row maxima fit behind the regions");
-                char* maxima = reinterpret_cast<char*>(sb0) + kMax;
-#pragma unroll
-                for (int i = 0; i < NF; ++i)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        uint32_t m[2];
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            const uint32_t a = __float_as_uint(acc[i][2 * h][e]) & 0x7fffffffu;
-                            const uint32_t b = __float_as_uint(acc[i][2 * h + 1][e]) & 0x7fffffffu;
-                            m[h] = row16_max_u32(a > b ? a : b);
-                        }
-                        const int trow = (wm + WMW * i) * 16 + (ln >> 4) * 4 + e;
-                        if ((ln & 15) == 0)
-                            *reinterpret_cast<uint2*>(maxima + (trow * WNW + wn) * 8) = make_uint2(m[0], m[1]);
-                        __builtin_amdgcn_sched_barrier(0);       // (all rows at once would spill)
-                    }
-                wait_lgkm0();
-                block_barrier();
-                const int nb = (N + kCkptBlock - 1) / kCkptBlock;
-                constexpr int CPITCH = 32 + 16;                 // staged codes of a row: 32 bytes, padded
-                constexpr int CPF = PF * OPITCH / (2 * CPITCH); // fragments a pass, g and u
-                static_assert(CPF >= 1, "staged codes fit in a region");
-#pragma unroll
-                for (int p0 = 0; p0 < NF; p0 += CPF) {
-#pragma unroll
-                    for (int ii = 0; ii < CPF; ++ii) {
-                        const int i = p0 + ii;
-                        if (i < NF) {
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                const int trow = (wm + WMW * i) * 16 + (ln >> 4) * 4 + e;
-                                const uint4 a = *reinterpret_cast<const uint4*>(maxima + trow * WNW * 8);
-                                const uint4 b = *reinterpret_cast<const uint4*>(maxima + trow * WNW * 8 + 16);
-                                const float gs = ckpt_scale(max(max(a.x, a.z), max(b.x, b.z)));
-                                const float us = ckpt_scale(max(max(a.y, a.w), max(b.y, b.w)));
-                                const float grs = ckpt_recip(gs), urs = ckpt_recip(us);
-                                if (wn == 0 && (ln & 15) == 0 && trow < nvalid) {
-                                    p.gate_s[(size_t)(row0 + trow) * nb + tc.nt] = gs;
-                                    p.up_s[(size_t)(row0 + trow) * nb + tc.nt] = us;
-                                }
-                                char* at = region + (ii * 16 + (ln >> 4) * 4 + e) * 2 * CPITCH + (ln & 15);
-#pragma unroll
-                                for (int f = 0; f < 2; ++f) {
-                                    at[f * 16] = gs == gs ? (char)ckpt_code(acc[i][f][e], grs) : (char)0;
-                                    at[CPITCH + f * 16] = us == us ? (char)ckpt_code(acc[i][f + 2][e], urs) : (char)0;
-                                }
-                                __builtin_amdgcn_sched_barrier(0);
-                            }
-                        }
-                    }
-                    // out in 8-byte pieces: 4 of a row's 32 bytes of g, then 4 of u
-#pragma unroll
-                    for (int q = 0; q < CPF * 16 * 8 / 64; ++q) {
-                        const int piece = q * 64 + ln, lrow = piece / 8, half = (piece / 4) & 1, ch = piece & 3;
-                        const int i = p0 + lrow / 16;
-                        const int trow = (wm + WMW * i) * 16 + lrow % 16;
-                        const int col = colbase + ch * 8;
-                        if (i < NF && trow < nvalid && col < N) {
-                            const uint2 v = *reinterpret_cast<const uint2*>(region + lrow * 2 * CPITCH + half * CPITCH + ch * 8);
-                            *reinterpret_cast<uint2*>((half ? p.up_q : p.gate_q) + (size_t)(row0 + trow) * N + col) = v;
-                        }
-                    }
-                }
             }
         };
         // a switch, not a chain of ifs: with the chain the compiler no longer
