@@ -68,7 +68,7 @@ __global__ __launch_bounds__(512, 1) void dgrad_wide_kernel(FfnArgs p) {
     __shared__ uint4 s_r6[4 * BLK / 16];             // blocks 6 to 9, or the third weight stage
     __shared__ int s_pre[kMaxExperts + 1];
     __shared__ uint16_t s_ord[kMaxExperts];
-    static_assert(sizeof(s_b0) >= kMaxExperts * sizeof(int), "row counts fit in the first weight stage");
+    static_assert(sizeof(s_b0) >= 2 * kMaxExperts * sizeof(int), "row counts and blocks' loads fit in the first weight stage");
     static_assert(sizeof(s_r6) == sizeof(s_b0), "a weight stage");
     __shared__ int s_tmp[NT / kWave];
 
@@ -91,9 +91,13 @@ __global__ __launch_bounds__(512, 1) void dgrad_wide_kernel(FfnArgs p) {
     const int G = gridDim.x;
     const int v = total <= G ? xcd_chunk_order() : xcd_block_order();
 
-    for (int rnd = 0; rnd * (long long)G < total; ++rnd) {
-        const int tau = round_tile_back(rnd, v, G, total);
-        if (tau < 0) continue;                           // (an odd last round fills from the other end)
+    const int full = total / G;
+    int last = round_tile_back(full, v, G, total);
+    if (full > 0 && full <= kLookBack && total > full * G && G <= kMaxExperts)
+        last = last_round_tile<NT, kBM>(full, v, G, total, n_tiles_n, p.E_loc, s_pre, s_ord, reinterpret_cast<int*>(s_b0), s_tmp);
+    for (int rnd = 0; rnd <= full; ++rnd) {
+        const int tau = rnd < full ? round_tile_back(rnd, v, G, total) : last;
+        if (tau < 0) break;
         const TileCoord tc = decode_tile<kBM>(tau, n_tiles_n, s_pre, p, s_ord);
         const int j = tc.j, row0 = tc.row0, nvalid = tc.nvalid;
         const int col0 = tc.nt * BN;

@@ -233,10 +233,18 @@ __global__ __launch_bounds__(512, 1) void grouped_gemm_bf16_wide_kernel(FfnArgs 
     const uint16_t* __restrict__ W1 = static_cast<const uint16_t*>(p.w1);
     uint16_t* __restrict__ Out = static_cast<uint16_t*>(p.out);
 
-    for (int rnd = 0, tau = v; CKPT ? rnd * (long long)G < total : tau < total; ++rnd, tau += G) {
+    const int full = CKPT ? total / G : 0;
+    int last = -1;
+    if constexpr (CKPT) {
+        static_assert(sizeof(sa0) >= 2 * kMaxExperts * sizeof(int), "row counts and blocks' loads fit in the first row stage");
+        last = round_tile_back(full, v, G, total);
+        if (full > 0 && full <= kLookBack && total > full * G && G <= kMaxExperts)
+            last = last_round_tile<NT, BM>(full, v, G, total, n_tiles_n, p.E_loc, s_pre, s_ord, reinterpret_cast<int*>(sa0), s_tmp);
+    }
+    for (int rnd = 0, tau = v; CKPT ? rnd <= full : tau < total; ++rnd, tau += G) {
         if constexpr (CKPT) {
-            tau = round_tile_back(rnd, v, G, total);
-            if (tau < 0) continue;
+            tau = rnd < full ? round_tile_back(rnd, v, G, total) : last;
+            if (tau < 0) break;
         }
         const TileCoord tc = decode_tile<BM>(tau, n_tiles_n, s_pre, p, s_ord);
         const int j = tc.j, row0 = tc.row0, nvalid = tc.nvalid;

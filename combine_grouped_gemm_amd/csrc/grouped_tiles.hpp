@@ -173,12 +173,54 @@ __device__ __forceinline__ int round_tile(int r, int v, int b, int G, int total)
 
 // Tile of round r for position v of G when the tiles lie in decreasing cost: every other
 // round runs backwards, so that a block with a large tile of one round has a small one of
-// the next (-1: none).  A rank with 26 to 1131 rows an expert, 1.3 rounds of dgrad tiles: 309
-// -> 302 us; 2.6 rounds of gate/up with checkpoints: 607 -> 581.
+// the next (-1: none).
 __device__ __forceinline__ int round_tile_back(int r, int v, int G, int total) {
     const long long tau = (long long)r * G + ((r & 1) != 0 ? G - 1 - v : v);
     return tau < total ? (int)tau : -1;
 }
+
+// Tile of the last, partly filled round: after full rounds of round_tile_back the largest tile
+// left goes to the block with the least work so far (the tiles in build_tile_prefix_sorted's
+// BY_TILE order, s_rows as it left them, with G more ints behind its first kMaxExperts).  A
+// tile's cost: a step of wide tiles takes the time of its weights up to 128 rows and grows from
+// there to 1.5 times that at 320.  Ends with a barrier.  (128 experts of 6 to 500 rows, a pair at
+// 2880 x 2880, 6.3 rounds: 898 -> 879 us; gate/up of an EP share, 2.7 rounds, 581 -> 578.)
+template <int NT, int BM>
+__device__ __forceinline__ int last_round_tile(int full, int v, int G, int total, int n_tiles_n, int E_loc,
+                                               const int* s_pre, const uint16_t* s_ord, int* s_rows, int* s_tmp) {
+    const int tid = threadIdx.x;
+    int* load = s_rows + kMaxExperts;
+    for (int t = tid; t < G; t += NT) {
+        int sum = 0;
+        for (int r = 0; r < full; ++r) {
+            const int tau = round_tile_back(r, t, G, total);
+            int lo = 0, hi = E_loc;
+            while (hi - lo > 1) {
+                const int mid = (lo + hi) >> 1;
+                if (n_tiles_n * s_pre[mid] <= tau) lo = mid; else hi = mid;
+            }
+            const int rows = (s_rows[s_ord[lo]] + s_pre[lo + 1] - s_pre[lo] - 1) / (s_pre[lo + 1] - s_pre[lo]);
+            sum += max(140, 96 + rows * 3 / 8);
+        }
+        load[t] = sum;
+    }
+    __syncthreads();
+    const int mine = load[v];
+    int less = 0;
+    for (int t = tid; t < G; t += NT) less += load[t] < mine || (load[t] == mine && t < v) ? 1 : 0;
+#pragma unroll
+    for (int d = 32; d > 0; d >>= 1) less += __shfl_xor(less, d, kWave);
+    if (tid % kWave == 0) s_tmp[tid / kWave] = less;
+    __syncthreads();
+    int rank = 0;
+#pragma unroll
+    for (int w = 0; w < NT / kWave; ++w) rank += s_tmp[w];
+    __syncthreads();
+    const int tau = __builtin_amdgcn_readfirstlane(full * G + rank);
+    return tau < total ? tau : -1;
+}
+// rounds that last_round_tile looks back on: what it gains falls with their number
+constexpr int kLookBack = 12;
 
 // XCD-major renumbering of the block index (identity when G % 8 != 0).
 __device__ __forceinline__ int xcd_block_order() {
