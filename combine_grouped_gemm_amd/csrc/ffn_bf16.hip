@@ -63,7 +63,7 @@ __global__ __launch_bounds__(64 * WMW * WNW) void grouped_gemm_bf16_kernel(FfnAr
     const int total = n_tiles_n * s_pre[p.E_loc];
 
     const int G = gridDim.x;
-    const int v = xcd_block_order();
+    const int v = CKPT && total <= G ? xcd_chunk_order() : xcd_block_order();
 
     const uint16_t* __restrict__ A = static_cast<const uint16_t*>(p.a);
     const uint16_t* __restrict__ W0 = static_cast<const uint16_t*>(p.w0);
@@ -275,9 +275,11 @@ bool wide_reaches(const FfnArgs& a) {
 }  // namespace
 
 hipError_t launch_ffn_ckpt_bf16(const FfnArgs& a, hipStream_t stream) {
+    // tiles whose width is a checkpoint block of both products; 32 experts, 7168 -> 2048: of 40
+    // rows 294 us in 64-row tiles, 315 in wide ones, of 100 rows 474 and 331; of 2 rows, 2880 ->
+    // 2880, 174 us in 16-row tiles, 191 in 64-row ones
     const bool wide_ok = wide_reaches(a);
-    if (wide_ok && a.rows_hint >= 192) return launch_wide<320, true, true>(a, stream);
-    if (wide_ok && a.rows_hint >= 64) return launch_wide<256, true, true>(a, stream);
+    if (wide_ok && a.rows_hint >= 64) return launch_wide<320, true, true>(a, stream);
     if (a.rows_hint < 24) return launch_cfg<16, 256, 1, 4, true, true>(a, stream);
     return launch_cfg<64, 256, 1, 4, true, true>(a, stream);
 }

@@ -14,6 +14,9 @@
 // then written once, each lane finding its experts among the picks (K compares an
 // expert, by lane reads), so that no store depends on another.  1 - s of the
 // sigmoid comes from e^-|l|, which does not cancel.
+//
+// 8192 tokens of 256 experts, 8 picks, sigmoid: 8.8 us, of which 8.4 MB of dlogits take 1.3 at
+// the rate of a fill and a launch 2 to 3; 64 tokens of 16, 3.4 us.
 #include "device_common.hpp"
 #include "launch.hpp"
 #include "moeep.h"

@@ -9,7 +9,13 @@
 // What bounds it is writing dw: with a few hundred rows an expert a 256 x 256 tile has 4 to
 // 8 steps and 256 KB of fp32 to write.  So the steps of all of a block's tiles run as one
 // sequence: the first step of the next tile is loaded under the last one of this tile,
-// and the tile's stores drain under the next tile's steps.
+// and the tile's stores drain under the next tile's steps.  32 experts of 85 to 1026 rows, a pair of
+// 2048 x 7168 in fp32 from a checkpoint: 1063 us, 3.76 GB of dw at 3.5 TB/s (in bf16 800 us); with
+// a base, 2.12 GB at 2880 x 2880, 447 us, the rate of a copy.  256 CUs that do nothing but store
+// such tiles reach 5.5 TB/s, and a load waits behind the stores of all of its CU's waves, not only
+// its own's (stores alone 384 us, loads alone 98, both 469), so deeper rings, waves that only
+// load and blocks side by side do not help: a ring of four 32-row stages 1057 us where this
+// takes 900, two 128 x 128 blocks a CU 1549.
 //
 // The row of a gathered operand (src_of) is looked up once per piece of work (a tile, or
 // 1024 rows of one): the piece's rows are listed in LDS during the piece before, so that a
@@ -546,7 +552,10 @@ hipError_t launch_any(const WgradArgs& a, hipStream_t stream) {
     const unsigned long long y_rows = a.gather_dy ? a.src_rows : kPieceRows;
     const unsigned long long x_rows = a.gather_x ? a.src_rows : CKPT ? a.cap : kPieceRows;
     const bool far = y_rows * a.N * 2 >= kReach || x_rows * a.M * (CKPT ? 1 : 2) >= kReach || 256ull * a.M * 4 >= kReach;
+    // (64-bit addresses where not needed: 32 experts of 256 rows, 2048 x 7168, 575 us beside 456)
     if (far) return launch_tiles<256, 256, CKPT, F32, true>(a, stream);
+    // large tiles once there is one for every CU: that case 456 us, in small ones 525; 8 experts of
+    // 64 rows, 1024 x 1024 (128 large tiles) 15.3, small 13.1; 4 of 512 rows, 512 x 512, 25.4 and 13.0
     const long long large = (long long)a.E_loc * (a.dy[1] != nullptr ? 2 : 1) * ((a.N + 255) / 256) * ((a.M + 255) / 256);
     if (large >= device_cu_count()) return launch_tiles<256, 256, CKPT, F32, false>(a, stream);
     return launch_tiles<128, 128, CKPT, F32, false>(a, stream);
