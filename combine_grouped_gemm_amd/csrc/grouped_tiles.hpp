@@ -231,7 +231,7 @@ __device__ __forceinline__ int xcd_block_order() {
 // This block's position where there are fewer tiles than blocks: chunks of 8 (tiles that share
 // weights or rows in L2) go to the XCDs in turn, whose links to memory a few tiles would
 // otherwise share one of (dgrad, 7168 x 2048, 16 rows an expert: 4 experts 97 -> 81 us, 16
-// experts 126 -> 94; gate/up with checkpoints of 28 experts of a few rows, 2880 -> 2880, 162 -> 135;
+// experts 126 -> 94; gate/up with checkpoints of 28 experts of a few rows, 2880 -> 2880, 164 -> 155;
 // with every block busy the XCD-major order is the better one, 256 rows of 32
 // experts 214 us, in chunks 228).
 __device__ __forceinline__ int xcd_chunk_order() {
