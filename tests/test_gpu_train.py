@@ -678,6 +678,50 @@ def test_layer_trains_on_a_side_stream_and_in_a_graph():
         assert torch.equal(a, b)
 
 
+def _ragged(E, most, seed):
+    return [int(v) for v in np.random.default_rng(seed).integers(0, most + 1, E)]
+
+
+@pytest.mark.parametrize("E,most,cols", [(70, 400, 1032), (70, 400, 2056), (200, 900, 264), (33, 100, 2048), (300, 700, 2056)])
+def test_rounds_of_ragged_tiles(E, most, cols):
+    """From less than one round of wide tiles to more than the last one's assignment looks back on:
+    each tile is done once, whichever block gets it."""
+    import combine_grouped_gemm_amd as m
+    counts = _ragged(E, most, E + cols)
+    print(f"[rounds] E={E} rows={sum(counts)} cols={cols}", flush=True)
+    _check_dgrad(m, counts, 72, cols, torch.bfloat16, 200, 0, True)
+    _check_gate_up(m, counts, 72, cols, torch.bfloat16, 200)
+
+
+def test_two_layers_at_once_on_two_streams():
+    import combine_grouped_gemm_amd as m
+    sets = [_train_layer(m, T, 8, 2, 264, 136, 0, 8, torch.bfloat16, seed=T) for T in (300, 170)]
+    grads = [s[0].new_grads() for s in sets]
+
+    def step(k):
+        layer, x, lg, w, dout = sets[k]
+        layer.forward(x, lg, w)
+        layer.backward(dout, lg, w, grads[k])
+
+    def seen(k):
+        return [t.clone() for t in (sets[k][0].out, sets[k][0].dx, sets[k][0].dlogits, *grads[k].values())]
+
+    alone = []
+    for k in range(2):
+        step(k)
+        alone.append(seen(k))
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(5):
+        for k in range(2):
+            with torch.cuda.stream(streams[k]):
+                step(k)
+    torch.cuda.synchronize()
+    for k in range(2):
+        for a, b in zip(alone[k], seen(k)):
+            assert torch.equal(a, b)
+
+
 # ------------------------------------------------------------------ far offsets
 def test_wgrad_and_dgrad_past_4_gib():
     """The last expert's matrices lie beyond 2^32 bytes, and beyond 2^31 elements of dw."""
