@@ -39,8 +39,8 @@ __device__ __forceinline__ int dy_row(const FfnArgs& p, int r) {
 // stream of weights (16 rows 141 us, 128 rows 151: 6.7 and 6.2 TB/s; with two stages of each 150
 // and 160); from 192 rows on the matrix instructions beside it (256 rows 208 us, 1.15 PFLOP/s;
 // 640 rows 460 us, 1.31); of ragged experts the rounds that tiles of unlike cost do not fill (a
-// rank with 26 to 1131 rows an expert, 336 to 400 tiles: 300 us).  A pair at 2880 x 2880, 128
-// experts of 128 rows on average: 888 us, with two stages 980.
+// rank with 26 to 1131 rows an expert, 336 to 400 tiles: 289 us).  A pair at 2880 x 2880, 128
+// experts of 128 rows on average: 870 us, with two stages 980.
 constexpr int kBM = 320;
 
 // A tile's plan: MODE 0, 1, 2 as above with the row fragments NF of a wave
