@@ -3,10 +3,16 @@
 //
 // With picks P of a token, dw the gradient of its weights w and s the scores:
 //   softmax over the picks     dl_e = w_e (dw_e - sum_P w dw)               e in P
-//   scored                     a_e = scale / S (dw_e - sum_P (s / S) dw)    renormalised, S = sum_P s (0 if S is 0)
-//                              a_e = scale dw_e                             otherwise
+//   scored, renormalised       with the shares q = s / sum_P s: a_e = scale q_e (dw_e - sum_P q dw)
+//     sigmoid                  dl_e = a_e (1 - s_e)                         e in P
+//     softmax over all         dl_e = a_e (sum_P a = 0: the other experts have none)
+//   scored, as they are        a_e = scale dw_e
 //     sigmoid                  dl_e = a_e s_e (1 - s_e)                     e in P
 //     softmax over all         dl_e = s_e ([e in P] a_e - sum_P s a)        every e that is not masked
+// The shares come from scores relative to the largest pick's, so that they hold where
+// the scores themselves underflow: the forward call forms them in 64 bits, and weights
+// and gradients of picks at -90 are ordinary numbers.  Where its sum is zero in 64
+// bits too the weights are zeros and pass nothing.
 // The choice itself is a step and passes no gradient, so neither does the bias.
 //
 // A wave takes a token.  Lane k holds pick k (picks beyond 64 in further
@@ -46,11 +52,14 @@ __device__ __forceinline__ float logit(const void* l, size_t i) {
     else return static_cast<const float*>(l)[i];
 }
 
-// s and 1 - s of the sigmoid
-__device__ __forceinline__ void sigmoid2(float l, float& s, float& rest) {
-    const float e = expf(-fabsf(l)), big = 1.0f / (1.0f + e), small = e * big;
-    s = l >= 0.0f ? big : small;
-    rest = l >= 0.0f ? small : big;
+// 1 / (1 + e^-l) is zero in 64 bits from here down: e^-l passes the largest double, e^709.78271289
+constexpr float kNoSigmoid = -0x1.62e43p9f;
+
+// s / e^low and 1 - s of the sigmoid; low is 0, or negative and the largest l
+__device__ __forceinline__ void sigmoid2(float l, float low, float& s, float& rest) {
+    const float e = expf(-fabsf(l)), big = 1.0f / (1.0f + e);
+    s = l >= 0.0f ? big : expf(l - low) * big;
+    rest = l >= 0.0f ? e * big : big;
 }
 
 // NP: picks a lane (K <= 64 NP)
@@ -85,6 +94,7 @@ __global__ __launch_bounds__(kWaves * kWave) void route_backward_kernel(RouteBwd
             total = wave_sum(total);
         }
         // the picks
+        bool none = false;                     // the scores' sum is zero in 64 bits
         int at[NP];
         float s[NP], rest[NP], dw[NP];
 #pragma unroll
@@ -121,14 +131,29 @@ __global__ __launch_bounds__(kWaves * kWave) void route_backward_kernel(RouteBwd
 #pragma unroll
             for (int i = 0; i < NP; ++i) s[i] = at[i] >= 0 ? s[i] / z : 0.0f;
         } else {
+            // renormalised: scores divided by e^low (softmax: by the largest pick's), so that they hold
+            // in 32 bits
+            float low = 0.0f;
+            if (p.renorm) {
+                low = -INFINITY;
+#pragma unroll
+                for (int i = 0; i < NP; ++i) low = fmaxf(low, at[i] >= 0 ? s[i] : -INFINITY);
+                low = wave_max(low);
+                if constexpr (SCORE == MOE_SCORE_SIGMOID) {
+                    none = low <= kNoSigmoid;
+                    low = fminf(low, 0.0f);
+                } else if (low - top < -700.0f) {
+                    none = exp((double)low - (double)top) / (double)total == 0.0;
+                }
+            }
 #pragma unroll
             for (int i = 0; i < NP; ++i) {
-                if constexpr (SCORE == MOE_SCORE_SIGMOID) sigmoid2(s[i], s[i], rest[i]);
-                else s[i] = expf(s[i] - top) / total;
+                if constexpr (SCORE == MOE_SCORE_SIGMOID) sigmoid2(s[i], low, s[i], rest[i]);
+                else s[i] = p.renorm ? expf(s[i] - low) : expf(s[i] - top) / total;
                 if (at[i] < 0) s[i] = 0.0f;
             }
         }
-        // a: the gradient of the scores (picks: of the logits)
+        // a: the gradient of the logits (scores as they are, softmax over all: of the scores)
         float a[NP], sum = 0.0f;
         if constexpr (SCORE == MOE_SCORE_PICKS) {
 #pragma unroll
@@ -141,20 +166,27 @@ __global__ __launch_bounds__(kWaves * kWave) void route_backward_kernel(RouteBwd
 #pragma unroll
             for (int i = 0; i < NP; ++i) S += s[i];
             S = wave_sum(S);
+            const bool some = S > 0.0f && !none;
 #pragma unroll
-            for (int i = 0; i < NP; ++i) sum += S > 0.0f ? s[i] / S * dw[i] : 0.0f;
+            for (int i = 0; i < NP; ++i) {
+                s[i] = some ? s[i] / S : 0.0f;
+                sum += s[i] * dw[i];
+            }
             sum = wave_sum(sum);
 #pragma unroll
-            for (int i = 0; i < NP; ++i) a[i] = S > 0.0f ? p.scale / S * (dw[i] - sum) : 0.0f;
+            for (int i = 0; i < NP; ++i) {
+                a[i] = some ? p.scale * (s[i] * (dw[i] - sum)) : 0.0f;
+                if constexpr (SCORE == MOE_SCORE_SIGMOID) a[i] *= rest[i];
+            }
         } else {
 #pragma unroll
-            for (int i = 0; i < NP; ++i) a[i] = p.scale * dw[i];
+            for (int i = 0; i < NP; ++i) {
+                a[i] = p.scale * dw[i];
+                if constexpr (SCORE == MOE_SCORE_SIGMOID) a[i] *= s[i] * rest[i];
+            }
         }
-        float all = 0.0f;                      // softmax over all: sum_P s a
-        if constexpr (SCORE == MOE_SCORE_SIGMOID) {
-#pragma unroll
-            for (int i = 0; i < NP; ++i) a[i] *= s[i] * rest[i];
-        } else if constexpr (SCORE == MOE_SCORE_SOFTMAX) {
+        float all = 0.0f;                      // softmax over all, scores as they are: sum_P s a
+        if (SCORE == MOE_SCORE_SOFTMAX && !p.renorm) {
 #pragma unroll
             for (int i = 0; i < NP; ++i) all += at[i] >= 0 ? s[i] * a[i] : 0.0f;
             all = wave_sum(all);
@@ -171,7 +203,7 @@ __global__ __launch_bounds__(kWaves * kWave) void route_backward_kernel(RouteBwd
                 }
             }
             if (e < E) {
-                if constexpr (SCORE == MOE_SCORE_SOFTMAX) {
+                if (SCORE == MOE_SCORE_SOFTMAX && !p.renorm) {
                     const float l = logit<BF16>(p.logits, row + e);
                     v = l > kLow ? expf(l - top) / total * (v - all) : 0.0f;
                 }

@@ -592,10 +592,11 @@ moe_status_t moe_ffn_wgrad(const void* dy, const void* dy2, const void* x, moe_d
  *   topk_ids (B, K + n_shared) as it wrote them, dtopk_w (B, K + n_shared) fp32; the
  *   shared slots' weights are constant, their columns are not read.
  *   dlogits (B, E) fp32 out, every entry written: 0 for experts that the weights
- *   do not depend on (softmax over all: for masked ones only).  Slots with id -1
- *   add nothing.
+ *   do not depend on (all but the picks; softmax over all without renorm: the
+ *   masked ones).  Slots with id -1 add nothing.
  * The choice of experts is piecewise constant and passes no gradient; neither
- * does the balance bias.  Weights renormalised by a sum of zero pass none.
+ * does the balance bias.  Weights renormalised by a sum that is zero in 64 bits, as
+ * moe_route_scored forms it, are zeros and pass none.
  */
 moe_status_t moe_route_backward(const void* logits, moe_dtype_t logits_dt, const int32_t* topk_ids,
                                 const float* dtopk_w, int B, int E, int K, moe_score_t score, int renorm, float scale,
