@@ -84,12 +84,12 @@ __global__ __launch_bounds__(kWaves * kWave) void route_backward_kernel(RouteBwd
         if constexpr (SCORE == MOE_SCORE_SOFTMAX) {
             for (int e = lane; e < E; e += kWave) {
                 const float l = logit<BF16>(p.logits, row + e);
-                if (l > kLow) top = fmaxf(top, l);
+                if (!(l <= kLow)) top = fmaxf(top, l);
             }
             top = wave_max(top);
             for (int e = lane; e < E; e += kWave) {
                 const float l = logit<BF16>(p.logits, row + e);
-                if (l > kLow) total += expf(l - top);
+                if (!(l <= kLow)) total += expf(l - top);        // a NaN makes it NaN
             }
             total = wave_sum(total);
         }
@@ -166,7 +166,9 @@ __global__ __launch_bounds__(kWaves * kWave) void route_backward_kernel(RouteBwd
 #pragma unroll
             for (int i = 0; i < NP; ++i) S += s[i];
             S = wave_sum(S);
-            const bool some = S > 0.0f && !none;
+            // a NaN sum is not zero: it reaches the gradients, as it does the weights
+            if (SCORE == MOE_SCORE_SOFTMAX && total != total) S = total;
+            const bool some = S != 0.0f && (!none || S != S);
 #pragma unroll
             for (int i = 0; i < NP; ++i) {
                 s[i] = some ? s[i] / S : 0.0f;
@@ -203,9 +205,9 @@ __global__ __launch_bounds__(kWaves * kWave) void route_backward_kernel(RouteBwd
                 }
             }
             if (e < E) {
-                if (SCORE == MOE_SCORE_SOFTMAX && !p.renorm) {
+                if (SCORE == MOE_SCORE_SOFTMAX && (!p.renorm || total != total)) {
                     const float l = logit<BF16>(p.logits, row + e);
-                    v = l > kLow ? expf(l - top) / total * (v - all) : 0.0f;
+                    v = !(l <= kLow) ? expf(l - top) / total * (v - all) : 0.0f;
                 }
                 p.dlogits[row + e] = v;
             }

@@ -597,6 +597,8 @@ moe_status_t moe_ffn_wgrad(const void* dy, const void* dy2, const void* x, moe_d
  * The choice of experts is piecewise constant and passes no gradient; neither
  * does the balance bias.  Weights renormalised by a sum that is zero in 64 bits, as
  * moe_route_scored forms it, are zeros and pass none.
+ * NaN weights of moe_route_scored have NaN gradients: a NaN logit's own where it is
+ * picked, with renorm all of the token's picks', with softmax all that are not masked.
  */
 moe_status_t moe_route_backward(const void* logits, moe_dtype_t logits_dt, const int32_t* topk_ids,
                                 const float* dtopk_w, int B, int E, int K, moe_score_t score, int renorm, float scale,
