@@ -231,7 +231,7 @@ __global__ __launch_bounds__(kThreads) void wgrad_kernel(WgradArgs p, int tiles)
         rest /= tm;
         const int n0 = rest % tn * T;
         rest /= tn;
-        const int pairs = p.dy[1] != nullptr ? 2 : 1, q = rest % pairs, j = rest / pairs;
+        const int pairs = p.dw[1] != nullptr ? 2 : 1, q = rest % pairs, j = rest / pairs;
         const float* dy = static_cast<const float*>(p.dy[q]);
         const int r0 = clampi(p.offsets[j], 0, p.cap), r1 = clampi(p.offsets[j + 1], r0, p.cap);
         float4 ry[F], rx[F];
@@ -316,13 +316,13 @@ hipError_t launch_dgrad_f32(const FfnArgs& a, hipStream_t stream) {
 template <int T>
 hipError_t launch_wgrad_tiles(const WgradArgs& a, hipStream_t stream) {
     // (api.hip bounds dw)
-    const int tiles = a.E_loc * (a.dy[1] != nullptr ? 2 : 1) * ((a.N + T - 1) / T) * ((a.M + T - 1) / T);
+    const int tiles = a.E_loc * (a.dw[1] != nullptr ? 2 : 1) * ((a.N + T - 1) / T) * ((a.M + T - 1) / T);
     const int most = device_cu_count() * 8;
     hipLaunchKernelGGL(wgrad_kernel<T>, dim3(tiles < most ? tiles : most), dim3(kThreads), 0, stream, a, tiles);
     return hipGetLastError();
 }
 hipError_t launch_wgrad_f32(const WgradArgs& a, hipStream_t stream) {
-    const long long large = (long long)a.E_loc * (a.dy[1] != nullptr ? 2 : 1) * ((a.N + 63) / 64) * ((a.M + 63) / 64);
+    const long long large = (long long)a.E_loc * (a.dw[1] != nullptr ? 2 : 1) * ((a.N + 63) / 64) * ((a.M + 63) / 64);
     return large >= device_cu_count() ? launch_wgrad_tiles<64>(a, stream) : launch_wgrad_tiles<32>(a, stream);
 }
 

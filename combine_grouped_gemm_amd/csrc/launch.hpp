@@ -159,7 +159,7 @@ hipError_t launch_dgrad_bf16(const FfnArgs& a, hipStream_t stream);            /
 // weight gradients: dw_j = base_j + sum over expert j's rows r of dy[r]^T x[r], for one
 // or two dy that share x
 struct WgradArgs {
-    const void* dy[2];        // (rows, N); dy[1] may be null
+    const void* dy[2];        // (rows, N); null where there are no rows, or no pair
     const void* x;            // (rows, M)
     const float* x_scales;    // checkpoint x: (rows, ceil(M/128)); else nullptr
     const int32_t* src_of;    // (cap): the gathered operand's row of r is src_of[r] / per
@@ -169,7 +169,7 @@ struct WgradArgs {
     const int32_t* offsets;   // (E_loc + 1)
     int E_loc, cap, N, M;
     const void* base[2];      // (E_loc, N, M) or null; may be dw itself
-    void* dw[2];
+    void* dw[2];              // dw[1] null: no pair
     bool dw_f32;
 };
 hipError_t launch_wgrad_f32(const WgradArgs& a, hipStream_t stream);           // grad_f32.hip

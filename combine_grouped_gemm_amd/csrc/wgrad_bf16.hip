@@ -128,7 +128,7 @@ __global__ __launch_bounds__(512, 1) void wgrad_kernel(WgradArgs p, int tiles_n,
         // Groups of kGroup tiles along the in columns, within them all tiles along the out
         // columns, then the pair: the 32 tiles that run together on an XCD share 8 + 4 operand
         // columns of tiles in its L2, and the next ones go on with the 4.
-        const unsigned pairs = p.dy[1] != nullptr ? 2 : 1, per = (unsigned)tiles_n * (unsigned)tiles_m * pairs;
+        const unsigned pairs = p.dw[1] != nullptr ? 2 : 1, per = (unsigned)tiles_n * (unsigned)tiles_m * pairs;
         w.j = uniform((int)((unsigned)tau / per));
         unsigned rest = (unsigned)tau - (unsigned)w.j * per;
         const unsigned band = (unsigned)tiles_n * kGroup * pairs, b = rest / band;
@@ -538,7 +538,7 @@ hipError_t launch_tiles(const WgradArgs& a, hipStream_t stream) {
         per_cu = n;
     }
     const int tn = (a.N + TN - 1) / TN, tm = (a.M + TM - 1) / TM;
-    const int tiles = a.E_loc * (a.dy[1] != nullptr ? 2 : 1) * tn * tm;      // (api.hip bounds dw)
+    const int tiles = a.E_loc * (a.dw[1] != nullptr ? 2 : 1) * tn * tm;      // (api.hip bounds dw)
     const int most = device_cu_count() * per_cu;
     hipLaunchKernelGGL((wgrad_kernel<TN, TM, CKPT, F32, FAR>), dim3(tiles < most ? tiles : most), dim3(512), 0, stream, a, tn, tm,
                        tiles);
@@ -556,7 +556,7 @@ hipError_t launch_any(const WgradArgs& a, hipStream_t stream) {
     if (far) return launch_tiles<256, 256, CKPT, F32, true>(a, stream);
     // large tiles once there is one for every CU: that case 456 us, in small ones 525; 8 experts of
     // 64 rows, 1024 x 1024 (128 large tiles) 15.3, small 13.1; 4 of 512 rows, 512 x 512, 25.4 and 13.0
-    const long long large = (long long)a.E_loc * (a.dy[1] != nullptr ? 2 : 1) * ((a.N + 255) / 256) * ((a.M + 255) / 256);
+    const long long large = (long long)a.E_loc * (a.dw[1] != nullptr ? 2 : 1) * ((a.N + 255) / 256) * ((a.M + 255) / 256);
     if (large >= device_cu_count()) return launch_tiles<256, 256, CKPT, F32, false>(a, stream);
     return launch_tiles<128, 128, CKPT, F32, false>(a, stream);
 }
