@@ -86,13 +86,15 @@ class MoELayer:
         self.expected_rows = max(1, (self.T * self.K_routed) // self.E_routed)
         dev = torch.device(device)
         i32 = dict(dtype=torch.int32, device=dev)
-        T, cap = self.T, max(self.cap, 1)
+        # the training calls take the row count from the buffers' shapes: a row that the layout does
+        # not know would count as an expert's
+        T, cap = self.T, self.cap if self.train else max(self.cap, 1)
         self.topk_ids = torch.empty((T, K), **i32)
         self.topk_w = torch.empty((T, K), dtype=torch.float32, device=dev)
         self.counts = torch.empty(E, **i32)
         self.offsets = torch.empty(self.E_loc + 1, **i32)     # contiguous: offsets; masked: m (E_loc)
         self.row_of = torch.empty((T, K), **i32)
-        self.src_of = torch.empty(cap, **i32)
+        self.src_of = torch.empty(max(cap, 1), **i32)
         self.layout_ws = torch.empty(max(moe_layout_workspace_bytes(T, K, E), 256),
                                      dtype=torch.uint8, device=dev)
         act = _TORCH[act_dtype]
