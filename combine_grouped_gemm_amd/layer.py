@@ -212,7 +212,13 @@ class MoELayer:
         return self.out
 
     # the backward pass ----------------------------------------------------------
+    def _need_dout(self, dout):
+        # (a token's row is looked up in dout, and one that it lacks reads as zeros)
+        if dout.dim() != 2 or dout.shape[0] < self.T or dout.shape[1] != self.H:
+            raise ValueError(f"dout must have shape {(self.T, self.H)} (got {tuple(dout.shape)})")
+
     def dgrad_down(self, dout, w, stream=None):
+        self._need_dout(dout)
         moe_ffn_dgrad(dout, self.offsets, w["down"], src_of=self.src_of, slots_per_token=self.K, dx=self.dh,
                       expected_rows=self.expected_rows, stream=stream)
 
@@ -221,6 +227,7 @@ class MoELayer:
                             self.dgate, self.dup, self.hw, self.dtopk_w, stream=stream)
 
     def wgrad_down(self, dout, grads, accumulate=False, stream=None):
+        self._need_dout(dout)
         moe_ffn_wgrad(dout, self.hw, self.offsets, src_of=self.src_of, slots_per_token=self.K, gather="dy",
                       base=grads["down"] if accumulate else None, dw=grads["down"],
                       expected_rows=self.expected_rows, stream=stream)
@@ -264,11 +271,11 @@ class MoELayer:
 
     def backward(self, dout, logits, w, grads, accumulate=False, stream=None):
         """Gradients of the last forward for dout (T, H), the loss gradient of its out in
-        the storage type.  logits and w as forward took them; grads from new_grads():
-        the weights' gradients are written there (accumulate: added).  Returns dx (T, H)
-        and dlogits (T, E), the layer's own buffers; dtopk_w holds the gradient of the
-        routing weights.  dx is that of the experts; the router's projection, outside
-        the layer, adds its own from dlogits."""
+        the storage type (rows behind the T tokens' are not read).  logits and w as
+        forward took them; grads from new_grads(): the weights' gradients are written
+        there (accumulate: added).  Returns dx (T, H) and dlogits (T, E), the layer's own
+        buffers; dtopk_w holds the gradient of the routing weights.  dx is that of the
+        experts; the router's projection, outside the layer, adds its own from dlogits."""
         for _, run in self.backward_stages(dout, logits, w, grads, accumulate):
             run(stream)
         return self.dx, self.dlogits
