@@ -5,6 +5,7 @@
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
+#include <initializer_list>
 
 #include "launch.hpp"
 #include "moeep.h"
@@ -270,10 +271,34 @@ moe_status_t check_gather(bool gathers, int slots_per_token, int src_rows) {
     return MOE_OK;
 }
 
-// whether two buffers share no byte (a null one shares none)
+// whether two buffers share no byte (a null or an empty one shares none)
 bool apart(const void* a, size_t na, const void* b, size_t nb) {
     const char *p = static_cast<const char*>(a), *q = static_cast<const char*>(b);
-    return !p || !q || p + na <= q || q + nb <= p;
+    return !p || !q || na == 0 || nb == 0 || p + na <= q || q + nb <= p;
+}
+
+struct Span {
+    const void* p;
+    size_t bytes;
+};
+bool apart(const Span& a, const Span& b) { return apart(a.p, a.bytes, b.p, b.bytes); }
+
+// whether the outputs share no byte with each other or with an input: blocks of a launch
+// write them while others still read
+bool outputs_apart(std::initializer_list<Span> outs, std::initializer_list<Span> ins) {
+    for (const Span* o = outs.begin(); o != outs.end(); ++o) {
+        for (const Span* q = o + 1; q != outs.end(); ++q)
+            if (!apart(*o, *q)) return false;
+        for (const Span& i : ins)
+            if (!apart(*o, i)) return false;
+    }
+    return true;
+}
+
+Span ints(const int32_t* p, long long n) { return Span{p, (size_t)n * sizeof(int32_t)}; }
+// fp32 scales of rows of checkpoints
+Span ckpt_scales(const float* p, int rows, int cols) {
+    return Span{p, (size_t)rows * (((size_t)cols + MOE_CKPT_BLOCK - 1) / MOE_CKPT_BLOCK) * sizeof(float)};
 }
 
 // (columns are counted in ints, a tile's last ones past the end too)
@@ -294,7 +319,10 @@ moe_status_t checkpoint(void* x, moe_dtype_t x_dt, const int32_t* offsets, int E
         REQUIRE(aligned16(x), "%s must be 16-byte aligned", write ? "x" : "out");
         REQUIRE((reinterpret_cast<uintptr_t>(q) & 7u) == 0, "q must be 8-byte aligned");
         const size_t n = (size_t)cap_rows * cols;
-        REQUIRE(apart(x, n * elem_size(x_dt), q, n), "%s and q must not overlap", write ? "x" : "out");
+        const Span values{x, n * elem_size(x_dt)}, codes{q, n}, sc = ckpt_scales(scales, cap_rows, cols);
+        const Span off = ints(offsets, (long long)E_local + 1);
+        REQUIRE(write ? outputs_apart({codes, sc}, {values, off}) : outputs_apart({values}, {codes, sc, off}),
+                write ? "q and scales must not overlap each other, x or offsets" : "out must not overlap q, scales or offsets");
     }
     moeep::CkptArgs a;
     a.x = x;
@@ -725,11 +753,11 @@ moe_status_t moe_ffn_gate_up_train(const void* xd, const int32_t* offsets, int E
     REQUIRE((h && gate_q && gate_scales && up_q && up_scales) || cap_rows == 0, "null h or checkpoint pointer");
     REQUIRE(aligned16(w_gate) && aligned16(w_up) && aligned16(h) && aligned16(gate_q) && aligned16(up_q),
             "weights, h and codes must be 16-byte aligned");
-    const size_t n = (size_t)cap_rows * I, esz = elem_size(act_dt);
-    REQUIRE(apart(h, n * esz, gate_q, n) && apart(h, n * esz, up_q, n) && apart(gate_q, n, up_q, n) &&
-                apart(h, n * esz, xd, (size_t)cap_rows * H * esz) && apart(gate_q, n, xd, (size_t)cap_rows * H * esz) &&
-                apart(up_q, n, xd, (size_t)cap_rows * H * esz),
-            "h and the codes must overlap neither each other nor xd");
+    const size_t n = (size_t)cap_rows * I, esz = elem_size(act_dt), w_bytes = (size_t)E_local * I * weight_ld(wt, H) * esz;
+    REQUIRE(outputs_apart({{h, n * esz}, {gate_q, n}, {up_q, n}, ckpt_scales(gate_scales, cap_rows, I),
+                           ckpt_scales(up_scales, cap_rows, I)},
+                          {{xd, (size_t)cap_rows * H * esz}, {w_gate, w_bytes}, {w_up, w_bytes}, ints(offsets, E_local + 1)}),
+            "h and the checkpoints must overlap neither each other nor an input");
     auto f = ffn_args(xd, nullptr, Rows{offsets, nullptr, 0}, E_local, cap_rows, H, I, w_gate, w_up, nullptr, nullptr,
                       h, nullptr, expected_rows, wt.dt, weight_ld(wt, H));
     f.gate_q = gate_q;
@@ -756,14 +784,14 @@ moe_status_t moe_swiglu_backward(const void* dh, moe_dtype_t act_dt, const int8_
         REQUIRE(aligned16(dh) && aligned16(gate_q) && aligned16(up_q) && aligned16(dgate) && aligned16(dup) &&
                     aligned16(hw),
                 "dh, codes, dgate, dup and hw must be 16-byte aligned");
-        const size_t n = (size_t)cap_rows * I, nf = n * elem_size(act_dt);
-        REQUIRE(apart(dgate, nf, dup, nf) && apart(dgate, nf, hw, nf) && apart(dup, nf, hw, nf),
-                "dgate, dup and hw must not overlap");
-        for (const void* o : {dgate, dup, hw})
-            REQUIRE(apart(o, nf, dh, nf) && apart(o, nf, gate_q, n) && apart(o, nf, up_q, n),
-                    "dgate, dup and hw must not overlap dh or the codes");
     }
     if (B > 0) REQUIRE(row_of && topk_w && dtopk_w, "null row_of, topk_w or dtopk_w");
+    const size_t n = (size_t)cap_rows * I, nf = n * elem_size(act_dt);
+    const Span slots = ints(row_of, (long long)B * K), w{topk_w, slots.bytes}, dw{dtopk_w, slots.bytes};
+    const Span gs = ckpt_scales(gate_scales, cap_rows, I), us = ckpt_scales(up_scales, cap_rows, I);
+    REQUIRE(outputs_apart({{dgate, nf}, {dup, nf}, {hw, nf}, dw}, {{dh, nf}, {gate_q, n}, {up_q, n}, gs, us, slots}) &&
+                outputs_apart({{dgate, nf}, {dup, nf}, {hw, nf}}, {w}) && (dtopk_w == topk_w || apart(dw, w)),
+            "outputs must overlap neither each other nor an input (dtopk_w may be topk_w)");
     moeep::SwigluBwdArgs a;
     a.dh = dh;
     a.gate_q = gate_q;
@@ -803,8 +831,11 @@ moe_status_t moe_ffn_dgrad(const void* dy, const void* dy2, const int32_t* src_o
     REQUIRE(aligned16(dy) && aligned16(dy2) && aligned16(w) && aligned16(w2) && aligned16(dx),
             "dy, weights and dx must be 16-byte aligned");
     const size_t esz = elem_size(act_dt), dy_bytes = (size_t)(src_of ? src_rows : cap_rows) * out_dim * esz,
-                 dx_bytes = (size_t)cap_rows * in_dim * esz;
-    REQUIRE(apart(dx, dx_bytes, dy, dy_bytes) && apart(dx, dx_bytes, dy2, dy_bytes), "dx must not overlap dy or dy2");
+                 w_bytes = (size_t)E_local * out_dim * weight_ld(wt, in_dim) * esz;
+    REQUIRE(outputs_apart({{dx, (size_t)cap_rows * in_dim * esz}},
+                          {{dy, dy_bytes}, {dy2, dy_bytes}, {w, w_bytes}, {w2, w_bytes}, ints(src_of, cap_rows),
+                           ints(offsets, E_local + 1)}),
+            "dx must not overlap an input");
     auto f = ffn_args(dy, nullptr, Rows{offsets, nullptr, 0}, E_local, cap_rows, out_dim, in_dim, w, w2, nullptr,
                       nullptr, dx, nullptr, expected_rows, wt.dt, weight_ld(wt, in_dim));
     f.a2 = w2 ? dy2 : nullptr;
@@ -849,7 +880,6 @@ moe_status_t moe_ffn_wgrad(const void* dy, const void* dy2, const void* x, moe_d
             "dy, x, base and dw must be 16-byte aligned");
     REQUIRE((long long)out_dim * in_dim <= (1ll << 38) / E_local, "dw is too large");
     const size_t dw_bytes = (size_t)E_local * out_dim * in_dim * elem_size(dw_dt);
-    REQUIRE(!dw2 || apart(dw, dw_bytes, dw2, dw_bytes), "dw and dw2 must not overlap");
     const void* const bases[2] = {base, base2};
     void* const dws[2] = {dw, dw2};
     for (int j = 0; j < 2; ++j)
@@ -858,9 +888,11 @@ moe_status_t moe_ffn_wgrad(const void* dy, const void* dy2, const void* x, moe_d
                 "a base must be its own dw or lie apart from both");
     const size_t dy_bytes = (size_t)dy_rows * out_dim * elem_size(act_dt),
                  x_bytes = (size_t)x_rows * in_dim * (x_dt == MOE_CKPT8 ? 1 : elem_size(act_dt));
-    for (const void* d : {static_cast<const void*>(dw), static_cast<const void*>(dw2)})
-        REQUIRE(apart(d, dw_bytes, dy, dy_bytes) && apart(d, dw_bytes, dy2, dy_bytes) && apart(d, dw_bytes, x, x_bytes),
-                "dw must not overlap dy, dy2 or x");
+    REQUIRE(outputs_apart({{dw, dw_bytes}, {dw2, dw_bytes}},
+                          {{dy, dy_bytes}, {dy2, dy_bytes}, {x, x_bytes},
+                           ckpt_scales(x_dt == MOE_CKPT8 ? x_scales : nullptr, x_rows, in_dim),
+                           ints(gathers ? src_of : nullptr, cap_rows), ints(offsets, E_local + 1)}),
+            "dw and dw2 must overlap neither each other nor an input but their own bases");
     moeep::WgradArgs a;
     a.dy[0] = dy;
     a.dy[1] = dw2 ? dy2 : nullptr;
@@ -904,6 +936,12 @@ moe_status_t moe_route_backward(const void* logits, moe_dtype_t logits_dt, const
     REQUIRE(n_shared >= 0 && n_shared <= 1024 - E, "need 0 <= n_shared and E + n_shared <= 1024");
     REQUIRE((long long)B * (K + n_shared) <= 0x7fffffffLL, "B*(K+n_shared) must fit in int32");
     if (B > 0) REQUIRE(logits && topk_ids && dtopk_w && dlogits, "null pointer argument");
+    const size_t slots = (size_t)B * (K + n_shared), grid = (size_t)B * E;
+    const Span out{dlogits, grid * sizeof(float)};
+    // (a token's wave has read a logit before it writes the gradient there)
+    REQUIRE(outputs_apart({out}, {ints(topk_ids, slots), {dtopk_w, slots * sizeof(float)}, ints(phys_of_logical, E)}) &&
+                ((logits_dt == MOE_F32 && logits == dlogits) || apart(out, Span{logits, grid * elem_size(logits_dt)})),
+            "dlogits must not overlap an input (fp32 logits may be its own)");
     moeep::RouteBwdArgs a;
     a.logits = logits;
     a.ids = topk_ids;

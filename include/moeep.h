@@ -495,19 +495,22 @@ moe_status_t moe_combine(const void* y, moe_dtype_t y_dt, int cap_rows, const in
  * depend on expected_rows beyond the order of fp32 sums (moe_ffn_wgrad's not at all),
  * and are the same from run to run.  Columns of any operand: a multiple of 8, at most
  * 2^24.
+ * Outputs overlap neither each other nor an input; three may be an input itself:
+ * moe_ffn_wgrad's dw its own base, moe_swiglu_backward's dtopk_w its topk_w, and
+ * moe_route_backward's dlogits its fp32 logits.
  *
  * moe_checkpoint_rows -- an 8-bit checkpoint (MOE_CKPT8) of the rows of x.
  *   x       (cap_rows, cols) F32 or BF16.
  *   Valid rows: as in moe_quant_rows (offsets NULL: all).  Other rows of q and
  *   scales are not written.
- *   q       (cap_rows, cols) int8 out, 8-byte aligned, not overlapping x.
+ *   q       (cap_rows, cols) int8 out, 8-byte aligned.
  *   scales  (cap_rows, ceil(cols/128)) fp32 out: the smallest 2^e, -126 <= e <=
  *           121, with max |v| <= 127 * 2^e over the block; 1 for a block of zeros.
  *   code = v / scale to the nearest integer, ties to even, within +-127.  A block
  *   with a NaN or an infinity gets scale NaN and codes 0.  bf16 holds every
  *   code * scale exactly.
  * moe_checkpoint_values -- the values back: out (cap_rows, cols) of out_dt (F32 or
- *   BF16) = code * scale on the valid rows; out does not overlap q.
+ *   BF16) = code * scale on the valid rows.
  */
 moe_status_t moe_checkpoint_rows(const void* x, moe_dtype_t x_dt, const int32_t* offsets, int E_local, int cap_rows,
                                  int cols, int8_t* q, float* scales, hipStream_t stream);
@@ -519,7 +522,7 @@ moe_status_t moe_checkpoint_values(const int8_t* q, const float* scales, const i
  * MOE_W_PACKED) that also leaves g and u, before SwiGLU, as 8-bit checkpoints
  * taken from their fp32 sums:
  *   gate_q, up_q (cap_rows, I) int8, gate_scales, up_scales (cap_rows,
- *   ceil(I/128)) fp32 out.  h and the codes overlap neither each other nor xd.
+ *   ceil(I/128)) fp32 out.
  * Rows past offsets[E_local] of the outputs are not written.
  */
 moe_status_t moe_ffn_gate_up_train(const void* xd, const int32_t* offsets, int E_local, int cap_rows, int H, int I,
@@ -533,9 +536,8 @@ moe_status_t moe_ffn_gate_up_train(const void* xd, const int32_t* offsets, int E
  * topk_w[t,k], sg = 1 / (1 + exp(-g)) and h = g sg u:
  *   dgate[r] = w dh[r] u sg (1 + g (1 - sg)),  dup[r] = w dh[r] g sg,
  *   hw[r] = w h,  dtopk_w[t,k] = sum_i dh[r,i] h_i.
- *   dh (cap_rows, I), dgate, dup, hw (cap_rows, I) of act_dt, the outputs
- *   overlapping neither each other nor dh and the codes; row_of, topk_w, dtopk_w
- *   (B, K).
+ *   dh (cap_rows, I), dgate, dup, hw (cap_rows, I) of act_dt; row_of, topk_w,
+ *   dtopk_w (B, K).
  * Slots whose row lies outside [0, cap_rows) get dtopk_w 0; rows that no slot
  * names are not written.  Two slots must not name one row.
  */
@@ -555,7 +557,7 @@ moe_status_t moe_swiglu_backward(const void* dh, moe_dtype_t act_dt, const int8_
  *   moe_layout: row r reads dy's row src_of[r] / slots_per_token of src_rows (a
  *   token's gradient, sent back to all of its rows); rows that name none of them
  *   read zeros.  src_rows and slots_per_token are unused without src_of.
- * Rows past offsets[E_local] of dx are not written; dx overlaps neither dy nor dy2.
+ * Rows past offsets[E_local] of dx are not written.
  */
 moe_status_t moe_ffn_dgrad(const void* dy, const void* dy2, const int32_t* src_of, int slots_per_token, int src_rows,
                            const int32_t* offsets, int E_local, int cap_rows, int out_dim, int in_dim,
@@ -571,7 +573,7 @@ moe_status_t moe_ffn_dgrad(const void* dy, const void* dy2, const int32_t* src_o
  *   out_dim, in_dim) of dw_dt: F32, or BF16 with BF16 activations.
  *   base NULL: zeros.  base may be dw itself (gradients accumulated over
  *   micro-batches), else it must not overlap dw or dw2.  dy2 and dw2 NULL: one
- *   product.  dw overlaps none of dy, dy2, x.
+ *   product.
  *   gather: the operand (x; dy and dy2) whose row of r is src_of[r] /
  *   slots_per_token of src_rows; rows that name none of them add nothing.  The
  *   other has cap_rows rows.  MOE_GATHER_NONE: both do; src_of, slots_per_token
