@@ -9,10 +9,10 @@
 //   scored, as they are        a_e = scale dw_e
 //     sigmoid                  dl_e = a_e s_e (1 - s_e)                     e in P
 //     softmax over all         dl_e = s_e ([e in P] a_e - sum_P s a)        every e that is not masked
-// The shares come from scores relative to the largest pick's, so that they hold where
-// the scores themselves underflow: the forward call forms them in 64 bits, and weights
-// and gradients of picks at -90 are ordinary numbers.  Where its sum is zero in 64
-// bits too the weights are zeros and pass nothing.
+// The forward call forms the shares in 64 bits, so weights and gradients of picks at -90 are
+// ordinary numbers: where the scores' sum is too small for 32 bits they are taken relative to
+// the largest pick's.  (Relative ones throughout cost 8192 tokens of 256 experts 0.7 us.)  Where
+// the sum is zero in 64 bits too the weights are zeros and pass nothing.
 // The choice itself is a step and passes no gradient, so neither does the bias.
 //
 // A wave takes a token.  Lane k holds pick k (picks beyond 64 in further
@@ -55,15 +55,19 @@ __device__ __forceinline__ float logit(const void* l, size_t i) {
 // 1 / (1 + e^-l) is zero in 64 bits from here down: e^-l passes the largest double, e^709.78271289
 constexpr float kNoSigmoid = -0x1.62e43p9f;
 
-// s / e^low and 1 - s of the sigmoid; low is 0, or negative and the largest l
-__device__ __forceinline__ void sigmoid2(float l, float low, float& s, float& rest) {
-    const float e = expf(-fabsf(l)), big = 1.0f / (1.0f + e);
-    s = l >= 0.0f ? big : expf(l - low) * big;
-    rest = l >= 0.0f ? e * big : big;
+// Renormalised scores whose sum lies below are formed anew: from here up a pick of 2^-26 of the
+// sum and more is a normal number.
+constexpr float kSmallSum = 0x1p-100f;
+
+// s and 1 - s of the sigmoid
+__device__ __forceinline__ void sigmoid2(float l, float& s, float& rest) {
+    const float e = expf(-fabsf(l)), big = 1.0f / (1.0f + e), small = e * big;
+    s = l >= 0.0f ? big : small;
+    rest = l >= 0.0f ? small : big;
 }
 
-// NP: picks a lane (K <= 64 NP)
-template <bool BF16, int SCORE, int NP>
+// RENORM: of a scored router; NP: picks a lane (K <= 64 NP)
+template <bool BF16, int SCORE, bool RENORM, int NP>
 __global__ __launch_bounds__(kWaves * kWave) void route_backward_kernel(RouteBwdArgs p) {
     __shared__ int s_inv[kMaxE];              // expert of a physical id, -1: none
     const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
@@ -94,7 +98,6 @@ __global__ __launch_bounds__(kWaves * kWave) void route_backward_kernel(RouteBwd
             total = wave_sum(total);
         }
         // the picks
-        bool none = false;                     // the scores' sum is zero in 64 bits
         int at[NP];
         float s[NP], rest[NP], dw[NP];
 #pragma unroll
@@ -131,25 +134,10 @@ __global__ __launch_bounds__(kWaves * kWave) void route_backward_kernel(RouteBwd
 #pragma unroll
             for (int i = 0; i < NP; ++i) s[i] = at[i] >= 0 ? s[i] / z : 0.0f;
         } else {
-            // renormalised: scores divided by e^low (softmax: by the largest pick's), so that they hold
-            // in 32 bits
-            float low = 0.0f;
-            if (p.renorm) {
-                low = -INFINITY;
-#pragma unroll
-                for (int i = 0; i < NP; ++i) low = fmaxf(low, at[i] >= 0 ? s[i] : -INFINITY);
-                low = wave_max(low);
-                if constexpr (SCORE == MOE_SCORE_SIGMOID) {
-                    none = low <= kNoSigmoid;
-                    low = fminf(low, 0.0f);
-                } else if (low - top < -700.0f) {
-                    none = exp((double)low - (double)top) / (double)total == 0.0;
-                }
-            }
 #pragma unroll
             for (int i = 0; i < NP; ++i) {
-                if constexpr (SCORE == MOE_SCORE_SIGMOID) sigmoid2(s[i], low, s[i], rest[i]);
-                else s[i] = p.renorm ? expf(s[i] - low) : expf(s[i] - top) / total;
+                if constexpr (SCORE == MOE_SCORE_SIGMOID) sigmoid2(s[i], s[i], rest[i]);
+                else s[i] = expf(s[i] - top) / total;
                 if (at[i] < 0) s[i] = 0.0f;
             }
         }
@@ -161,14 +149,33 @@ __global__ __launch_bounds__(kWaves * kWave) void route_backward_kernel(RouteBwd
             sum = wave_sum(sum);
 #pragma unroll
             for (int i = 0; i < NP; ++i) a[i] = s[i] * (dw[i] - sum);
-        } else if (p.renorm) {
+        } else if constexpr (RENORM) {
             float S = 0.0f;
 #pragma unroll
             for (int i = 0; i < NP; ++i) S += s[i];
             S = wave_sum(S);
+            bool none = false;
+            if (S < kSmallSum) {               // the scores anew, over that of the largest pick
+                float low = -INFINITY;
+#pragma unroll
+                for (int i = 0; i < NP; ++i) {
+                    s[i] = at[i] >= 0 ? logit<BF16>(p.logits, row + at[i]) : -INFINITY;
+                    low = fmaxf(low, s[i]);
+                }
+                low = wave_max(low);
+                none = SCORE == MOE_SCORE_SIGMOID ? low <= kNoSigmoid
+                                                  : exp((double)low - (double)top) / (double)total == 0.0;
+                S = 0.0f;
+#pragma unroll
+                for (int i = 0; i < NP; ++i) {
+                    // (so small a sigmoid is e^l)
+                    s[i] = at[i] >= 0 ? expf(s[i] - low) : 0.0f;
+                    S += s[i];
+                }
+                S = wave_sum(S);
+            }
             // a NaN sum is not zero: it reaches the gradients, as it does the weights
-            if (SCORE == MOE_SCORE_SOFTMAX && total != total) S = total;
-            const bool some = S != 0.0f && (!none || S != S);
+            const bool some = S != 0.0f && !none;
 #pragma unroll
             for (int i = 0; i < NP; ++i) {
                 s[i] = some ? s[i] / S : 0.0f;
@@ -188,11 +195,14 @@ __global__ __launch_bounds__(kWaves * kWave) void route_backward_kernel(RouteBwd
             }
         }
         float all = 0.0f;                      // softmax over all, scores as they are: sum_P s a
-        if (SCORE == MOE_SCORE_SOFTMAX && !p.renorm) {
+        if constexpr (SCORE == MOE_SCORE_SOFTMAX && !RENORM) {
 #pragma unroll
             for (int i = 0; i < NP; ++i) all += at[i] >= 0 ? s[i] * a[i] : 0.0f;
             all = wave_sum(all);
         }
+        // whether experts that are no picks have a gradient
+        const bool every = SCORE == MOE_SCORE_SOFTMAX &&
+                           (!RENORM || __builtin_amdgcn_readfirstlane(total != total ? 1 : 0) != 0);
         for (int e = lane; e - lane < E; e += kWave) {
             float v = 0.0f;
 #pragma unroll
@@ -205,7 +215,7 @@ __global__ __launch_bounds__(kWaves * kWave) void route_backward_kernel(RouteBwd
                 }
             }
             if (e < E) {
-                if (SCORE == MOE_SCORE_SOFTMAX && (!p.renorm || total != total)) {
+                if (every) {
                     const float l = logit<BF16>(p.logits, row + e);
                     v = !(l <= kLow) ? expf(l - top) / total * (v - all) : 0.0f;
                 }
@@ -215,27 +225,28 @@ __global__ __launch_bounds__(kWaves * kWave) void route_backward_kernel(RouteBwd
     }
 }
 
-template <bool BF16, int SCORE>
+template <bool BF16, int SCORE, bool RENORM>
 hipError_t launch_as(const RouteBwdArgs& a, hipStream_t stream) {
     const int need = (int)(((long long)a.B + kWaves - 1) / kWaves), most = device_cu_count() * 8;
     const dim3 grid(need < most ? need : most), block(kWaves * kWave);
-    if (a.K <= 64) hipLaunchKernelGGL((route_backward_kernel<BF16, SCORE, 1>), grid, block, 0, stream, a);
-    else hipLaunchKernelGGL((route_backward_kernel<BF16, SCORE, 16>), grid, block, 0, stream, a);
+    if (a.K <= 64) hipLaunchKernelGGL((route_backward_kernel<BF16, SCORE, RENORM, 1>), grid, block, 0, stream, a);
+    else hipLaunchKernelGGL((route_backward_kernel<BF16, SCORE, RENORM, 16>), grid, block, 0, stream, a);
     return hipGetLastError();
 }
 
 template <int SCORE>
-hipError_t launch_type(const RouteBwdArgs& a, hipStream_t stream) {
-    return a.bf16 ? launch_as<true, SCORE>(a, stream) : launch_as<false, SCORE>(a, stream);
+hipError_t launch_scored(const RouteBwdArgs& a, hipStream_t stream) {
+    if (a.renorm) return a.bf16 ? launch_as<true, SCORE, true>(a, stream) : launch_as<false, SCORE, true>(a, stream);
+    return a.bf16 ? launch_as<true, SCORE, false>(a, stream) : launch_as<false, SCORE, false>(a, stream);
 }
 
 }  // namespace
 
 hipError_t launch_route_backward(const RouteBwdArgs& a, hipStream_t stream) {
     if (a.B == 0) return hipSuccess;
-    if (a.score == MOE_SCORE_PICKS) return launch_type<MOE_SCORE_PICKS>(a, stream);
-    if (a.score == MOE_SCORE_SIGMOID) return launch_type<MOE_SCORE_SIGMOID>(a, stream);
-    return launch_type<MOE_SCORE_SOFTMAX>(a, stream);
+    if (a.score == MOE_SCORE_PICKS) return launch_as<false, MOE_SCORE_PICKS, false>(a, stream);      // (fp32 logits: api.hip)
+    if (a.score == MOE_SCORE_SIGMOID) return launch_scored<MOE_SCORE_SIGMOID>(a, stream);
+    return launch_scored<MOE_SCORE_SOFTMAX>(a, stream);
 }
 
 }  // namespace moeep

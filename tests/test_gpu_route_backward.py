@@ -41,7 +41,7 @@ def _shares(l, picks):
 
 
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
-@pytest.mark.parametrize("low", [-20.0, -60.0, -89.0, -90.0, -103.0, -110.0, -300.0, -500.0, -690.0])
+@pytest.mark.parametrize("low", [-20.0, -60.0, -69.5, -89.0, -90.0, -103.0, -110.0, -300.0, -500.0, -690.0])
 @pytest.mark.parametrize("T,E,K", [(65, 16, 2), (130, 256, 8), (9, 130, 70)])
 @pytest.mark.parametrize("score", ["sigmoid", "softmax"])
 def test_renormalised_weights_of_small_scores(score, T, E, K, low, dtype):
