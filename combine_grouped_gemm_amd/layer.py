@@ -163,11 +163,12 @@ class MoELayer:
         return self.offsets[:self.E_loc] if self.masked else self.offsets
 
     def dispatch(self, x_segments, stream=None):
+        x_segments = [x_segments] if isinstance(x_segments, torch.Tensor) else list(x_segments)
         moe_dispatch(x_segments, self.row_of, self.cap, self.act_dtype, self.xd, self.xd_scales,
                      stream=stream)
         if self.train:
             t = 0
-            for x in [x_segments] if isinstance(x_segments, torch.Tensor) else x_segments:
+            for x in x_segments:
                 part = slice(t, t + x.shape[0])
                 moe_checkpoint_rows(x, q=self.x_q[part], scales=self.x_s[part], stream=stream)
                 t = part.stop
