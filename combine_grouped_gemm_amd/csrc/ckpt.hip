@@ -4,7 +4,8 @@
 // All three kernels move data and little else: 8 consecutive columns a lane, so
 // that a block of 128 is a DPP row of 16 lanes and its amax four lane moves.  A row goes in
 // pieces of 2048 columns, whose loads are all in flight at once.  8192 rows of 7168 bf16
-// columns: 32 us to pack (5.6 TB/s), 27 back (6.5); a copy 4.9.
+// columns: 44 us to pack (4.1 TB/s; 31 where x lies in the Infinity Cache), 28 back (6.4, the codes
+// still in that cache); a copy 4.9 TB/s.
 #include "ckpt_common.hpp"
 #include "launch.hpp"
 
@@ -165,7 +166,7 @@ __global__ __launch_bounds__(kWaves * kWave) void checkpoint_values_kernel(CkptA
 // A block takes `per` consecutive slots (4 to 32).  Its first wave reads their rows, writes the
 // zeros of those that have none and lists the others in LDS; the waves share the list a row
 // each.  So ranks that hold an eighth of the slots keep their waves busy alike (8192 of
-// 65536 slots, 2048 columns: a wave that walked its own 8 slots 54 us, this 43, 3.9 TB/s), and a
+// 65536 slots, 2048 columns: a wave that walked its own 8 slots 54 us, this 44, 3.8 TB/s), and a
 // wave has all loads of 2048 columns in flight.
 constexpr int kSlots = 32;
 

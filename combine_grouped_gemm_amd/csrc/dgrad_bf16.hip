@@ -36,11 +36,11 @@ __device__ __forceinline__ int dy_row(const FfnArgs& p, int r) {
 // fragments of a step in registers, so that the stage is free before the step's matrix
 // instructions.
 // What bounds it, 32 experts of 7168 x 2048 (256 tiles, one a CU): up to 128 rows each the
-// stream of weights (16 rows 141 us, 128 rows 151: 6.7 and 6.2 TB/s; with two stages of each 150
-// and 160); from 192 rows on the matrix instructions beside it (256 rows 208 us, 1.15 PFLOP/s;
-// 640 rows 460 us, 1.31); of ragged experts the rounds that tiles of unlike cost do not fill (a
-// rank with 26 to 1131 rows an expert, 336 to 400 tiles: 289 us).  A pair at 2880 x 2880, 128
-// experts of 128 rows on average: 870 us, with two stages 980.
+// stream of weights (16 rows 146 us, 128 rows 155: 6.4 and 6.1 TB/s; over one set of operands 141
+// and 151, with two stages of each 150 and 160); from 192 rows on the matrix instructions beside
+// it (256 rows 221 us, 1.09 PFLOP/s; 640 rows 476 us, 1.26); of ragged experts the rounds that
+// tiles of unlike cost do not fill (a rank with 26 to 1131 rows an expert, 336 to 400 tiles: 275
+// us).  A pair at 2880 x 2880, 128 experts of 128 rows on average: 865 us, with two stages 980.
 constexpr int kBM = 320;
 
 // A tile's plan: MODE 0, 1, 2 as above with the row fragments NF of a wave

@@ -276,8 +276,8 @@ bool wide_reaches(const FfnArgs& a) {
 
 hipError_t launch_ffn_ckpt_bf16(const FfnArgs& a, hipStream_t stream) {
     // tiles whose width is a checkpoint block of both products; 32 experts, 7168 -> 2048: of 40
-    // rows 294 us in 64-row tiles, 315 in wide ones, of 100 rows 474 and 331; of 2 rows, 2880 ->
-    // 2880, 174 us in 16-row tiles, 191 in 64-row ones
+    // rows 280 us in 64-row tiles, 314 in wide ones, of 100 rows 442 and 328; of 2 rows, 2880 ->
+    // 2880, 164 us in 16-row tiles, 181 in 64-row ones
     const bool wide_ok = wide_reaches(a);
     if (wide_ok && a.rows_hint >= 64) return launch_wide<320, true, true>(a, stream);
     if (a.rows_hint < 24) return launch_cfg<16, 256, 1, 4, true, true>(a, stream);

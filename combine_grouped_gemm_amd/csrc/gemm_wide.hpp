@@ -162,8 +162,8 @@ __device__ __forceinline__ uint32_t lds_addr(const void* p) {
 // 128 up rows are one checkpoint block each, its columns spread over four waves: the
 // epilogue joins the waves' row maxima in LDS.  With the weights as the matrix instructions'
 // row operand a lane has its row's maxima and four neighbouring codes in registers, and nothing
-// else goes through LDS: 32 experts of 288 rows, 7168 -> 2048, 474 us (without checkpoints
-// 468; codes a byte at a time through LDS 470 beside 447 on another card, a ragged EP share 600
+// else goes through LDS: 32 experts of 288 rows, 7168 -> 2048, 483 us (without checkpoints
+// 473; codes a byte at a time through LDS 470 beside 447 on another card, a ragged EP share 600
 // -> 582 with the values of both checkpoints).
 template <int BM, bool GATED, bool CKPT = false>
 __global__ __launch_bounds__(512, 1) void grouped_gemm_bf16_wide_kernel(FfnArgs p) {

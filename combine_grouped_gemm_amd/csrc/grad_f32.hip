@@ -13,10 +13,10 @@
 // columns, 16 banks apart.
 //
 // Bound by latency at the toy layer's sizes, by LDS reads and few blocks a CU beyond: 8
-// experts, 1024 x 1024, gate/up of 128 rows each 101 us with both checkpoints' values (43
-// TFLOP/s), a pair's input gradient of 512 rows 174 us (98); 16 experts of 256 rows, 512 x
-// 1024, weight gradients 66 us (65).  Where 32 x 32 tiles are taken: 4 experts of 10 rows, a
-// pair at 1024 x 1024, 34 us (64 x 64: 61); 256 x 256 weight gradients of 512 rows 16 us (29).
+// experts, 1024 x 1024, gate/up of 128 rows each 58 us (74 TFLOP/s), a pair's input gradient of
+// 512 rows 160 us (107); 16 experts of 256 rows, 512 x 1024, weight gradients 52 us (82).  Where
+// 32 x 32 tiles are taken, beside 64 x 64 ones on one card: 4 experts of 10 rows, a pair at 1024 x
+// 1024, 34 us and 61; 256 x 256 weight gradients of 512 rows 16 us and 29.
 #include "ckpt_common.hpp"
 #include "grouped_tiles.hpp"
 

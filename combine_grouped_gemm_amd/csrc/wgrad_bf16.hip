@@ -10,8 +10,8 @@
 // 8 steps and 256 KB of fp32 to write.  So the steps of all of a block's tiles run as one
 // sequence: the first step of the next tile is loaded under the last one of this tile,
 // and the tile's stores drain under the next tile's steps.  32 experts of 85 to 1026 rows, a pair of
-// 2048 x 7168 in fp32 from a checkpoint: 1063 us, 3.76 GB of dw at 3.5 TB/s (in bf16 800 us); with
-// a base, 2.12 GB at 2880 x 2880, 447 us, the rate of a copy.  256 CUs that do nothing but store
+// 2048 x 7168 in fp32 from a checkpoint: 1110 us, 3.76 GB of dw at 3.4 TB/s (in bf16 844 us); with
+// a base, 2.12 GB at 2880 x 2880, 444 us, the rate of a copy.  256 CUs that do nothing but store
 // such tiles reach 5.5 TB/s, and a load waits behind the stores of all of its CU's waves, not only
 // its own's (stores alone 384 us, loads alone 98, both 469), so deeper rings, waves that only
 // load and blocks side by side do not help: a ring of four 32-row stages 1057 us where this
@@ -22,8 +22,9 @@
 // load's address is one LDS read away.  Rows past the expert's last one get an offset outside
 // the operand's extent, read nothing and land zeros in both operands.  So do rows of the gathered
 // operand that src_of names nowhere; a list says whether it has any, and then their rows of the
-// other operand are cleared in LDS, so that they add nothing whatever it holds.  (Without a word
-// of this EP share 1045 us, so 1063; with both operands' offsets from the list 1080.)
+// other operand are cleared in LDS, so that they add nothing whatever it holds.  (The EP
+// share above, one set of operands: with no such list 1045 us, so 1063, with both operands'
+// offsets from the list 1080.)
 //
 // A checkpoint x comes through registers: 16 codes a load, issued a step ahead as the
 // direct loads are, turned into the bf16 values they stand for (exact) after the step's
@@ -321,7 +322,7 @@ __global__ __launch_bounds__(512, 1) void wgrad_kernel(WgradArgs p, int tiles_n,
     // dw of a finished tile.  Lane l of a fragment has row n = l % 16 and columns 4 (l / 16) ..
     // + 3.  Lanes exchange values so that a unit is 16 bytes and a store covers whole 128-byte
     // lines (8 rows of them; bf16 in 128-column tiles half lines): such stores can be
-    // non-temporal, and dw, 56 MB a pair at 2048 x 7168, does not push the operands out of L2.
+    // non-temporal, and dw, 117 MB a pair in fp32 at 2048 x 7168, does not push the operands out of L2.
     // (Half lines, kept in L2: EP share 1509 us; whole ones, not kept, 1238 us.)  All stores go
     // out, those past the borders to an offset out of range, so that their number is known to
     // the wait of the next step.  A base is read one row of fragments ahead of the stores.
@@ -552,7 +553,8 @@ hipError_t launch_any(const WgradArgs& a, hipStream_t stream) {
     const unsigned long long y_rows = a.gather_dy ? a.src_rows : kPieceRows;
     const unsigned long long x_rows = a.gather_x ? a.src_rows : CKPT ? a.cap : kPieceRows;
     const bool far = y_rows * a.N * 2 >= kReach || x_rows * a.M * (CKPT ? 1 : 2) >= kReach || 256ull * a.M * 4 >= kReach;
-    // (64-bit addresses where not needed: 32 experts of 256 rows, 2048 x 7168, 575 us beside 456)
+    // (64-bit addresses where not needed: 32 experts of 256 rows, 2048 x 7168, 575 us beside 456, one
+    // set of operands that stays in the Infinity Cache; of several sets 578 for those 456)
     if (far) return launch_tiles<256, 256, CKPT, F32, true>(a, stream);
     // large tiles once there is one for every CU: that case 456 us, in small ones 525; 8 experts of
     // 64 rows, 1024 x 1024 (128 large tiles) 15.3, small 13.1; 4 of 512 rows, 512 x 512, 25.4 and 13.0
