@@ -214,6 +214,8 @@ class MoELayer:
 
     # the backward pass ----------------------------------------------------------
     def _need_dout(self, dout):
+        if not isinstance(dout, torch.Tensor):
+            raise TypeError("dout must be a torch.Tensor")
         # (a token's row is looked up in dout, and one that it lacks reads as zeros)
         if dout.dim() != 2 or dout.shape[0] < self.T or dout.shape[1] != self.H:
             raise ValueError(f"dout must have shape {(self.T, self.H)} (got {tuple(dout.shape)})")

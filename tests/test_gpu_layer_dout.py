@@ -41,3 +41,10 @@ def test_rows_behind_the_tokens():
         seen.append([t.clone() for t in (dx, dlogits, layer.dtopk_w, *grads.values())])
     for a, b in zip(*seen):
         assert bool(torch.isfinite(a).all()) and torch.equal(a, b)
+
+
+def test_dout_that_is_no_tensor():
+    import combine_grouped_gemm_amd as m
+    layer, lg, w, grads = _layer(m)
+    with pytest.raises(TypeError, match="dout must be a torch.Tensor"):
+        layer.backward([[0.0] * 64] * 6, lg, w, grads)
